@@ -30,7 +30,9 @@ SF_K_COUNT = len(FAMILIES)
 EXPORTS = ["sf_create", "sf_verify", "sf_set_debug", "sf_set_rho_dump", "sf_set_attention_mode", "sf_sync_status", "sf_destroy", "sf_status_str",
            "sf_last_error", "sf_get_stats", "sf_set_graphs", "sf_timing_begin", "sf_timing_read", "sf_timing_list",
            "sfk_gemm_bf16", "sfk_gate_noalloc", "sf_inject_stall",
-           "sf_head_create", "sf_head_verify", "sf_head_last_error", "sf_head_destroy"]
+           "sf_head_create", "sf_head_verify", "sf_head_last_error", "sf_head_destroy",
+           "sf_cache_create", "sf_cache_append", "sf_cache_attend", "sf_cache_evict", "sf_cache_sync_status",
+           "sf_cache_last_error", "sf_cache_destroy"]
 
 
 class SfShapes(ctypes.Structure):
@@ -49,6 +51,13 @@ class SfLayerWeights(ctypes.Structure):
 class SfHeadShapes(ctypes.Structure):
     _fields_ = [("d_model", ctypes.c_int), ("vocab", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("rms_eps", ctypes.c_float), ("max_rows", ctypes.c_int)]
+
+
+class SfCacheShapes(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("page_size", ctypes.c_int), ("max_seqs", ctypes.c_int),
+                ("max_len", ctypes.c_int), ("max_pos", ctypes.c_int), ("rms_eps", ctypes.c_float),
+                ("rope_theta", ctypes.c_float), ("track_weights", ctypes.c_int)]
 
 
 class SfStats(ctypes.Structure):
@@ -92,9 +101,21 @@ def _load() -> ctypes.CDLL:
     lib.sf_head_last_error.argtypes = [vp]
     lib.sf_head_last_error.restype = ctypes.c_char_p
     lib.sf_head_destroy.argtypes = [vp]
+    i64 = ctypes.c_int64
+    lib.sf_cache_create.argtypes = [ctypes.POINTER(SfCacheShapes), ctypes.POINTER(vp)]
+    lib.sf_cache_append.argtypes = [vp, vp, vp, i64, c_int, vp, vp, vp, vp, vp, vp, c_int, c_int, i64, vp, vp, i64,
+                                    vp, i64]
+    lib.sf_cache_attend.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp, c_int, c_int, i64, vp, c_float, vp, i64, vp, vp,
+                                    i64]
+    lib.sf_cache_evict.argtypes = [vp, vp, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, i64, c_int, c_int, c_int, vp,
+                                   vp, i64, vp, c_int, i64, vp, vp, vp]
+    lib.sf_cache_sync_status.argtypes = [vp, vp]
+    lib.sf_cache_last_error.argtypes = [vp]
+    lib.sf_cache_last_error.restype = ctypes.c_char_p
+    lib.sf_cache_destroy.argtypes = [vp]
     for name in EXPORTS:
         fn = getattr(lib, name)
-        if name not in ("sf_status_str", "sf_last_error", "sf_head_last_error"):
+        if name not in ("sf_status_str", "sf_last_error", "sf_head_last_error", "sf_cache_last_error"):
             fn.restype = c_int
     return lib
 
@@ -115,11 +136,12 @@ class _LazyLib:
 lib = _LazyLib()
 
 
-def _check(st: int, ctx=None, what: str = "", head=None):
+def _check(st: int, ctx=None, what: str = "", head=None, cache=None):
     if st != SF_OK:
         msg = lib.sf_status_str(st).decode()
-        if ctx or head:
-            extra = (lib.sf_last_error(ctx) if ctx else lib.sf_head_last_error(head)).decode()
+        if ctx or head or cache:
+            extra = (lib.sf_last_error(ctx) if ctx else lib.sf_head_last_error(head) if head else
+                     lib.sf_cache_last_error(cache)).decode()
             if extra:
                 msg += f": {extra}"
         raise SpecFoldError(st, f"{what}: {msg}" if what else msg)
@@ -241,6 +263,43 @@ def sf_head_destroy(head) -> None:
     _check(lib.sf_head_destroy(head), None, "sf_head_destroy")
 
 
+def sf_cache_create(shapes: SfCacheShapes) -> int:
+    c = ctypes.c_void_p()
+    _check(lib.sf_cache_create(ctypes.byref(shapes), ctypes.byref(c)), None, "sf_cache_create")
+    return c.value
+
+
+def sf_cache_append(cache, stream, qkv, ld_qkv, T, q_gain, k_gain, index, pos, seq, page_table, S, table_cols,
+                    ld_table, k_pages, v_pages, n_pages, q_out, ld_q) -> None:
+    _check(lib.sf_cache_append(cache, stream, qkv, ld_qkv, T, q_gain, k_gain, index, pos, seq, page_table, S,
+                               table_cols, ld_table, k_pages, v_pages, n_pages, q_out, ld_q),
+           None, "sf_cache_append", cache=cache)
+
+
+def sf_cache_attend(cache, stream, q, ld_q, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table, lens,
+                    scale, out, ld_out, weights_in=None, weights_out=None, ld_w=0) -> None:
+    _check(lib.sf_cache_attend(cache, stream, q, ld_q, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table,
+                               lens, scale, out, ld_out, weights_in, weights_out, ld_w),
+           None, "sf_cache_attend", cache=cache)
+
+
+def sf_cache_evict(cache, stream, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table, lens, weights, ld_w,
+                   budget, n_first, n_recent, k_out, v_out, n_pages_out, table_out, table_out_cols, ld_table_out,
+                   weights_out, lens_out, kept) -> None:
+    _check(lib.sf_cache_evict(cache, stream, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table, lens,
+                              weights, ld_w, budget, n_first, n_recent, k_out, v_out, n_pages_out, table_out,
+                              table_out_cols, ld_table_out, weights_out, lens_out, kept),
+           None, "sf_cache_evict", cache=cache)
+
+
+def sf_cache_sync_status(cache, stream) -> None:
+    _check(lib.sf_cache_sync_status(cache, stream), None, "sf_cache_sync_status", cache=cache)
+
+
+def sf_cache_destroy(cache) -> None:
+    _check(lib.sf_cache_destroy(cache), None, "sf_cache_destroy")
+
+
 # ---------------------------------------------------------------- torch convenience
 
 class SpecFold:
@@ -359,6 +418,185 @@ class Head:
         sf_head_verify(self.head, _stream_handle(stream), _ptr(hidden), _ptr(tokens), parent, R, Bp - 1, L,
                        _ptr(pred), _ptr(accepted), _ptr(chosen))
         return pred, accepted, chosen
+
+
+class PagedCache:
+    """Operators on a paged key-value cache over torch tensors (include/specfold_cache.h).
+
+    Keys and values live in pools [n_pages, page_size, n_kv_heads, head_dim]
+    that the caller owns, one pair per layer; table is int32 [S, columns],
+    lens int32 [S].  A layer's prefix buffer of SpecFold.verify, viewed as
+    [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool.
+    Tensors must be on the object's device, of the documented type and shape
+    with contiguous rows (ValueError otherwise); outputs that are not given
+    are allocated for the call's stream."""
+
+    def __init__(self, *, n_q_heads, n_kv_heads, head_dim, dtype, page_size, max_seqs, max_len, max_pos=None,
+                 rms_eps=1e-6, rope_theta=10000.0, track_weights=False):
+        import torch
+        bf16 = dtype in ("bf16", SF_BF16)
+        self.shapes = SfCacheShapes(n_q_heads, n_kv_heads, head_dim, SF_BF16 if bf16 else SF_F32, page_size,
+                                    max_seqs, max_len, max_len if max_pos is None else max_pos, rms_eps, rope_theta,
+                                    int(bool(track_weights)))
+        self.dtype = torch.bfloat16 if bf16 else torch.float32
+        self.cache = sf_cache_create(self.shapes)
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._nq, self._nkv, self._hd, self._page = n_q_heads, n_kv_heads, head_dim, page_size
+
+    def close(self):
+        if getattr(self, "cache", None):
+            sf_cache_destroy(self.cache)
+            self.cache = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # -- checks: type, device, shape, rows without gaps inside
+
+    def _want(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.device}: got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, heads):
+        """Row stride of [T, heads, head_dim] or [T, heads * head_dim] with contiguous rows."""
+        sh, st = t.shape, t.stride()
+        if len(sh) == 3:
+            ok = sh[1] == heads and sh[2] == self._hd and st[2] == 1 and (heads == 1 or st[1] == self._hd)
+        else:
+            ok = len(sh) == 2 and sh[1] == heads * self._hd and st[1] == 1
+        if not ok or t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name} must be {self.dtype} [T, {heads}, {self._hd}] on {self.device} with contiguous "
+                             f"rows: got {t.dtype} {tuple(sh)} strides {tuple(st)} on {t.device}")
+        return st[0]
+
+    def _pool(self, k, v):
+        sh = k.shape
+        if (len(sh) != 4 or sh[1] != self._page or sh[2] != self._nkv or sh[3] != self._hd or v.shape != sh
+                or k.dtype != self.dtype or v.dtype != self.dtype or k.device != self.device
+                or v.device != self.device or not k.is_contiguous() or not v.is_contiguous()):
+            raise ValueError(f"pools must be contiguous {self.dtype} [n_pages, {self._page}, {self._nkv}, {self._hd}] "
+                             f"on {self.device}: got {k.dtype} {tuple(sh)} on {k.device}, {v.dtype} "
+                             f"{tuple(v.shape)} on {v.device}")
+        return sh[0]
+
+    def _table(self, name, t):
+        import torch
+        sh, st = t.shape, t.stride()
+        if len(sh) != 2 or t.dtype != torch.int32 or t.device != self.device or (sh[1] > 1 and st[1] != 1):
+            raise ValueError(f"{name} must be int32 [S, columns] on {self.device} with contiguous rows: got {t.dtype} "
+                             f"{tuple(sh)} strides {tuple(st)} on {t.device}")
+        return sh[0], sh[1], st[0]
+
+    def _empty(self, stream, *shape, dtype):
+        """A new output, allocated for the stream that writes it."""
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        t.record_stream(stream)
+        return t
+
+    # -- operators
+
+    def append(self, qkv, index, table, k_pages, v_pages, *, pos=None, seq=None, q_gain=None, k_gain=None, q=None,
+               stream=None):
+        """Norm (where a gain is given), rotate and store T new rows; returns the rotated queries [T, n_q_heads,
+        head_dim].  qkv [T, n_q_heads + 2 n_kv_heads, head_dim] (or its two last dimensions flattened)."""
+        import torch
+        i32, T = torch.int32, qkv.shape[0]
+        ld = self._rows("qkv", qkv, self._nq + 2 * self._nkv)
+        n_pages = self._pool(k_pages, v_pages)
+        S, cols, ld_t = self._table("table", table)
+        if q is None:
+            q = self._empty(stream, T, self._nq, self._hd, dtype=self.dtype)
+        ld_q = self._rows("q", q, self._nq)
+        if q.shape[0] != T:
+            raise ValueError(f"q has {q.shape[0]} rows, qkv {T}")
+        sf_cache_append(self.cache, _stream_handle(stream), qkv.data_ptr(), ld, T,
+                        None if q_gain is None else self._want("q_gain", q_gain, torch.float32, (self._hd,)),
+                        None if k_gain is None else self._want("k_gain", k_gain, torch.float32, (self._hd,)),
+                        self._want("index", index, i32, (T,)),
+                        None if pos is None else self._want("pos", pos, i32, (T,)),
+                        None if seq is None else self._want("seq", seq, i32, (T,)),
+                        table.data_ptr(), S, cols, ld_t, k_pages.data_ptr(), v_pages.data_ptr(), n_pages,
+                        q.data_ptr(), ld_q)
+        return q
+
+    def attend(self, q, k_pages, v_pages, table, lens, *, scale=None, out=None, weights=None, weights_out=None,
+               stream=None):
+        """Attention of one new token per sequence, q [S, n_q_heads, head_dim]; returns [S, n_q_heads, head_dim].
+        weights (fp32 [S, n_kv_heads, at least max_len]) gets every position's attention weight added, in place
+        or into weights_out; weights_out alone gets this call's weights."""
+        import torch
+        S, cols, ld_t = self._table("table", table)
+        ld_q = self._rows("q", q, self._nq)
+        if q.shape[0] != S:
+            raise ValueError(f"q has {q.shape[0]} rows, table {S}")
+        n_pages = self._pool(k_pages, v_pages)
+        if out is None:
+            out = self._empty(stream, S, self._nq, self._hd, dtype=self.dtype)
+        elif out.shape[0] != S:
+            raise ValueError(f"out has {out.shape[0]} rows, table {S}")
+        ld_o = self._rows("out", out, self._nq)
+        w_in = w_out = None
+        ld_w = 0
+        if weights is not None or weights_out is not None:
+            if weights_out is None:
+                weights_out = weights
+            ld_w = weights_out.shape[-1]
+            w_out = self._want("weights_out", weights_out, torch.float32, (S, self._nkv, ld_w))
+            if weights is not None:
+                w_in = self._want("weights", weights, torch.float32, (S, self._nkv, ld_w))
+        sf_cache_attend(self.cache, _stream_handle(stream), q.data_ptr(), ld_q, k_pages.data_ptr(),
+                        v_pages.data_ptr(), n_pages, table.data_ptr(), S, cols, ld_t,
+                        self._want("lens", lens, torch.int32, (S,)),
+                        self._hd ** -0.5 if scale is None else scale, out.data_ptr(), ld_o, w_in, w_out, ld_w)
+        return out
+
+    def evict(self, k_pages, v_pages, table, lens, weights, budget, *, n_first=0, n_recent=0, k_out=None, v_out=None,
+              table_out=None, weights_out=None, lens_out=None, kept=None, stream=None):
+        """Keep at most `budget` positions of every sequence and KV head: the first n_first, the last n_recent and
+        the heaviest others, moved in order to the front of the same pages, or of k_out / v_out / table_out (given
+        together).  weights moves along, in place or into weights_out.  Returns (lens_out [S], kept [S, n_kv_heads,
+        budget])."""
+        import torch
+        i32 = torch.int32
+        S, cols, ld_t = self._table("table", table)
+        n_pages = self._pool(k_pages, v_pages)
+        if (k_out is None) != (v_out is None) or (k_out is None) != (table_out is None):
+            raise ValueError("k_out, v_out and table_out are given together")
+        if k_out is None:
+            k_out, v_out, table_out = k_pages, v_pages, table
+            n_pages_out, cols_o, ld_to = n_pages, cols, ld_t
+        else:
+            n_pages_out = self._pool(k_out, v_out)
+            S_o, cols_o, ld_to = self._table("table_out", table_out)
+            if S_o != S:
+                raise ValueError(f"table_out has {S_o} rows, table {S}")
+        ld_w = weights.shape[-1]
+        w = self._want("weights", weights, torch.float32, (S, self._nkv, ld_w))
+        w_out = w if weights_out is None else self._want("weights_out", weights_out, torch.float32,
+                                                         (S, self._nkv, ld_w))
+        if lens_out is None:
+            lens_out = self._empty(stream, S, dtype=i32)
+        if kept is None:
+            kept = self._empty(stream, S, self._nkv, max(budget, 0), dtype=i32)
+        sf_cache_evict(self.cache, _stream_handle(stream), k_pages.data_ptr(), v_pages.data_ptr(), n_pages,
+                       table.data_ptr(), S, cols, ld_t, self._want("lens", lens, i32, (S,)), w, ld_w, budget,
+                       n_first, n_recent, k_out.data_ptr(), v_out.data_ptr(), n_pages_out, table_out.data_ptr(),
+                       cols_o, ld_to, w_out, self._want("lens_out", lens_out, i32, (S,)),
+                       self._want("kept", kept, i32, (S, self._nkv, max(budget, 0))))
+        return lens_out, kept
+
+    def sync(self, stream=None):
+        sf_cache_sync_status(self.cache, _stream_handle(stream))
 
 
 def from_config(cfg, weights, max_requests=None, max_branches=None, max_prefix=None) -> SpecFold:

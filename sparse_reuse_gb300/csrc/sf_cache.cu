@@ -1,0 +1,397 @@
+// Paged-cache operators: the object, argument checks and the C ABI
+// (specfold_cache.h), the rotary table and the append kernel.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "sf_cache.h"
+
+namespace sf {
+namespace {
+
+// Rotary table, angles and functions in double: far positions (10^5 radians
+// and more) lose the angle in fp32.
+__global__ void rope_table_kernel(float2* out, int max_pos, int half, double theta) {
+  const int64_t n = (int64_t)max_pos * half;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int j = (int)(i % half);
+    const double a = (double)(i / half) * pow(theta, -(double)j / half);
+    double sn, cs;
+    sincos(a, &sn, &cs);
+    out[i] = make_float2((float)cs, (float)sn);
+  }
+}
+
+template <typename T, int N>
+struct alignas(16) Vec {
+  T v[N];
+};
+
+constexpr int kAppendThreads = 256;
+
+// Norm, rotation and store of one head of one row by a group of lanes: a lane
+// holds 16 bytes of the head's lower half and the same 16 of its upper half,
+// so both members of its rotation pairs are in its registers and the norm
+// needs log2(lanes) shuffles.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
+  constexpr int VEC = 16 / sizeof(T), LANES = HD / 2 / VEC;
+  using V = Vec<T, VEC>;
+  pdl_wait();
+  pdl_trigger();
+  const int NH = a.nq + 2 * a.nkv;
+  const int64_t item = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int t = (int)(item / NH), head = (int)(item % NH);
+  if (t >= a.T) return;  // whole groups: the shuffles below stay inside a group
+  const unsigned mask = (LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u)) << ((threadIdx.x & 31) / LANES * LANES);
+  const int idx = a.index[t];
+  const int pos = a.pos ? a.pos[t] : idx;
+  if (pos < 0) return;
+  if (pos >= a.max_pos) {
+    if (lane == 0) cache_error(a.err, kCacheBadRow);
+    return;
+  }
+  int64_t slot = -1;
+  if (head >= a.nq && idx >= 0) {
+    const int s = a.seq ? a.seq[t] : t;
+    if (s < 0 || s >= a.S || idx >= a.limit) {
+      if (lane == 0) cache_error(a.err, kCacheBadRow);
+    } else {
+      slot = page_slot(a.table, s, idx);
+      if (slot < 0 && lane == 0) cache_error(a.err, kCacheBadPage);
+    }
+  }
+  if (head >= a.nq && slot < 0) return;
+  const T* src = static_cast<const T*>(a.qkv) + (int64_t)t * a.ld_qkv + (int64_t)head * HD + lane * VEC;
+  V lo = *reinterpret_cast<const V*>(src), hi = *reinterpret_cast<const V*>(src + HD / 2);
+  T* dst;
+  if (head < a.nq)
+    dst = static_cast<T*>(a.q_out) + (int64_t)t * a.ld_q + (int64_t)head * HD;
+  else if (head < a.nq + a.nkv)
+    dst = static_cast<T*>(a.k) + (slot * a.nkv + (head - a.nq)) * HD;
+  else
+    dst = static_cast<T*>(a.v) + (slot * a.nkv + (head - a.nq - a.nkv)) * HD;
+  dst += lane * VEC;
+  if (head < a.nq + a.nkv) {
+    const float* gain = head < a.nq ? a.q_gain : a.k_gain;
+    float x[VEC], y[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      x[i] = to_f32<T>(lo.v[i]);
+      y[i] = to_f32<T>(hi.v[i]);
+    }
+    if (gain) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) ss += x[i] * x[i] + y[i] * y[i];
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+      const float r = 1.f / sqrtf(ss / (float)HD + a.eps);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        x[i] = x[i] * r * gain[lane * VEC + i];
+        y[i] = y[i] * r * gain[HD / 2 + lane * VEC + i];
+      }
+    }
+    const float2* cs = a.rope + (int64_t)pos * (HD / 2) + lane * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float2 c = cs[i];
+      lo.v[i] = from_f32<T>(x[i] * c.x - y[i] * c.y);
+      hi.v[i] = from_f32<T>(y[i] * c.x + x[i] * c.y);
+    }
+  }
+  *reinterpret_cast<V*>(dst) = lo;
+  *reinterpret_cast<V*>(dst + HD / 2) = hi;
+}
+
+template <typename T, int HD>
+cudaError_t append_t(cudaStream_t st, const CacheAppendArgs& a) {
+  constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
+  const int64_t threads = (int64_t)a.T * (a.nq + 2 * a.nkv) * LANES;
+  return launch_pdl(st, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0, 1,
+                    cache_append_kernel<T, HD>, a);
+}
+
+bool misaligned(const void* p, uintptr_t align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)); }
+
+sf_status fail(sf_cache* c, sf_status st, const char* fmt, ...) __attribute__((format(printf, 3, 4)));
+sf_status fail(sf_cache* c, sf_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(c->last_error, sizeof(c->last_error), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+void free_cache(sf_cache* c) {
+  if (!c) return;
+  cudaFree(c->rope);
+  cudaFree(c->scores);
+  cudaFree(c->lse);
+  if (c->err) cudaFreeHost(c->err);
+  delete c;
+}
+
+// What every call checks after its arguments: the object's device is current
+// and no earlier device check waits to be read.
+sf_status check_object(sf_cache* c) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device)
+    return fail(c, SF_ERR_INVALID_ARG, "the object lives on device %d, the current one is %d", c->device, dev);
+  const volatile unsigned* e = c->err;
+  if (e[kCacheBadPage] || e[kCacheBadLength] || e[kCacheBadRow])
+    return fail(c, SF_ERR_DEVICE_ASSERT, "device check fired:%s%s%s", e[kCacheBadPage] ? " page out of range" : "",
+                e[kCacheBadLength] ? " length out of range" : "", e[kCacheBadRow] ? " row out of range" : "");
+  return SF_OK;
+}
+
+sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages, const int32_t* table, int S,
+                      int cols, int64_t ld) {
+  if (!k || !v || !table) return fail(c, SF_ERR_INVALID_ARG, "null pool or page table");
+  if (misaligned(k, 16) || misaligned(v, 16) || misaligned(table, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "pools need 16-byte alignment, page tables 4-byte");
+  if (S < 0 || cols < 1 || n_pages < 1 || (S > 1 && ld < cols))
+    return fail(c, SF_ERR_INVALID_ARG, "S=%d table_cols=%d ld_table=%lld n_pages=%lld", S, cols, (long long)ld,
+                (long long)n_pages);
+  if (S > c->s.max_seqs) return fail(c, SF_ERR_SHAPE, "S=%d beyond the object's %d sequences", S, c->s.max_seqs);
+  return SF_OK;
+}
+
+bool bad_row(const sf_cache* c, const void* p, int64_t ld, int64_t width, int rows) {
+  const int es = c->s.dtype == SF_BF16 ? 2 : 4;
+  return !p || misaligned(p, 16) || (rows > 1 && (ld < width || ld * es % 16 != 0));
+}
+
+PageTable page_table(const sf_cache* c, const int32_t* table, int cols, int64_t ld, int64_t n_pages) {
+  return PageTable{table, ld, cols, c->s.page_size, n_pages};
+}
+
+sf_status launched(sf_cache* c, cudaError_t e) {
+  if (e == cudaSuccess) return SF_OK;
+  cudaGetLastError();
+  return fail(c, SF_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(cudaStream_t st, const CacheAppendArgs& a, int bf16, int) {
+  if (bf16) return a.hd == 128 ? append_t<__nv_bfloat16, 128>(st, a) : append_t<__nv_bfloat16, 64>(st, a);
+  return a.hd == 128 ? append_t<float, 128>(st, a) : append_t<float, 64>(st, a);
+}
+
+}  // namespace sf
+
+using namespace sf;
+
+extern "C" {
+
+sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
+  if (!out) return SF_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!shapes) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes s = *shapes;
+  if (s.n_q_heads < 1 || s.n_kv_heads < 1 || s.head_dim < 1 || s.page_size < 1 || s.max_seqs < 1 || s.max_len < 1 ||
+      s.max_pos < 1 || !(s.rms_eps >= 0.f) || !std::isfinite(s.rms_eps) || !(s.rope_theta > 0.f) ||
+      !std::isfinite(s.rope_theta) || (s.dtype != SF_F32 && s.dtype != SF_BF16))
+    return SF_ERR_INVALID_ARG;
+  if ((s.head_dim != 64 && s.head_dim != 128) || s.n_q_heads % s.n_kv_heads != 0 || s.n_q_heads > 1024 ||
+      s.page_size > 65536 || s.max_seqs > 4096 || s.max_len > 262144 || s.max_pos > 4194304)
+    return SF_ERR_UNSUPPORTED;
+  sf_cache* c = new (std::nothrow) sf_cache();
+  if (!c) return SF_ERR_OOM;
+  c->s = s;
+  cudaError_t e = cudaGetDevice(&c->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
+  if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * (s.head_dim / 2) * sizeof(float2));
+  if (e == cudaSuccess && s.track_weights)
+    e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * s.max_len * sizeof(float));
+  if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
+  if (e == cudaSuccess) e = cudaHostAlloc(&c->err, kCacheErrWords * sizeof(unsigned), cudaHostAllocMapped);
+  if (e == cudaSuccess) e = cudaHostGetDevicePointer(&c->err_dev, c->err, 0);
+  if (e == cudaSuccess) {
+    for (int i = 0; i < kCacheErrWords; ++i) c->err[i] = 0;
+    const int64_t n = (int64_t)s.max_pos * (s.head_dim / 2);
+    const int64_t blocks = (n + 255) / 256;
+    rope_table_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256>>>(c->rope, s.max_pos, s.head_dim / 2,
+                                                                          (double)s.rope_theta);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    free_cache(c);
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? SF_ERR_OOM : SF_ERR_CUDA;
+  }
+  *out = c;
+  return SF_OK;
+}
+
+sf_status sf_cache_append(sf_cache* c, void* stream, const void* qkv, int64_t ld_qkv, int T, const float* q_gain,
+                          const float* k_gain, const int32_t* index, const int32_t* pos, const int32_t* seq,
+                          const int32_t* page_table_, int S, int table_cols, int64_t ld_table, void* k_pages,
+                          void* v_pages, int64_t n_pages, void* q_out, int64_t ld_q) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes& s = c->s;
+  sf_status st = SF_OK;
+  if (T == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if (k_pages == v_pages) return fail(c, SF_ERR_INVALID_ARG, "one pool for keys and values");
+  if (T < 0 || !index || misaligned(index, 4) || misaligned(pos, 4) || misaligned(seq, 4) || misaligned(q_gain, 16) ||
+      misaligned(k_gain, 16))
+    return fail(c, SF_ERR_INVALID_ARG, "T=%d, null index, or index/pos/seq/gain misaligned", T);
+  const int64_t wq = (int64_t)s.n_q_heads * s.head_dim, w = wq + 2 * (int64_t)s.n_kv_heads * s.head_dim;
+  if (bad_row(c, qkv, ld_qkv, w, T) || bad_row(c, q_out, ld_q, wq, T))
+    return fail(c, SF_ERR_INVALID_ARG, "qkv/q_out null, misaligned, or rows closer than their width");
+  if (T > 16777216 || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
+  if ((st = check_object(c)) != SF_OK) return st;
+  CacheAppendArgs a{};
+  a.qkv = qkv;
+  a.ld_qkv = ld_qkv;
+  a.q_out = q_out;
+  a.ld_q = ld_q;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.index = index;
+  a.pos = pos;
+  a.seq = seq;
+  a.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  a.k = k_pages;
+  a.v = v_pages;
+  a.rope = c->rope;
+  a.T = T;
+  a.S = S;
+  a.nq = s.n_q_heads;
+  a.nkv = s.n_kv_heads;
+  a.hd = s.head_dim;
+  a.max_pos = s.max_pos;
+  a.limit = length_limit(s.max_len, table_cols, s.page_size);
+  a.eps = s.rms_eps;
+  a.err = c->err_dev;
+  return launched(c, launch_cache_append((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
+}
+
+sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q, const void* k_pages,
+                          const void* v_pages, int64_t n_pages, const int32_t* page_table_, int S, int table_cols,
+                          int64_t ld_table, const int32_t* lens, float scale, void* out, int64_t ld_out,
+                          const float* weights_in, float* weights_out, int64_t ld_w) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes& s = c->s;
+  sf_status st = SF_OK;
+  if (S == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if (!lens || misaligned(lens, 4) || misaligned(weights_in, 4) || misaligned(weights_out, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "null lens, or lens/weights misaligned");
+  const int64_t wq = (int64_t)s.n_q_heads * s.head_dim;
+  if (bad_row(c, q, ld_q, wq, S) || bad_row(c, out, ld_out, wq, S))
+    return fail(c, SF_ERR_INVALID_ARG, "q/out null, misaligned, or rows closer than their width");
+  if (!std::isfinite(scale)) return fail(c, SF_ERR_INVALID_ARG, "scale must be finite");
+  if (weights_in && !weights_out) return fail(c, SF_ERR_INVALID_ARG, "weights_in without weights_out");
+  if (weights_out && !s.track_weights)
+    return fail(c, SF_ERR_INVALID_ARG, "the object was created without track_weights");
+  const int64_t limit = length_limit(s.max_len, table_cols, s.page_size);
+  if (weights_out && ld_w < limit)
+    return fail(c, SF_ERR_SHAPE, "ld_w=%lld below the %lld positions of a sequence", (long long)ld_w,
+                (long long)limit);
+  if ((st = check_object(c)) != SF_OK) return st;
+  CacheAttendArgs a{};
+  a.q = q;
+  a.ld_q = ld_q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  a.lens = lens;
+  a.S = S;
+  a.nq = s.n_q_heads;
+  a.nkv = s.n_kv_heads;
+  a.hd = s.head_dim;
+  a.limit = limit;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.w_in = weights_in;
+  a.w_out = weights_out;
+  a.ld_w = ld_w;
+  a.scores = c->scores;
+  a.ld_scores = s.max_len;
+  a.lse = c->lse;
+  a.err = c->err_dev;
+  return launched(c, launch_cache_attend((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
+}
+
+sf_status sf_cache_evict(sf_cache* c, void* stream, const void* k_pages, const void* v_pages, int64_t n_pages,
+                         const int32_t* page_table_, int S, int table_cols, int64_t ld_table, const int32_t* lens,
+                         const float* weights, int64_t ld_w, int budget, int n_first, int n_recent, void* k_out,
+                         void* v_out, int64_t n_pages_out, const int32_t* table_out, int table_out_cols,
+                         int64_t ld_table_out, float* weights_out, int32_t* lens_out, int32_t* kept) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes& s = c->s;
+  sf_status st = SF_OK;
+  if (S == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if ((st = check_table(c, k_out, v_out, n_pages_out, table_out, S, table_out_cols, ld_table_out)) != SF_OK) return st;
+  if (!lens || !weights || !weights_out || !lens_out || !kept)
+    return fail(c, SF_ERR_INVALID_ARG, "null lens/weights/weights_out/lens_out/kept");
+  if (misaligned(lens, 4) || misaligned(weights, 4) || misaligned(weights_out, 4) || misaligned(lens_out, 4) ||
+      misaligned(kept, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "lens/weights/lens_out/kept need 4-byte alignment");
+  if (budget < 1 || n_first < 0 || n_recent < 0 || (int64_t)n_first + n_recent > budget)
+    return fail(c, SF_ERR_INVALID_ARG, "budget=%d n_first=%d n_recent=%d", budget, n_first, n_recent);
+  const int same = (k_out == k_pages) + (v_out == v_pages) + (table_out == page_table_);
+  if ((same != 0 && same != 3) || (same == 3 && (ld_table_out != ld_table || n_pages_out != n_pages)) ||
+      k_out == v_out || k_out == v_pages || v_out == k_pages)
+    return fail(c, SF_ERR_INVALID_ARG, "output pools and table are the input's in part only");
+  const int64_t limit = length_limit(s.max_len, table_cols, s.page_size);
+  if (ld_w < limit)
+    return fail(c, SF_ERR_SHAPE, "ld_w=%lld below the %lld positions of a sequence", (long long)ld_w,
+                (long long)limit);
+  if (budget > s.max_len || budget > (int64_t)table_out_cols * s.page_size)
+    return fail(c, SF_ERR_SHAPE, "budget=%d beyond max_len=%d or the output table", budget, s.max_len);
+  if ((st = check_object(c)) != SF_OK) return st;
+  CacheEvictArgs a{};
+  a.k = k_pages;
+  a.v = v_pages;
+  a.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.table_out = page_table(c, table_out, table_out_cols, ld_table_out, n_pages_out);
+  a.lens = lens;
+  a.w = weights;
+  a.w_out = weights_out;
+  a.ld_w = ld_w;
+  a.lens_out = lens_out;
+  a.kept = kept;
+  a.S = S;
+  a.nkv = s.n_kv_heads;
+  a.hd = s.head_dim;
+  a.budget = budget;
+  a.n_first = n_first;
+  a.n_recent = n_recent;
+  a.limit = limit;
+  a.in_place = same == 3;
+  a.err = c->err_dev;
+  return launched(c, launch_cache_evict((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
+}
+
+sf_status sf_cache_sync_status(sf_cache* c, void* stream) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(c, SF_ERR_CUDA, "%s", cudaGetErrorString(e));
+  sf_status st = check_object(c);
+  if (st == SF_ERR_DEVICE_ASSERT)
+    for (int i = 0; i < kCacheErrWords; ++i) c->err[i] = 0;
+  return st;
+}
+
+const char* sf_cache_last_error(const sf_cache* c) { return c ? c->last_error : ""; }
+
+sf_status sf_cache_destroy(sf_cache* c) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  cudaError_t e = cudaDeviceSynchronize();
+  free_cache(c);
+  return e == cudaSuccess ? SF_OK : SF_ERR_CUDA;
+}
+
+}  // extern "C"
