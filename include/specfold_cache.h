@@ -129,11 +129,12 @@ sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_
  * Results do not depend on what else is in the batch only up to rounding (the
  * sums are split by the batch's total length); the same call gives the same
  * bits.  Values: keys, values and queries as stored; products and sums fp32.
- * Infinities and NaN among the live positions follow the formula; what pools
- * hold behind a sequence's length is never read into it.
- * A sequence whose length is negative or beyond max_len, table_cols *
- * page_size counts as empty, a position on a page out of range as absent
- * (device check).
+ * NaN and infinite values, and NaN and +infinite scores, among the live
+ * positions make the outputs that they enter non-finite; a score of -infinity
+ * weighs nothing.  What pools hold behind a sequence's length is never read.
+ * A sequence whose length is negative or beyond max_len or table_cols *
+ * page_size counts as empty, a position on a page out of range as one of score
+ * -infinity (device check).
  * Errors: as above; SF_ERR_INVALID_ARG for a scale that is not finite, for
  * weights on an object without track_weights or weights_in without
  * weights_out; SF_ERR_SHAPE for an ld_w too small. */

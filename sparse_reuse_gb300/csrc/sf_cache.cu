@@ -131,6 +131,8 @@ void free_cache(sf_cache* c) {
   cudaFree(c->rope);
   cudaFree(c->scores);
   cudaFree(c->lse);
+  cudaFree(c->parts);
+  cudaFree(c->arrived);
   if (c->err) cudaFreeHost(c->err);
   delete c;
 }
@@ -156,6 +158,9 @@ sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages
   if (S < 0 || cols < 1 || n_pages < 1 || (S > 1 && ld < cols))
     return fail(c, SF_ERR_INVALID_ARG, "S=%d table_cols=%d ld_table=%lld n_pages=%lld", S, cols, (long long)ld,
                 (long long)n_pages);
+  // slots are 32-bit in the kernels, the last value meaning none
+  if (n_pages > 4294967294ll / c->s.page_size)
+    return fail(c, SF_ERR_SHAPE, "n_pages=%lld pages of %d positions", (long long)n_pages, c->s.page_size);
   if (S > c->s.max_seqs) return fail(c, SF_ERR_SHAPE, "S=%d beyond the object's %d sequences", S, c->s.max_seqs);
   return SF_OK;
 }
@@ -209,6 +214,10 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if (e == cudaSuccess && s.track_weights)
     e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * s.max_len * sizeof(float));
   if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->parts, (size_t)(c->sm_count * cache_attend_part_floats(s)) * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)c->sm_count * sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)c->sm_count * sizeof(unsigned));
+  if (e == cudaSuccess) e = prepare_cache_attend();
   if (e == cudaSuccess) e = cudaHostAlloc(&c->err, kCacheErrWords * sizeof(unsigned), cudaHostAllocMapped);
   if (e == cudaSuccess) e = cudaHostGetDevicePointer(&c->err_dev, c->err, 0);
   if (e == cudaSuccess) {
@@ -317,6 +326,8 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.scores = c->scores;
   a.ld_scores = s.max_len;
   a.lse = c->lse;
+  a.parts = c->parts;
+  a.arrived = c->arrived;
   a.err = c->err_dev;
   return launched(c, launch_cache_attend((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
 }

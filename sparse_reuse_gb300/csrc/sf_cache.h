@@ -15,6 +15,8 @@ struct sf_cache {
   float2* rope = nullptr;     // [max_pos][head_dim / 2] (cos, sin)
   float* scores = nullptr;    // [max_seqs][n_q_heads][max_len] scaled scores in log2 units (track_weights)
   float* lse = nullptr;       // [max_seqs][n_q_heads] log2 of each softmax denominator (track_weights)
+  float* parts = nullptr;     // partial results of sf_cache_attend, two per SM
+  unsigned* arrived = nullptr;  // [sm_count] arrival counters, 0 between calls
   unsigned* err = nullptr;    // [kCacheErrWords] pinned, written by the kernels through its device address
   unsigned* err_dev = nullptr;
   char last_error[256] = {0};
@@ -58,8 +60,14 @@ struct CacheAttendArgs {
   const float* w_in; float* w_out; int64_t ld_w;
   float* scores; int64_t ld_scores;
   float* lse;
+  float* parts;       // two partial results per block: output [heads][hd], max [heads], denominator [heads]
+  unsigned* arrived;  // [blocks] arrivals at a cut segment, by its first block; 0 between calls
+  int least;          // units a block takes at least
   unsigned* err;
 };
+// Floats of `parts` that a block needs, and the kernels' shared-memory limits (once per process and device).
+int64_t cache_attend_part_floats(const sf_cache_shapes& s);
+cudaError_t prepare_cache_attend();
 cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& a, int bf16, int sm_count);
 
 struct CacheEvictArgs {

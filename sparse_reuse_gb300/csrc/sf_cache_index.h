@@ -46,4 +46,31 @@ SF_HD int checked_len(int len, int64_t limit, bool* bad) {
   return *bad ? 0 : len;
 }
 
+// ---- the split of a batch's attention over thread blocks ---------------------
+//
+// The work is a line of units: sequence after sequence, head group after head
+// group, tile of kTileKeys keys after tile.  Block k takes units
+// [k * per, (k + 1) * per).  A segment (one sequence and head group) that lies
+// in one block is finished there.  One that is cut leaves a partial result per
+// block; a block is the inside or the end of at most one cut segment (its
+// first) and the start of at most one (its last), so two partial slots and one
+// arrival counter per block are enough for any batch.
+
+constexpr int kTileKeys = 16;
+
+SF_HD int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+
+// Units per block: all blocks busy, but at least `least` units each.
+SF_HD int64_t units_per_block(int64_t units, int blocks, int least) {
+  const int64_t per = (units + blocks - 1) / blocks;
+  return per < least ? least : per;
+}
+
+// Blocks that share the segment of `tiles` units starting at unit `first`.
+SF_HD int first_block(int64_t first, int64_t per) { return (int)(first / per); }
+SF_HD int last_block(int64_t first, int tiles, int64_t per) { return (int)((first + tiles - 1) / per); }
+
+// Partial slot of block `block` for the cut segment starting at `first`.
+SF_HD int part_slot(int block, int64_t first, int64_t per) { return 2 * block + (first > block * per ? 1 : 0); }
+
 }  // namespace sf

@@ -71,6 +71,13 @@ long long slot(const int* pages, long long ld, int cols, int page, long long n_p
   return sf::page_slot(sf::PageTable{pages, ld, cols, page, n_pages}, s, j);
 }
 long long limit(int max_len, int cols, int page) { return sf::length_limit(max_len, cols, page); }
+long long per(long long u, int blocks, int least) { return sf::units_per_block(u, blocks, least); }
+int tiles(int n) { return sf::tiles_of(n); }
+void cut(long long first, int tiles, long long per, int* b0, int* b1) {
+  *b0 = sf::first_block(first, per);
+  *b1 = sf::last_block(first, tiles, per);
+}
+int part(int block, long long first, long long per) { return sf::part_slot(block, first, per); }
 int len(int n, long long lim, int* bad) { bool b; int r = sf::checked_len(n, lim, &b); *bad = b; return r; }
 }
 """)
@@ -81,7 +88,7 @@ int len(int n, long long lim, int* bad) { bool b; int r = sf::checked_len(n, lim
     lib.slot.restype = ctypes.c_longlong
     lib.slot.argtypes = [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong,
                          ctypes.c_int, ctypes.c_int]
-    lib.limit.restype = ctypes.c_longlong
+    lib.limit.restype = lib.per.restype = ctypes.c_longlong
     return lib
 
 
@@ -111,6 +118,40 @@ def test_length_limits(index_lib):
     assert index_lib.limit(262144, 2 ** 20, 65536) == 262144
     for n, want, b in ((0, 0, 0), (700, 700, 0), (701, 0, 1), (-1, 0, 1), (-2 ** 31, 0, 1)):
         assert index_lib.len(n, ctypes.c_longlong(700), ctypes.byref(bad)) == want and bad.value == b
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_split_of_a_batch(index_lib, seed):
+    """Every unit belongs to one block; a cut segment's blocks are first..last;
+    no two cut segments share a partial slot or an arrival counter, whatever the
+    batch; sizes beyond 32 bits of units."""
+    ll = ctypes.c_longlong
+    rng = np.random.default_rng(seed)
+    S, H, blocks, least = int(rng.integers(1, 40)), int(rng.integers(1, 9)), int(rng.integers(1, 153)), 16
+    top = int(rng.choice([5, 40, 2000, 262144]))
+    lens = rng.integers(0, top + 1, S) * (rng.random(S) < 0.8)
+    tiles = [index_lib.tiles(int(n)) for n in lens]
+    assert tiles == [-(-int(n) // 16) for n in lens]
+    units = sum(tiles) * H
+    per = index_lib.per(ll(units), blocks, least)
+    assert per >= least and per * blocks >= units and (per == least or (per - 1) * blocks < units)
+    at, slots, counters = 0, set(), set()
+    for t in tiles:
+        for _ in range(H):
+            if t:
+                b0, b1 = ctypes.c_int(), ctypes.c_int()
+                index_lib.cut(ll(at), t, ll(per), ctypes.byref(b0), ctypes.byref(b1))
+                b0, b1 = b0.value, b1.value
+                assert b0 == at // per and b1 == (at + t - 1) // per < blocks
+                if b0 != b1:
+                    assert b0 not in counters
+                    counters.add(b0)
+                    for b in range(b0, b1 + 1):
+                        p = index_lib.part(b, ll(at), ll(per))
+                        assert 0 <= p < 2 * blocks and p not in slots
+                        slots.add(p)
+            at += t
+    assert index_lib.per(ll(2 ** 40), 152, least) == -(-2 ** 40 // 152)
 
 
 # ---------------------------------------------------------------- refusals
