@@ -218,6 +218,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)c->sm_count * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)c->sm_count * sizeof(unsigned));
   if (e == cudaSuccess) e = prepare_cache_attend();
+  if (e == cudaSuccess) e = prepare_cache_evict();
   if (e == cudaSuccess) e = cudaHostAlloc(&c->err, kCacheErrWords * sizeof(unsigned), cudaHostAllocMapped);
   if (e == cudaSuccess) e = cudaHostGetDevicePointer(&c->err_dev, c->err, 0);
   if (e == cudaSuccess) {

@@ -83,6 +83,7 @@ struct CacheEvictArgs {
   bool in_place;
   unsigned* err;
 };
+cudaError_t prepare_cache_evict();
 cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf16, int sm_count);
 
 }  // namespace sf
