@@ -133,6 +133,7 @@ void free_cache(sf_cache* c) {
   cudaFree(c->lse);
   cudaFree(c->parts);
   cudaFree(c->arrived);
+  cudaFree(c->joins);
   if (c->err) cudaFreeHost(c->err);
   delete c;
 }
@@ -171,7 +172,7 @@ bool bad_row(const sf_cache* c, const void* p, int64_t ld, int64_t width, int ro
 }
 
 PageTable page_table(const sf_cache* c, const int32_t* table, int cols, int64_t ld, int64_t n_pages) {
-  return PageTable{table, ld, cols, c->s.page_size, n_pages};
+  return make_page_table(table, ld, cols, c->s.page_size, n_pages);
 }
 
 sf_status launched(sf_cache* c, cudaError_t e) {
@@ -203,7 +204,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
       !std::isfinite(s.rope_theta) || (s.dtype != SF_F32 && s.dtype != SF_BF16))
     return SF_ERR_INVALID_ARG;
   if ((s.head_dim != 64 && s.head_dim != 128) || s.n_q_heads % s.n_kv_heads != 0 || s.n_q_heads > 1024 ||
-      s.page_size > 65536 || s.max_seqs > 4096 || s.max_len > 262144 || s.max_pos > 4194304)
+      s.page_size > kMaxPageSize || s.max_seqs > 4096 || s.max_len > kMaxLen || s.max_pos > 4194304)
     return SF_ERR_UNSUPPORTED;
   sf_cache* c = new (std::nothrow) sf_cache();
   if (!c) return SF_ERR_OOM;
@@ -215,6 +216,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
     e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * s.max_len * sizeof(float));
   if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&c->parts, (size_t)(c->sm_count * cache_attend_part_floats(s)) * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->joins, (size_t)c->sm_count * sizeof(CacheJoin));
   if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)c->sm_count * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)c->sm_count * sizeof(unsigned));
   if (e == cudaSuccess) e = prepare_cache_attend();
@@ -329,6 +331,7 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.lse = c->lse;
   a.parts = c->parts;
   a.arrived = c->arrived;
+  a.joins = c->joins;
   a.err = c->err_dev;
   return launched(c, launch_cache_attend((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
 }

@@ -8,6 +8,15 @@
 #include "sf_common.cuh"
 #include "specfold_cache.h"
 
+namespace sf {
+// A cut segment that the join kernel finishes, by its first block.
+struct CacheJoin {
+  int n;      // partial results; 0 = nothing to do
+  int s, h0, nh;
+  int first;  // slot of the first one; the others are slots 2 (block + 1), 2 (block + 2), ...
+};
+}  // namespace sf
+
 struct sf_cache {
   sf_cache_shapes s{};
   int device = 0;
@@ -17,6 +26,7 @@ struct sf_cache {
   float* lse = nullptr;       // [max_seqs][n_q_heads] log2 of each softmax denominator (track_weights)
   float* parts = nullptr;     // partial results of sf_cache_attend, two per SM
   unsigned* arrived = nullptr;  // [sm_count] arrival counters, 0 between calls
+  sf::CacheJoin* joins = nullptr;  // [sm_count]
   unsigned* err = nullptr;    // [kCacheErrWords] pinned, written by the kernels through its device address
   unsigned* err_dev = nullptr;
   char last_error[256] = {0};
@@ -62,6 +72,8 @@ struct CacheAttendArgs {
   float* lse;
   float* parts;       // two partial results per block: output [heads][hd], max [heads], denominator [heads]
   unsigned* arrived;  // [blocks] arrivals at a cut segment, by its first block; 0 between calls
+  CacheJoin* joins;   // [blocks]
+  bool join;          // a join kernel follows
   int least;          // units a block takes at least
   unsigned* err;
 };

@@ -6,6 +6,9 @@
 //   weights_j += sum over the KV head's query heads of 2^(score_j - lse),
 //   lse = m + log2(sum_j p_j)
 //
+// m is not kept exact: a tile whose scores stay below m + kSlack uses the old
+// m, so the maximum is reduced and sums are rescaled only while it still grows
+// by more than that (a few tiles of a sequence), and a tile costs one vote.
 // The p_j are kept 2^-kRoom times smaller than written (the quotient does not
 // change): at most 2^18 of them then sum to less than 1, so the unnormalised
 // output stays within the largest value and cannot overflow where the result
@@ -25,7 +28,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kRoom = 19.f;
+constexpr float kSlack = 8.f;
+constexpr float kRoom = 19.f + kSlack;
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -44,11 +48,23 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -65,233 +81,237 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t x) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
 }
 
-// Query heads that a block takes together: the 8 columns of one or two
-// tensor-core tiles (bf16), 8 (fp32).
-template <typename T, int NT>
-struct Group {
-  static constexpr int kHeads = 8 * NT;
-};
-
-// Work of one warp: tiles [t, end) in steps of `step` of one segment.
+// One sequence and group of query heads h0 .. h0 + nh - 1 of KV head kvh.
 struct Segment {
   int s, kvh, h0, nh, len;
 };
 
-// Slot of key 16 t + (lane & 15), or ~0 where there is none.
-__device__ __forceinline__ uint32_t tile_slot(const CacheAttendArgs& a, const Segment& g, int t, int lane) {
-  const int j = t * kTileKeys + (lane & 15);
-  if (j >= g.len) return ~0u;
-  const int64_t slot = page_slot(a.table, g.s, j);
-  if (slot < 0) {
-    cache_error(a.err, kCacheBadPage);
-    return ~0u;
+// A warp's ring of stages in shared memory: `KEYS` keys, then their values,
+// rows of HD * sizeof(T) bytes whose 16-byte chunks are permuted by the row
+// (chunk ^ turn(row)) so that the lanes of a load meet no bank twice: eight rows
+// at one chunk (bf16, ldmatrix), two rows at four (fp32).
+// Only this warp fills and reads it: cp.async groups and __syncwarp order it.
+template <typename T, int HD, int KEYS, int STAGES>
+struct Ring {
+  static constexpr int kRowBytes = HD * (int)sizeof(T);
+  static constexpr int kStageBytes = 2 * KEYS * kRowBytes;
+  static constexpr int kBytes = STAGES * kStageBytes;
+  static constexpr int CH = kRowBytes / 16;   // chunks of a row
+  static constexpr int RPC = CH < 32 ? 32 / CH : 1;  // rows of one copy instruction
+  static_assert(CH <= 32 && KEYS * STAGES <= 64, "a row per copy at least; one bit per key of the ring in `live`");
+
+  static __device__ __forceinline__ int turn(int row) { return sizeof(T) == 2 ? row & 7 : (row & 1) << 2; }
+
+  uint32_t base;
+  int fill = 0, use = 0;        // stages
+  uint64_t live = 0;            // which keys are there, KEYS bits per stage in use order
+  int in_ring = 0;
+
+  int page_j;                   // position of this lane's key of the next tile, and its page entry, which was
+  int32_t page;                 // asked for a tile ago: its latency is not waited for
+
+  __device__ __forceinline__ void look(const CacheAttendArgs& a, const Segment& g, int key0, int lane) {
+    page_j = key0 + lane % KEYS;
+    page = page_j < g.len ? page_entry(a.table, g.s, page_j) : -1;
   }
-  return (uint32_t)slot;
-}
+
+  // Copy the looked-up tile into the next stage.
+  __device__ __forceinline__ void push(const CacheAttendArgs& a, const Segment& g, int lane) {
+    int64_t slot = -1;
+    if (page_j < g.len) {
+      slot = entry_slot(a.table, page, page_j);
+      if (slot < 0) cache_error(a.err, kCacheBadPage);
+    }
+    const uint32_t sl = (uint32_t)slot;
+    live |= (uint64_t)(__ballot_sync(kFull, sl != ~0u) & (uint32_t)((1ull << KEYS) - 1)) << (KEYS * in_ring);
+    ++in_ring;
+    const int ch = lane % CH, r0 = lane / CH;
+    const char* kb = static_cast<const char*>(a.k) + (int64_t)g.kvh * kRowBytes + ch * 16;
+    const char* vb = static_cast<const char*>(a.v) + (int64_t)g.kvh * kRowBytes + ch * 16;
+    const int64_t stride = (int64_t)a.nkv * kRowBytes;
+    const uint32_t dst = base + fill * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < KEYS / RPC; ++i) {
+      const int r = i * RPC + r0;
+      const uint32_t x = __shfl_sync(kFull, sl, r);
+      const bool on = x != ~0u;
+      const int64_t off = on ? (int64_t)x * stride : 0;
+      const uint32_t to = dst + r * kRowBytes + ((ch ^ turn(r)) << 4);
+      cp_async16(to, kb + off, on);
+      cp_async16(to + KEYS * kRowBytes, vb + off, on);
+    }
+    fill = fill + 1 == STAGES ? 0 : fill + 1;
+  }
+
+  __device__ __forceinline__ uint32_t front() const { return base + use * kStageBytes; }
+  __device__ __forceinline__ uint32_t front_live() const { return (uint32_t)(live & ((1ull << KEYS) - 1)); }
+  __device__ __forceinline__ void pop() {
+    use = use + 1 == STAGES ? 0 : use + 1;
+    live >>= KEYS;
+    --in_ring;
+  }
+};
 
 // ---- bf16: tensor cores ------------------------------------------------------
 //
 // S^T = K Q^T and O^T = V^T P^T with m16n8k16: 16 keys (then 16 dimensions) are
 // the rows, the group's query heads the columns, so a group of up to 8 heads
-// wastes nothing but columns.  The contraction index may be permuted freely if
-// both operands agree, which lets a lane take 16 contiguous bytes of a key row
-// (8 dimensions) as its operand of two steps.  For V a lane takes 16 bytes of
-// four rows and pairs them by byte permutation: the transpose costs 4 PRMT per
-// step.  No operand passes through a shuffle or ldmatrix, and every lane reads
-// back exactly the bytes it copied itself: the ring needs no barrier.
+// wastes nothing but columns.  (tcgen05 tiles have 128 rows and one issuing
+// thread per block; here 8 warps each stream their own tiles with no barrier
+// between them, and the tensor pipe is busy under a tenth of the time.)
 //
 // P enters as the sum of two bf16 numbers (16 bits of it), twice the PV steps,
-// so that the result is as good as fp32 weights; the tensor pipe is idle
-// otherwise.
+// so that the result is as good as fp32 weights.
 template <int HD, int NT>
 struct WarpBf16 {
-  static constexpr int kStageBytes = 4 * kTileKeys * HD;      // K and V of a tile
-  static constexpr int kStages = HD == 128 ? 3 : 5;
-  static constexpr int kRing = kStages * kStageBytes;         // bytes a warp
-  static constexpr int KC = HD / 32, VC = HD / 64;            // 16-byte chunks of a lane: per key row, per value row
+  using R = Ring<__nv_bfloat16, HD, kTileKeys, HD == 128 ? 3 : 4>;
+  static constexpr int kStages = R::kBytes / R::kStageBytes;
+  static constexpr int kHeads = 8 * NT;        // query heads a block takes together
+  static constexpr int kRow = HD + 4;          // floats of a head's row in store(): no bank conflict
+  static constexpr int kBytes = R::kBytes > kHeads * kRow * 4 ? R::kBytes : kHeads * kRow * 4;
+  static constexpr int KS = HD / 16;
 
-  float o[4 * VC][NT][4];
+  float o[KS][NT][4];
   float m[NT][2], l[NT][2];
 
-  __device__ __forceinline__ void issue(const CacheAttendArgs& a, const Segment& g, uint32_t ring, uint32_t slot,
-                                        int lane) {
-    const int r = lane >> 2, c = lane & 3;
-    const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k) + (int64_t)g.kvh * HD;
-    const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v) + (int64_t)g.kvh * HD;
-    const int64_t row = (int64_t)a.nkv * HD;
-    uint32_t dst = ring + lane * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t sl = __shfl_sync(kFull, slot, r + 8 * i);
-      const bool live = sl != ~0u;
-      const __nv_bfloat16* p = kb + (live ? sl : 0u) * row + c * 8;
-#pragma unroll
-      for (int x = 0; x < KC; ++x) cp_async16(dst + (i * KC + x) * 512, p + x * 32, live);
-    }
-    dst += 2 * KC * 512;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t sl = __shfl_sync(kFull, slot, 2 * c + (i & 1) + 8 * (i >> 1));
-      const bool live = sl != ~0u;
-      const __nv_bfloat16* p = vb + (live ? sl : 0u) * row + r * 8;
-#pragma unroll
-      for (int x = 0; x < VC; ++x) cp_async16(dst + (i * VC + x) * 512, p + x * 64, live);
-    }
-  }
-
+  // Tiles t, t + step, ... below `end` of one segment.
   template <bool TRACK>
-  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, uint32_t ring, int t, int step,
-                                      int end, int lane) {
+  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float*,
+                                      int t, int step, int end, int lane) {
     const int r = lane >> 2, c = lane & 3;
     // Q as the right operand: column r of a tile is query head h0 + 8 n + r
-    uint4 q[NT][KC];
+    uint32_t q[NT][KS][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + r;
+      const __nv_bfloat16* p =
+          static_cast<const __nv_bfloat16*>(a.q) + (int64_t)g.s * a.ld_q + (int64_t)(g.h0 + h) * HD + 2 * c;
 #pragma unroll
-      for (int x = 0; x < KC; ++x) {
-        const int h = 8 * n + r;
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)g.s * a.ld_q +
-                                 (int64_t)(g.h0 + h) * HD + x * 32 + c * 8;
-        q[n][x] = h < g.nh ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-      }
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          q[n][x][y] = h < g.nh ? *reinterpret_cast<const uint32_t*>(p + 16 * x + 8 * y) : 0u;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4 * VC; ++i)
+      for (int x = 0; x < KS; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[x][n][e] = 0.f;
     }
-    // fill the ring; slots are looked up one tile ahead of their copy
+    R ring;
+    ring.base = tc::smem_u32(mem);
     int ti = t;
-    uint32_t slot = ti < end ? tile_slot(a, g, ti, lane) : ~0u;
-    uint32_t live_slots[kStages];  // which keys of a stage are there
-#pragma unroll
-    for (int st = 0; st < kStages; ++st) {
-      live_slots[st] = slot;
+    ring.look(a, g, ti * kTileKeys, lane);
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) {
       if (ti < end) {
-        issue(a, g, ring + st * kStageBytes, slot, lane);
+        ring.push(a, g, lane);
         ti += step;
-        slot = ti < end ? tile_slot(a, g, ti, lane) : ~0u;
+        ring.look(a, g, ti * kTileKeys, lane);
       }
       cp_async_commit();
     }
-    for (;;) {
+    // this lane's row and chunk of the operand loads (chunk 2 x + .. of step x)
+    const int krow = lane & 15, kch = lane >> 4;
+    const int vrow = (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
+#pragma unroll 1
+    for (; t < end; t += step) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t kbase = ring.front() + krow * R::kRowBytes;
+      const uint32_t vbase = ring.front() + kTileKeys * R::kRowBytes + vrow * R::kRowBytes;
+      const uint32_t live = ring.front_live();
+      float sc[NT][4], s2[NT][4];
 #pragma unroll
-      for (int st = 0; st < kStages; ++st) {
-        if (t >= end) goto done;
-        cp_async_wait<kStages - 1>();
-        const uint32_t base = ring + st * kStageBytes + lane * 16;
-        float sc[NT][4];
-        {
-          float s2[NT][4];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 4; ++e) sc[n][e] = s2[n][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[n][e] = s2[n][e] = 0.f;
-#pragma unroll
-          for (int x = 0; x < KC; ++x) {
-            uint32_t u[4], w[4];
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                         : "r"(base + x * 512));
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(base + (KC + x) * 512));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816(sc[n], u[0], w[0], u[1], w[1], q[n][x].x, q[n][x].y);
-              mma16816(s2[n], u[2], w[2], u[3], w[3], q[n][x].z, q[n][x].w);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[n][e] = (sc[n][e] + s2[n][e]) * a.scale_log2;
-        }
-        // keys r and r + 8 of the tile; absent ones weigh nothing
-        const bool live0 = __shfl_sync(kFull, live_slots[st], r) != ~0u;
-        const bool live1 = __shfl_sync(kFull, live_slots[st], r + 8) != ~0u;
-        const int j0 = t * kTileKeys + r;
-        uint32_t ph[NT][2], pl[NT][2];
-        bool grew = false;
-        float f[NT][2];
+      for (int x = 0; x < KS; x += 2) {
+        uint32_t k0[4], k1[4];
+        ldmatrix4(k0, kbase + (((2 * x + kch) ^ R::turn(krow)) << 4));
+        ldmatrix4(k1, kbase + (((2 * x + 2 + kch) ^ R::turn(krow)) << 4));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (!live0) sc[n][0] = sc[n][1] = -INFINITY;
-          if (!live1) sc[n][2] = sc[n][3] = -INFINITY;
-          if (TRACK) {
+          mma16816(sc[n], k0, q[n][x][0], q[n][x][1]);
+          mma16816(s2[n], k1, q[n][x + 1][0], q[n][x + 1][1]);
+        }
+      }
+      // keys r and r + 8 of the tile; absent ones weigh nothing
+      const bool whole = live == 0xffffu;
+      bool grew = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int h = 8 * n + 2 * c + (e & 1), j = j0 + 8 * (e >> 1);
-              if (h < g.nh && j < g.len) a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + j] = sc[n][e];
-            }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float raw = (sc[n][e] + s2[n][e]) * a.scale_log2;
+          sc[n][e] = whole || (live >> (r + 8 * (e >> 1)) & 1) ? raw : -INFINITY;
+          if (TRACK) {
+            const int h = 8 * n + 2 * c + (e & 1), j = t * kTileKeys + r + 8 * (e >> 1);
+            if (h < g.nh && j < g.len) a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + j] = sc[n][e];
           }
+          grew |= !(sc[n][e] <= m[n][e & 1] + kSlack);
+        }
+      if (__any_sync(kFull, grew)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float x = fmaxf(sc[n][e], sc[n][2 + e]);
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-            const float mn = fmaxf(m[n][e], x);
-            const float b = mn == -INFINITY ? 0.f : mn;
-            grew |= mn > m[n][e];
-            f[n][e] = ex2(m[n][e] - b);
-            m[n][e] = mn;
-            sc[n][e] = ex2((sc[n][e] - b) - kRoom);
-            sc[n][2 + e] = ex2((sc[n][2 + e] - b) - kRoom);
-            l[n][e] = l[n][e] * f[n][e] + (sc[n][e] + sc[n][2 + e]);
-          }
+            x = fmaxf(m[n][e], x);
+            const float f = m[n][e] == x ? 1.f : ex2(m[n][e] - x);
+            m[n][e] = x;
+            l[n][e] *= f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t hi = pack_bf16(sc[n][2 * i], sc[n][2 * i + 1]);
-            const float2 hf = unpack_bf16(hi);
-            ph[n][i] = transpose8x8(hi);
-            pl[n][i] = transpose8x8(pack_bf16(sc[n][2 * i] - hf.x, sc[n][2 * i + 1] - hf.y));
-          }
-        }
-        if (__any_sync(kFull, grew)) {
-#pragma unroll
-          for (int i = 0; i < 4 * VC; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[i][n][e] *= f[n][e & 1];
-        }
-        const uint32_t vbase = base + 2 * KC * 512;
-#pragma unroll
-        for (int x = 0; x < VC; ++x) {
-          uint32_t v[4][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                         : "r"(vbase + (i * VC + x) * 512));
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410), a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-            const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410), a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816(o[4 * x + w][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
-              mma16816(o[4 * x + w][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+            for (int y = 0; y < KS; ++y) {
+              o[y][n][e] *= f;
+              o[y][n][2 + e] *= f;
             }
           }
-        }
-        // the stage's bytes are in registers: refill it
-        __syncwarp();
-        live_slots[st] = slot;
-        if (ti < end) {
-          issue(a, g, ring + st * kStageBytes, slot, lane);
-          ti += step;
-          slot = ti < end ? tile_slot(a, g, ti, lane) : ~0u;
-        }
-        cp_async_commit();
-        t += step;
       }
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float b = m[n][e] == -INFINITY ? 0.f : m[n][e];
+          sc[n][e] = ex2((sc[n][e] - b) - kRoom);
+          sc[n][2 + e] = ex2((sc[n][2 + e] - b) - kRoom);
+          l[n][e] += sc[n][e] + sc[n][2 + e];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t hi = pack_bf16(sc[n][2 * i], sc[n][2 * i + 1]);
+          const float2 hf = unpack_bf16(hi);
+          ph[n][i] = transpose8x8(hi);
+          pl[n][i] = transpose8x8(pack_bf16(sc[n][2 * i] - hf.x, sc[n][2 * i + 1] - hf.y));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        uint32_t v[4];
+        ldmatrix4_trans(v, vbase + (((2 * x + vch) ^ R::turn(vrow)) << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816(o[x][n], v, ph[n][0], ph[n][1]);
+          mma16816(o[x][n], v, pl[n][0], pl[n][1]);
+        }
+      }
+      __syncwarp();  // the stage is read: refill it
+      ring.pop();
+      if (ti < end) {
+        ring.push(a, g, lane);
+        ti += step;
+        ring.look(a, g, ti * kTileKeys, lane);
+      }
+      cp_async_commit();
     }
-  done:
     cp_async_wait<0>();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -303,7 +323,7 @@ struct WarpBf16 {
       }
   }
 
-  // Unnormalised output [head][HD] and (max, denominator) of the warp.
+  // Unnormalised output [head][kRow] and (reference, denominator) of the warp.
   __device__ __forceinline__ void store(float* so, float2* sml, int lane) const {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -313,12 +333,9 @@ struct WarpBf16 {
         const int h = 8 * n + 2 * c + e;
         if (r == 0) sml[h] = make_float2(m[n][e], l[n][e]);
 #pragma unroll
-        for (int x = 0; x < VC; ++x) {
-          float* p = so + h * HD + 64 * x + 8 * r;
-          *reinterpret_cast<float4*>(p) = make_float4(o[4 * x][n][e], o[4 * x][n][2 + e], o[4 * x + 1][n][e],
-                                                      o[4 * x + 1][n][2 + e]);
-          *reinterpret_cast<float4*>(p + 4) = make_float4(o[4 * x + 2][n][e], o[4 * x + 2][n][2 + e],
-                                                          o[4 * x + 3][n][e], o[4 * x + 3][n][2 + e]);
+        for (int x = 0; x < KS; ++x) {
+          so[h * kRow + 16 * x + r] = o[x][n][e];
+          so[h * kRow + 16 * x + 8 + r] = o[x][n][2 + e];
         }
       }
   }
@@ -326,25 +343,32 @@ struct WarpBf16 {
 
 // ---- fp32: CUDA cores --------------------------------------------------------
 //
-// 8 keys at a time: for the scores lane (r, c) holds a quarter of key r's
+// 8 keys a stage: for the scores lane (r, c) takes a quarter of key r's
 // dimensions (queries come from shared memory, the four quarters meet in two
 // shuffles); for the output a lane holds 4 dimensions of every key and the
 // weights come back through shared memory.
 template <int HD>
 struct WarpF32 {
-  static constexpr int KI = HD / 16;           // 16-byte pieces of a key a lane holds
-  static constexpr int LPR = HD / 4;           // lanes on one value row
-  static constexpr int RPI = 32 / LPR;         // value rows per load
-  static constexpr int kRing = 8 * HD * 4 + 512;  // bytes a warp: output, then weights [8 keys][8 heads]
+  static constexpr int KEYS = 8;
+  using R = Ring<float, HD, KEYS, HD == 128 ? 2 : 4>;
+  static constexpr int kStages = R::kBytes / R::kStageBytes;
+  static constexpr int kHeads = 8;
+  static constexpr int kRow = HD;
+  static constexpr int kBytes = R::kBytes + 256;  // the ring (then the output), weights [8 keys][8 heads]
+  static constexpr int KI = HD / 16;              // 16-byte pieces of a key a lane takes
+  static constexpr int LPR = HD / 4;              // lanes on one value row
+  static constexpr int RPI = 32 / LPR;            // value rows per load
+  static_assert(kHeads * kRow * 4 <= R::kBytes, "output over the ring");
 
   float o[8][4];
   float m[8], l[8];
 
   template <bool TRACK>
-  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, const float* sq, float* sp, int t,
-                                      int step, int end, int lane) {
+  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float* sq,
+                                      int t, int step, int end, int lane) {
     const int r = lane >> 2, c = lane & 3;
     const int vr = lane / LPR, vd = lane % LPR;
+    float* sp = reinterpret_cast<float*>(mem + R::kBytes);
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
       m[h] = -INFINITY;
@@ -352,78 +376,102 @@ struct WarpF32 {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
     }
-    const float* kb = static_cast<const float*>(a.k) + (int64_t)g.kvh * HD;
-    const float* vb = static_cast<const float*>(a.v) + (int64_t)g.kvh * HD;
-    const int64_t row = (int64_t)a.nkv * HD;
-    for (; t < end; t += step) {
-      const uint32_t slots = tile_slot(a, g, t, lane);
+    R ring;
+    ring.base = tc::smem_u32(mem);
+    // stages in order: both halves of tile t, then those of t + step, ...; those past the end or the length are
+    // left out
+    int ki = t * kTileKeys, ku = ki;
+    const int stop = min(end * kTileKeys, g.len);
+    auto next = [&](int k) { return (k & KEYS) ? k - KEYS + step * kTileKeys : k + KEYS; };
+    ring.look(a, g, ki, lane);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int j = t * kTileKeys + 8 * half + r;
-        if (t * kTileKeys + 8 * half >= g.len) break;
-        float4 k[KI], v[8 / RPI];
-        const uint32_t sl = __shfl_sync(kFull, slots, 8 * half + r);
-        const bool live = sl != ~0u;
-        const float* kp = kb + (live ? sl : 0u) * row + c * 4;
+    for (int i = 0; i < kStages; ++i) {
+      if (ki < stop) {
+        ring.push(a, g, lane);
+        ki = next(ki);
+        ring.look(a, g, ki, lane);
+      }
+      cp_async_commit();
+    }
+#pragma unroll 1
+    for (; ku < stop; ku = next(ku)) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const unsigned char* st = mem + (ring.front() - ring.base);
+      const bool live = ring.front_live() >> r & 1;
+      float4 k[KI];
 #pragma unroll
-        for (int i = 0; i < KI; ++i)
-          k[i] = live ? *reinterpret_cast<const float4*>(kp + 16 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < KI; ++i)
+        k[i] = *reinterpret_cast<const float4*>(st + r * R::kRowBytes + (((c + 4 * i) ^ R::turn(r)) << 4));
+      float x[8];
+      bool grew = false;
 #pragma unroll
-        for (int i = 0; i < 8 / RPI; ++i) {
-          const uint32_t vs = __shfl_sync(kFull, slots, 8 * half + i * RPI + vr);
-          v[i] = vs != ~0u ? *reinterpret_cast<const float4*>(vb + (int64_t)vs * row + vd * 4)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float f[8];
-        bool grew = false;
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          float x = 0.f;
+      for (int h = 0; h < 8; ++h) {
+        x[h] = 0.f;
+        if (h < g.nh) {
 #pragma unroll
           for (int i = 0; i < KI; ++i) {
             const float4 q = *reinterpret_cast<const float4*>(sq + h * HD + c * 4 + 16 * i);
-            x += q.x * k[i].x + q.y * k[i].y + q.z * k[i].z + q.w * k[i].w;
+            x[h] += q.x * k[i].x + q.y * k[i].y + q.z * k[i].z + q.w * k[i].w;
           }
-          x += __shfl_xor_sync(kFull, x, 1);
-          x += __shfl_xor_sync(kFull, x, 2);
-          x = live ? x * a.scale_log2 : -INFINITY;
-          if (TRACK && c == (h & 3) && h < g.nh && j < g.len)
-            a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + j] = x;
-          float y = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-          y = fmaxf(y, __shfl_xor_sync(kFull, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(kFull, y, 16));
-          const float mn = fmaxf(m[h], y);
-          const float b = mn == -INFINITY ? 0.f : mn;
-          grew |= mn > m[h];
-          f[h] = ex2(m[h] - b);
-          m[h] = mn;
-          const float p = ex2((x - b) - kRoom);
-          l[h] = l[h] * f[h] + p;
+          x[h] += __shfl_xor_sync(kFull, x[h], 1);
+          x[h] += __shfl_xor_sync(kFull, x[h], 2);
+          x[h] = live ? x[h] * a.scale_log2 : -INFINITY;
+          if (TRACK && c == (h & 3) && ku + r < g.len)
+            a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + ku + r] = x[h];
+          grew |= !(x[h] <= m[h] + kSlack);
+        }
+      }
+      if (__any_sync(kFull, grew)) {
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (h < g.nh) {
+            float y = fmaxf(x[h], __shfl_xor_sync(kFull, x[h], 4));
+            y = fmaxf(y, __shfl_xor_sync(kFull, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(kFull, y, 16));
+            y = fmaxf(m[h], y);
+            const float f = m[h] == y ? 1.f : ex2(m[h] - y);
+            m[h] = y;
+            l[h] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[h][e] *= f;
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (h < g.nh) {
+          const float p = ex2((x[h] - (m[h] == -INFINITY ? 0.f : m[h])) - kRoom);
+          l[h] += p;
           if (c == (h & 3)) sp[r * 8 + h] = p;
         }
-        __syncwarp();
-        if (__any_sync(kFull, grew)) {
+      __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
+      for (int i = 0; i < 8 / RPI; ++i) {
+        const int row = i * RPI + vr;
+        const float4 v =
+            *reinterpret_cast<const float4*>(st + KEYS * R::kRowBytes + row * R::kRowBytes + ((vd ^ R::turn(row)) << 4));
+        const float4 p0 = *reinterpret_cast<const float4*>(sp + row * 8);
+        const float4 p1 = *reinterpret_cast<const float4*>(sp + row * 8 + 4);
+        const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] *= f[h];
-        }
-#pragma unroll
-        for (int i = 0; i < 8 / RPI; ++i) {
-          const float4 p0 = *reinterpret_cast<const float4*>(sp + (i * RPI + vr) * 8);
-          const float4 p1 = *reinterpret_cast<const float4*>(sp + (i * RPI + vr) * 8 + 4);
-          const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            o[h][0] += p[h] * v[i].x;
-            o[h][1] += p[h] * v[i].y;
-            o[h][2] += p[h] * v[i].z;
-            o[h][3] += p[h] * v[i].w;
+        for (int h = 0; h < 8; ++h)
+          if (h < g.nh) {
+            o[h][0] += p[h] * v.x;
+            o[h][1] += p[h] * v.y;
+            o[h][2] += p[h] * v.z;
+            o[h][3] += p[h] * v.w;
           }
-        }
-        __syncwarp();
       }
+      __syncwarp();  // the stage and the weights are read
+      ring.pop();
+      if (ki < stop) {
+        ring.push(a, g, lane);
+        ki = next(ki);
+        ring.look(a, g, ki, lane);
+      }
+      cp_async_commit();
     }
+    cp_async_wait<0>();
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
       l[h] += __shfl_xor_sync(kFull, l[h], 4);
@@ -442,12 +490,12 @@ struct WarpF32 {
     for (int h = 0; h < 8; ++h) {
       if (lane == 0) sml[h] = make_float2(m[h], l[h]);
       if (lane < LPR)
-        *reinterpret_cast<float4*>(so + h * HD + vd * 4) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
+        *reinterpret_cast<float4*>(so + h * kRow + vd * 4) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
     }
   }
 };
 
-// ---- the kernel --------------------------------------------------------------
+// ---- the kernels -------------------------------------------------------------
 
 template <typename T, int HD, int NT>
 struct WarpOf {
@@ -458,8 +506,10 @@ struct WarpOf<float, HD, NT> {
   using type = WarpF32<HD>;
 };
 
-// Block-wide exclusive scan of tiles per sequence into first[0..S].
-__device__ __forceinline__ void scan_tiles(const CacheAttendArgs& a, int* first, int* sums) {
+// Block-wide exclusive scan of units_of(length) per sequence into
+// first[0..S]; kThreads threads, `sums` one int per warp.
+template <typename F>
+__device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, int* sums, F units_of) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int carry = 0;
   for (int s0 = 0; s0 < a.S; s0 += kThreads) {
@@ -467,7 +517,7 @@ __device__ __forceinline__ void scan_tiles(const CacheAttendArgs& a, int* first,
     int x = 0;
     if (s < a.S) {
       bool bad;
-      x = tiles_of(checked_len(a.lens[s], a.limit, &bad));
+      x = units_of(checked_len(a.lens[s], a.limit, &bad));
       if (bad && blockIdx.x == 0) cache_error(a.err, kCacheBadLength);
     }
     int y = x;
@@ -492,35 +542,64 @@ __device__ __forceinline__ void scan_tiles(const CacheAttendArgs& a, int* first,
   __syncthreads();
 }
 
-// out[s][h] of one segment from its unnormalised sum and denominator.
+// The sequence that unit u (of H per entry of first) belongs to: the last one
+// that starts at or before it, which is not an empty one.
+__device__ __forceinline__ int find_sequence(const int* first, int S, int64_t u, int H) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)first[mid] * H <= u)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 template <typename T>
 __device__ __forceinline__ void write_out(const CacheAttendArgs& a, int s, int h, int hd, int d, float4 o, float l) {
   T* p = static_cast<T*>(a.out) + (int64_t)s * a.ld_out + (int64_t)h * hd + d;
   store4<T>(p, make_float4(o.x / l, o.y / l, o.z / l, o.w / l));
 }
 
+__device__ __forceinline__ void write_lse(const CacheAttendArgs& a, int s, int h, float m, float l) {
+  a.lse[(int64_t)s * a.nq + h] = (m == -INFINITY ? 0.f : m) + (kRoom + log2f(l));
+}
+
+// ex2(m - top) with an empty part (m = -inf) weighing 0 even where all are.
+__device__ __forceinline__ float part_factor(float m, float top) { return ex2(m - (top == -INFINITY ? 0.f : top)); }
+
+// Floats of a partial result: output [NH][HD], reference [NH], denominator [NH].
+template <int NH, int HD>
+__device__ __forceinline__ float* part_of(const CacheAttendArgs& a, int slot) {
+  return a.parts + (int64_t)slot * NH * (HD + 2);
+}
+
+constexpr int kShort = 4;        // tiles of a segment that one warp takes alone
+constexpr int kInlineParts = 6;  // partial results that the last block to arrive joins itself
+
 // Blocks walk the line of units (sf_cache_index.h).  The 8 warps of a block
 // take the tiles of a segment in turn, or, where the next segments are whole
-// and short, one segment each.
+// and short, one segment each.  A segment cut over few blocks is joined by the
+// last of them to finish, one cut over many by the join kernel.
 template <typename T, int HD, int NT, bool TRACK>
 __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_constant__ CacheAttendArgs a) {
   using Warp = typename WarpOf<T, HD, NT>::type;
-  constexpr int NH = Group<T, NT>::kHeads;
+  constexpr int NH = Warp::kHeads, ROW = Warp::kRow;
   constexpr bool F32 = sizeof(T) == 4;
-  constexpr int kShort = 4;  // tiles of a segment that one warp takes alone
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float2 sml[kWarps][NH];
   __shared__ float sfac[kWarps][NH];
-  __shared__ int s_sums[kWarps];
+  __shared__ int sums[kWarps];
   __shared__ int s_last;
   __shared__ __align__(16) float sq[F32 ? kWarps : 1][F32 ? 8 * HD : 4];
-  int* first = reinterpret_cast<int*>(smem + kWarps * Warp::kRing);
+  int* first = reinterpret_cast<int*>(smem + kWarps * Warp::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* mine = smem + warp * Warp::kRing;
-  const uint32_t ring = tc::smem_u32(mine);
+  unsigned char* mine = smem + warp * Warp::kBytes;
+  float* my_out = reinterpret_cast<float*>(mine);
   pdl_wait();
   pdl_trigger();
-  scan_tiles(a, first, s_sums);
+  scan_lens(a, first, sums, [](int len) { return tiles_of(len); });
   const int G = a.nq / a.nkv, nsub = (G + NH - 1) / NH, H = a.nkv * nsub;
   // empty sequences have no units: zeros
   for (int s = blockIdx.x; s < a.S; s += gridDim.x)
@@ -531,16 +610,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
   const int64_t per = units_per_block(units, gridDim.x, a.least);
   int64_t u = (int64_t)blockIdx.x * per;
   const int64_t u_end = u + per < units ? u + per : units;
+  if (a.join && threadIdx.x == 0) a.joins[blockIdx.x].n = 0;
   if (u >= u_end) return;
-  int s;
-  {
-    int lo = 0, hi = a.S - 1;  // last s with first[s] * H <= u, never an empty one: take the last of equals
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)first[mid] * H <= u) lo = mid; else hi = mid - 1;
-    }
-    s = lo;
-  }
+  int s = find_sequence(first, a.S, u, H);
   auto segment = [&](int ss, int hs) {
     Segment g;
     g.s = ss;
@@ -553,19 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
   };
   auto load_q = [&](const Segment& g, float* to, int i0, int step) {
     if constexpr (F32) {
-      for (int i = i0; i < 8 * HD; i += step)
-        to[i] = i / HD < g.nh ? static_cast<const float*>(a.q)[(int64_t)g.s * a.ld_q + (int64_t)g.h0 * HD + i] : 0.f;
+      for (int i = i0; i < g.nh * HD; i += step)
+        to[i] = static_cast<const float*>(a.q)[(int64_t)g.s * a.ld_q + (int64_t)g.h0 * HD + i];
     }
   };
   Warp w;
-  auto walk = [&](const Segment& g, float* q, int t, int step, int end) {
-    if constexpr (F32)
-      w.template run<TRACK>(a, g, q, reinterpret_cast<float*>(mine) + 8 * HD, t, step, end, lane);
-    else
-      w.template run<TRACK>(a, g, ring, t, step, end, lane);
-  };
   while (u < u_end) {
-    int tiles = first[s + 1] - first[s];
+    const int tiles = first[s + 1] - first[s];
     const int in_s = (int)(u - (int64_t)first[s] * H);
     const int hs = in_s / tiles, t0 = in_s % tiles;
     // ---- short whole segments: a warp each
@@ -591,26 +657,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
       if (n > 1) {
         if (my_s >= 0) {
           const Segment g = segment(my_s, my_hs);
-          if constexpr (F32) {
-            load_q(g, sq[warp], lane, 32);
-            __syncwarp();
-          }
-          walk(g, sq[F32 ? warp : 0], 0, 1, tiles_of(g.len));
+          load_q(g, sq[F32 ? warp : 0], lane, 32);
           __syncwarp();
-          w.store(reinterpret_cast<float*>(mine), sml[warp], lane);
+          w.template run<TRACK>(a, g, mine, sq[F32 ? warp : 0], 0, 1, tiles_of(g.len), lane);
+          __syncwarp();
+          w.store(my_out, sml[warp], lane);
           __syncwarp();
           for (int i = lane; i < g.nh * HD / 4; i += 32) {
             const int h = i / (HD / 4), d = i % (HD / 4) * 4;
-            write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(mine + (h * HD + d) * 4),
+            write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
                          sml[warp][h].y);
           }
-          if (TRACK && lane < g.nh) {
-            const float2 ml = sml[warp][lane];
-            a.lse[(int64_t)g.s * a.nq + g.h0 + lane] = (ml.x == -INFINITY ? 0.f : ml.x) + (kRoom + log2f(ml.y));
-          }
-          __syncwarp();
+          if (TRACK && lane < g.nh) write_lse(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
         }
-        __syncthreads();  // the warps' tables are free again
+        __syncthreads();  // the warps' memory is free again
         u = v;
         s = cs;
         continue;
@@ -619,110 +679,106 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
     // ---- one segment by all warps
     const int end = (int)(u_end - u < tiles - t0 ? u_end - u : tiles - t0) + t0;
     const Segment g = segment(s, hs);
-    if constexpr (F32) {
-      load_q(g, sq[0], threadIdx.x, kThreads);
-      __syncthreads();
-    }
-    walk(g, sq[0], t0 + warp, kWarps, end);
+    load_q(g, sq[0], threadIdx.x, kThreads);
+    if (F32) __syncthreads();
+    w.template run<TRACK>(a, g, mine, sq[0], t0 + warp, kWarps, end, lane);
     __syncwarp();
-    w.store(reinterpret_cast<float*>(mine), sml[warp], lane);
+    w.store(my_out, sml[warp], lane);
     __syncthreads();
     const int64_t seg0 = (int64_t)first[s] * H + (int64_t)hs * tiles;
-    const int b0 = first_block(seg0, per), b1 = last_block(seg0, tiles, per);
-    float* part = a.parts + (int64_t)part_slot(blockIdx.x, seg0, per) * NH * (HD + 2);
-    // factors of the warps, by 8 * NH threads; the first NH keep the total
+    const int b0 = first_block(seg0, per), b1 = last_block(seg0, tiles, per), n = b1 - b0 + 1;
+    float* part = part_of<NH, HD>(a, part_slot(blockIdx.x, seg0, per));
     if (threadIdx.x < kWarps * NH) {
       const int x = threadIdx.x / NH, h = threadIdx.x % NH;
-      float mm = sml[0][h].x;
+      float top = sml[0][h].x;
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) mm = fmaxf(mm, sml[i][h].x);
-      const float b = mm == -INFINITY ? 0.f : mm;
-      sfac[x][h] = ex2(sml[x][h].x - b);
+      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sml[i][h].x);
+      sfac[x][h] = part_factor(sml[x][h].x, top);
     }
     __syncthreads();
-    if (threadIdx.x < g.nh) {
+    if (threadIdx.x < g.nh && (n > 1 || TRACK)) {
       const int h = threadIdx.x;
-      float mm = -INFINITY, ll = 0.f;
+      float top = -INFINITY, l = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        mm = fmaxf(mm, sml[i][h].x);
-        ll += sml[i][h].y * sfac[i][h];
+        top = fmaxf(top, sml[i][h].x);
+        l += sml[i][h].y * sfac[i][h];
       }
-      if (b0 != b1) {
-        part[NH * HD + h] = mm;
-        part[NH * HD + NH + h] = ll;
-      } else if (TRACK) {
-        a.lse[(int64_t)g.s * a.nq + g.h0 + h] = (mm == -INFINITY ? 0.f : mm) + (kRoom + log2f(ll));
+      if (n > 1) {
+        part[NH * HD + h] = top;
+        part[NH * HD + NH + h] = l;
+      } else {
+        write_lse(a, g.s, g.h0 + h, top, l);
       }
     }
     for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
       const int h = i / (HD / 4), d = i % (HD / 4) * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float ll = 0.f;
+      float l = 0.f;
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) {
-        const float4 y = *reinterpret_cast<const float4*>(smem + x * Warp::kRing + (h * HD + d) * 4);
+        const float4 y = *reinterpret_cast<const float4*>(smem + x * Warp::kBytes + (h * ROW + d) * 4);
         const float f = sfac[x][h];
         o.x += y.x * f;
         o.y += y.y * f;
         o.z += y.z * f;
         o.w += y.w * f;
-        ll += sml[x][h].y * f;
+        l += sml[x][h].y * f;
       }
-      if (b0 != b1)
+      if (n > 1)
         *reinterpret_cast<float4*>(part + h * HD + d) = o;
       else
-        write_out<T>(a, g.s, g.h0 + h, HD, d, o, ll);
+        write_out<T>(a, g.s, g.h0 + h, HD, d, o, l);
     }
-    if (b0 != b1) {
+    if (n > kInlineParts) {
+      if (blockIdx.x == b0 && threadIdx.x == 0)
+        a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, part_slot(b0, seg0, per)};
+    } else if (n > 1) {
       // the last block to arrive joins the parts, in block order
       __threadfence();
       __syncthreads();
-      const int n = b1 - b0 + 1;
       if (threadIdx.x == 0) s_last = atomicInc(a.arrived + b0, n - 1) == (unsigned)(n - 1);
       __syncthreads();
       if (s_last) {
         __threadfence();
-        float* fac = reinterpret_cast<float*>(smem);  // [n][NH], over the rings: nobody uses them now
-        float2* tot = &sml[0][0];                      // [NH] (max, denominator)
-        for (int h = warp; h < g.nh; h += kWarps) {
-          float mm = -INFINITY;
-          for (int x = lane; x < n; x += 32)
-            mm = fmaxf(mm, __ldcg(a.parts + (int64_t)part_slot(b0 + x, seg0, per) * NH * (HD + 2) + NH * HD + h));
-          mm = warp_max(mm);
-          const float b = mm == -INFINITY ? 0.f : mm;
-          float ll = 0.f;
-          for (int x = lane; x < n; x += 32) {
-            const float* p = a.parts + (int64_t)part_slot(b0 + x, seg0, per) * NH * (HD + 2) + NH * HD + h;
-            const float f = ex2(__ldcg(p) - b);
-            fac[x * NH + h] = f;
-            ll += __ldcg(p + NH) * f;
+        if (threadIdx.x < NH * kInlineParts) {
+          const int x = threadIdx.x / NH, h = threadIdx.x % NH;
+          float2 ml = make_float2(-INFINITY, 0.f);
+          if (x < n && h < g.nh) {
+            const float* p = part_of<NH, HD>(a, part_slot(b0 + x, seg0, per)) + NH * HD + h;
+            ml = make_float2(__ldcg(p), __ldcg(p + NH));
           }
-          ll = sf::warp_sum(ll);
-          if (lane == 0) tot[h] = make_float2(mm, ll);
+          sml[x][h] = ml;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
           const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+          float4 y[kInlineParts];
+#pragma unroll
+          for (int x = 0; x < kInlineParts; ++x)
+            if (x < n)
+              y[x] = __ldcg(reinterpret_cast<const float4*>(part_of<NH, HD>(a, part_slot(b0 + x, seg0, per)) + h * HD + d));
+          float top = sml[0][h].x;
+#pragma unroll
+          for (int x = 1; x < kInlineParts; ++x) top = fmaxf(top, sml[x][h].x);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int x = 0; x < n; ++x) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(
-                a.parts + (int64_t)part_slot(b0 + x, seg0, per) * NH * (HD + 2) + h * HD + d));
-            const float f = fac[x * NH + h];
-            o.x += y.x * f;
-            o.y += y.y * f;
-            o.z += y.z * f;
-            o.w += y.w * f;
-          }
-          write_out<T>(a, g.s, g.h0 + h, HD, d, o, tot[h].y);
+          float l = 0.f;
+#pragma unroll
+          for (int x = 0; x < kInlineParts; ++x)
+            if (x < n) {
+              const float f = part_factor(sml[x][h].x, top);
+              o.x += y[x].x * f;
+              o.y += y[x].y * f;
+              o.z += y[x].z * f;
+              o.w += y[x].w * f;
+              l += sml[x][h].y * f;
+            }
+          write_out<T>(a, g.s, g.h0 + h, HD, d, o, l);
+          if (TRACK && d == 0) write_lse(a, g.s, g.h0 + h, top, l);
         }
-        if (TRACK && threadIdx.x < g.nh)
-          a.lse[(int64_t)g.s * a.nq + g.h0 + threadIdx.x] =
-              (tot[threadIdx.x].x == -INFINITY ? 0.f : tot[threadIdx.x].x) + (kRoom + log2f(tot[threadIdx.x].y));
       }
     }
-    __syncthreads();  // rings and tables free for the next segment
+    __syncthreads();  // the warps' memory and tables are free for the next segment
     u += end - t0;
     if (end == tiles && hs + 1 == H) {
       do ++s;
@@ -731,44 +787,139 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
   }
 }
 
-// weights_out[s][c][j] = weights_in + the group's normalised weights of key j.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const __grid_constant__ CacheAttendArgs a) {
+// Joins a segment cut over more than kInlineParts blocks: a block per (its
+// first block, head), the parts dealt over kJoinGroups groups of threads.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int HD, int NH>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttendArgs a) {
+  constexpr int COLS = HD / 4, GROUPS = kJoinThreads / COLS;
+  __shared__ float fac[kJoinThreads];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ __align__(16) float4 acc[GROUPS][COLS];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, s = blockIdx.y, G = a.nq / a.nkv;
-  bool bad;
-  const int len = checked_len(a.lens[s], a.limit, &bad);
-  for (int j = threadIdx.x; j < len; j += 256) {
-    const int64_t at = ((int64_t)s * a.nkv + c) * a.ld_w + j;
-    float w = 0.f;
-    for (int g = 0; g < G; ++g) {
-      const int64_t h = (int64_t)s * a.nq + c * G + g;
-      const float x = a.scores[h * a.ld_scores + j];
-      w += x == -INFINITY ? 0.f : ex2(x - a.lse[h]);
+  const CacheJoin j = a.joins[blockIdx.x];
+  const int h = blockIdx.y;
+  if (h >= j.nh || j.n == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto part = [&](int x) { return part_of<NH, HD>(a, x ? 2 * ((int)blockIdx.x + x) : j.first); };
+  const int g = threadIdx.x / COLS, d = threadIdx.x % COLS * 4;
+  float m = -INFINITY, l = 0.f;
+  if (threadIdx.x < j.n) {  // j.n <= blocks <= kJoinThreads
+    const float* p = part(threadIdx.x) + NH * HD + h;
+    m = p[0];
+    l = p[NH];
+  }
+  float top = warp_max(m);
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  top = red[0][0];
+#pragma unroll
+  for (int i = 1; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[0][i]);
+  const float f = part_factor(m, top);
+  fac[threadIdx.x] = f;
+  l = warp_sum(threadIdx.x < j.n ? l * f : 0.f);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int x = g; x < j.n; x += GROUPS) {
+    const float4 y = *reinterpret_cast<const float4*>(part(x) + h * HD + d);
+    const float fx = fac[x];
+    o.x += y.x * fx;
+    o.y += y.y * fx;
+    o.z += y.z * fx;
+    o.w += y.w * fx;
+  }
+  acc[g][threadIdx.x % COLS] = o;
+  __syncthreads();
+  if (g == 0) {
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 y = acc[i][threadIdx.x];
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
     }
-    a.w_out[at] = (a.w_in ? a.w_in[at] : 0.f) + w;
+    write_out<T>(a, j.s, j.h0 + h, HD, d, o, l);
+    if (a.w_out && threadIdx.x == 0) write_lse(a, j.s, j.h0 + h, top, l);
   }
 }
 
-template <typename T, int HD, int NT, bool TRACK>
-cudaError_t attend_t(cudaStream_t st, const CacheAttendArgs& a, int blocks) {
-  using Warp = typename WarpOf<T, HD, NT>::type;
-  const size_t smem = (size_t)kWarps * Warp::kRing + ((size_t)a.S + 1) * sizeof(int);
-  return launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1, cache_attend_kernel<T, HD, NT, TRACK>, a);
+// weights_out[s][c][j] = weights_in + the group's normalised weights of key j.
+// Blocks take units of kWeightKeys keys of one (sequence, KV head) in turn.
+constexpr int kWeightKeys = 4 * kThreads;
+
+__global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ CacheAttendArgs a) {
+  extern __shared__ int first[];
+  __shared__ int sums[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int G = a.nq / a.nkv;
+  scan_lens(a, first, sums, [](int len) { return (len + kWeightKeys - 1) / kWeightKeys; });
+  const int64_t units = (int64_t)first[a.S] * a.nkv;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int s = find_sequence(first, a.S, u, a.nkv), n = first[s + 1] - first[s];
+    const int in_s = (int)(u - (int64_t)first[s] * a.nkv), c = in_s / n;
+    const int j0 = in_s % n * kWeightKeys + (int)threadIdx.x, len = a.lens[s];
+    const int64_t at = ((int64_t)s * a.nkv + c) * a.ld_w;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+      const int64_t h = (int64_t)s * a.nq + c * G + g;
+      const float lse = a.lse[h];
+      const float* sc = a.scores + h * a.ld_scores;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * kThreads;
+        const float x = j < len ? sc[j] : -INFINITY;
+        w[i] += x == -INFINITY ? 0.f : ex2(x - lse);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + i * kThreads;
+      if (j < len) a.w_out[at + j] = (a.w_in ? a.w_in[at + j] : 0.f) + w[i];
+    }
+  }
 }
 
 template <typename T, int HD, int NT>
-cudaError_t attend_n(cudaStream_t st, const CacheAttendArgs& a, int blocks) {
-  cudaError_t e = a.w_out ? attend_t<T, HD, NT, true>(st, a, blocks) : attend_t<T, HD, NT, false>(st, a, blocks);
-  if (e == cudaSuccess && a.w_out)
-    e = launch_pdl(st, dim3(a.nkv, a.S), dim3(256), 0, 1, cache_weights_kernel, a);
+constexpr int ring_bytes() {
+  return kWarps * WarpOf<T, HD, NT>::type::kBytes;
+}
+
+template <typename T, int HD, int NT>
+cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
+  constexpr int NH = WarpOf<T, HD, NT>::type::kHeads;
+  const int G = a.nq / a.nkv, longest = tiles_of((int)a.limit);
+  a.least = 2 * kWarps;
+  // no more blocks than the longest batch of this table could keep busy
+  const int64_t want = ((int64_t)a.S * a.nkv * ((G + NH - 1) / NH) * longest + a.least - 1) / a.least;
+  const int blocks = (int)(want < sm_count ? want : sm_count);
+  // a segment lies in at most (longest - 1) / least + 2 blocks
+  a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks > kInlineParts;
+  const size_t table = ((size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
+  cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
+                             a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);
+  if (e == cudaSuccess && a.join)
+    e = launch_pdl(st, dim3(blocks, NH < G ? NH : G), dim3(kJoinThreads), 0, 1, cache_join_kernel<T, HD, NH>, a);
+  if (e == cudaSuccess && a.w_out) {
+    const int64_t most = (int64_t)a.S * a.nkv * ((a.limit + kWeightKeys - 1) / kWeightKeys);
+    e = launch_pdl(st, dim3((unsigned)(most < 4 * sm_count ? most : 4 * sm_count)), dim3(kThreads), table, 1,
+                   cache_weights_kernel, a);
+  }
   return e;
 }
 
 template <typename T, int HD, int NT>
 cudaError_t allow_smem() {
-  using Warp = typename WarpOf<T, HD, NT>::type;
-  const int bytes = kWarps * Warp::kRing + 4097 * (int)sizeof(int);
+  const int bytes = ring_bytes<T, HD, NT>() + 4097 * (int)sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<T, HD, NT, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
@@ -790,19 +941,13 @@ cudaError_t prepare_cache_attend() {
   return e;
 }
 
-cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& args, int bf16, int sm_count) {
-  CacheAttendArgs a = args;
-  const int G = a.nq / a.nkv;
-  const int NH = bf16 && G > 8 ? 16 : 8;
-  a.least = 2 * kWarps;
-  // no more blocks than the longest batch of this table could keep busy
-  const int64_t most = (int64_t)a.S * a.nkv * ((G + NH - 1) / NH) * tiles_of((int)a.limit);
-  const int64_t want = (most + a.least - 1) / a.least;
-  const int blocks = (int)(want < sm_count ? (want < 1 ? 1 : want) : sm_count);
-  if (!bf16) return a.hd == 128 ? attend_n<float, 128, 1>(st, a, blocks) : attend_n<float, 64, 1>(st, a, blocks);
+cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& a, int bf16, int sm_count) {
+  if (sm_count > kJoinThreads) sm_count = kJoinThreads;
+  if (!bf16) return a.hd == 128 ? attend_t<float, 128, 1>(st, a, sm_count) : attend_t<float, 64, 1>(st, a, sm_count);
+  const bool wide = a.nq / a.nkv > 8;
   if (a.hd == 128)
-    return NH == 16 ? attend_n<__nv_bfloat16, 128, 2>(st, a, blocks) : attend_n<__nv_bfloat16, 128, 1>(st, a, blocks);
-  return NH == 16 ? attend_n<__nv_bfloat16, 64, 2>(st, a, blocks) : attend_n<__nv_bfloat16, 64, 1>(st, a, blocks);
+    return wide ? attend_t<__nv_bfloat16, 128, 2>(st, a, sm_count) : attend_t<__nv_bfloat16, 128, 1>(st, a, sm_count);
+  return wide ? attend_t<__nv_bfloat16, 64, 2>(st, a, sm_count) : attend_t<__nv_bfloat16, 64, 1>(st, a, sm_count);
 }
 
 }  // namespace sf

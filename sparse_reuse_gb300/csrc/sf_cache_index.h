@@ -13,6 +13,9 @@
 
 namespace sf {
 
+constexpr int kMaxLen = 262144;      // positions of a sequence
+constexpr int kMaxPageSize = 65536;
+
 // One page table: entry (s, c) is the page of positions c * page_size ...
 struct PageTable {
   const int32_t* pages;
@@ -20,18 +23,36 @@ struct PageTable {
   int cols;         // entries of a row that may be read
   int page_size;
   int64_t n_pages;  // pages of the pool
+  uint64_t inverse;  // ceil(2^40 / page_size)
 };
 
-// Slot (page * page_size + offset) of position j of sequence s, or -1 when j
-// lies outside the table or on a page outside the pool.  s must be in range.
-SF_HD int64_t page_slot(const PageTable& t, int s, int j) {
-  if (j < 0) return -1;
-  const int c = j / t.page_size;
-  if (c >= t.cols) return -1;
-  const int64_t page = t.pages[(int64_t)s * t.ld + c];
-  if (page < 0 || page >= t.n_pages) return -1;
-  return page * t.page_size + (j - c * t.page_size);
+SF_HD PageTable make_page_table(const int32_t* pages, int64_t ld, int cols, int page_size, int64_t n_pages) {
+  return PageTable{pages, ld, cols, page_size, n_pages, ((1ull << 40) + page_size - 1) / page_size};
 }
+
+// j / page_size for 0 <= j < kMaxLen by one product.  inverse exceeds
+// 2^40 / page_size by less than 1, so the product exceeds 2^40 j / page_size by
+// less than j < 2^18, while a quotient that is no integer lies at least
+// 2^40 / page_size >= 2^24 below the next one.
+SF_HD int page_of(const PageTable& t, int j) { return (int)(((uint64_t)(uint32_t)j * t.inverse) >> 40); }
+
+// Entry that holds position j of sequence s, -1 when j lies outside the table.
+// s must be in range.
+SF_HD int32_t page_entry(const PageTable& t, int s, int j) {
+  if (j < 0 || j >= kMaxLen) return -1;
+  const int c = page_of(t, j);
+  return c < t.cols ? t.pages[(int64_t)s * t.ld + c] : -1;
+}
+
+// Slot (page * page_size + offset) of position j on `page`, or -1 for a page
+// outside the pool.
+SF_HD int64_t entry_slot(const PageTable& t, int32_t page, int j) {
+  if (page < 0 || page >= t.n_pages) return -1;
+  return (int64_t)page * t.page_size + (j - page_of(t, j) * t.page_size);
+}
+
+// Both: -1 when j lies outside the table or on a page outside the pool.
+SF_HD int64_t page_slot(const PageTable& t, int s, int j) { return entry_slot(t, page_entry(t, s, j), j); }
 
 // Longest sequence a call can address.
 SF_HD int64_t length_limit(int max_len, int cols, int page_size) {

@@ -68,7 +68,13 @@ def index_lib(tmp_path_factory):
 #include "sf_cache_index.h"
 extern "C" {
 long long slot(const int* pages, long long ld, int cols, int page, long long n_pages, int s, int j) {
-  return sf::page_slot(sf::PageTable{pages, ld, cols, page, n_pages}, s, j);
+  return sf::page_slot(sf::make_page_table(pages, ld, cols, page, n_pages), s, j);
+}
+int quotients(int page) {  // positions whose page is not their quotient
+  const sf::PageTable t = sf::make_page_table(nullptr, 0, 0, page, 0);
+  int wrong = 0;
+  for (int j = 0; j < sf::kMaxLen; ++j) wrong += sf::page_of(t, j) != j / page;
+  return wrong;
 }
 long long limit(int max_len, int cols, int page) { return sf::length_limit(max_len, cols, page); }
 long long per(long long u, int blocks, int least) { return sf::units_per_block(u, blocks, least); }
@@ -105,6 +111,12 @@ def test_slots_and_bad_pages(index_lib, page):
             c = j // page
             ok = 0 <= j < 9 * page and 0 <= table[s, c] < 50
             assert got == (int(table[s, c]) * page + j % page if ok else -1), (s, j)
+
+
+def test_page_of_every_position(index_lib):
+    rng = np.random.default_rng(0)
+    for page in [1, 2, 3, 5, 7, 16, 24, 100, 4095, 4097, 65521, 65535, 65536] + rng.integers(1, 65537, 60).tolist():
+        assert index_lib.quotients(int(page)) == 0, page
 
 
 def test_slots_beyond_32_bits(index_lib):
