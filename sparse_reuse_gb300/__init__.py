@@ -136,6 +136,15 @@ class _LazyLib:
 lib = _LazyLib()
 
 
+def _marshal():
+    """The compiled marshalling of the paged-cache calls (csrc/sf_torch.cpp); ImportError if it is not built."""
+    import torch  # noqa: F401  (the module links against torch's libraries)
+    if not os.path.exists(os.path.join(_PKG, "_sf_torch.so")):
+        raise ImportError("_sf_torch.so is not built; run sparse_reuse_gb300/build.py")
+    from . import _sf_torch
+    return _sf_torch
+
+
 def _check(st: int, ctx=None, what: str = "", head=None, cache=None):
     if st != SF_OK:
         msg = lib.sf_status_str(st).decode()
@@ -428,8 +437,9 @@ class PagedCache:
     lens int32 [S].  A layer's prefix buffer of SpecFold.verify, viewed as
     [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool.
     Tensors must be on the object's device, of the documented type and shape
-    with contiguous rows (ValueError otherwise); outputs that are not given
-    are allocated for the call's stream."""
+    with contiguous rows (ValueError otherwise).  Work runs on `stream` (a
+    torch stream or its handle; default: the current one of the device); the
+    caller orders the tensors it passes with that stream."""
 
     def __init__(self, *, n_q_heads, n_kv_heads, head_dim, dtype, page_size, max_seqs, max_len, max_pos=None,
                  rms_eps=1e-6, rope_theta=10000.0, track_weights=False):
@@ -441,10 +451,18 @@ class PagedCache:
         self.dtype = torch.bfloat16 if bf16 else torch.float32
         self.cache = sf_cache_create(self.shapes)
         self.device = torch.device("cuda", torch.cuda.current_device())
-        self._nq, self._nkv, self._hd, self._page = n_q_heads, n_kv_heads, head_dim, page_size
+        self._bind(self.cache, self.device.index)
+
+    def _bind(self, cache, device):
+        s = self.shapes
+        self._call = _marshal()
+        self._state = self._call.state(cache, device, int(s.dtype == SF_BF16), s.n_q_heads, s.n_kv_heads, s.head_dim,
+                                       s.page_size)
+        self._scale = s.head_dim ** -0.5
 
     def close(self):
         if getattr(self, "cache", None):
+            self._state = None
             sf_cache_destroy(self.cache)
             self.cache = None
 
@@ -454,79 +472,25 @@ class PagedCache:
         except Exception:
             pass
 
-    # -- checks: type, device, shape, rows without gaps inside
-
-    def _want(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.device}: got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
-
-    def _rows(self, name, t, heads):
-        """Row stride of [T, heads, head_dim] or [T, heads * head_dim] with contiguous rows."""
-        sh, st = t.shape, t.stride()
-        if len(sh) == 3:
-            ok = sh[1] == heads and sh[2] == self._hd and st[2] == 1 and (heads == 1 or st[1] == self._hd)
-        else:
-            ok = len(sh) == 2 and sh[1] == heads * self._hd and st[1] == 1
-        if not ok or t.dtype != self.dtype or t.device != self.device:
-            raise ValueError(f"{name} must be {self.dtype} [T, {heads}, {self._hd}] on {self.device} with contiguous "
-                             f"rows: got {t.dtype} {tuple(sh)} strides {tuple(st)} on {t.device}")
-        return st[0]
-
-    def _pool(self, k, v):
-        sh = k.shape
-        if (len(sh) != 4 or sh[1] != self._page or sh[2] != self._nkv or sh[3] != self._hd or v.shape != sh
-                or k.dtype != self.dtype or v.dtype != self.dtype or k.device != self.device
-                or v.device != self.device or not k.is_contiguous() or not v.is_contiguous()):
-            raise ValueError(f"pools must be contiguous {self.dtype} [n_pages, {self._page}, {self._nkv}, {self._hd}] "
-                             f"on {self.device}: got {k.dtype} {tuple(sh)} on {k.device}, {v.dtype} "
-                             f"{tuple(v.shape)} on {v.device}")
-        return sh[0]
-
-    def _table(self, name, t):
-        import torch
-        sh, st = t.shape, t.stride()
-        if len(sh) != 2 or t.dtype != torch.int32 or t.device != self.device or (sh[1] > 1 and st[1] != 1):
-            raise ValueError(f"{name} must be int32 [S, columns] on {self.device} with contiguous rows: got {t.dtype} "
-                             f"{tuple(sh)} strides {tuple(st)} on {t.device}")
-        return sh[0], sh[1], st[0]
-
     def _empty(self, stream, *shape, dtype):
-        """A new output, allocated for the stream that writes it."""
+        """A new output, kept by the allocator until `stream` is done with it."""
         import torch
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        t.record_stream(stream)
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            t.record_stream(stream)
         return t
-
-    # -- operators
 
     def append(self, qkv, index, table, k_pages, v_pages, *, pos=None, seq=None, q_gain=None, k_gain=None, q=None,
                stream=None):
         """Norm (where a gain is given), rotate and store T new rows; returns the rotated queries [T, n_q_heads,
         head_dim].  qkv [T, n_q_heads + 2 n_kv_heads, head_dim] (or its two last dimensions flattened)."""
-        import torch
-        i32, T = torch.int32, qkv.shape[0]
-        ld = self._rows("qkv", qkv, self._nq + 2 * self._nkv)
-        n_pages = self._pool(k_pages, v_pages)
-        S, cols, ld_t = self._table("table", table)
         if q is None:
-            q = self._empty(stream, T, self._nq, self._hd, dtype=self.dtype)
-        ld_q = self._rows("q", q, self._nq)
-        if q.shape[0] != T:
-            raise ValueError(f"q has {q.shape[0]} rows, qkv {T}")
-        sf_cache_append(self.cache, _stream_handle(stream), qkv.data_ptr(), ld, T,
-                        None if q_gain is None else self._want("q_gain", q_gain, torch.float32, (self._hd,)),
-                        None if k_gain is None else self._want("k_gain", k_gain, torch.float32, (self._hd,)),
-                        self._want("index", index, i32, (T,)),
-                        None if pos is None else self._want("pos", pos, i32, (T,)),
-                        None if seq is None else self._want("seq", seq, i32, (T,)),
-                        table.data_ptr(), S, cols, ld_t, k_pages.data_ptr(), v_pages.data_ptr(), n_pages,
-                        q.data_ptr(), ld_q)
+            q = self._empty(stream, qkv.shape[0], self.shapes.n_q_heads, self.shapes.head_dim, dtype=self.dtype)
+        st = self._call.append(self._state, qkv, index, table, k_pages, v_pages, pos, seq, q_gain, k_gain, q, stream)
+        if st:
+            _check(st, None, "sf_cache_append", cache=self.cache)
         return q
 
     def attend(self, q, k_pages, v_pages, table, lens, *, scale=None, out=None, weights=None, weights_out=None,
@@ -534,30 +498,12 @@ class PagedCache:
         """Attention of one new token per sequence, q [S, n_q_heads, head_dim]; returns [S, n_q_heads, head_dim].
         weights (fp32 [S, n_kv_heads, at least max_len]) gets every position's attention weight added, in place
         or into weights_out; weights_out alone gets this call's weights."""
-        import torch
-        S, cols, ld_t = self._table("table", table)
-        ld_q = self._rows("q", q, self._nq)
-        if q.shape[0] != S:
-            raise ValueError(f"q has {q.shape[0]} rows, table {S}")
-        n_pages = self._pool(k_pages, v_pages)
         if out is None:
-            out = self._empty(stream, S, self._nq, self._hd, dtype=self.dtype)
-        elif out.shape[0] != S:
-            raise ValueError(f"out has {out.shape[0]} rows, table {S}")
-        ld_o = self._rows("out", out, self._nq)
-        w_in = w_out = None
-        ld_w = 0
-        if weights is not None or weights_out is not None:
-            if weights_out is None:
-                weights_out = weights
-            ld_w = weights_out.shape[-1]
-            w_out = self._want("weights_out", weights_out, torch.float32, (S, self._nkv, ld_w))
-            if weights is not None:
-                w_in = self._want("weights", weights, torch.float32, (S, self._nkv, ld_w))
-        sf_cache_attend(self.cache, _stream_handle(stream), q.data_ptr(), ld_q, k_pages.data_ptr(),
-                        v_pages.data_ptr(), n_pages, table.data_ptr(), S, cols, ld_t,
-                        self._want("lens", lens, torch.int32, (S,)),
-                        self._hd ** -0.5 if scale is None else scale, out.data_ptr(), ld_o, w_in, w_out, ld_w)
+            out = self._empty(stream, q.shape[0], self.shapes.n_q_heads, self.shapes.head_dim, dtype=self.dtype)
+        st = self._call.attend(self._state, q, k_pages, v_pages, table, lens, self._scale if scale is None else scale,
+                               out, weights, weights if weights_out is None else weights_out, stream)
+        if st:
+            _check(st, None, "sf_cache_attend", cache=self.cache)
         return out
 
     def evict(self, k_pages, v_pages, table, lens, weights, budget, *, n_first=0, n_recent=0, k_out=None, v_out=None,
@@ -566,33 +512,22 @@ class PagedCache:
         the heaviest others, moved in order to the front of the same pages, or of k_out / v_out / table_out (given
         together).  weights moves along, in place or into weights_out.  Returns (lens_out [S], kept [S, n_kv_heads,
         budget])."""
-        import torch
-        i32 = torch.int32
-        S, cols, ld_t = self._table("table", table)
-        n_pages = self._pool(k_pages, v_pages)
-        if (k_out is None) != (v_out is None) or (k_out is None) != (table_out is None):
-            raise ValueError("k_out, v_out and table_out are given together")
-        if k_out is None:
+        if k_out is None or v_out is None or table_out is None:
+            if not (k_out is None and v_out is None and table_out is None):
+                raise ValueError("k_out, v_out and table_out are given together")
             k_out, v_out, table_out = k_pages, v_pages, table
-            n_pages_out, cols_o, ld_to = n_pages, cols, ld_t
-        else:
-            n_pages_out = self._pool(k_out, v_out)
-            S_o, cols_o, ld_to = self._table("table_out", table_out)
-            if S_o != S:
-                raise ValueError(f"table_out has {S_o} rows, table {S}")
-        ld_w = weights.shape[-1]
-        w = self._want("weights", weights, torch.float32, (S, self._nkv, ld_w))
-        w_out = w if weights_out is None else self._want("weights_out", weights_out, torch.float32,
-                                                         (S, self._nkv, ld_w))
-        if lens_out is None:
-            lens_out = self._empty(stream, S, dtype=i32)
-        if kept is None:
-            kept = self._empty(stream, S, self._nkv, max(budget, 0), dtype=i32)
-        sf_cache_evict(self.cache, _stream_handle(stream), k_pages.data_ptr(), v_pages.data_ptr(), n_pages,
-                       table.data_ptr(), S, cols, ld_t, self._want("lens", lens, i32, (S,)), w, ld_w, budget,
-                       n_first, n_recent, k_out.data_ptr(), v_out.data_ptr(), n_pages_out, table_out.data_ptr(),
-                       cols_o, ld_to, w_out, self._want("lens_out", lens_out, i32, (S,)),
-                       self._want("kept", kept, i32, (S, self._nkv, max(budget, 0))))
+        if lens_out is None or kept is None:
+            import torch
+            S = lens.shape[0]
+            if lens_out is None:
+                lens_out = self._empty(stream, S, dtype=torch.int32)
+            if kept is None:
+                kept = self._empty(stream, S, self.shapes.n_kv_heads, max(int(budget), 0), dtype=torch.int32)
+        st = self._call.evict(self._state, k_pages, v_pages, table, lens, weights, budget, n_first, n_recent, k_out,
+                              v_out, table_out, weights if weights_out is None else weights_out, lens_out, kept,
+                              stream)
+        if st:
+            _check(st, None, "sf_cache_evict", cache=self.cache)
         return lens_out, kept
 
     def sync(self, stream=None):

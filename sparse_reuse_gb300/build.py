@@ -1,8 +1,9 @@
 """Build libspecfold.so in-tree with nvcc for sm_103a (GB300).
 
 Translation units compile in parallel into sparse_reuse_gb300/_build/ and
-link into sparse_reuse_gb300/libspecfold.so.  A rebuild is skipped when the
-library is newer than every source and header.
+link into sparse_reuse_gb300/libspecfold.so; the CPython module that marshals
+torch tensors for the paged-cache calls links against it.  A rebuild is
+skipped when both are newer than every source and header.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecfold.so")
+TORCH_EXT = os.path.join(PKG, "_sf_torch.so")  # torch argument marshalling of the paged-cache calls
 
 SOURCES = ["sf_api.cu", "sf_gate.cu", "sf_gemm.cu", "sf_gemm_tc.cu", "sf_attn.cu", "sf_head.cu",
            "sf_cache.cu", "sf_cache_attend.cu", "sf_cache_evict.cu"]
@@ -41,9 +44,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TORCH_EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -56,12 +59,43 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _compile_torch_ext() -> str:
+    """Object of the CPython module that marshals torch tensors (host code only)."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "sf_torch.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    incs = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE]
+    for i in incs:
+        cmd += ["-isystem", i]
+    cmd += ["-c", os.path.join(CSRC, "sf_torch.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for sf_torch.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch_ext(obj: str) -> None:
+    import torch
+    tmp = TORCH_EXT + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-L", PKG,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libspecfold.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_EXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not extra and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        torch_obj = ex.submit(_compile_torch_ext)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
@@ -69,6 +103,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_torch_ext(torch_obj.result())
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

@@ -28,24 +28,38 @@ struct alignas(16) Vec {
   T v[N];
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendHeads = 2;
+constexpr int kAppendWide = 4096;  // (lane, head) pairs per SM from which a group takes several heads
 
-// Norm, rotation and store of one head of one row by a group of lanes: a lane
-// holds 16 bytes of the head's lower half and the same 16 of its upper half,
-// so both members of its rotation pairs are in its registers and the norm
-// needs log2(lanes) shuffles.
-template <typename T, int HD>
+// Norm, rotation and store of HPT heads of one row by a group of lanes: a lane
+// holds 16 bytes of a head's lower half and the same 16 of its upper half, so
+// both members of its rotation pairs are in its registers and the norm needs
+// log2(lanes) shuffles.  Bytes bound it (each row in and out once); HPT heads
+// keep 2 HPT loads in flight and share the row's angles and its page lookup.
+template <typename T, int HD, int HPT>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
-  constexpr int VEC = 16 / sizeof(T), LANES = HD / 2 / VEC;
+  constexpr int VEC = 16 / sizeof(T), LANES = HD / 2 / VEC, GROUPS = kAppendThreads / LANES;
   using V = Vec<T, VEC>;
   pdl_wait();
   pdl_trigger();
-  const int NH = a.nq + 2 * a.nkv;
-  const int64_t item = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) / LANES;
+  const int NH = a.nq + 2 * a.nkv, NB = (NH + HPT - 1) / HPT;
+  // items (row, head block) in order; the block's first one in 64 bits, the rest in 32
+  const int64_t base = (int64_t)blockIdx.x * GROUPS;
+  const int base_t = (int)(base / NB), item = (int)(base - (int64_t)base_t * NB) + (int)threadIdx.x / LANES;
   const int lane = threadIdx.x % LANES;
-  const int t = (int)(item / NH), head = (int)(item % NH);
+  const int t = base_t + item / NB, h0 = item % NB * HPT;
   if (t >= a.T) return;  // whole groups: the shuffles below stay inside a group
   const unsigned mask = (LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u)) << ((threadIdx.x & 31) / LANES * LANES);
+  // the row itself first: it waits for nothing, its place and angles arrive meanwhile
+  const T* src = static_cast<const T*>(a.qkv) + (int64_t)t * a.ld_qkv + (int64_t)h0 * HD + lane * VEC;
+  V lo[HPT], hi[HPT];
+#pragma unroll
+  for (int i = 0; i < HPT; ++i)
+    if (h0 + i < NH) {
+      lo[i] = *reinterpret_cast<const V*>(src + i * HD);
+      hi[i] = *reinterpret_cast<const V*>(src + i * HD + HD / 2);
+    }
   const int idx = a.index[t];
   const int pos = a.pos ? a.pos[t] : idx;
   if (pos < 0) return;
@@ -53,8 +67,18 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     if (lane == 0) cache_error(a.err, kCacheBadRow);
     return;
   }
+  float2 cs[VEC];
+  if (h0 < a.nq + a.nkv) {
+    const float4* p = reinterpret_cast<const float4*>(a.rope + (int64_t)pos * (HD / 2) + lane * VEC);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      const float4 x = p[i];
+      cs[2 * i] = make_float2(x.x, x.y);
+      cs[2 * i + 1] = make_float2(x.z, x.w);
+    }
+  }
   int64_t slot = -1;
-  if (head >= a.nq && idx >= 0) {
+  if (h0 + HPT > a.nq && idx >= 0) {
     const int s = a.seq ? a.seq[t] : t;
     if (s < 0 || s >= a.S || idx >= a.limit) {
       if (lane == 0) cache_error(a.err, kCacheBadRow);
@@ -63,56 +87,72 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
       if (slot < 0 && lane == 0) cache_error(a.err, kCacheBadPage);
     }
   }
-  if (head >= a.nq && slot < 0) return;
-  const T* src = static_cast<const T*>(a.qkv) + (int64_t)t * a.ld_qkv + (int64_t)head * HD + lane * VEC;
-  V lo = *reinterpret_cast<const V*>(src), hi = *reinterpret_cast<const V*>(src + HD / 2);
-  T* dst;
-  if (head < a.nq)
-    dst = static_cast<T*>(a.q_out) + (int64_t)t * a.ld_q + (int64_t)head * HD;
-  else if (head < a.nq + a.nkv)
-    dst = static_cast<T*>(a.k) + (slot * a.nkv + (head - a.nq)) * HD;
-  else
-    dst = static_cast<T*>(a.v) + (slot * a.nkv + (head - a.nq - a.nkv)) * HD;
-  dst += lane * VEC;
-  if (head < a.nq + a.nkv) {
-    const float* gain = head < a.nq ? a.q_gain : a.k_gain;
-    float x[VEC], y[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      x[i] = to_f32<T>(lo.v[i]);
-      y[i] = to_f32<T>(hi.v[i]);
-    }
-    if (gain) {
-      float ss = 0.f;
+  for (int i = 0; i < HPT; ++i) {
+    const int head = h0 + i;
+    if (head >= NH || (head >= a.nq && slot < 0)) break;  // the rest are keys and values too
+    T* dst;
+    if (head < a.nq)
+      dst = static_cast<T*>(a.q_out) + (int64_t)t * a.ld_q + (int64_t)head * HD;
+    else if (head < a.nq + a.nkv)
+      dst = static_cast<T*>(a.k) + (slot * a.nkv + (head - a.nq)) * HD;
+    else
+      dst = static_cast<T*>(a.v) + (slot * a.nkv + (head - a.nq - a.nkv)) * HD;
+    dst += lane * VEC;
+    if (head < a.nq + a.nkv) {
+      const float* gain = head < a.nq ? a.q_gain : a.k_gain;
+      float x[VEC], y[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) ss += x[i] * x[i] + y[i] * y[i];
+      for (int e = 0; e < VEC; ++e) {
+        x[e] = to_f32<T>(lo[i].v[e]);
+        y[e] = to_f32<T>(hi[i].v[e]);
+      }
+      if (gain) {
+        float ss = 0.f;
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      const float r = 1.f / sqrtf(ss / (float)HD + a.eps);
+        for (int e = 0; e < VEC; ++e) ss += x[e] * x[e] + y[e] * y[e];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        x[i] = x[i] * r * gain[lane * VEC + i];
-        y[i] = y[i] * r * gain[HD / 2 + lane * VEC + i];
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+        const float r = 1.f / sqrtf(ss / (float)HD + a.eps);
+        const float4* gl = reinterpret_cast<const float4*>(gain + lane * VEC);
+        const float4* gh = reinterpret_cast<const float4*>(gain + HD / 2 + lane * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC / 4; ++e) {
+          const float4 u = gl[e], w = gh[e];
+          x[4 * e] *= r * u.x;
+          x[4 * e + 1] *= r * u.y;
+          x[4 * e + 2] *= r * u.z;
+          x[4 * e + 3] *= r * u.w;
+          y[4 * e] *= r * w.x;
+          y[4 * e + 1] *= r * w.y;
+          y[4 * e + 2] *= r * w.z;
+          y[4 * e + 3] *= r * w.w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        lo[i].v[e] = from_f32<T>(x[e] * cs[e].x - y[e] * cs[e].y);
+        hi[i].v[e] = from_f32<T>(y[e] * cs[e].x + x[e] * cs[e].y);
       }
     }
-    const float2* cs = a.rope + (int64_t)pos * (HD / 2) + lane * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float2 c = cs[i];
-      lo.v[i] = from_f32<T>(x[i] * c.x - y[i] * c.y);
-      hi.v[i] = from_f32<T>(y[i] * c.x + x[i] * c.y);
-    }
+    *reinterpret_cast<V*>(dst) = lo[i];
+    *reinterpret_cast<V*>(dst + HD / 2) = hi[i];
   }
-  *reinterpret_cast<V*>(dst) = lo;
-  *reinterpret_cast<V*>(dst + HD / 2) = hi;
+}
+
+template <typename T, int HD, int HPT>
+cudaError_t append_n(cudaStream_t st, const CacheAppendArgs& a) {
+  constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
+  const int64_t threads = (int64_t)a.T * ((a.nq + 2 * a.nkv + HPT - 1) / HPT) * LANES;
+  return launch_pdl(st, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0, 1,
+                    cache_append_kernel<T, HD, HPT>, a);
 }
 
 template <typename T, int HD>
-cudaError_t append_t(cudaStream_t st, const CacheAppendArgs& a) {
+cudaError_t append_t(cudaStream_t st, const CacheAppendArgs& a, int sm_count) {
   constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
   const int64_t threads = (int64_t)a.T * (a.nq + 2 * a.nkv) * LANES;
-  return launch_pdl(st, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0, 1,
-                    cache_append_kernel<T, HD>, a);
+  return threads <= (int64_t)sm_count * kAppendWide ? append_n<T, HD, 1>(st, a) : append_n<T, HD, kAppendHeads>(st, a);
 }
 
 bool misaligned(const void* p, uintptr_t align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)); }
@@ -166,6 +206,8 @@ sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages
   return SF_OK;
 }
 
+int64_t scores_ld(const sf_cache_shapes& s) { return ((int64_t)s.max_len + 3) / 4 * 4; }
+
 bool bad_row(const sf_cache* c, const void* p, int64_t ld, int64_t width, int rows) {
   const int es = c->s.dtype == SF_BF16 ? 2 : 4;
   return !p || misaligned(p, 16) || (rows > 1 && (ld < width || ld * es % 16 != 0));
@@ -183,9 +225,9 @@ sf_status launched(sf_cache* c, cudaError_t e) {
 
 }  // namespace
 
-cudaError_t launch_cache_append(cudaStream_t st, const CacheAppendArgs& a, int bf16, int) {
-  if (bf16) return a.hd == 128 ? append_t<__nv_bfloat16, 128>(st, a) : append_t<__nv_bfloat16, 64>(st, a);
-  return a.hd == 128 ? append_t<float, 128>(st, a) : append_t<float, 64>(st, a);
+cudaError_t launch_cache_append(cudaStream_t st, const CacheAppendArgs& a, int bf16, int sm_count) {
+  if (bf16) return a.hd == 128 ? append_t<__nv_bfloat16, 128>(st, a, sm_count) : append_t<__nv_bfloat16, 64>(st, a, sm_count);
+  return a.hd == 128 ? append_t<float, 128>(st, a, sm_count) : append_t<float, 64>(st, a, sm_count);
 }
 
 }  // namespace sf
@@ -211,14 +253,15 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   c->s = s;
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
+  const int blocks = cache_attend_blocks(c->sm_count);
   if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * (s.head_dim / 2) * sizeof(float2));
   if (e == cudaSuccess && s.track_weights)
-    e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * s.max_len * sizeof(float));
+    e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * scores_ld(s) * sizeof(float));
   if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&c->parts, (size_t)(c->sm_count * cache_attend_part_floats(s)) * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&c->joins, (size_t)c->sm_count * sizeof(CacheJoin));
-  if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)c->sm_count * sizeof(unsigned));
-  if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)c->sm_count * sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMalloc(&c->parts, (size_t)(blocks * cache_attend_part_floats(s)) * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->joins, (size_t)blocks * sizeof(CacheJoin));
+  if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)blocks * sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)blocks * sizeof(unsigned));
   if (e == cudaSuccess) e = prepare_cache_attend();
   if (e == cudaSuccess) e = prepare_cache_evict();
   if (e == cudaSuccess) e = cudaHostAlloc(&c->err, kCacheErrWords * sizeof(unsigned), cudaHostAllocMapped);
@@ -327,7 +370,7 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.w_out = weights_out;
   a.ld_w = ld_w;
   a.scores = c->scores;
-  a.ld_scores = s.max_len;
+  a.ld_scores = scores_ld(s);
   a.lse = c->lse;
   a.parts = c->parts;
   a.arrived = c->arrived;

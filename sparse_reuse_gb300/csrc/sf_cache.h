@@ -22,11 +22,11 @@ struct sf_cache {
   int device = 0;
   int sm_count = 148;
   float2* rope = nullptr;     // [max_pos][head_dim / 2] (cos, sin)
-  float* scores = nullptr;    // [max_seqs][n_q_heads][max_len] scaled scores in log2 units (track_weights)
+  float* scores = nullptr;    // [max_seqs][n_q_heads][max_len, padded to 4] scaled scores in log2 units (track_weights)
   float* lse = nullptr;       // [max_seqs][n_q_heads] log2 of each softmax denominator (track_weights)
-  float* parts = nullptr;     // partial results of sf_cache_attend, two per SM
-  unsigned* arrived = nullptr;  // [sm_count] arrival counters, 0 between calls
-  sf::CacheJoin* joins = nullptr;  // [sm_count]
+  float* parts = nullptr;     // partial results of sf_cache_attend, two per block
+  unsigned* arrived = nullptr;  // [blocks] arrival counters, 0 between calls
+  sf::CacheJoin* joins = nullptr;  // [blocks]
   unsigned* err = nullptr;    // [kCacheErrWords] pinned, written by the kernels through its device address
   unsigned* err_dev = nullptr;
   char last_error[256] = {0};
@@ -77,7 +77,8 @@ struct CacheAttendArgs {
   int least;          // units a block takes at least
   unsigned* err;
 };
-// Floats of `parts` that a block needs, and the kernels' shared-memory limits (once per process and device).
+// Blocks of the largest launch on sm_count SMs, floats of `parts` that each needs, and the kernels' shared-memory limits (once per process and device).
+int cache_attend_blocks(int sm_count);
 int64_t cache_attend_part_floats(const sf_cache_shapes& s);
 cudaError_t prepare_cache_attend();
 cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& a, int bf16, int sm_count);

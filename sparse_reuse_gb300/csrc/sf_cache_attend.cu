@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kBlocksPerSM = 1;
+constexpr int kLeast = 8;  // units a block takes at least
 constexpr float kSlack = 8.f;
 constexpr float kRoom = 19.f + kSlack;
 constexpr unsigned kFull = 0xffffffffu;
@@ -175,8 +177,8 @@ struct WarpBf16 {
   float m[NT][2], l[NT][2];
 
   // Tiles t, t + step, ... below `end` of one segment.
-  template <bool TRACK>
-  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float*,
+  template <bool TRACK, typename F>
+  __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float*, F,
                                       int t, int step, int end, int lane) {
     const int r = lane >> 2, c = lane & 3;
     // Q as the right operand: column r of a tile is query head h0 + 8 n + r
@@ -363,9 +365,9 @@ struct WarpF32 {
   float o[8][4];
   float m[8], l[8];
 
-  template <bool TRACK>
+  template <bool TRACK, typename F>
   __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float* sq,
-                                      int t, int step, int end, int lane) {
+                                      F load_q, int t, int step, int end, int lane) {
     const int r = lane >> 2, c = lane & 3;
     const int vr = lane / LPR, vd = lane % LPR;
     float* sp = reinterpret_cast<float*>(mem + R::kBytes);
@@ -393,6 +395,7 @@ struct WarpF32 {
       }
       cp_async_commit();
     }
+    load_q();  // queries to shared memory, behind the first copies
 #pragma unroll 1
     for (; ku < stop; ku = next(ku)) {
       cp_async_wait<kStages - 1>();
@@ -507,17 +510,19 @@ struct WarpOf<float, HD, NT> {
 };
 
 // Block-wide exclusive scan of units_of(length) per sequence into
-// first[0..S]; kThreads threads, `sums` one int per warp.
-template <typename F>
-__device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, int* sums, F units_of) {
+// first[0..S], the lengths themselves into lens[0..S-1]; `sums` one int per warp.
+template <int THREADS, typename F>
+__device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, int* lens, int* sums, F units_of) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int carry = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kThreads) {
+  for (int s0 = 0; s0 < a.S; s0 += THREADS) {
     const int s = s0 + threadIdx.x;
     int x = 0;
     if (s < a.S) {
       bool bad;
-      x = units_of(checked_len(a.lens[s], a.limit, &bad));
+      const int len = checked_len(a.lens[s], a.limit, &bad);
+      lens[s] = len;
+      x = units_of(len);
       if (bad && blockIdx.x == 0) cache_error(a.err, kCacheBadLength);
     }
     int y = x;
@@ -530,7 +535,7 @@ __device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, 
     __syncthreads();
     int before = carry, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before += sums[w];
       total += sums[w];
     }
@@ -583,23 +588,24 @@ constexpr int kInlineParts = 6;  // partial results that the last block to arriv
 // and short, one segment each.  A segment cut over few blocks is joined by the
 // last of them to finish, one cut over many by the join kernel.
 template <typename T, int HD, int NT, bool TRACK>
-__global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_constant__ CacheAttendArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(const __grid_constant__ CacheAttendArgs a) {
   using Warp = typename WarpOf<T, HD, NT>::type;
   constexpr int NH = Warp::kHeads, ROW = Warp::kRow;
   constexpr bool F32 = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 sml[kWarps][NH];
+  __shared__ float2 sml[kWarps > kInlineParts ? kWarps : kInlineParts][NH];
   __shared__ float sfac[kWarps][NH];
   __shared__ int sums[kWarps];
   __shared__ int s_last;
   __shared__ __align__(16) float sq[F32 ? kWarps : 1][F32 ? 8 * HD : 4];
   int* first = reinterpret_cast<int*>(smem + kWarps * Warp::kBytes);
+  int* lens = first + a.S + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* mine = smem + warp * Warp::kBytes;
   float* my_out = reinterpret_cast<float*>(mine);
   pdl_wait();
   pdl_trigger();
-  scan_lens(a, first, sums, [](int len) { return tiles_of(len); });
+  scan_lens<kThreads>(a, first, lens, sums, [](int len) { return tiles_of(len); });
   const int G = a.nq / a.nkv, nsub = (G + NH - 1) / NH, H = a.nkv * nsub;
   // empty sequences have no units: zeros
   for (int s = blockIdx.x; s < a.S; s += gridDim.x)
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
     const int sub = hs % nsub;
     g.h0 = g.kvh * G + sub * NH;
     g.nh = min(NH, G - sub * NH);
-    g.len = a.lens[ss];
+    g.len = lens[ss];
     return g;
   };
   auto load_q = [&](const Segment& g, float* to, int i0, int step) {
@@ -657,9 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
       if (n > 1) {
         if (my_s >= 0) {
           const Segment g = segment(my_s, my_hs);
-          load_q(g, sq[F32 ? warp : 0], lane, 32);
-          __syncwarp();
-          w.template run<TRACK>(a, g, mine, sq[F32 ? warp : 0], 0, 1, tiles_of(g.len), lane);
+          float* q = sq[F32 ? warp : 0];
+          auto queries = [&]() {
+            load_q(g, q, lane, 32);
+            __syncwarp();
+          };
+          w.template run<TRACK>(a, g, mine, q, queries, 0, 1, tiles_of(g.len), lane);
           __syncwarp();
           w.store(my_out, sml[warp], lane);
           __syncwarp();
@@ -679,9 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
     // ---- one segment by all warps
     const int end = (int)(u_end - u < tiles - t0 ? u_end - u : tiles - t0) + t0;
     const Segment g = segment(s, hs);
-    load_q(g, sq[0], threadIdx.x, kThreads);
-    if (F32) __syncthreads();
-    w.template run<TRACK>(a, g, mine, sq[0], t0 + warp, kWarps, end, lane);
+    auto queries = [&]() {
+      load_q(g, sq[0], threadIdx.x, kThreads);
+      __syncthreads();
+    };
+    w.template run<TRACK>(a, g, mine, sq[0], queries, t0 + warp, kWarps, end, lane);
     __syncwarp();
     w.store(my_out, sml[warp], lane);
     __syncthreads();
@@ -790,11 +801,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attend_kernel(const __grid_
 // Joins a segment cut over more than kInlineParts blocks: a block per (its
 // first block, head), the parts dealt over kJoinGroups groups of threads.
 constexpr int kJoinThreads = 256;
+constexpr int kMaxBlocks = 512;  // of the attention kernel
 
 template <typename T, int HD, int NH>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttendArgs a) {
   constexpr int COLS = HD / 4, GROUPS = kJoinThreads / COLS;
-  __shared__ float fac[kJoinThreads];
+  __shared__ float fac[kMaxBlocks];
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ __align__(16) float4 acc[GROUPS][COLS];
   pdl_wait();
@@ -806,20 +818,20 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   auto part = [&](int x) { return part_of<NH, HD>(a, x ? 2 * ((int)blockIdx.x + x) : j.first); };
   const int g = threadIdx.x / COLS, d = threadIdx.x % COLS * 4;
   float m = -INFINITY, l = 0.f;
-  if (threadIdx.x < j.n) {  // j.n <= blocks <= kJoinThreads
-    const float* p = part(threadIdx.x) + NH * HD + h;
-    m = p[0];
-    l = p[NH];
-  }
+  for (int x = threadIdx.x; x < j.n; x += kJoinThreads) m = fmaxf(m, part(x)[NH * HD + h]);
   float top = warp_max(m);
   if (lane == 0) red[0][warp] = top;
   __syncthreads();
   top = red[0][0];
 #pragma unroll
   for (int i = 1; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[0][i]);
-  const float f = part_factor(m, top);
-  fac[threadIdx.x] = f;
-  l = warp_sum(threadIdx.x < j.n ? l * f : 0.f);
+  for (int x = threadIdx.x; x < j.n; x += kJoinThreads) {
+    const float* p = part(x) + NH * HD + h;
+    const float f = part_factor(p[0], top);
+    fac[x] = f;
+    l += p[NH] * f;
+  }
+  l = warp_sum(l);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -853,39 +865,42 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 
 // weights_out[s][c][j] = weights_in + the group's normalised weights of key j.
 // Blocks take units of kWeightKeys keys of one (sequence, KV head) in turn.
-constexpr int kWeightKeys = 4 * kThreads;
+constexpr int kWeightThreads = 256;
+constexpr int kWeightKeys = 4 * kWeightThreads;
 
-__global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ CacheAttendArgs a) {
+__global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __grid_constant__ CacheAttendArgs a) {
   extern __shared__ int first[];
-  __shared__ int sums[kWarps];
+  __shared__ int sums[kWeightThreads / 32];
+  int* lens = first + a.S + 1;
   pdl_wait();
   pdl_trigger();
   const int G = a.nq / a.nkv;
-  scan_lens(a, first, sums, [](int len) { return (len + kWeightKeys - 1) / kWeightKeys; });
+  scan_lens<kWeightThreads>(a, first, lens, sums, [](int len) { return (len + kWeightKeys - 1) / kWeightKeys; });
   const int64_t units = (int64_t)first[a.S] * a.nkv;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int s = find_sequence(first, a.S, u, a.nkv), n = first[s + 1] - first[s];
     const int in_s = (int)(u - (int64_t)first[s] * a.nkv), c = in_s / n;
-    const int j0 = in_s % n * kWeightKeys + (int)threadIdx.x, len = a.lens[s];
-    const int64_t at = ((int64_t)s * a.nkv + c) * a.ld_w;
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    const int j = in_s % n * kWeightKeys + 4 * (int)threadIdx.x, len = lens[s];
+    if (j >= len) continue;
+    // the rows of scores are padded to 4 floats: behind the length there is something to read, if nothing to use
+    const int64_t at = ((int64_t)s * a.nkv + c) * a.ld_w + j;
+    const int64_t h = (int64_t)s * a.nq + c * G;
+    const float4* sc = reinterpret_cast<const float4*>(a.scores + h * a.ld_scores + j);
+    float before[4], w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) before[i] = a.w_in && j + i < len ? a.w_in[at + i] : 0.f;
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
-      const int64_t h = (int64_t)s * a.nq + c * G + g;
-      const float lse = a.lse[h];
-      const float* sc = a.scores + h * a.ld_scores;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kThreads;
-        const float x = j < len ? sc[j] : -INFINITY;
-        w[i] += x == -INFINITY ? 0.f : ex2(x - lse);
-      }
+      const float lse = a.lse[h + g];
+      const float4 x = sc[g * (a.ld_scores / 4)];
+      w[0] += x.x == -INFINITY ? 0.f : ex2(x.x - lse);
+      w[1] += x.y == -INFINITY ? 0.f : ex2(x.y - lse);
+      w[2] += x.z == -INFINITY ? 0.f : ex2(x.z - lse);
+      w[3] += x.w == -INFINITY ? 0.f : ex2(x.w - lse);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = j0 + i * kThreads;
-      if (j < len) a.w_out[at + j] = (a.w_in ? a.w_in[at + j] : 0.f) + w[i];
-    }
+    for (int i = 0; i < 4; ++i)
+      if (j + i < len) a.w_out[at + i] = before[i] + w[i];
   }
 }
 
@@ -896,22 +911,23 @@ constexpr int ring_bytes() {
 
 template <typename T, int HD, int NT>
 cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
+  const int most_blocks = cache_attend_blocks(sm_count);
   constexpr int NH = WarpOf<T, HD, NT>::type::kHeads;
   const int G = a.nq / a.nkv, longest = tiles_of((int)a.limit);
-  a.least = 2 * kWarps;
+  a.least = kLeast;
   // no more blocks than the longest batch of this table could keep busy
   const int64_t want = ((int64_t)a.S * a.nkv * ((G + NH - 1) / NH) * longest + a.least - 1) / a.least;
-  const int blocks = (int)(want < sm_count ? want : sm_count);
+  const int blocks = (int)(want < most_blocks ? want : most_blocks);
   // a segment lies in at most (longest - 1) / least + 2 blocks
   a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks > kInlineParts;
-  const size_t table = ((size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
+  const size_t table = (2 * (size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
   cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
                              a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);
   if (e == cudaSuccess && a.join)
     e = launch_pdl(st, dim3(blocks, NH < G ? NH : G), dim3(kJoinThreads), 0, 1, cache_join_kernel<T, HD, NH>, a);
   if (e == cudaSuccess && a.w_out) {
     const int64_t most = (int64_t)a.S * a.nkv * ((a.limit + kWeightKeys - 1) / kWeightKeys);
-    e = launch_pdl(st, dim3((unsigned)(most < 4 * sm_count ? most : 4 * sm_count)), dim3(kThreads), table, 1,
+    e = launch_pdl(st, dim3((unsigned)(most < 8 * sm_count ? most : 8 * sm_count)), dim3(kWeightThreads), table, 1,
                    cache_weights_kernel, a);
   }
   return e;
@@ -919,7 +935,7 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
 
 template <typename T, int HD, int NT>
 cudaError_t allow_smem() {
-  const int bytes = ring_bytes<T, HD, NT>() + 4097 * (int)sizeof(int);
+  const int bytes = ring_bytes<T, HD, NT>() + (2 * 4096 + 1) * (int)sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<T, HD, NT, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
@@ -930,6 +946,10 @@ cudaError_t allow_smem() {
 }  // namespace
 
 int64_t cache_attend_part_floats(const sf_cache_shapes& s) { return 2 * 16 * (int64_t)(s.head_dim + 2); }
+
+int cache_attend_blocks(int sm_count) {
+  return kBlocksPerSM * sm_count < kMaxBlocks ? kBlocksPerSM * sm_count : kMaxBlocks;
+}
 
 cudaError_t prepare_cache_attend() {
   cudaError_t e = allow_smem<__nv_bfloat16, 128, 1>();
@@ -942,7 +962,6 @@ cudaError_t prepare_cache_attend() {
 }
 
 cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& a, int bf16, int sm_count) {
-  if (sm_count > kJoinThreads) sm_count = kJoinThreads;
   if (!bf16) return a.hd == 128 ? attend_t<float, 128, 1>(st, a, sm_count) : attend_t<float, 64, 1>(st, a, sm_count);
   const bool wide = a.nq / a.nkv > 8;
   if (a.hd == 128)

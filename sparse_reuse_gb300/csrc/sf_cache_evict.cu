@@ -322,22 +322,26 @@ __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid
   }
 }
 
-// Blocks of a cluster for weights of up to `limit` positions: 16,384 of them
-// (64 KB) a block, up to 8 blocks.
-int select_cluster(int64_t limit) {
+// Blocks of a cluster for `heads` (sequence, KV head) pairs of up to `limit`
+// weights: kSelCap of them a block at most; more blocks while each keeps
+// kSelKeys and the launch stays one wave of two blocks per SM.
+constexpr int kSelCap = 32768, kSelKeys = 8192;
+int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   int cl = 1;
-  while (cl < 8 && limit > (int64_t)cl * 16384) cl *= 2;
+  while (cl < 8 && (limit > (int64_t)cl * kSelCap ||
+                    (limit >= 2 * cl * kSelKeys && heads * cl * 2 <= 2 * sm_count)))
+    cl *= 2;
   return cl;
 }
 
 }  // namespace
 
 cudaError_t prepare_cache_evict() {
-  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4);
+  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
 }
 
-cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf16, int) {
-  const int cl = select_cluster(a.limit);
+cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf16, int sm_count) {
+  const int cl = select_cluster(a.limit, (int64_t)a.S * a.nkv, sm_count);
   const size_t smem = (size_t)((a.limit + cl - 1) / cl) * sizeof(float);
   cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(kSelThreads), smem, dim3(cl), cache_select_kernel,
                                      a, cl);

@@ -253,16 +253,26 @@ def test_null_objects(sf):
 # ---------------------------------------------------------------- binding
 
 @pytest.fixture
-def bound(sf, monkeypatch):
-    """A PagedCache on CPU tensors whose calls are recorded instead of made."""
+def bound(sf):
+    """A PagedCache over an object of which only the shapes are filled in, with
+    its checks set to CPU tensors: a call that they let through stops at the
+    library's last check (no such device), one that they refuse raises."""
     c = sf.PagedCache.__new__(sf.PagedCache)
-    c.cache, c.device, c.dtype = None, torch.device("cpu"), torch.bfloat16
-    c._nq, c._nkv, c._hd, c._page = 4, 2, 64, 16
-    calls = []
-    for name in ("sf_cache_append", "sf_cache_attend", "sf_cache_evict"):
-        monkeypatch.setattr(sf, name, lambda *a, n=name: calls.append((n, a)))
-    monkeypatch.setattr(sf, "_stream_handle", lambda s: None)
-    return c, calls
+    obj = _object(sf)
+    c.keep, c.cache, c.device, c.dtype, c.shapes = obj, None, torch.device("cpu"), torch.bfloat16, _shapes(sf)
+    c._bind(ctypes.addressof(obj), -1)
+    return c
+
+
+def _let_through(sf, call):
+    with pytest.raises(sf.SpecFoldError) as e:
+        call()
+    assert e.value.status == sf.SF_ERR_INVALID_ARG
+    return e
+
+
+def _reached_device_check(c, sf):
+    return "lives on device" in sf.lib.sf_cache_last_error(c.keep).decode()
 
 
 def _tensors():
@@ -273,31 +283,32 @@ def _tensors():
                 w=torch.zeros(3, 2, 64))
 
 
-def test_binding_passes_strides(bound):
-    c, calls = bound
-    t = _tensors()
-    packed = torch.zeros(3, 700, dtype=torch.bfloat16)          # rows of a wider projection output
-    qkv = packed[:, :512]
-    table = torch.zeros(3, 11, dtype=torch.int32)[:, 2:6]
-    q = c.append(qkv, t["index"], table, t["k"], t["v"], q=qkv[:, :256])
-    a = calls[-1][1]
-    assert a[2] == packed.data_ptr() and a[3:5] == (700, 3) and a[10:14] == (table.data_ptr(), 3, 4, 11)
-    assert a[17:] == (packed.data_ptr(), 700) and q.data_ptr() == packed.data_ptr()
-    out = c.attend(packed.view(3, 700)[:, :256], t["k"], t["v"], table, t["lens"], weights=t["w"])
-    a = calls[-1][1]
-    assert a[3] == 700 and a[12] == 0.125 and a[15:] == (t["w"].data_ptr(), t["w"].data_ptr(), 64)
-    assert out.shape == (3, 4, 64)
-    lens, kept = c.evict(t["k"], t["v"], table, t["lens"], t["w"], 20, n_first=1)
-    a = calls[-1][1]
-    assert a[12:17] == (20, 1, 0, t["k"].data_ptr(), t["v"].data_ptr()) and a[18:21] == (table.data_ptr(), 4, 11)
-    assert lens.shape == (3,) and kept.shape == (3, 2, 20)
+def test_binding_lets_strided_rows_through(bound, sf):
+    c, t = bound, _tensors()
+    packed = torch.zeros(3, 704, dtype=torch.bfloat16)          # rows of a wider projection output
+    qkv, table = packed[:, :512], torch.zeros(3, 11, dtype=torch.int32)[:, 2:6]
+    calls = [lambda: c.append(qkv, t["index"], table, t["k"], t["v"], q=qkv[:, :256]),
+             lambda: c.append(t["qkv"], t["index"], table, t["k"], t["v"], pos=t["index"], seq=t["index"],
+                              q_gain=torch.ones(64)),
+             lambda: c.attend(qkv[:, :256], t["k"], t["v"], table, t["lens"], weights=t["w"]),
+             lambda: c.attend(t["q"], t["k"], t["v"], table, t["lens"], weights_out=t["w"], scale=2),
+             lambda: c.evict(t["k"], t["v"], table, t["lens"], t["w"], 20, n_first=1),
+             lambda: c.evict(t["k"], t["v"], table, t["lens"], t["w"], 20, k_out=t["k"].clone(), v_out=t["v"].clone(),
+                             table_out=t["table"], weights_out=t["w"].clone(), lens_out=t["lens"])]
+    for call in calls:
+        _let_through(sf, call)
+        assert _reached_device_check(c, sf)
+    # what the library itself refuses comes back with its text
+    _let_through(sf, lambda: c.append(packed[:, 1:513], t["index"], table, t["k"], t["v"]))
+    assert "misaligned" in sf.lib.sf_cache_last_error(c.keep).decode()
 
 
-@pytest.mark.parametrize("what", ["qkv dtype", "qkv inner", "qkv heads", "k dtype", "k page", "v shape", "table dtype",
-                                  "table inner", "index dtype", "index size", "gain dtype", "q rows", "device"])
-def test_binding_refuses_append(bound, what):
-    c, calls = bound
-    t = _tensors()
+@pytest.mark.parametrize("what", ["qkv dtype", "qkv inner", "qkv heads", "qkv dim", "k dtype", "k page", "v shape",
+                                  "k stride", "table dtype", "table inner", "table dim", "index dtype", "index size",
+                                  "index stride", "gain dtype", "gain size", "q rows", "q heads", "device",
+                                  "no tensor"])
+def test_binding_refuses_append(bound, sf, what):
+    c, t = bound, _tensors()
     kw = {}
     if what == "qkv dtype":
         t["qkv"] = t["qkv"].float()
@@ -305,42 +316,69 @@ def test_binding_refuses_append(bound, what):
         t["qkv"] = torch.zeros(3, 8, 128, dtype=torch.bfloat16)[..., ::2]
     elif what == "qkv heads":
         t["qkv"] = t["qkv"][:, :7]
+    elif what == "qkv dim":
+        t["qkv"] = t["qkv"][None]
+        kw["q"] = t["q"]
     elif what == "k dtype":
         t["k"] = t["k"].float()
     elif what == "k page":
         t["k"] = t["k"][:, :8]
+    elif what == "k stride":
+        t["k"] = torch.zeros(9, 16, 2, 128, dtype=torch.bfloat16)[..., :64]
     elif what == "v shape":
         t["v"] = t["v"][:8]
     elif what == "table dtype":
         t["table"] = t["table"].long()
     elif what == "table inner":
         t["table"] = torch.zeros(4, 3, dtype=torch.int32).t()
+    elif what == "table dim":
+        t["table"] = t["table"][0]
     elif what == "index dtype":
         t["index"] = t["index"].long()
     elif what == "index size":
         t["index"] = t["index"][:2]
+    elif what == "index stride":
+        t["index"] = torch.zeros(6, dtype=torch.int32)[::2]
     elif what == "gain dtype":
         kw["q_gain"] = torch.ones(64, dtype=torch.bfloat16)
+    elif what == "gain size":
+        kw["k_gain"] = torch.ones(128)
     elif what == "q rows":
         kw["q"] = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    elif what == "q heads":
+        kw["q"] = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    elif what == "device":
+        kw["pos"] = torch.zeros(3, dtype=torch.int32, device="meta")
     else:
-        c.device = torch.device("cuda", 0)
+        t["index"] = [0, 1, 2]
     with pytest.raises(ValueError):
         c.append(t["qkv"], t["index"], t["table"], t["k"], t["v"], **kw)
-    assert not calls
+    assert not _reached_device_check(c, sf)
 
 
-def test_binding_refuses_attend_and_evict(bound):
-    c, calls = bound
-    t = _tensors()
+def test_binding_refuses_cpu_tensors_on_a_gpu_object(sf, bound):
+    c, t = bound, _tensors()
+    c._bind(ctypes.addressof(c.keep), 0)
+    with pytest.raises(ValueError, match="on device 0"):
+        c.append(t["qkv"], t["index"], t["table"], t["k"], t["v"], q=t["q"])
+
+
+def test_binding_refuses_attend_and_evict(bound, sf):
+    c, t = bound, _tensors()
     for kw in (dict(weights=t["w"].double()), dict(weights=t["w"], weights_out=t["w"][:, :1]),
-               dict(out=t["q"][:2]), dict(weights=t["w"][..., ::2])):
+               dict(weights=t["w"], weights_out=t["w"][..., :63]), dict(out=t["q"][:2]), dict(weights=t["w"][..., ::2]),
+               dict(weights=t["w"][0]), dict(out=t["q"].float())):
         with pytest.raises(ValueError):
             c.attend(t["q"], t["k"], t["v"], t["table"], t["lens"], **kw)
     with pytest.raises(ValueError):
         c.attend(t["q"][:2], t["k"], t["v"], t["table"], t["lens"])
+    with pytest.raises(TypeError):
+        c.attend(t["q"], t["k"], t["v"], t["table"], t["lens"], scale="x")
     for kw in (dict(k_out=t["k"]), dict(k_out=t["k"], v_out=t["v"], table_out=t["table"][:2]),
-               dict(lens_out=t["lens"].long()), dict(kept=torch.zeros(3, 2, 19, dtype=torch.int32))):
+               dict(lens_out=t["lens"].long()), dict(kept=torch.zeros(3, 2, 19, dtype=torch.int32)),
+               dict(weights_out=t["w"][..., :60]), dict(n_first=2 ** 31)):
         with pytest.raises(ValueError):
             c.evict(t["k"], t["v"], t["table"], t["lens"], t["w"], 20, **kw)
-    assert not calls
+    with pytest.raises(TypeError):
+        c.evict(t["k"], t["v"], t["table"], t["lens"], t["w"], 20.5, kept=torch.zeros(3, 2, 20, dtype=torch.int32))
+    assert not _reached_device_check(c, sf)

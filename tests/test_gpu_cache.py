@@ -455,8 +455,9 @@ def test_attend_reports_bad_lengths_and_pages(sf):
         with pytest.raises(sf.SpecFoldError) as e:
             a["c"].sync()
         assert e.value.status == sf.SF_ERR_DEVICE_ASSERT and "length" in str(e.value)
-        assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2]) and not out[1].any()
-        assert torch.equal(w[1], a["w"][1])
+        # without sequence 1 the batch is split elsewhere: the others to rounding
+        check_attend(heads, "bf16", page, a, out, None, seqs=(0, 2))
+        assert not out[1].any() and torch.equal(w[1], a["w"][1])
     for bad in (-1, a["k"].shape[0], 2 ** 31 - 1):
         t = a["table"].copy()
         t[1, 1] = bad                                   # positions 16..31 of sequence 1
