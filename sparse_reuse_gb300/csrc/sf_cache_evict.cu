@@ -29,37 +29,52 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-constexpr int kSelThreads = 1024;
+__device__ __forceinline__ void red_cluster_add(uint32_t addr, unsigned v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2 * kSelThreads;
+constexpr int kBins = 4 * kSelThreads;  // 2^11
+constexpr int kList = 256;              // keys that are ranked by comparing all pairs
+constexpr int kSelCap = 32768;          // weights a block holds at most
+static_assert(kSelCap / 32 <= 2 * kSelThreads, "two words of a bitmap a thread");
 
 // A cluster of `cl` blocks per (sequence, KV head); block r holds the r-th
 // part of the weights in shared memory.
 //
 // The need-th largest candidate key is found by narrowing [lo, hi]: the range
 // is cut into at most kBins equal bins (keys of positive floats are piecewise
-// logarithmic, so weights spread over many bins), the bin that holds it is the
-// next range: three passes at most for any 32-bit keys.  The lowest bin is
+// logarithmic, so weights spread over many bins), and the bin that holds it is
+// the next range, three passes at most for any 32-bit keys.  The lowest bin is
 // never counted (if the others do not reach, it is the one), which keeps the
-// usual crowd of zero weights out of the shared-memory atomics.
-// Then positions are written in order: all keys above the threshold, and the
-// first `ties` equal to it.
-__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const __grid_constant__ CacheEvictArgs a, int cl) {
-  extern __shared__ float sw[];
-  __shared__ unsigned hist[2][kBins];
-  __shared__ unsigned red[2][kSelWarps];
-  __shared__ unsigned pub[2][2];  // published to the cluster: (min, max), then (above, equal)
-  __shared__ unsigned found[3];   // bin, keys above it, keys in it
+// usual crowd of zero weights out of the shared-memory atomics.  A block that
+// is alone ranks the keys of the bin by comparison once they are few, usually
+// after one pass.
+//
+// The choice is two bitmaps, positions certainly kept and positions at the
+// threshold, of which the first `ties` are kept; a scan of their populations
+// gives every kept position its place.
+__global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __grid_constant__ CacheEvictArgs a, int cl,
+                                                                      int cap) {
+  extern __shared__ __align__(16) float sw[];                    // [cap] weights of this block's positions
+  unsigned* sure = reinterpret_cast<unsigned*>(sw + cap);        // [cap / 32] kept; later the final choice
+  unsigned* tied = sure + cap / 32;                              // [cap / 32] at the threshold; later places
+  __shared__ __align__(16) unsigned hist[kBins];
+  __shared__ unsigned red[2][32];
+  __shared__ unsigned pub[2][2];                                 // to the cluster: (min, max), then (kept, tied)
+  __shared__ unsigned found[3];                                  // bin, keys above it, keys in it
+  __shared__ uint2 list[kList];                                  // (key, position)
+  __shared__ unsigned n_list, s_ties;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x / cl, s = blockIdx.y;
-  const int rank = blockIdx.x % cl;
+  const int c = blockIdx.x / cl, s = blockIdx.y, rank = blockIdx.x % cl;
   auto meet = [&]() {
     if (cl > 1)
       tc::cluster_sync_all();
     else
       __syncthreads();
   };
-  auto remote = [&](const unsigned* p, int r) {
+  auto of_rank = [&](const unsigned* p, int r) {
     return r == rank ? *p : ld_cluster_u32(tc::map_to_rank(tc::smem_u32(p), r));
   };
   pdl_wait();
@@ -81,8 +96,9 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const __grid_
   }
   const int chunk = (len + cl - 1) / cl, j0 = min(rank * chunk, len), n = min(chunk, len - j0);
   const int lo_j = a.n_first - j0, hi_j = len - a.n_recent - j0;  // candidates, in this block's indexes
+  const int words = (n + 31) / 32;
   unsigned kmin = ~0u, kmax = 0u;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += kSelThreads) {
     const float x = w[j0 + i];
     sw[i] = x;
@@ -92,52 +108,63 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const __grid_
       kmax = max(kmax, k);
     }
   }
+  reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) n_list = s_ties = 0u;
   kmin = __reduce_min_sync(kFull, kmin);
   kmax = __reduce_max_sync(kFull, kmax);
   if (lane == 0) {
     red[0][warp] = kmin;
     red[1][warp] = kmax;
   }
-  for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[0][i] = 0u;
   __syncthreads();
-  kmin = __reduce_min_sync(kFull, red[0][lane]);
-  kmax = __reduce_max_sync(kFull, red[1][lane]);
-  if (threadIdx.x == 0) {
-    pub[0][0] = kmin;
-    pub[0][1] = kmax;
-  }
-  meet();  // also: every weight of this head is in shared memory, w_out may be w
-  for (int r = 0; r < cl; ++r) {
-    kmin = min(kmin, remote(&pub[0][0], r));
-    kmax = max(kmax, remote(&pub[0][1], r));
+  kmin = __reduce_min_sync(kFull, red[0][lane % kSelWarps]);
+  kmax = __reduce_max_sync(kFull, red[1][lane % kSelWarps]);
+  if (cl > 1) {
+    if (threadIdx.x == 0) {
+      pub[0][0] = kmin;
+      pub[0][1] = kmax;
+    }
+    meet();  // every weight of this head is in shared memory (w_out may be w), every histogram empty
+    for (int r = 0; r < cl; ++r) {
+      kmin = min(kmin, of_rank(&pub[0][0], r));
+      kmax = max(kmax, of_rank(&pub[0][1], r));
+    }
   }
   int need = a.budget - a.n_first - a.n_recent;  // below the number of candidates, since budget < len
-  uint32_t thr = ~0u;                            // keys above it are kept (none is above ~0)
+  uint32_t lo = kmin, hi = kmax;                 // the need-th largest key lies in [lo, hi]
+  uint32_t thr = ~0u;                            // keys above it are kept (none is above ~0),
   int ties = 0;                                  // and the first `ties` equal to it
-  if (need > 0) {
-    uint32_t lo = kmin, hi = kmax;
-    for (int p = 0;; p ^= 1) {
-      const uint32_t range = hi - lo;
-      const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;  // kBins = 2^11
+  bool rank_list = false;
+  while (need > 0) {
+    const uint32_t range = hi - lo;
+    const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
 #pragma unroll 4
-      for (int i = threadIdx.x; i < n; i += kSelThreads) {
-        const uint32_t k = weight_key(sw[i]);
-        if (i >= lo_j && i < hi_j && k >= lo && k <= hi) {
-          const uint32_t b = (k - lo) >> shift;
-          if (b) atomicAdd(&hist[p][b], 1u);
-        }
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+      const uint32_t k = weight_key(sw[i]);
+      if (i >= lo_j && i < hi_j && k >= lo && k <= hi) {
+        const uint32_t b = (k - lo) >> shift;
+        if (b) atomicAdd(&hist[b], 1u);
       }
-      if (threadIdx.x == 0) found[0] = 0u;
+    }
+    __syncthreads();
+    // thread t holds bins kBins - 1 - 4 t and the three below it
+    uint4* mine = reinterpret_cast<uint4*>(hist) + (kSelThreads - 1 - threadIdx.x);
+    uint4 h = *mine;
+    if (rank != 0) {
+      const unsigned v[4] = {h.x, h.y, h.z, h.w};
+      const uint32_t to = tc::map_to_rank(tc::smem_u32(mine), 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (v[i]) red_cluster_add(to + 4 * i, v[i]);
+      *mine = make_uint4(0, 0, 0, 0);
+    }
+    if (cl > 1) {
       meet();
-      // thread t takes bins kBins - 1 - 2 t and the one below it
-      const int b1 = kBins - 1 - 2 * threadIdx.x;
-      unsigned h1 = 0, h0 = 0;
-      for (int r = 0; r < cl; ++r) {
-        h1 += remote(&hist[p][b1], r);
-        h0 += remote(&hist[p][b1 - 1], r);
-      }
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[p ^ 1][i] = 0u;
-      unsigned sum = h1 + h0;
+      h = *mine;
+    }
+    if (rank == 0) {
+      *mine = make_uint4(0, 0, 0, 0);
+      unsigned sum = h.x + h.y + h.z + h.w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_up_sync(kFull, sum, o);
@@ -145,86 +172,139 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const __grid_
       }
       if (lane == 31) red[0][warp] = sum;
       __syncthreads();
-      const unsigned others = red[0][lane];
-      const unsigned before = __reduce_add_sync(kFull, lane < warp ? others : 0u);
+      const unsigned others = lane < kSelWarps ? red[0][lane] : 0u;
+      unsigned at = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - (h.x + h.y + h.z + h.w);
       const unsigned total = __reduce_add_sync(kFull, others);
-      const unsigned incl = before + sum, mid = incl - h0, excl = mid - h1;
-      if (b1 > 0 && excl < (unsigned)need && mid >= (unsigned)need) {
-        found[0] = b1;
-        found[1] = excl;
-        found[2] = h1;
-      } else if (b1 > 1 && mid < (unsigned)need && incl >= (unsigned)need) {
-        found[0] = b1 - 1;
-        found[1] = mid;
-        found[2] = h0;
+      const unsigned v[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at < (unsigned)need && at + v[i] >= (unsigned)need) {
+          found[0] = kBins - 1 - 4 * threadIdx.x - i;
+          found[1] = at;
+          found[2] = v[i];
+        }
+        at += v[i];
       }
-      __syncthreads();
-      const uint32_t bin = found[0];
-      const unsigned above = bin ? found[1] : total;
-      const bool whole = bin && found[2] == (unsigned)need - above;
-      need -= (int)above;
-      lo += bin << shift;
-      if (whole) {  // the bin's keys are the last ones needed
-        thr = lo - 1;
-        break;
+      if (threadIdx.x == 0 && total < (unsigned)need) {  // the lowest bin; how many it holds is not known
+        found[0] = 0u;
+        found[1] = total;
+        found[2] = ~0u;
       }
-      hi = min(hi, lo + ((1u << shift) - 1u));
-      if (shift == 0 || lo == hi) {
-        thr = lo;
-        ties = need;
-        break;
-      }
-      __syncthreads();  // found and red are read
     }
+    meet();
+    const uint32_t bin = of_rank(&found[0], 0);
+    const unsigned above = of_rank(&found[1], 0), inside = of_rank(&found[2], 0);
+    need -= (int)above;
+    lo += bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    if (inside == (unsigned)need) {  // the bin's keys are the last ones needed
+      thr = lo - 1;
+      break;
+    }
+    if (lo == hi) {
+      thr = lo;
+      ties = need;
+      break;
+    }
+    if (cl == 1 && inside <= kList) {
+      thr = hi;
+      rank_list = true;
+      break;
+    }
+    // found is written again only after everybody has come to the next pass's meeting
   }
-  // order: warp w of the block takes a run of its positions
-  const int run = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int i0 = min(warp * run, n), i1 = min(i0 + run, n);
-  unsigned n_above = 0, n_equal = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const int x = i + lane;
-    const bool in = x < i1, cand = in && x >= lo_j && x < hi_j;
-    const uint32_t k = in ? weight_key(sw[x]) : 0u;
-    n_above += __popc(__ballot_sync(kFull, (in && !cand) || (cand && k > thr)));
-    n_equal += __popc(__ballot_sync(kFull, cand && k == thr));
+  // bitmaps; the keys still to be ranked into the list
+  for (int x = warp; x < words; x += kSelWarps) {
+    const int i = 32 * x + lane;
+    const bool in = i < n, cand = in && i >= lo_j && i < hi_j;
+    const uint32_t k = in ? weight_key(sw[i]) : 0u;
+    const unsigned b = __ballot_sync(kFull, (in && !cand) || (cand && k > thr));
+    const unsigned e = __ballot_sync(kFull, !rank_list && cand && k == thr);
+    if (lane == 0) {
+      sure[x] = b;
+      tied[x] = e;
+    }
+    if (rank_list && cand && k >= lo && k <= hi) list[atomicAdd(&n_list, 1u)] = make_uint2(k, i);
   }
   __syncthreads();
-  if (lane == 0) {
-    red[0][warp] = n_above;
-    red[1][warp] = n_equal;
+  if (rank_list) {
+    const int m = n_list;  // <= kList: the bin's population
+    if (threadIdx.x < m) {
+      const uint2 me = list[threadIdx.x];
+      int greater = 0, equal = 0;
+      for (int x = 0; x < m; ++x) {
+        const uint32_t k = list[x].x;
+        greater += k > me.x;
+        equal += k == me.x;
+      }
+      const unsigned bit = 1u << (me.y & 31);
+      if (greater + equal <= need) {
+        atomicOr(&sure[me.y >> 5], bit);
+      } else if (greater < need) {
+        atomicOr(&tied[me.y >> 5], bit);
+        s_ties = need - greater;  // the same from all of them
+      }
+    }
+    __syncthreads();
+    ties = s_ties;
   }
+  // places: thread t takes words 2 t and 2 t + 1
+  unsigned ws[2], we[2], pop = 0;  // populations, kept in the low half, tied in the high one (each <= 2^15)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = 2 * threadIdx.x + i;
+    ws[i] = x < words ? sure[x] : 0u;
+    we[i] = x < words ? tied[x] : 0u;
+    pop += __popc(ws[i]) + (__popc(we[i]) << 16);
+  }
+  unsigned sum = pop;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) red[1][warp] = sum;
   __syncthreads();
-  const unsigned ra = red[0][lane], re = red[1][lane];
-  unsigned at_above = __reduce_add_sync(kFull, lane < warp ? ra : 0u);
-  unsigned at_equal = __reduce_add_sync(kFull, lane < warp ? re : 0u);
+  const unsigned others = lane < kSelWarps ? red[1][lane] : 0u;
+  const unsigned before = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - pop;
+  unsigned at_sure = before & 0xffffu, at_tied = before >> 16;
   if (cl > 1) {
-    const unsigned ta = __reduce_add_sync(kFull, ra), te = __reduce_add_sync(kFull, re);
+    const unsigned total = __reduce_add_sync(kFull, others);
     if (threadIdx.x == 0) {
-      pub[1][0] = ta;
-      pub[1][1] = te;
+      pub[1][0] = total & 0xffffu;
+      pub[1][1] = total >> 16;
     }
     meet();
     for (int r = 0; r < rank; ++r) {
-      at_above += remote(&pub[1][0], r);
-      at_equal += remote(&pub[1][1], r);
+      at_sure += of_rank(&pub[1][0], r);
+      at_tied += of_rank(&pub[1][1], r);
     }
   }
-  for (int i = i0; i < i1; i += 32) {
-    const int x = i + lane;
-    const bool in = x < i1, cand = in && x >= lo_j && x < hi_j;
-    const float v = in ? sw[x] : 0.f;
-    const uint32_t k = weight_key(v);
-    const bool above = (in && !cand) || (cand && k > thr), equal = cand && k == thr;
-    const unsigned ba = __ballot_sync(kFull, above), be = __ballot_sync(kFull, equal);
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned ia = at_above + __popc(ba & below), ie = at_equal + __popc(be & below);
-    const unsigned at = ia + min(ie, (unsigned)ties);
-    if ((above || (equal && ie < (unsigned)ties)) && at < (unsigned)a.budget) {
-      kept[at] = j0 + x;
-      w_out[at] = v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int x = 2 * threadIdx.x + i;
+    const unsigned pe = __popc(we[i]);
+    unsigned take = at_tied >= (unsigned)ties ? 0u : min(pe, (unsigned)ties - at_tied), some = 0u;
+    if (take == pe) {
+      some = we[i];
+    } else {
+      for (unsigned left = we[i]; take; --take, left &= left - 1) some |= left & (0u - left);
     }
-    at_above += __popc(ba);
-    at_equal += __popc(be);
+    if (x < words) {
+      sure[x] = ws[i] | some;
+      tied[x] = at_sure + min(at_tied, (unsigned)ties);
+    }
+    at_sure += __popc(ws[i]);
+    at_tied += pe;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int x = warp; x < words; x += kSelWarps) {
+    const unsigned keep = sure[x], at = tied[x] + __popc(keep & ((1u << lane) - 1u));
+    if ((keep >> lane & 1u) && at < (unsigned)a.budget) {
+      kept[at] = j0 + 32 * x + lane;
+      w_out[at] = sw[32 * x + lane];
+    }
   }
   for (int i = a.budget + all; i < len; i += stride) w_out[i] = 0.f;
   if (cl > 1) tc::cluster_sync_all();  // nobody leaves while its shared memory may be read
@@ -232,48 +312,63 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const __grid_
 
 // ---- keys and values -----------------------------------------------------------
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveItems = 4;  // 16-byte pieces a thread has in flight
+constexpr int kMoveItems = 4;
+constexpr int kCopyThreads = 128;
 
-// To other pages: every 16-byte piece on its own.  Consecutive threads take
-// consecutive pieces of an output position (all heads of it), a thread
-// kMoveItems positions of the block's run.
-__global__ void __launch_bounds__(kMoveThreads) cache_copy_kernel(const __grid_constant__ CacheEvictArgs a, int row16) {
+// To other pages.  A warp takes `rows` output positions of one (sequence, KV
+// head): a lane finds where one of them comes from and goes to, then the warp
+// moves their keys and values with kMoveItems pieces of each in flight a lane,
+// LANES lanes on a row.
+template <int LANES>
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CacheEvictArgs a, int rows) {
+  constexpr int RPI = 32 / LANES;  // rows of one load
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.y, part = blockIdx.x & 1;
-  const int wide = a.nkv * row16;                       // pieces of a position
+  const int s = blockIdx.z, c = blockIdx.y, lane = threadIdx.x & 31;
+  const int i0 = (blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5)) * rows;
   bool bad;
   const int n_keep = min(checked_len(a.lens[s], a.limit, &bad), a.budget);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;  // lens_out may be lens: n_keep reads back as itself
-  const uint4* src = static_cast<const uint4*>(part ? a.v : a.k);
-  uint4* dst = static_cast<uint4*>(part ? a.v_out : a.k_out);
-  // the block's first piece as (position, piece of it); the rest in 32 bits
-  const int64_t base = (int64_t)(blockIdx.x >> 1) * kMoveThreads * kMoveItems;
-  const int base_i = (int)(base / wide), base_p = (int)(base - (int64_t)base_i * wide);
-  if (base_i >= n_keep) return;
-  uint4 x[kMoveItems];
-  int64_t to[kMoveItems];
-#pragma unroll
-  for (int u = 0; u < kMoveItems; ++u) {
-    const int e = base_p + (int)threadIdx.x + u * kMoveThreads;
-    const int i = base_i + e / wide, hp = e % wide;
-    to[u] = -1;
-    if (i < n_keep) {
-      const int c = hp / row16;
-      const int64_t from = page_slot(a.table, s, a.kept[((int64_t)s * a.nkv + c) * a.budget + i]);
-      const int64_t dst_slot = page_slot(a.table_out, s, i);
-      if (from < 0 || dst_slot < 0) {
-        cache_error(a.err, kCacheBadPage);
-      } else {
-        to[u] = dst_slot * wide + hp;
-        x[u] = src[from * wide + hp];
-      }
+  // lens_out may be lens: the blocks that read it later find n_keep, which gives n_keep again
+  if (blockIdx.x == 0 && c == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;
+  const int n = min(rows, n_keep - i0);
+  if (n <= 0) return;
+  uint32_t from = ~0u, to = ~0u;
+  if (lane < n) {
+    const int64_t f = page_slot(a.table, s, a.kept[((int64_t)s * a.nkv + c) * a.budget + i0 + lane]);
+    const int64_t t = page_slot(a.table_out, s, i0 + lane);
+    if (f < 0 || t < 0) {
+      cache_error(a.err, kCacheBadPage);
+    } else {
+      from = (uint32_t)f;
+      to = (uint32_t)t;
     }
   }
+  const int64_t stride = (int64_t)a.nkv * LANES;  // pieces from one position to the next
+  const uint4* ks = static_cast<const uint4*>(a.k) + c * LANES + lane % LANES;
+  const uint4* vs = static_cast<const uint4*>(a.v) + c * LANES + lane % LANES;
+  uint4* kd = static_cast<uint4*>(a.k_out) + c * LANES + lane % LANES;
+  uint4* vd = static_cast<uint4*>(a.v_out) + c * LANES + lane % LANES;
+  for (int r0 = 0; r0 < n; r0 += RPI * kMoveItems) {
+    uint4 k[kMoveItems], v[kMoveItems];
+    uint32_t dst[kMoveItems];
 #pragma unroll
-  for (int u = 0; u < kMoveItems; ++u)
-    if (to[u] >= 0) dst[to[u]] = x[u];
+    for (int u = 0; u < kMoveItems; ++u) {
+      const int r = r0 + u * RPI + lane / LANES;  // rows <= 32; behind n: lanes without a slot
+      const uint32_t f = __shfl_sync(kFull, from, r & 31);
+      dst[u] = __shfl_sync(kFull, to, r & 31);
+      if (r >= n) dst[u] = ~0u;
+      if (dst[u] != ~0u) {
+        k[u] = __ldcs(ks + (int64_t)f * stride);
+        v[u] = __ldcs(vs + (int64_t)f * stride);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveItems; ++u)
+      if (dst[u] != ~0u) {
+        kd[(int64_t)dst[u] * stride] = k[u];
+        vd[(int64_t)dst[u] * stride] = v[u];
+      }
+  }
 }
 
 constexpr int kShiftThreads = 512;
@@ -323,28 +418,37 @@ __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid
 }
 
 // Blocks of a cluster for `heads` (sequence, KV head) pairs of up to `limit`
-// weights: kSelCap of them a block at most; more blocks while each keeps
-// kSelKeys and the launch stays one wave of two blocks per SM.
-constexpr int kSelCap = 32768, kSelKeys = 8192;
+// weights: as few as hold them, but more, of at least kSelKeys each, while the
+// launch leaves SMs idle.
+constexpr int kSelKeys = 8192;
 int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   int cl = 1;
-  while (cl < 8 && (limit > (int64_t)cl * kSelCap ||
-                    (limit >= 2 * cl * kSelKeys && heads * cl * 2 <= 2 * sm_count)))
+  while (cl < 8 && (limit > (int64_t)cl * kSelCap || (limit >= 2 * cl * kSelKeys && heads * cl * 2 <= sm_count)))
     cl *= 2;
   return cl;
+}
+
+template <int LANES>
+cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
+  // 32 positions a warp, or 8 where that leaves SMs without a warp to hide latency behind
+  const int rows = (int64_t)a.S * a.nkv * ((a.budget + 31) / 32) < 8 * sm_count ? 8 : 32;
+  const int per_block = rows * (kCopyThreads / 32);
+  return launch_pdl(st, dim3((a.budget + per_block - 1) / per_block, a.nkv, a.S), dim3(kCopyThreads), 0, 1,
+                    cache_copy_kernel<LANES>, a, rows);
 }
 
 }  // namespace
 
 cudaError_t prepare_cache_evict() {
-  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
+  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSelCap * 4 + kSelCap / 4);
 }
 
 cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf16, int sm_count) {
   const int cl = select_cluster(a.limit, (int64_t)a.S * a.nkv, sm_count);
-  const size_t smem = (size_t)((a.limit + cl - 1) / cl) * sizeof(float);
-  cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(kSelThreads), smem, dim3(cl), cache_select_kernel,
-                                     a, cl);
+  const int cap = (int)((a.limit + cl - 1) / cl + 31) / 32 * 32;
+  cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(kSelThreads), (size_t)cap * 4 + cap / 4, dim3(cl),
+                                     cache_select_kernel, a, cl, cap);
   if (e != cudaSuccess) return e;
   const int row16 = a.hd * (bf16 ? 2 : 4) / 16;
   if (a.in_place) {
@@ -352,9 +456,8 @@ cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf1
     return launch_pdl(st, dim3(a.nkv * 2 * (row16 / pieces), a.S), dim3(kShiftThreads), 0, 1, cache_shift_kernel, a,
                       row16, pieces);
   }
-  const int64_t items = (int64_t)a.budget * a.nkv * row16;
-  const int64_t runs = (items + kMoveThreads * kMoveItems - 1) / (kMoveThreads * kMoveItems);
-  return launch_pdl(st, dim3((unsigned)(2 * runs), a.S), dim3(kMoveThreads), 0, 1, cache_copy_kernel, a, row16);
+  if (row16 == 8) return copy_rows<8>(st, a, sm_count);
+  return row16 == 16 ? copy_rows<16>(st, a, sm_count) : copy_rows<32>(st, a, sm_count);
 }
 
 }  // namespace sf
