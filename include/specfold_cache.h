@@ -150,7 +150,7 @@ sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t 
  *          largest weight (equal weights: the lower index first; NaN below
  *          every number, -0 equal to 0), in ascending order;
  *   position i of sequence s, head c of the output := position kept[s,c,i];
- *   weights_out[s,c,i] = weights[s,c,kept[s,c,i]], and 0 for
+ *   weights_out[s,c,i] = weights[s,c,kept[s,c,i]] (-0 as 0), and 0 for
  *          lens_out[s] <= i < lens[s], so that tokens stored there later start
  *          from 0;
  *   lens_out[s] = min(lens[s], budget).

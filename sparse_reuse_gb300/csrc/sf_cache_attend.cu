@@ -109,19 +109,19 @@ struct Ring {
   uint64_t live = 0;            // which keys are there, KEYS bits per stage in use order
   int in_ring = 0;
 
-  int page_j;                   // position of this lane's key of the next tile, and its page entry, which was
-  int32_t page;                 // asked for a tile ago: its latency is not waited for
-
-  __device__ __forceinline__ void look(const CacheAttendArgs& a, const Segment& g, int key0, int lane) {
-    page_j = key0 + lane % KEYS;
-    page = page_j < g.len ? page_entry(a.table, g.s, page_j) : -1;
+  // Page entry of this lane's key of the tile at key0.  Asked for a tile before it is pushed: its latency is not
+  // waited for.
+  static __device__ __forceinline__ int32_t look(const CacheAttendArgs& a, const Segment& g, int key0, int lane) {
+    const int j = key0 + lane % KEYS;
+    return j < g.len ? page_entry(a.table, g.s, j) : -1;
   }
 
-  // Copy the looked-up tile into the next stage.
-  __device__ __forceinline__ void push(const CacheAttendArgs& a, const Segment& g, int lane) {
+  // Copy the tile at key0 into the next stage.
+  __device__ __forceinline__ void push(const CacheAttendArgs& a, const Segment& g, int key0, int32_t page, int lane) {
     int64_t slot = -1;
-    if (page_j < g.len) {
-      slot = entry_slot(a.table, page, page_j);
+    const int j = key0 + lane % KEYS;
+    if (j < g.len) {
+      slot = entry_slot(a.table, page, j);
       if (slot < 0) cache_error(a.err, kCacheBadPage);
     }
     const uint32_t sl = (uint32_t)slot;
@@ -206,16 +206,18 @@ struct WarpBf16 {
     R ring;
     ring.base = tc::smem_u32(mem);
     int ti = t;
-    ring.look(a, g, ti * kTileKeys, lane);
-#pragma unroll 1
+    int32_t pages[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) pages[i] = R::look(a, g, (t + i * step) * kTileKeys, lane);
+#pragma unroll
     for (int i = 0; i < kStages; ++i) {
       if (ti < end) {
-        ring.push(a, g, lane);
+        ring.push(a, g, ti * kTileKeys, pages[i], lane);
         ti += step;
-        ring.look(a, g, ti * kTileKeys, lane);
       }
       cp_async_commit();
     }
+    int32_t page = R::look(a, g, ti * kTileKeys, lane);
     // this lane's row and chunk of the operand loads (chunk 2 x + .. of step x)
     const int krow = lane & 15, kch = lane >> 4;
     const int vrow = (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
@@ -308,9 +310,9 @@ struct WarpBf16 {
       __syncwarp();  // the stage is read: refill it
       ring.pop();
       if (ti < end) {
-        ring.push(a, g, lane);
+        ring.push(a, g, ti * kTileKeys, page, lane);
         ti += step;
-        ring.look(a, g, ti * kTileKeys, lane);
+        page = R::look(a, g, ti * kTileKeys, lane);
       }
       cp_async_commit();
     }
@@ -349,21 +351,21 @@ struct WarpBf16 {
 // dimensions (queries come from shared memory, the four quarters meet in two
 // shuffles); for the output a lane holds 4 dimensions of every key and the
 // weights come back through shared memory.
-template <int HD>
+template <int HD, int NH>
 struct WarpF32 {
   static constexpr int KEYS = 8;
   using R = Ring<float, HD, KEYS, HD == 128 ? 2 : 4>;
   static constexpr int kStages = R::kBytes / R::kStageBytes;
-  static constexpr int kHeads = 8;
+  static constexpr int kHeads = NH;      // query heads a block takes together
   static constexpr int kRow = HD;
-  static constexpr int kBytes = R::kBytes + 256;  // the ring (then the output), weights [8 keys][8 heads]
+  static constexpr int kBytes = R::kBytes + KEYS * NH * 4;  // the ring (then the output), weights [keys][heads]
   static constexpr int KI = HD / 16;              // 16-byte pieces of a key a lane takes
   static constexpr int LPR = HD / 4;              // lanes on one value row
   static constexpr int RPI = 32 / LPR;            // value rows per load
   static_assert(kHeads * kRow * 4 <= R::kBytes, "output over the ring");
 
-  float o[8][4];
-  float m[8], l[8];
+  float o[NH][4];
+  float m[NH], l[NH];
 
   template <bool TRACK, typename F>
   __device__ __forceinline__ void run(const CacheAttendArgs& a, const Segment& g, unsigned char* mem, const float* sq,
@@ -372,7 +374,7 @@ struct WarpF32 {
     const int vr = lane / LPR, vd = lane % LPR;
     float* sp = reinterpret_cast<float*>(mem + R::kBytes);
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
+    for (int h = 0; h < NH; ++h) {
       m[h] = -INFINITY;
       l[h] = 0.f;
 #pragma unroll
@@ -385,16 +387,18 @@ struct WarpF32 {
     int ki = t * kTileKeys, ku = ki;
     const int stop = min(end * kTileKeys, g.len);
     auto next = [&](int k) { return (k & KEYS) ? k - KEYS + step * kTileKeys : k + KEYS; };
-    ring.look(a, g, ki, lane);
-#pragma unroll 1
+    int32_t pages[kStages];
+#pragma unroll
+    for (int i = 0, k = ki; i < kStages; ++i, k = next(k)) pages[i] = R::look(a, g, k, lane);
+#pragma unroll
     for (int i = 0; i < kStages; ++i) {
       if (ki < stop) {
-        ring.push(a, g, lane);
+        ring.push(a, g, ki, pages[i], lane);
         ki = next(ki);
-        ring.look(a, g, ki, lane);
       }
       cp_async_commit();
     }
+    int32_t page = R::look(a, g, ki, lane);
     load_q();  // queries to shared memory, behind the first copies
 #pragma unroll 1
     for (; ku < stop; ku = next(ku)) {
@@ -406,77 +410,81 @@ struct WarpF32 {
 #pragma unroll
       for (int i = 0; i < KI; ++i)
         k[i] = *reinterpret_cast<const float4*>(st + r * R::kRowBytes + (((c + 4 * i) ^ R::turn(r)) << 4));
-      float x[8];
+      float x[NH];
       bool grew = false;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        x[h] = 0.f;
-        if (h < g.nh) {
+      for (int h = 0; h < NH; ++h) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < KI; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(sq + h * HD + c * 4 + 16 * i);
-            x[h] += q.x * k[i].x + q.y * k[i].y + q.z * k[i].z + q.w * k[i].w;
-          }
-          x[h] += __shfl_xor_sync(kFull, x[h], 1);
-          x[h] += __shfl_xor_sync(kFull, x[h], 2);
-          x[h] = live ? x[h] * a.scale_log2 : -INFINITY;
-          if (TRACK && c == (h & 3) && ku + r < g.len)
-            a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + ku + r] = x[h];
-          grew |= !(x[h] <= m[h] + kSlack);
+        for (int i = 0; i < KI; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(sq + h * HD + c * 4 + 16 * i);
+          y.x += q.x * k[i].x;
+          y.y += q.y * k[i].y;
+          y.z += q.z * k[i].z;
+          y.w += q.w * k[i].w;
         }
+        x[h] = (y.x + y.y) + (y.z + y.w);
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        x[h] += __shfl_xor_sync(kFull, x[h], 1);
+        x[h] += __shfl_xor_sync(kFull, x[h], 2);
+        x[h] = live ? x[h] * a.scale_log2 : -INFINITY;
+        if (TRACK && c == (h & 3) && h < g.nh && ku + r < g.len)
+          a.scores[((int64_t)g.s * a.nq + g.h0 + h) * a.ld_scores + ku + r] = x[h];
+        grew |= !(x[h] <= m[h] + kSlack);
       }
       if (__any_sync(kFull, grew)) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h)
-          if (h < g.nh) {
-            float y = fmaxf(x[h], __shfl_xor_sync(kFull, x[h], 4));
-            y = fmaxf(y, __shfl_xor_sync(kFull, y, 8));
-            y = fmaxf(y, __shfl_xor_sync(kFull, y, 16));
-            y = fmaxf(m[h], y);
-            const float f = m[h] == y ? 1.f : ex2(m[h] - y);
-            m[h] = y;
-            l[h] *= f;
+        for (int h = 0; h < NH; ++h) {
+          float y = fmaxf(x[h], __shfl_xor_sync(kFull, x[h], 4));
+          y = fmaxf(y, __shfl_xor_sync(kFull, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(kFull, y, 16));
+          y = fmaxf(m[h], y);
+          const float f = m[h] == y ? 1.f : ex2(m[h] - y);
+          m[h] = y;
+          l[h] *= f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] *= f;
-          }
+          for (int e = 0; e < 4; ++e) o[h][e] *= f;
+        }
       }
 #pragma unroll
-      for (int h = 0; h < 8; ++h)
-        if (h < g.nh) {
-          const float p = ex2((x[h] - (m[h] == -INFINITY ? 0.f : m[h])) - kRoom);
-          l[h] += p;
-          if (c == (h & 3)) sp[r * 8 + h] = p;
-        }
+      for (int h = 0; h < NH; ++h) {
+        const float p = ex2((x[h] - (m[h] == -INFINITY ? 0.f : m[h])) - kRoom);
+        l[h] += p;
+        if (c == (h & 3)) sp[r * NH + h] = p;
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 8 / RPI; ++i) {
         const int row = i * RPI + vr;
         const float4 v =
             *reinterpret_cast<const float4*>(st + KEYS * R::kRowBytes + row * R::kRowBytes + ((vd ^ R::turn(row)) << 4));
-        const float4 p0 = *reinterpret_cast<const float4*>(sp + row * 8);
-        const float4 p1 = *reinterpret_cast<const float4*>(sp + row * 8 + 4);
-        const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-        for (int h = 0; h < 8; ++h)
-          if (h < g.nh) {
-            o[h][0] += p[h] * v.x;
-            o[h][1] += p[h] * v.y;
-            o[h][2] += p[h] * v.z;
-            o[h][3] += p[h] * v.w;
-          }
+        for (int h = 0; h < NH; h += 2) {
+          const float2 p = *reinterpret_cast<const float2*>(sp + row * NH + h);
+          o[h][0] += p.x * v.x;
+          o[h][1] += p.x * v.y;
+          o[h][2] += p.x * v.z;
+          o[h][3] += p.x * v.w;
+          o[h + 1][0] += p.y * v.x;
+          o[h + 1][1] += p.y * v.y;
+          o[h + 1][2] += p.y * v.z;
+          o[h + 1][3] += p.y * v.w;
+        }
       }
       __syncwarp();  // the stage and the weights are read
       ring.pop();
       if (ki < stop) {
-        ring.push(a, g, lane);
+        ring.push(a, g, ki, page, lane);
         ki = next(ki);
-        ring.look(a, g, ki, lane);
+        page = R::look(a, g, ki, lane);
       }
       cp_async_commit();
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
+    for (int h = 0; h < NH; ++h) {
       l[h] += __shfl_xor_sync(kFull, l[h], 4);
       l[h] += __shfl_xor_sync(kFull, l[h], 8);
       l[h] += __shfl_xor_sync(kFull, l[h], 16);
@@ -490,7 +498,7 @@ struct WarpF32 {
   __device__ __forceinline__ void store(float* so, float2* sml, int lane) const {
     const int vd = lane % LPR;
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
+    for (int h = 0; h < NH; ++h) {
       if (lane == 0) sml[h] = make_float2(m[h], l[h]);
       if (lane < LPR)
         *reinterpret_cast<float4*>(so + h * kRow + vd * 4) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
@@ -500,13 +508,14 @@ struct WarpF32 {
 
 // ---- the kernels -------------------------------------------------------------
 
+// NT: column tiles of 8 query heads (bf16), or query heads (fp32).
 template <typename T, int HD, int NT>
 struct WarpOf {
   using type = WarpBf16<HD, NT>;
 };
 template <int HD, int NT>
 struct WarpOf<float, HD, NT> {
-  using type = WarpF32<HD>;
+  using type = WarpF32<HD, NT>;
 };
 
 // Block-wide exclusive scan of units_of(length) per sequence into
@@ -593,11 +602,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   constexpr int NH = Warp::kHeads, ROW = Warp::kRow;
   constexpr bool F32 = sizeof(T) == 4;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float2 sml[kWarps > kInlineParts ? kWarps : kInlineParts][NH];
+  __shared__ float2 sml[kWarps][NH];
   __shared__ float sfac[kWarps][NH];
   __shared__ int sums[kWarps];
   __shared__ int s_last;
-  __shared__ __align__(16) float sq[F32 ? kWarps : 1][F32 ? 8 * HD : 4];
+  __shared__ __align__(16) float sq[F32 ? kWarps : 1][F32 ? NH * HD : 4];
   int* first = reinterpret_cast<int*>(smem + kWarps * Warp::kBytes);
   int* lens = first + a.S + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -631,15 +640,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   };
   auto load_q = [&](const Segment& g, float* to, int i0, int step) {
     if constexpr (F32) {
-      for (int i = i0; i < g.nh * HD; i += step)
-        to[i] = static_cast<const float*>(a.q)[(int64_t)g.s * a.ld_q + (int64_t)g.h0 * HD + i];
+      for (int i = i0; i < NH * HD; i += step)
+        to[i] = i < g.nh * HD ? static_cast<const float*>(a.q)[(int64_t)g.s * a.ld_q + (int64_t)g.h0 * HD + i] : 0.f;
     }
   };
   Warp w;
   while (u < u_end) {
     const int tiles = first[s + 1] - first[s];
     const int in_s = (int)(u - (int64_t)first[s] * H);
-    const int hs = in_s / tiles, t0 = in_s % tiles;
+    const int hs = (unsigned)in_s / (unsigned)tiles, t0 = in_s - hs * tiles;
     // ---- short whole segments: a warp each
     if (t0 == 0 && tiles <= kShort) {
       int n = 0, my_s = -1, my_hs = 0;
@@ -746,43 +755,42 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
         a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, part_slot(b0, seg0, per)};
     } else if (n > 1) {
       // the last block to arrive joins the parts, in block order
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicInc(a.arrived + b0, n - 1) == (unsigned)(n - 1);
+      if (threadIdx.x == 0) {
+        __threadfence();  // the block's part, which the barrier ordered before this
+        s_last = atomicInc(a.arrived + b0, n - 1) == (unsigned)(n - 1);
+        __threadfence();
+      }
       __syncthreads();
       if (s_last) {
-        __threadfence();
-        if (threadIdx.x < NH * kInlineParts) {
-          const int x = threadIdx.x / NH, h = threadIdx.x % NH;
-          float2 ml = make_float2(-INFINITY, 0.f);
-          if (x < n && h < g.nh) {
-            const float* p = part_of<NH, HD>(a, part_slot(b0 + x, seg0, per)) + NH * HD + h;
-            ml = make_float2(__ldcg(p), __ldcg(p + NH));
-          }
-          sml[x][h] = ml;
-        }
-        __syncthreads();
         for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
           const int h = i / (HD / 4), d = i % (HD / 4) * 4;
           float4 y[kInlineParts];
+          float pm[kInlineParts], pl[kInlineParts];
 #pragma unroll
-          for (int x = 0; x < kInlineParts; ++x)
-            if (x < n)
-              y[x] = __ldcg(reinterpret_cast<const float4*>(part_of<NH, HD>(a, part_slot(b0 + x, seg0, per)) + h * HD + d));
-          float top = sml[0][h].x;
+          for (int x = 0; x < kInlineParts; ++x) {
+            pm[x] = -INFINITY;
+            if (x < n) {
+              const float* p = part_of<NH, HD>(a, part_slot(b0 + x, seg0, per));
+              y[x] = __ldcg(reinterpret_cast<const float4*>(p + h * HD + d));
+              pm[x] = __ldcg(p + NH * HD + h);
+              pl[x] = __ldcg(p + NH * HD + NH + h);
+            }
+          }
+          float top = pm[0];
 #pragma unroll
-          for (int x = 1; x < kInlineParts; ++x) top = fmaxf(top, sml[x][h].x);
+          for (int x = 1; x < kInlineParts; ++x) top = fmaxf(top, pm[x]);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
           float l = 0.f;
 #pragma unroll
           for (int x = 0; x < kInlineParts; ++x)
             if (x < n) {
-              const float f = part_factor(sml[x][h].x, top);
+              const float f = part_factor(pm[x], top);
               o.x += y[x].x * f;
               o.y += y[x].y * f;
               o.z += y[x].z * f;
               o.w += y[x].w * f;
-              l += sml[x][h].y * f;
+              l += pl[x] * f;
             }
           write_out<T>(a, g.s, g.h0 + h, HD, d, o, l);
           if (TRACK && d == 0) write_lse(a, g.s, g.h0 + h, top, l);
@@ -956,13 +964,19 @@ cudaError_t prepare_cache_attend() {
   if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 128, 2>();
   if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 64, 1>();
   if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, 64, 2>();
-  if (e == cudaSuccess) e = allow_smem<float, 128, 1>();
-  if (e == cudaSuccess) e = allow_smem<float, 64, 1>();
+  if (e == cudaSuccess) e = allow_smem<float, 128, 2>();
+  if (e == cudaSuccess) e = allow_smem<float, 128, 8>();
+  if (e == cudaSuccess) e = allow_smem<float, 64, 2>();
+  if (e == cudaSuccess) e = allow_smem<float, 64, 8>();
   return e;
 }
 
 cudaError_t launch_cache_attend(cudaStream_t st, const CacheAttendArgs& a, int bf16, int sm_count) {
-  if (!bf16) return a.hd == 128 ? attend_t<float, 128, 1>(st, a, sm_count) : attend_t<float, 64, 1>(st, a, sm_count);
+  if (!bf16) {
+    const bool few = a.nq / a.nkv <= 2;
+    if (a.hd == 128) return few ? attend_t<float, 128, 2>(st, a, sm_count) : attend_t<float, 128, 8>(st, a, sm_count);
+    return few ? attend_t<float, 64, 2>(st, a, sm_count) : attend_t<float, 64, 8>(st, a, sm_count);
+  }
   const bool wide = a.nq / a.nkv > 8;
   if (a.hd == 128)
     return wide ? attend_t<__nv_bfloat16, 128, 2>(st, a, sm_count) : attend_t<__nv_bfloat16, 128, 1>(st, a, sm_count);

@@ -16,11 +16,16 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 
 // Order-preserving map of a weight to an unsigned key: NaN 0, then -inf ... -0
-// = 0 ... +inf (0xff800000).
+// = 0 ... +inf (0xff800000); and back (-0 comes back as 0).
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 becomes +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  if (k == 0u) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -40,8 +45,8 @@ constexpr int kList = 256;              // keys that are ranked by comparing all
 constexpr int kSelCap = 32768;          // weights a block holds at most
 static_assert(kSelCap / 32 <= 2 * kSelThreads, "two words of a bitmap a thread");
 
-// A cluster of `cl` blocks per (sequence, KV head); block r holds the r-th
-// part of the weights in shared memory.
+// A cluster of `cl` blocks per (sequence, KV head); block r holds the keys
+// of the r-th part of the weights in shared memory.
 //
 // The need-th largest candidate key is found by narrowing [lo, hi]: the range
 // is cut into at most kBins equal bins (keys of positive floats are piecewise
@@ -57,8 +62,8 @@ static_assert(kSelCap / 32 <= 2 * kSelThreads, "two words of a bitmap a thread")
 // gives every kept position its place.
 __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __grid_constant__ CacheEvictArgs a, int cl,
                                                                       int cap) {
-  extern __shared__ __align__(16) float sw[];                    // [cap] weights of this block's positions
-  unsigned* sure = reinterpret_cast<unsigned*>(sw + cap);        // [cap / 32] kept; later the final choice
+  extern __shared__ __align__(16) unsigned keys[];               // [cap] of this block's positions
+  unsigned* sure = keys + cap;                                   // [cap / 32] kept; later the final choice
   unsigned* tied = sure + cap / 32;                              // [cap / 32] at the threshold; later places
   __shared__ __align__(16) unsigned hist[kBins];
   __shared__ unsigned red[2][32];
@@ -95,15 +100,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     return;
   }
   const int chunk = (len + cl - 1) / cl, j0 = min(rank * chunk, len), n = min(chunk, len - j0);
-  const int lo_j = a.n_first - j0, hi_j = len - a.n_recent - j0;  // candidates, in this block's indexes
+  // candidates, in this block's indexes
+  const int lo_j = min(max(a.n_first - j0, 0), n), hi_j = max(min(len - a.n_recent - j0, n), lo_j);
   const int words = (n + 31) / 32;
   unsigned kmin = ~0u, kmax = 0u;
 #pragma unroll 8
   for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    const float x = w[j0 + i];
-    sw[i] = x;
+    const uint32_t k = weight_key(w[j0 + i]);
+    keys[i] = k;
     if (i >= lo_j && i < hi_j) {
-      const uint32_t k = weight_key(x);
       kmin = min(kmin, k);
       kmax = max(kmax, k);
     }
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
       pub[0][0] = kmin;
       pub[0][1] = kmax;
     }
-    meet();  // every weight of this head is in shared memory (w_out may be w), every histogram empty
+    meet();  // every weight of this head is read (w_out may be w), every histogram empty
     for (int r = 0; r < cl; ++r) {
       kmin = min(kmin, of_rank(&pub[0][0], r));
       kmax = max(kmax, of_rank(&pub[0][1], r));
@@ -138,13 +143,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   while (need > 0) {
     const uint32_t range = hi - lo;
     const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
-      const uint32_t k = weight_key(sw[i]);
-      if (i >= lo_j && i < hi_j && k >= lo && k <= hi) {
-        const uint32_t b = (k - lo) >> shift;
-        if (b) atomicAdd(&hist[b], 1u);
-      }
+#pragma unroll 8
+    for (int i = lo_j + threadIdx.x; i < hi_j; i += kSelThreads) {
+      const uint32_t k = keys[i] - lo, b = k >> shift;
+      if (k <= range && b) atomicAdd(&hist[b], 1u);
     }
     __syncthreads();
     // thread t holds bins kBins - 1 - 4 t and the three below it
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   for (int x = warp; x < words; x += kSelWarps) {
     const int i = 32 * x + lane;
     const bool in = i < n, cand = in && i >= lo_j && i < hi_j;
-    const uint32_t k = in ? weight_key(sw[i]) : 0u;
+    const uint32_t k = in ? keys[i] : 0u;
     const unsigned b = __ballot_sync(kFull, (in && !cand) || (cand && k > thr));
     const unsigned e = __ballot_sync(kFull, !rank_list && cand && k == thr);
     if (lane == 0) {
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     const unsigned keep = sure[x], at = tied[x] + __popc(keep & ((1u << lane) - 1u));
     if ((keep >> lane & 1u) && at < (unsigned)a.budget) {
       kept[at] = j0 + 32 * x + lane;
-      w_out[at] = sw[32 * x + lane];
+      w_out[at] = key_weight(keys[32 * x + lane]);
     }
   }
   for (int i = a.budget + all; i < len; i += stride) w_out[i] = 0.f;
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
 
 constexpr int kMoveItems = 4;
 constexpr int kCopyThreads = 128;
+constexpr int kCopyWarps = 16;  // per SM
 
 // To other pages.  A warp takes `rows` output positions of one (sequence, KV
 // head): a lane finds where one of them comes from and goes to, then the warp
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid
 // Blocks of a cluster for `heads` (sequence, KV head) pairs of up to `limit`
 // weights: as few as hold them, but more, of at least kSelKeys each, while the
 // launch leaves SMs idle.
-constexpr int kSelKeys = 8192;
+constexpr int kSelKeys = 4096;
 int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   int cl = 1;
   while (cl < 8 && (limit > (int64_t)cl * kSelCap || (limit >= 2 * cl * kSelKeys && heads * cl * 2 <= sm_count)))
@@ -430,8 +433,8 @@ int select_cluster(int64_t limit, int64_t heads, int sm_count) {
 
 template <int LANES>
 cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
-  // 32 positions a warp, or 8 where that leaves SMs without a warp to hide latency behind
-  const int rows = (int64_t)a.S * a.nkv * ((a.budget + 31) / 32) < 8 * sm_count ? 8 : 32;
+  // 32 positions a warp, or 8 where that leaves too few warps to hide the latency of their loads
+  const int rows = (int64_t)a.S * a.nkv * ((a.budget + 31) / 32) < kCopyWarps * sm_count ? 8 : 32;
   const int per_block = rows * (kCopyThreads / 32);
   return launch_pdl(st, dim3((a.budget + per_block - 1) / per_block, a.nkv, a.S), dim3(kCopyThreads), 0, 1,
                     cache_copy_kernel<LANES>, a, rows);

@@ -81,15 +81,22 @@ constexpr int kTileKeys = 16;
 
 SF_HD int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
 
+// a / b for non-negative a and positive b, in 32 bits where they fit (a 64-bit
+// quotient costs a block some 400 cycles, and it is on the critical path).
+SF_HD int64_t quotient(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Units per block: all blocks busy, but at least `least` units each.
 SF_HD int64_t units_per_block(int64_t units, int blocks, int least) {
-  const int64_t per = (units + blocks - 1) / blocks;
+  const int64_t per = quotient(units + blocks - 1, blocks);
   return per < least ? least : per;
 }
 
 // Blocks that share the segment of `tiles` units starting at unit `first`.
-SF_HD int first_block(int64_t first, int64_t per) { return (int)(first / per); }
-SF_HD int last_block(int64_t first, int tiles, int64_t per) { return (int)((first + tiles - 1) / per); }
+SF_HD int first_block(int64_t first, int64_t per) { return (int)quotient(first, per); }
+SF_HD int last_block(int64_t first, int tiles, int64_t per) { return (int)quotient(first + tiles - 1, per); }
 
 // Partial slot of block `block` for the cut segment starting at `first`.
 SF_HD int part_slot(int block, int64_t first, int64_t per) { return 2 * block + (first > block * per ? 1 : 0); }
