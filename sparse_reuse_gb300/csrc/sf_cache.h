@@ -75,6 +75,7 @@ struct CacheAttendArgs {
   CacheJoin* joins;   // [blocks]
   bool join;          // a join kernel follows
   int least;          // units a block takes at least
+  int group, nsub, heads;  // query heads of a KV head, parts they are taken in, nkv * nsub
   unsigned* err;
 };
 // Blocks of the largest launch on sm_count SMs, floats of `parts` that each needs, and the kernels' shared-memory limits (once per process and device).

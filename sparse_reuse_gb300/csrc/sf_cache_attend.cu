@@ -519,11 +519,12 @@ struct WarpOf<float, HD, NT> {
 };
 
 // Block-wide exclusive scan of units_of(length) per sequence into
-// first[0..S], the lengths themselves into lens[0..S-1]; `sums` one int per warp.
+// first[0..S], the lengths themselves into lens[0..S-1]; `sums` one int per
+// warp.  Returns the number of sequences that are not empty.
 template <int THREADS, typename F>
-__device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, int* lens, int* sums, F units_of) {
+__device__ __forceinline__ int scan_lens(const CacheAttendArgs& a, int* first, int* lens, int* sums, F units_of) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int carry = 0;
+  int carry = 0, filled = 0;
   for (int s0 = 0; s0 < a.S; s0 += THREADS) {
     const int s = s0 + threadIdx.x;
     int x = 0;
@@ -541,7 +542,7 @@ __device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, 
       if (lane >= o) y += z;
     }
     if (lane == 31) sums[warp] = y;
-    __syncthreads();
+    filled += __syncthreads_count(x > 0);
     int before = carry, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
@@ -550,10 +551,10 @@ __device__ __forceinline__ void scan_lens(const CacheAttendArgs& a, int* first, 
     }
     if (s < a.S) first[s] = before + y - x;
     carry += total;
+    if (s0 + THREADS >= a.S && threadIdx.x == 0) first[a.S] = carry;
     __syncthreads();
   }
-  if (threadIdx.x == 0) first[a.S] = carry;
-  __syncthreads();
+  return filled;
 }
 
 // The sequence that unit u (of H per entry of first) belongs to: the last one
@@ -591,11 +592,22 @@ __device__ __forceinline__ float* part_of(const CacheAttendArgs& a, int slot) {
 
 constexpr int kShort = 4;        // tiles of a segment that one warp takes alone
 constexpr int kInlineParts = 6;  // partial results that the last block to arrive joins itself
+constexpr int kWaste = 24;       // tiles a block may take beyond an even share to keep to one segment
 
-// Blocks walk the line of units (sf_cache_index.h).  The 8 warps of a block
-// take the tiles of a segment in turn, or, where the next segments are whole
-// and short, one segment each.  A segment cut over few blocks is joined by the
-// last of them to finish, one cut over many by the join kernel.
+// The work is cut over the blocks in one of two ways, by the batch's lengths.
+//
+// Chunks: where there is a block for every segment, every segment is cut into
+// chunks of the same number of tiles, the smallest that gives at most one chunk
+// per block.  A block has one segment, loads one query, joins once.
+//
+// Line: otherwise, or where chunks would leave blocks idle for more than
+// kWaste tiles' time (what a second segment in a block costs, about 5,000
+// cycles), blocks walk equal parts of the line of units (sf_cache_index.h).
+//
+// The 8 warps of a block take the tiles of a segment in turn, or, where the
+// next segments of a line are whole and short, one segment each.  A segment cut
+// over few blocks is joined by the last of them to finish, one cut over many by
+// the join kernel.
 template <typename T, int HD, int NT, bool TRACK>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(const __grid_constant__ CacheAttendArgs a) {
   using Warp = typename WarpOf<T, HD, NT>::type;
@@ -609,33 +621,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   __shared__ __align__(16) float sq[F32 ? kWarps : 1][F32 ? NH * HD : 4];
   int* first = reinterpret_cast<int*>(smem + kWarps * Warp::kBytes);
   int* lens = first + a.S + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blk = blockIdx.x;
   unsigned char* mine = smem + warp * Warp::kBytes;
   float* my_out = reinterpret_cast<float*>(mine);
+  const int H = a.heads;
   pdl_wait();
   pdl_trigger();
-  scan_lens<kThreads>(a, first, lens, sums, [](int len) { return tiles_of(len); });
-  const int G = a.nq / a.nkv, nsub = (G + NH - 1) / NH, H = a.nkv * nsub;
+  const int filled = scan_lens<kThreads>(a, first, lens, sums, [](int len) { return tiles_of(len); });
+  if (a.join && threadIdx.x == 0) a.joins[blk].n = 0;
   // empty sequences have no units: zeros
-  for (int s = blockIdx.x; s < a.S; s += gridDim.x)
-    if (first[s + 1] == first[s])
-      for (int i = threadIdx.x; i < a.nq * HD / 4; i += kThreads)
-        store4<T>(static_cast<T*>(a.out) + (int64_t)s * a.ld_out + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+  if (filled < a.S)
+    for (int s = blk; s < a.S; s += gridDim.x)
+      if (first[s + 1] == first[s])
+        for (int i = threadIdx.x; i < a.nq * HD / 4; i += kThreads)
+          store4<T>(static_cast<T*>(a.out) + (int64_t)s * a.ld_out + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   const int64_t units = (int64_t)first[a.S] * H;
-  const int64_t per = units_per_block(units, gridDim.x, a.least);
-  int64_t u = (int64_t)blockIdx.x * per;
-  const int64_t u_end = u + per < units ? u + per : units;
-  if (a.join && threadIdx.x == 0) a.joins[blockIdx.x].n = 0;
-  if (u >= u_end) return;
-  int s = find_sequence(first, a.S, u, H);
-  auto segment = [&](int ss, int hs) {
+  if (units == 0) return;
+  const int64_t share = units_per_block(units, gridDim.x, a.least);
+
+  auto segment = [&](int s, int hs) {
     Segment g;
-    g.s = ss;
-    g.kvh = hs / nsub;
-    const int sub = hs % nsub;
-    g.h0 = g.kvh * G + sub * NH;
-    g.nh = min(NH, G - sub * NH);
-    g.len = lens[ss];
+    g.s = s;
+    g.kvh = a.nsub == 1 ? hs : hs / a.nsub;
+    const int sub = hs - g.kvh * a.nsub;
+    g.h0 = g.kvh * a.group + sub * NH;
+    g.nh = min(NH, a.group - sub * NH);
+    g.len = lens[s];
     return g;
   };
   auto load_q = [&](const Segment& g, float* to, int i0, int step) {
@@ -645,58 +656,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
     }
   };
   Warp w;
-  while (u < u_end) {
-    const int tiles = first[s + 1] - first[s];
-    const int in_s = (int)(u - (int64_t)first[s] * H);
-    const int hs = (unsigned)in_s / (unsigned)tiles, t0 = in_s - hs * tiles;
-    // ---- short whole segments: a warp each
-    if (t0 == 0 && tiles <= kShort) {
-      int n = 0, my_s = -1, my_hs = 0;
-      int64_t v = u;
-      int cs = s, ch = hs;
-      while (n < kWarps && v < u_end) {
-        const int ct = first[cs + 1] - first[cs];
-        if (ct > kShort || v + ct > u_end) break;
-        if (n == warp) {
-          my_s = cs;
-          my_hs = ch;
-        }
-        ++n;
-        v += ct;
-        if (++ch == H) {
-          ch = 0;
-          do ++cs;
-          while (cs < a.S && first[cs + 1] == first[cs]);
-        }
-      }
-      if (n > 1) {
-        if (my_s >= 0) {
-          const Segment g = segment(my_s, my_hs);
-          float* q = sq[F32 ? warp : 0];
-          auto queries = [&]() {
-            load_q(g, q, lane, 32);
-            __syncwarp();
-          };
-          w.template run<TRACK>(a, g, mine, q, queries, 0, 1, tiles_of(g.len), lane);
-          __syncwarp();
-          w.store(my_out, sml[warp], lane);
-          __syncwarp();
-          for (int i = lane; i < g.nh * HD / 4; i += 32) {
-            const int h = i / (HD / 4), d = i % (HD / 4) * 4;
-            write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
-                         sml[warp][h].y);
-          }
-          if (TRACK && lane < g.nh) write_lse(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
-        }
-        __syncthreads();  // the warps' memory is free again
-        u = v;
-        s = cs;
-        continue;
-      }
-    }
-    // ---- one segment by all warps
-    const int end = (int)(u_end - u < tiles - t0 ? u_end - u : tiles - t0) + t0;
-    const Segment g = segment(s, hs);
+
+  // Tiles [t0, end) of a segment by all warps; the segment lies in n blocks from b0 on, whose partial results are
+  // in slots `slot0`, 2 (b0 + 1), 2 (b0 + 2), ...; this block's is `slot`.
+  auto take = [&](const Segment& g, int t0, int end, int n, int b0, int slot0, int slot) {
     auto queries = [&]() {
       load_q(g, sq[0], threadIdx.x, kThreads);
       __syncthreads();
@@ -705,9 +668,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
     __syncwarp();
     w.store(my_out, sml[warp], lane);
     __syncthreads();
-    const int64_t seg0 = (int64_t)first[s] * H + (int64_t)hs * tiles;
-    const int b0 = first_block(seg0, per), b1 = last_block(seg0, tiles, per), n = b1 - b0 + 1;
-    float* part = part_of<NH, HD>(a, part_slot(blockIdx.x, seg0, per));
+    float* part = part_of<NH, HD>(a, slot);
     if (threadIdx.x < kWarps * NH) {
       const int x = threadIdx.x / NH, h = threadIdx.x % NH;
       float top = sml[0][h].x;
@@ -751,8 +712,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
         write_out<T>(a, g.s, g.h0 + h, HD, d, o, l);
     }
     if (n > kInlineParts) {
-      if (blockIdx.x == b0 && threadIdx.x == 0)
-        a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, part_slot(b0, seg0, per)};
+      if (blk == b0 && threadIdx.x == 0) a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, slot0};
     } else if (n > 1) {
       // the last block to arrive joins the parts, in block order
       __syncthreads();
@@ -771,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           for (int x = 0; x < kInlineParts; ++x) {
             pm[x] = -INFINITY;
             if (x < n) {
-              const float* p = part_of<NH, HD>(a, part_slot(b0 + x, seg0, per));
+              const float* p = part_of<NH, HD>(a, x ? 2 * (b0 + x) : slot0);
               y[x] = __ldcg(reinterpret_cast<const float4*>(p + h * HD + d));
               pm[x] = __ldcg(p + NH * HD + h);
               pl[x] = __ldcg(p + NH * HD + NH + h);
@@ -797,12 +757,114 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
         }
       }
     }
-    __syncthreads();  // the warps' memory and tables are free for the next segment
-    u += end - t0;
-    if (end == tiles && hs + 1 == H) {
+  };
+
+  // ---- chunks.  Every warp works the plan out for itself (no barrier).
+  if ((int64_t)filled * H <= gridDim.x && a.S <= kThreads) {
+    int size = (int)share, chunks = 0;
+    for (int i = 0; i < 4; ++i) {
+      chunks = 0;
+      for (int s0 = 0; s0 < a.S; s0 += 32) {
+        const int s = s0 + lane, t = s < a.S ? first[s + 1] - first[s] : 0;
+        chunks += __reduce_add_sync(kFull, ((unsigned)t + size - 1) / (unsigned)size);
+      }
+      if (chunks * H <= (int)gridDim.x) break;
+      size += (int)quotient((int64_t)size * (chunks * H - (int)gridDim.x), gridDim.x) + 1;
+    }
+    if (chunks * H <= (int)gridDim.x && size <= share + kWaste) {
+      if (blk >= chunks * H) return;
+      int before = 0;  // chunks of the sequences in front
+      for (int s0 = 0;; s0 += 32) {
+        const int s = s0 + lane, t = s < a.S ? first[s + 1] - first[s] : 0;
+        const int c = ((unsigned)t + size - 1) / (unsigned)size;
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int z = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += z;
+        }
+        const unsigned hit = __ballot_sync(kFull, blk < (before + incl) * H);
+        if (hit) {
+          const int l = __ffs(hit) - 1, n = __shfl_sync(kFull, c, l);
+          const int r = blk - (before + __shfl_sync(kFull, incl, l) - n) * H;
+          const int hs = (unsigned)r / (unsigned)n, x = r - hs * n, tiles = __shfl_sync(kFull, t, l);
+          take(segment(s0 + l, hs), x * size, min(tiles, (x + 1) * size), n, blk - x, 2 * (blk - x), 2 * blk);
+          return;
+        }
+        before += __shfl_sync(kFull, incl, 31);
+      }
+    }
+  }
+
+  // ---- line
+  int64_t u = blk * share;
+  const int64_t u_end = u + share < units ? u + share : units;
+  if (u >= u_end) return;
+  int s = find_sequence(first, a.S, u, H), hs, t0;
+  {
+    const int in_s = (int)(u - (int64_t)first[s] * H), tiles = first[s + 1] - first[s];
+    hs = (unsigned)in_s / (unsigned)tiles;
+    t0 = in_s - hs * tiles;
+  }
+  auto advance = [&](int& s, int& hs) {  // to the next segment
+    if (++hs == H) {
+      hs = 0;
       do ++s;
       while (s < a.S && first[s + 1] == first[s]);
     }
+  };
+  while (u < u_end) {
+    const int tiles = first[s + 1] - first[s];
+    // short whole segments: a warp each
+    if (t0 == 0 && tiles <= kShort) {
+      int n = 0, my_s = -1, my_hs = 0;
+      int64_t v = u;
+      int cs = s, ch = hs;
+      while (n < kWarps && v < u_end) {
+        const int ct = first[cs + 1] - first[cs];
+        if (ct > kShort || v + ct > u_end) break;
+        if (n == warp) {
+          my_s = cs;
+          my_hs = ch;
+        }
+        ++n;
+        v += ct;
+        advance(cs, ch);
+      }
+      if (n > 1) {
+        if (my_s >= 0) {
+          const Segment g = segment(my_s, my_hs);
+          float* q = sq[F32 ? warp : 0];
+          auto queries = [&]() {
+            load_q(g, q, lane, 32);
+            __syncwarp();
+          };
+          w.template run<TRACK>(a, g, mine, q, queries, 0, 1, tiles_of(g.len), lane);
+          __syncwarp();
+          w.store(my_out, sml[warp], lane);
+          __syncwarp();
+          for (int i = lane; i < g.nh * HD / 4; i += 32) {
+            const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+            write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
+                         sml[warp][h].y);
+          }
+          if (TRACK && lane < g.nh) write_lse(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
+        }
+        __syncthreads();  // the warps' memory is free again
+        u = v;
+        s = cs;
+        hs = ch;
+        continue;
+      }
+    }
+    const int64_t seg0 = u - t0;
+    const int end = u_end - u < tiles - t0 ? t0 + (int)(u_end - u) : tiles;
+    const int b0 = t0 == 0 ? blk : first_block(seg0, share), b1 = end == tiles ? blk : last_block(seg0, tiles, share);
+    take(segment(s, hs), t0, end, b1 - b0 + 1, b0, part_slot(b0, seg0, share), part_slot(blk, seg0, share));
+    __syncthreads();  // the warps' memory and tables are free for the next segment
+    u += end - t0;
+    t0 = 0;
+    advance(s, hs);
   }
 }
 
@@ -923,8 +985,11 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   constexpr int NH = WarpOf<T, HD, NT>::type::kHeads;
   const int G = a.nq / a.nkv, longest = tiles_of((int)a.limit);
   a.least = kLeast;
+  a.group = G;
+  a.nsub = (G + NH - 1) / NH;
+  a.heads = a.nkv * a.nsub;
   // no more blocks than the longest batch of this table could keep busy
-  const int64_t want = ((int64_t)a.S * a.nkv * ((G + NH - 1) / NH) * longest + a.least - 1) / a.least;
+  const int64_t want = ((int64_t)a.S * a.heads * longest + a.least - 1) / a.least;
   const int blocks = (int)(want < most_blocks ? want : most_blocks);
   // a segment lies in at most (longest - 1) / least + 2 blocks
   a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks > kInlineParts;
