@@ -94,7 +94,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out);
  *            row's K and V are not stored.
  *   pos      device int32 [T]: rotary position, which after an eviction is
  *            further on than the place; NULL = index.  A row whose position is
- *            negative is padding: nothing of it is read or written.
+ *            negative is padding: nothing of it is written.
  *   seq      device int32 [T]: the row's sequence; NULL = row t belongs to
  *            sequence t (one new token each; T <= S).
  *   q_out    device [T] rows of n_q_heads * head_dim elements, ld_q apart; may
@@ -106,7 +106,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out);
  * 16 bytes, the gains 16-byte aligned, the int32 arrays 4-byte.
  * Errors (before anything is enqueued): SF_ERR_INVALID_ARG (null, misaligned
  * or overlapping-by-stride argument, another device is current), SF_ERR_SHAPE
- * (S beyond max_seqs, T above 16777216, T > S without seq),
+ * (S beyond max_seqs, T above 1048576, T > S without seq),
  * SF_ERR_DEVICE_ASSERT (an earlier check fired), SF_ERR_CUDA. */
 sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_t ld_qkv, int T, const float* q_gain,
                           const float* k_gain, const int32_t* index, const int32_t* pos, const int32_t* seq,

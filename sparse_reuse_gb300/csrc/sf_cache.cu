@@ -10,25 +10,93 @@
 namespace sf {
 namespace {
 
-// Rotary table, angles and functions in double: far positions (10^5 radians
-// and more) lose the angle in fp32.
-__global__ void rope_table_kernel(float2* out, int max_pos, int half, double theta) {
+// Rotary table [max_pos][cos half | sin half], angles and functions in double:
+// far positions (10^5 radians and more) lose the angle in fp32.
+__global__ void rope_table_kernel(float* out, int max_pos, int half, double theta) {
   const int64_t n = (int64_t)max_pos * half;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int j = (int)(i % half);
-    const double a = (double)(i / half) * pow(theta, -(double)j / half);
+    const int64_t pos = i / half;
+    const double a = (double)pos * pow(theta, -(double)j / half);
     double sn, cs;
     sincos(a, &sn, &cs);
-    out[i] = make_float2((float)cs, (float)sn);
+    out[pos * 2 * half + j] = (float)cs;
+    out[pos * 2 * half + half + j] = (float)sn;
   }
 }
 
-template <typename T, int N>
-struct alignas(16) Vec {
-  T v[N];
+// Two fp32 values in a register pair: sm_100's packed arithmetic does both in
+// one instruction, each rounded as the scalar one.
+struct Two {
+  unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// 16 bytes of a row as pairs of fp32, and back.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  static constexpr int PAIRS = 2;
+  static __device__ __forceinline__ void load(const uint4& u, Two (&x)[2]) {
+    x[0] = two(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = two(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ uint4 store(const Two (&x)[2]) {
+    const float2 a = both(x[0]), b = both(x[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int PAIRS = 4;
+  static __device__ __forceinline__ void load(const uint4& u, Two (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 store(const Two (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = both(x[i]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 
-constexpr int kAppendThreads = 128;
+template <int PAIRS>
+__device__ __forceinline__ void load_pairs(const float* p, Two (&x)[PAIRS]) {
+#pragma unroll
+  for (int i = 0; i < PAIRS / 2; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+    x[2 * i] = two(v.x, v.y);
+    x[2 * i + 1] = two(v.z, v.w);
+  }
+}
+
+constexpr int kAppendThreads = 64;
 constexpr int kAppendHeads = 2;
 constexpr int kAppendWide = 4096;  // (lane, head) pairs per SM from which a group takes several heads
 
@@ -39,26 +107,25 @@ constexpr int kAppendWide = 4096;  // (lane, head) pairs per SM from which a gro
 // keep 2 HPT loads in flight and share the row's angles and its page lookup.
 template <typename T, int HD, int HPT>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
-  constexpr int VEC = 16 / sizeof(T), LANES = HD / 2 / VEC, GROUPS = kAppendThreads / LANES;
-  using V = Vec<T, VEC>;
+  using P = Piece<T>;
+  constexpr int N = P::PAIRS, VEC = 2 * N, LANES = HD / 2 / VEC, GROUPS = kAppendThreads / LANES;
   pdl_wait();
   pdl_trigger();
-  const int NH = a.nq + 2 * a.nkv, NB = (NH + HPT - 1) / HPT;
-  // items (row, head block) in order; the block's first one in 64 bits, the rest in 32
-  const int64_t base = (int64_t)blockIdx.x * GROUPS;
-  const int base_t = (int)(base / NB), item = (int)(base - (int64_t)base_t * NB) + (int)threadIdx.x / LANES;
+  const int NH = a.nq + 2 * a.nkv;
+  const unsigned NB = (NH + HPT - 1) / HPT;
+  const unsigned item = blockIdx.x * GROUPS + threadIdx.x / LANES;  // (row, head block); T * NB < 2^31
   const int lane = threadIdx.x % LANES;
-  const int t = base_t + item / NB, h0 = item % NB * HPT;
+  const int t = item / NB, h0 = (item - t * NB) * HPT;
   if (t >= a.T) return;  // whole groups: the shuffles below stay inside a group
   const unsigned mask = (LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u)) << ((threadIdx.x & 31) / LANES * LANES);
   // the row itself first: it waits for nothing, its place and angles arrive meanwhile
-  const T* src = static_cast<const T*>(a.qkv) + (int64_t)t * a.ld_qkv + (int64_t)h0 * HD + lane * VEC;
-  V lo[HPT], hi[HPT];
+  const T* src = static_cast<const T*>(a.qkv) + t * a.ld_qkv + h0 * HD + lane * VEC;
+  uint4 lo[HPT], hi[HPT];
 #pragma unroll
   for (int i = 0; i < HPT; ++i)
     if (h0 + i < NH) {
-      lo[i] = *reinterpret_cast<const V*>(src + i * HD);
-      hi[i] = *reinterpret_cast<const V*>(src + i * HD + HD / 2);
+      lo[i] = *reinterpret_cast<const uint4*>(src + i * HD);
+      hi[i] = *reinterpret_cast<const uint4*>(src + i * HD + HD / 2);
     }
   const int idx = a.index[t];
   const int pos = a.pos ? a.pos[t] : idx;
@@ -67,15 +134,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     if (lane == 0) cache_error(a.err, kCacheBadRow);
     return;
   }
-  float2 cs[VEC];
+  Two cs[N], sn[N];
   if (h0 < a.nq + a.nkv) {
-    const float4* p = reinterpret_cast<const float4*>(a.rope + (int64_t)pos * (HD / 2) + lane * VEC);
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      const float4 x = p[i];
-      cs[2 * i] = make_float2(x.x, x.y);
-      cs[2 * i + 1] = make_float2(x.z, x.w);
-    }
+    const float* p = a.rope + (int64_t)pos * HD + lane * VEC;
+    load_pairs(p, cs);
+    load_pairs(p + HD / 2, sn);
   }
   int64_t slot = -1;
   if (h0 + HPT > a.nq && idx >= 0) {
@@ -93,7 +156,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     if (head >= NH || (head >= a.nq && slot < 0)) break;  // the rest are keys and values too
     T* dst;
     if (head < a.nq)
-      dst = static_cast<T*>(a.q_out) + (int64_t)t * a.ld_q + (int64_t)head * HD;
+      dst = static_cast<T*>(a.q_out) + t * a.ld_q + head * HD;
     else if (head < a.nq + a.nkv)
       dst = static_cast<T*>(a.k) + (slot * a.nkv + (head - a.nq)) * HD;
     else
@@ -101,42 +164,41 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     dst += lane * VEC;
     if (head < a.nq + a.nkv) {
       const float* gain = head < a.nq ? a.q_gain : a.k_gain;
-      float x[VEC], y[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[e] = to_f32<T>(lo[i].v[e]);
-        y[e] = to_f32<T>(hi[i].v[e]);
-      }
+      Two x[N], y[N];
+      P::load(lo[i], x);
+      P::load(hi[i], y);
       if (gain) {
-        float ss = 0.f;
+        Two s2 = x[0] * x[0];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss += x[e] * x[e] + y[e] * y[e];
+        for (int e = 1; e < N; ++e) s2 = fma2(x[e], x[e], s2);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s2 = fma2(y[e], y[e], s2);
+        float ss = both(s2).x + both(s2).y;
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float r = 1.f / sqrtf(ss / (float)HD + a.eps);
-        const float4* gl = reinterpret_cast<const float4*>(gain + lane * VEC);
-        const float4* gh = reinterpret_cast<const float4*>(gain + HD / 2 + lane * VEC);
+        const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+        const Two rr = two(r, r);
+        Two gl[N], gh[N];
+        load_pairs(gain + lane * VEC, gl);
+        load_pairs(gain + HD / 2 + lane * VEC, gh);
 #pragma unroll
-        for (int e = 0; e < VEC / 4; ++e) {
-          const float4 u = gl[e], w = gh[e];
-          x[4 * e] *= r * u.x;
-          x[4 * e + 1] *= r * u.y;
-          x[4 * e + 2] *= r * u.z;
-          x[4 * e + 3] *= r * u.w;
-          y[4 * e] *= r * w.x;
-          y[4 * e + 1] *= r * w.y;
-          y[4 * e + 2] *= r * w.z;
-          y[4 * e + 3] *= r * w.w;
+        for (int e = 0; e < N; ++e) {
+          x[e] = x[e] * rr * gl[e];
+          y[e] = y[e] * rr * gh[e];
         }
       }
+      const Two minus = two(-1.f, -1.f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        lo[i].v[e] = from_f32<T>(x[e] * cs[e].x - y[e] * cs[e].y);
-        hi[i].v[e] = from_f32<T>(y[e] * cs[e].x + x[e] * cs[e].y);
+      for (int e = 0; e < N; ++e) {
+        const Two u = x[e], w = y[e];
+        x[e] = fma2(w * minus, sn[e], u * cs[e]);
+        y[e] = fma2(u, sn[e], w * cs[e]);
       }
+      lo[i] = P::store(x);
+      hi[i] = P::store(y);
     }
-    *reinterpret_cast<V*>(dst) = lo[i];
-    *reinterpret_cast<V*>(dst + HD / 2) = hi[i];
+    *reinterpret_cast<uint4*>(dst) = lo[i];
+    *reinterpret_cast<uint4*>(dst + HD / 2) = hi[i];
   }
 }
 
@@ -254,7 +316,7 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
   const int blocks = cache_attend_blocks(c->sm_count);
-  if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * (s.head_dim / 2) * sizeof(float2));
+  if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * s.head_dim * sizeof(float));
   if (e == cudaSuccess && s.track_weights)
     e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * scores_ld(s) * sizeof(float));
   if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
@@ -300,7 +362,7 @@ sf_status sf_cache_append(sf_cache* c, void* stream, const void* qkv, int64_t ld
   const int64_t wq = (int64_t)s.n_q_heads * s.head_dim, w = wq + 2 * (int64_t)s.n_kv_heads * s.head_dim;
   if (bad_row(c, qkv, ld_qkv, w, T) || bad_row(c, q_out, ld_q, wq, T))
     return fail(c, SF_ERR_INVALID_ARG, "qkv/q_out null, misaligned, or rows closer than their width");
-  if (T > 16777216 || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
+  if (T > 1048576 || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
   if ((st = check_object(c)) != SF_OK) return st;
   CacheAppendArgs a{};
   a.qkv = qkv;

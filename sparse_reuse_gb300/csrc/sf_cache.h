@@ -21,7 +21,7 @@ struct sf_cache {
   sf_cache_shapes s{};
   int device = 0;
   int sm_count = 148;
-  float2* rope = nullptr;     // [max_pos][head_dim / 2] (cos, sin)
+  float* rope = nullptr;      // [max_pos][cos half | sin half]
   float* scores = nullptr;    // [max_seqs][n_q_heads][max_len, padded to 4] scaled scores in log2 units (track_weights)
   float* lse = nullptr;       // [max_seqs][n_q_heads] log2 of each softmax denominator (track_weights)
   float* parts = nullptr;     // partial results of sf_cache_attend, two per block
@@ -50,7 +50,7 @@ struct CacheAppendArgs {
   const int32_t* index; const int32_t* pos; const int32_t* seq;
   PageTable table;
   void* k; void* v;
-  const float2* rope;
+  const float* rope;
   int T, S, nq, nkv, hd, max_pos;
   int64_t limit;   // positions a sequence may have
   float eps;

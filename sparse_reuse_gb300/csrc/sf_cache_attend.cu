@@ -590,8 +590,56 @@ __device__ __forceinline__ float* part_of(const CacheAttendArgs& a, int slot) {
   return a.parts + (int64_t)slot * NH * (HD + 2);
 }
 
+// Running sum of partial results: 4 dimensions of one head.
+constexpr int kPartLoads = 8;  // parts whose loads are in flight together
+
+struct PartSum {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY, l = 0.f;
+
+  __device__ __forceinline__ void scale(float to) {
+    const float f = part_factor(top, to);
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    l *= f;
+    top = to;
+  }
+  __device__ __forceinline__ void add_one(float4 y, float m, float ly) {
+    const float f = part_factor(m, top);
+    o.x += y.x * f;
+    o.y += y.y * f;
+    o.z += y.z * f;
+    o.w += y.w * f;
+    l += ly * f;
+  }
+  // The first min(n, LOADS) of the parts slot(0), slot(1), ...
+  template <int NH, int HD, int LOADS, typename F>
+  __device__ __forceinline__ void add(const CacheAttendArgs& a, int h, int d, int n, F slot) {
+    float4 y[LOADS];
+    float m[LOADS], ly[LOADS], to = top;
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) {
+      m[x] = -INFINITY;
+      if (x < n) {
+        const float* p = part_of<NH, HD>(a, slot(x));
+        y[x] = __ldcg(reinterpret_cast<const float4*>(p + h * HD + d));
+        m[x] = __ldcg(p + NH * HD + h);
+        ly[x] = __ldcg(p + NH * HD + NH + h);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) to = fmaxf(to, m[x]);
+    scale(to);
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x)
+      if (x < n) add_one(y[x], m[x], ly[x]);
+  }
+};
+
 constexpr int kShort = 4;        // tiles of a segment that one warp takes alone
-constexpr int kInlineParts = 6;  // partial results that the last block to arrive joins itself
+constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself
 constexpr int kWaste = 24;       // tiles a block may take beyond an even share to keep to one segment
 
 // The work is cut over the blocks in one of two ways, by the batch's lengths.
@@ -725,33 +773,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       if (s_last) {
         for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
           const int h = i / (HD / 4), d = i % (HD / 4) * 4;
-          float4 y[kInlineParts];
-          float pm[kInlineParts], pl[kInlineParts];
-#pragma unroll
-          for (int x = 0; x < kInlineParts; ++x) {
-            pm[x] = -INFINITY;
-            if (x < n) {
-              const float* p = part_of<NH, HD>(a, x ? 2 * (b0 + x) : slot0);
-              y[x] = __ldcg(reinterpret_cast<const float4*>(p + h * HD + d));
-              pm[x] = __ldcg(p + NH * HD + h);
-              pl[x] = __ldcg(p + NH * HD + NH + h);
-            }
-          }
-          float top = pm[0];
-#pragma unroll
-          for (int x = 1; x < kInlineParts; ++x) top = fmaxf(top, pm[x]);
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          float l = 0.f;
-#pragma unroll
-          for (int x = 0; x < kInlineParts; ++x)
-            if (x < n) {
-              const float f = part_factor(pm[x], top);
-              o.x += y[x].x * f;
-              o.y += y[x].y * f;
-              o.z += y[x].z * f;
-              o.w += y[x].w * f;
-              l += pl[x] * f;
-            }
+          PartSum sum;
+          if (n <= 4)
+            sum.add<NH, HD, 4>(a, h, d, n, [&](int x) { return x ? 2 * (b0 + x) : slot0; });
+          else
+            for (int x0 = 0; x0 < n; x0 += kPartLoads)
+              sum.add<NH, HD, kPartLoads>(a, h, d, n - x0, [&](int x) { return x0 + x ? 2 * (b0 + x0 + x) : slot0; });
+          const float4 o = sum.o;
+          const float top = sum.top, l = sum.l;
           write_out<T>(a, g.s, g.h0 + h, HD, d, o, l);
           if (TRACK && d == 0) write_lse(a, g.s, g.h0 + h, top, l);
         }
@@ -869,67 +898,39 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
 }
 
 // Joins a segment cut over more than kInlineParts blocks: a block per (its
-// first block, head), the parts dealt over kJoinGroups groups of threads.
+// first block, head), the parts dealt over groups of HD / 4 threads.
 constexpr int kJoinThreads = 256;
 constexpr int kMaxBlocks = 512;  // of the attention kernel
 
 template <typename T, int HD, int NH>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttendArgs a) {
   constexpr int COLS = HD / 4, GROUPS = kJoinThreads / COLS;
-  __shared__ float fac[kMaxBlocks];
-  __shared__ float red[2][kJoinThreads / 32];
-  __shared__ __align__(16) float4 acc[GROUPS][COLS];
+  __shared__ float4 acc[GROUPS][COLS];
+  __shared__ float2 ml[GROUPS];
   pdl_wait();
   pdl_trigger();
   const CacheJoin j = a.joins[blockIdx.x];
   const int h = blockIdx.y;
   if (h >= j.nh || j.n == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto part = [&](int x) { return part_of<NH, HD>(a, x ? 2 * ((int)blockIdx.x + x) : j.first); };
-  const int g = threadIdx.x / COLS, d = threadIdx.x % COLS * 4;
-  float m = -INFINITY, l = 0.f;
-  for (int x = threadIdx.x; x < j.n; x += kJoinThreads) m = fmaxf(m, part(x)[NH * HD + h]);
-  float top = warp_max(m);
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  top = red[0][0];
-#pragma unroll
-  for (int i = 1; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[0][i]);
-  for (int x = threadIdx.x; x < j.n; x += kJoinThreads) {
-    const float* p = part(x) + NH * HD + h;
-    const float f = part_factor(p[0], top);
-    fac[x] = f;
-    l += p[NH] * f;
-  }
-  l = warp_sum(l);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int x = g; x < j.n; x += GROUPS) {
-    const float4 y = *reinterpret_cast<const float4*>(part(x) + h * HD + d);
-    const float fx = fac[x];
-    o.x += y.x * fx;
-    o.y += y.y * fx;
-    o.z += y.z * fx;
-    o.w += y.w * fx;
-  }
-  acc[g][threadIdx.x % COLS] = o;
+  const int g = threadIdx.x / COLS, col = threadIdx.x % COLS;
+  PartSum sum;
+  for (int x0 = g; x0 < j.n; x0 += GROUPS * kPartLoads)
+    sum.add<NH, HD, kPartLoads>(a, h, 4 * col, (j.n - x0 + GROUPS - 1) / GROUPS, [&](int x) {
+      const int p = x0 + x * GROUPS;
+      return p ? 2 * ((int)blockIdx.x + p) : j.first;
+    });
+  acc[g][col] = sum.o;
+  if (col == 0) ml[g] = make_float2(sum.top, sum.l);
   __syncthreads();
   if (g == 0) {
-    l = 0.f;
+    float to = ml[0].x;
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[1][i];
+    for (int i = 1; i < GROUPS; ++i) to = fmaxf(to, ml[i].x);
+    sum.scale(to);
 #pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-      const float4 y = acc[i][threadIdx.x];
-      o.x += y.x;
-      o.y += y.y;
-      o.z += y.z;
-      o.w += y.w;
-    }
-    write_out<T>(a, j.s, j.h0 + h, HD, d, o, l);
-    if (a.w_out && threadIdx.x == 0) write_lse(a, j.s, j.h0 + h, top, l);
+    for (int i = 1; i < GROUPS; ++i) sum.add_one(acc[i][col], ml[i].x, ml[i].y);
+    write_out<T>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, sum.l);
+    if (a.w_out && col == 0) write_lse(a, j.s, j.h0 + h, sum.top, sum.l);
   }
 }
 
@@ -991,8 +992,9 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   // no more blocks than the longest batch of this table could keep busy
   const int64_t want = ((int64_t)a.S * a.heads * longest + a.least - 1) / a.least;
   const int blocks = (int)(want < most_blocks ? want : most_blocks);
-  // a segment lies in at most (longest - 1) / least + 2 blocks
-  a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks > kInlineParts;
+  // a segment of t tiles has at least 1 / heads of all units: it lies in at most blocks / heads + 2 blocks, and in
+  // (t - 1) / least + 2
+  a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks / a.heads + 2 > kInlineParts;
   const size_t table = (2 * (size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
   cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
                              a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);

@@ -215,7 +215,7 @@ EVICT = dict(k=16, v=32, n_pages=9, page_table=16, S=4, cols=4, ld_table=4, lens
     ("append", APPEND, dict(v=40), 1, "pool"), ("append", APPEND, dict(page_table=17), 1, "table"),
     ("append", APPEND, dict(cols=0), 1, "table_cols"), ("append", APPEND, dict(ld_table=3), 1, "ld_table"),
     ("append", APPEND, dict(n_pages=0), 1, "n_pages"), ("append", APPEND, dict(S=5), 2, "S=5"),
-    ("append", APPEND, dict(seq=None, T=5), 2, "T=5"), ("append", APPEND, dict(T=16777217), 2, "T=16777217"),
+    ("append", APPEND, dict(seq=None, T=5), 2, "T=5"), ("append", APPEND, dict(T=1048577), 2, "T=1048577"),
     ("append", APPEND, dict(k=32), 1, "one pool"),
     ("attend", ATTEND, dict(q=8), 1, "q/out"), ("attend", ATTEND, dict(ld_out=255), 1, "q/out"),
     ("attend", ATTEND, dict(lens=None), 1, "lens"), ("attend", ATTEND, dict(scale=float("nan")), 1, "scale"),
