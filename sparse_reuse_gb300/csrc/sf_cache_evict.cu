@@ -34,43 +34,61 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void red_cluster_add(uint32_t addr, unsigned v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned atom_cluster_add(uint32_t addr, unsigned v) {
+  unsigned old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+  return old;
 }
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 4 * kSelThreads;  // 2^11
+constexpr int kBinBits = 11;
 constexpr int kList = 256;              // keys that are ranked by comparing all pairs
+constexpr int kSelLoads = 8;            // keys a thread handles together
+constexpr int kSelWords = 4;            // words of a bitmap a warp handles together
 constexpr int kSelCap = 32768;          // weights a block holds at most
 static_assert(kSelCap / 32 <= 2 * kSelThreads, "two words of a bitmap a thread");
 
-// A cluster of `cl` blocks per (sequence, KV head); block r holds the keys
-// of the r-th part of the weights in shared memory.
+// First cut: 2^20 keys a bin from that of 0.0 on, eight bins for every factor
+// of two; smaller keys count as the lowest bin.
+constexpr uint32_t kFirstKey = 0x80000000u;
+constexpr int kFirstShift = 20;
+static_assert((0xff800000u - kFirstKey) >> kFirstShift < (uint32_t)kBins, "bins to +inf");
+
+// A cluster of `cl` blocks per (sequence, KV head); block r holds the keys of
+// the r-th part of the weights in shared memory.
 //
-// The need-th largest candidate key is found by narrowing [lo, hi]: the range
-// is cut into at most kBins equal bins (keys of positive floats are piecewise
-// logarithmic, so weights spread over many bins), and the bin that holds it is
-// the next range, three passes at most for any 32-bit keys.  The lowest bin is
-// never counted (if the others do not reach, it is the one), which keeps the
-// usual crowd of zero weights out of the shared-memory atomics.  A block that
-// is alone ranks the keys of the bin by comparison once they are few, usually
-// after one pass.
+// The need-th largest candidate key is found by counting keys into bins and
+// narrowing [lo, hi] to the bin that holds it: first with bins of a fixed size,
+// counted while the weights arrive, then, while the bin holds more than kList
+// keys, in up to kBins equal parts of it (two such passes at most).  The lowest
+// bin is never counted (if the others do not reach, it is the one), which
+// keeps the usual crowd of zero weights out of the shared-memory atomics.  The
+// keys of the last bin are ranked by comparing all pairs.
 //
 // The choice is two bitmaps, positions certainly kept and positions at the
 // threshold, of which the first `ties` are kept; a scan of their populations
 // gives every kept position its place.
 __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __grid_constant__ CacheEvictArgs a, int cl,
                                                                       int cap) {
-  extern __shared__ __align__(16) unsigned keys[];               // [cap] of this block's positions
-  unsigned* sure = keys + cap;                                   // [cap / 32] kept; later the final choice
-  unsigned* tied = sure + cap / 32;                              // [cap / 32] at the threshold; later places
+  extern __shared__ __align__(16) unsigned keys[];    // [cap] of this block's positions
+  unsigned* sure = keys + cap;                        // [cap / 32] kept; later the final choice
+  unsigned* tied = sure + cap / 32;                   // [cap / 32] at the threshold; later places
   __shared__ __align__(16) unsigned hist[kBins];
-  __shared__ unsigned red[2][32];
-  __shared__ unsigned pub[2][2];                                 // to the cluster: (min, max), then (kept, tied)
-  __shared__ unsigned found[3];                                  // bin, keys above it, keys in it
-  __shared__ uint2 list[kList];                                  // (key, position)
-  __shared__ unsigned n_list, s_ties;
+  __shared__ unsigned red[32];
+  __shared__ unsigned pub[3];                         // to the cluster: kept, tied, ties
+  __shared__ unsigned found[3];                       // bin, keys above it, keys in it (all ones: not known)
+  __shared__ __align__(16) unsigned all_key[kList];   // keys to be ranked, of the whole cluster
+  __shared__ unsigned my_key[kList];                  // those of this block
+  __shared__ int my_pos[kList];
+  __shared__ unsigned n_all, n_mine, s_ties;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x / cl, s = blockIdx.y, rank = blockIdx.x % cl;
   auto meet = [&]() {
@@ -79,9 +97,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     else
       __syncthreads();
   };
-  auto of_rank = [&](const unsigned* p, int r) {
-    return r == rank ? *p : ld_cluster_u32(tc::map_to_rank(tc::smem_u32(p), r));
-  };
+  auto remote = [&](const void* p, int r) { return tc::map_to_rank(tc::smem_u32(p), r); };
+  auto of_rank = [&](const unsigned* p, int r) { return r == rank ? *p : ld_cluster_u32(remote(p, r)); };
+  reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) n_all = n_mine = s_ties = 0u;
   pdl_wait();
   pdl_trigger();
   bool bad;
@@ -103,58 +122,40 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   // candidates, in this block's indexes
   const int lo_j = min(max(a.n_first - j0, 0), n), hi_j = max(min(len - a.n_recent - j0, n), lo_j);
   const int words = (n + 31) / 32;
-  unsigned kmin = ~0u, kmax = 0u;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    const uint32_t k = weight_key(w[j0 + i]);
-    keys[i] = k;
-    if (i >= lo_j && i < hi_j) {
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
+  meet();  // every histogram and counter of the cluster is empty
+  for (int i0 = threadIdx.x; i0 < n; i0 += kSelThreads * kSelLoads) {
+    float x[kSelLoads];
+#pragma unroll
+    for (int u = 0; u < kSelLoads; ++u) {
+      const int i = i0 + u * kSelThreads;
+      if (i < n) x[u] = w[j0 + i];
     }
-  }
-  reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x == 0) n_list = s_ties = 0u;
-  kmin = __reduce_min_sync(kFull, kmin);
-  kmax = __reduce_max_sync(kFull, kmax);
-  if (lane == 0) {
-    red[0][warp] = kmin;
-    red[1][warp] = kmax;
-  }
-  __syncthreads();
-  kmin = __reduce_min_sync(kFull, red[0][lane % kSelWarps]);
-  kmax = __reduce_max_sync(kFull, red[1][lane % kSelWarps]);
-  if (cl > 1) {
-    if (threadIdx.x == 0) {
-      pub[0][0] = kmin;
-      pub[0][1] = kmax;
-    }
-    meet();  // every weight of this head is read (w_out may be w), every histogram empty
-    for (int r = 0; r < cl; ++r) {
-      kmin = min(kmin, of_rank(&pub[0][0], r));
-      kmax = max(kmax, of_rank(&pub[0][1], r));
+#pragma unroll
+    for (int u = 0; u < kSelLoads; ++u) {
+      const int i = i0 + u * kSelThreads;
+      if (i < n) {
+        const uint32_t k = weight_key(x[u]);
+        keys[i] = k;
+        if (i >= lo_j && i < hi_j && k >= kFirstKey + (1u << kFirstShift))
+          atomicAdd(&hist[(k - kFirstKey) >> kFirstShift], 1u);
+      }
     }
   }
   int need = a.budget - a.n_first - a.n_recent;  // below the number of candidates, since budget < len
-  uint32_t lo = kmin, hi = kmax;                 // the need-th largest key lies in [lo, hi]
+  uint32_t lo = 0u, hi = 0xff800000u;            // the need-th largest key lies in [lo, hi]
+  uint32_t base = kFirstKey;                     // bins start here,
+  int shift = kFirstShift;                       // of 2^shift keys
   uint32_t thr = ~0u;                            // keys above it are kept (none is above ~0),
   int ties = 0;                                  // and the first `ties` equal to it
   bool rank_list = false;
   while (need > 0) {
-    const uint32_t range = hi - lo;
-    const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
-#pragma unroll 8
-    for (int i = lo_j + threadIdx.x; i < hi_j; i += kSelThreads) {
-      const uint32_t k = keys[i] - lo, b = k >> shift;
-      if (k <= range && b) atomicAdd(&hist[b], 1u);
-    }
     __syncthreads();
     // thread t holds bins kBins - 1 - 4 t and the three below it
     uint4* mine = reinterpret_cast<uint4*>(hist) + (kSelThreads - 1 - threadIdx.x);
     uint4 h = *mine;
     if (rank != 0) {
       const unsigned v[4] = {h.x, h.y, h.z, h.w};
-      const uint32_t to = tc::map_to_rank(tc::smem_u32(mine), 0);
+      const uint32_t to = remote(mine, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (v[i]) red_cluster_add(to + 4 * i, v[i]);
@@ -172,9 +173,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
         const unsigned y = __shfl_up_sync(kFull, sum, o);
         if (lane >= o) sum += y;
       }
-      if (lane == 31) red[0][warp] = sum;
+      if (lane == 31) red[warp] = sum;
       __syncthreads();
-      const unsigned others = lane < kSelWarps ? red[0][lane] : 0u;
+      const unsigned others = lane < kSelWarps ? red[lane] : 0u;
       unsigned at = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - (h.x + h.y + h.z + h.w);
       const unsigned total = __reduce_add_sync(kFull, others);
       const unsigned v[4] = {h.w, h.z, h.y, h.x};
@@ -187,18 +188,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
         }
         at += v[i];
       }
-      if (threadIdx.x == 0 && total < (unsigned)need) {  // the lowest bin; how many it holds is not known
+      if (threadIdx.x == 0 && total < (unsigned)need) {
         found[0] = 0u;
         found[1] = total;
         found[2] = ~0u;
       }
     }
     meet();
+    // found is written again only after everybody has come to the next pass's meeting
     const uint32_t bin = of_rank(&found[0], 0);
     const unsigned above = of_rank(&found[1], 0), inside = of_rank(&found[2], 0);
     need -= (int)above;
-    lo += bin << shift;
-    hi = min(hi, lo + ((1u << shift) - 1u));
+    hi = min(hi, base + (bin << shift) + ((1u << shift) - 1u));
+    if (bin) lo = base + (bin << shift);
     if (inside == (unsigned)need) {  // the bin's keys are the last ones needed
       thr = lo - 1;
       break;
@@ -208,48 +210,111 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
       ties = need;
       break;
     }
-    if (cl == 1 && inside <= kList) {
+    if (inside <= kList) {
       thr = hi;
       rank_list = true;
       break;
     }
-    // found is written again only after everybody has come to the next pass's meeting
-  }
-  // bitmaps; the keys still to be ranked into the list
-  for (int x = warp; x < words; x += kSelWarps) {
-    const int i = 32 * x + lane;
-    const bool in = i < n, cand = in && i >= lo_j && i < hi_j;
-    const uint32_t k = in ? keys[i] : 0u;
-    const unsigned b = __ballot_sync(kFull, (in && !cand) || (cand && k > thr));
-    const unsigned e = __ballot_sync(kFull, !rank_list && cand && k == thr);
-    if (lane == 0) {
-      sure[x] = b;
-      tied[x] = e;
-    }
-    if (rank_list && cand && k >= lo && k <= hi) list[atomicAdd(&n_list, 1u)] = make_uint2(k, i);
-  }
-  __syncthreads();
-  if (rank_list) {
-    const int m = n_list;  // <= kList: the bin's population
-    if (threadIdx.x < m) {
-      const uint2 me = list[threadIdx.x];
-      int greater = 0, equal = 0;
-      for (int x = 0; x < m; ++x) {
-        const uint32_t k = list[x].x;
-        greater += k > me.x;
-        equal += k == me.x;
+    const uint32_t range = hi - lo;
+    const int bits = 32 - __clz(range);
+    base = lo;
+    shift = bits > kBinBits ? bits - kBinBits : 0;
+    for (int w0 = lo_j + warp * 32; w0 < hi_j; w0 += kSelThreads * kSelLoads) {
+      uint32_t k[kSelLoads];
+#pragma unroll
+      for (int u = 0; u < kSelLoads; ++u) {
+        const int i = w0 + lane + u * kSelThreads;
+        k[u] = i < hi_j ? keys[i] - lo : ~0u;  // no range is that long
       }
-      const unsigned bit = 1u << (me.y & 31);
+#pragma unroll
+      for (int u = 0; u < kSelLoads; ++u) {
+        // equal weights crowd here: the lanes that share the first one's bin add once
+        const uint32_t b = k[u] <= range ? k[u] >> shift : 0u;
+        const unsigned on = __ballot_sync(kFull, b != 0u);
+        if (on == 0u) continue;
+        const unsigned same = __ballot_sync(kFull, b == __shfl_sync(kFull, b, __ffs(on) - 1));
+        if (same >> lane & 1u ? lane == __ffs(on) - 1 : b != 0u)
+          atomicAdd(&hist[b], same >> lane & 1u ? __popc(same) : 1u);
+      }
+    }
+  }
+  if (need == 0) meet();  // every key is in place (the passes met otherwise); a.w is read by everybody: w_out may be w
+  // bitmaps; the keys still to be ranked into the lists.  kSelWords words at a time, so that their latencies overlap
+  for (int x0 = warp * kSelWords; x0 < words; x0 += kSelWarps * kSelWords) {
+    uint32_t k[kSelWords];
+    unsigned hit[kSelWords], hits = 0;
+#pragma unroll
+    for (int u = 0; u < kSelWords; ++u) {
+      const int i = 32 * (x0 + u) + lane;
+      k[u] = i < n ? keys[i] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kSelWords; ++u) {
+      const int i = 32 * (x0 + u) + lane;
+      const bool cand = i >= lo_j && i < hi_j;
+      const unsigned b = __ballot_sync(kFull, (i < n && !cand) || (cand && k[u] > thr));
+      const unsigned e = __ballot_sync(kFull, cand && k[u] >= (rank_list ? lo : thr) && k[u] <= thr);
+      hit[u] = rank_list ? e : 0u;
+      hits += __popc(hit[u]);
+      if (lane == 0 && x0 + u < words) {
+        sure[x0 + u] = b;
+        tied[x0 + u] = rank_list ? 0u : e;
+      }
+    }
+    if (hits) {  // at most kList in the whole cluster: the bin's population
+      unsigned at = 0, at_all = 0;
+      if (lane == 0) {
+        at = atomicAdd(&n_mine, hits);
+        at_all = cl > 1 ? atom_cluster_add(remote(&n_all, 0), hits) : at;
+      }
+      at = __shfl_sync(kFull, at, 0);
+      at_all = __shfl_sync(kFull, at_all, 0);
+#pragma unroll
+      for (int u = 0; u < kSelWords; ++u) {
+        if (hit[u] >> lane & 1u) {
+          const unsigned below = __popc(hit[u] & ((1u << lane) - 1u));
+          my_key[at + below] = k[u];
+          my_pos[at + below] = 32 * (x0 + u) + lane;
+          if (rank == 0)
+            all_key[at_all + below] = k[u];
+          else
+            st_cluster_u32(remote(all_key + at_all + below, 0), k[u]);
+        }
+        at += __popc(hit[u]);
+        at_all += __popc(hit[u]);
+      }
+    }
+  }
+  if (rank_list) {
+    meet();
+    const int m = cl > 1 ? (int)of_rank(&n_all, 0) : (int)n_mine, mine = (int)n_mine;
+    if (rank != 0) {
+      if (threadIdx.x < m) all_key[threadIdx.x] = ld_cluster_u32(remote(all_key + threadIdx.x, 0));
+      __syncthreads();
+    }
+    if (threadIdx.x < mine) {
+      const unsigned me = my_key[threadIdx.x];
+      int greater = 0, equal = 0, x = 0;
+      for (; x + 4 <= m; x += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(all_key + x);
+        greater += (k.x > me) + (k.y > me) + (k.z > me) + (k.w > me);
+        equal += (k.x == me) + (k.y == me) + (k.z == me) + (k.w == me);
+      }
+      for (; x < m; ++x) {
+        greater += all_key[x] > me;
+        equal += all_key[x] == me;
+      }
+      const int i = my_pos[threadIdx.x];
       if (greater + equal <= need) {
-        atomicOr(&sure[me.y >> 5], bit);
+        atomicOr(&sure[i >> 5], 1u << (i & 31));
       } else if (greater < need) {
-        atomicOr(&tied[me.y >> 5], bit);
+        atomicOr(&tied[i >> 5], 1u << (i & 31));
         s_ties = need - greater;  // the same from all of them
       }
     }
-    __syncthreads();
-    ties = s_ties;
   }
+  __syncthreads();
+  if (rank_list) ties = s_ties;  // 0 where this block has no tied key; the cluster's largest below
   // places: thread t takes words 2 t and 2 t + 1
   unsigned ws[2], we[2], pop = 0;  // populations, kept in the low half, tied in the high one (each <= 2^15)
 #pragma unroll
@@ -265,21 +330,25 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     const unsigned y = __shfl_up_sync(kFull, sum, o);
     if (lane >= o) sum += y;
   }
-  if (lane == 31) red[1][warp] = sum;
+  if (lane == 31) red[warp] = sum;
   __syncthreads();
-  const unsigned others = lane < kSelWarps ? red[1][lane] : 0u;
+  const unsigned others = lane < kSelWarps ? red[lane] : 0u;
   const unsigned before = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - pop;
   unsigned at_sure = before & 0xffffu, at_tied = before >> 16;
   if (cl > 1) {
     const unsigned total = __reduce_add_sync(kFull, others);
     if (threadIdx.x == 0) {
-      pub[1][0] = total & 0xffffu;
-      pub[1][1] = total >> 16;
+      pub[0] = total & 0xffffu;
+      pub[1] = total >> 16;
+      pub[2] = (unsigned)ties;
     }
     meet();
-    for (int r = 0; r < rank; ++r) {
-      at_sure += of_rank(&pub[1][0], r);
-      at_tied += of_rank(&pub[1][1], r);
+    for (int r = 0; r < cl; ++r) {
+      ties = max(ties, (int)of_rank(&pub[2], r));
+      if (r < rank) {
+        at_sure += of_rank(&pub[0], r);
+        at_tied += of_rank(&pub[1], r);
+      }
     }
   }
 #pragma unroll
@@ -300,12 +369,23 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     at_tied += pe;
   }
   __syncthreads();
-#pragma unroll 4
-  for (int x = warp; x < words; x += kSelWarps) {
-    const unsigned keep = sure[x], at = tied[x] + __popc(keep & ((1u << lane) - 1u));
-    if ((keep >> lane & 1u) && at < (unsigned)a.budget) {
-      kept[at] = j0 + 32 * x + lane;
-      w_out[at] = key_weight(keys[32 * x + lane]);
+  for (int x0 = warp * kSelWords; x0 < words; x0 += kSelWarps * kSelWords) {
+    unsigned keep[kSelWords], at[kSelWords];
+    uint32_t k[kSelWords];
+#pragma unroll
+    for (int u = 0; u < kSelWords; ++u) {
+      const bool in = x0 + u < words;
+      keep[u] = in ? sure[x0 + u] : 0u;
+      at[u] = in ? tied[x0 + u] : 0u;
+      k[u] = in ? keys[32 * (x0 + u) + lane] : 0u;  // words are whole in memory
+    }
+#pragma unroll
+    for (int u = 0; u < kSelWords; ++u) {
+      const unsigned to = at[u] + __popc(keep[u] & ((1u << lane) - 1u));
+      if ((keep[u] >> lane & 1u) && to < (unsigned)a.budget) {
+        kept[to] = j0 + 32 * (x0 + u) + lane;
+        w_out[to] = key_weight(k[u]);
+      }
     }
   }
   for (int i = a.budget + all; i < len; i += stride) w_out[i] = 0.f;
@@ -421,13 +501,16 @@ __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid
 }
 
 // Blocks of a cluster for `heads` (sequence, KV head) pairs of up to `limit`
-// weights: as few as hold them, but more, of at least kSelKeys each, while the
-// launch leaves SMs idle.
-constexpr int kSelKeys = 4096;
+// weights: as few as hold them, but four or eight, of at least 2,048 weights
+// each, where the launch leaves SMs free (32 heads of 16,384 weights: the whole
+// eviction takes 37.8 us with eight, 42 with one; two blocks of 2,500 weights
+// are slower than one of 5,000, 19.1 against 18.4 us: a pass meets the cluster
+// twice, at about 1,500 cycles).
 int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   int cl = 1;
-  while (cl < 8 && (limit > (int64_t)cl * kSelCap || (limit >= 2 * cl * kSelKeys && heads * cl * 2 <= sm_count)))
-    cl *= 2;
+  while (cl < 8 && limit > (int64_t)cl * kSelCap) cl *= 2;
+  if (cl < 4 && limit >= 4 * 2048 && 4 * heads <= sm_count) cl = 4;
+  if (cl < 8 && limit >= 8 * 2048 && 8 * heads <= 2 * sm_count) cl = 8;
   return cl;
 }
 
