@@ -10,18 +10,25 @@
 namespace sf {
 namespace {
 
-// Rotary table [max_pos][cos half | sin half], angles and functions in double:
-// far positions (10^5 radians and more) lose the angle in fp32.
+// Rotary table [max_pos][cos half | sin half] in double, rounded once: far
+// positions (10^5 radians and more) lose the angle in fp32.  A thread takes one
+// frequency over kRopeRun positions: sine and cosine of the first angle and of
+// the step, then the addition theorem (double rounding grows by about 2^-53 a
+// step, far below fp32's half step); FP64 rates make a sine per entry slow.
+constexpr int kRopeRun = 64;
+
 __global__ void rope_table_kernel(float* out, int max_pos, int half, double theta) {
-  const int64_t n = (int64_t)max_pos * half;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int j = (int)(i % half);
-    const int64_t pos = i / half;
-    const double a = (double)pos * pow(theta, -(double)j / half);
-    double sn, cs;
-    sincos(a, &sn, &cs);
-    out[pos * 2 * half + j] = (float)cs;
-    out[pos * 2 * half + half + j] = (float)sn;
+  const int j = threadIdx.x, p0 = blockIdx.x * kRopeRun, p1 = min(p0 + kRopeRun, max_pos);
+  const double freq = pow(theta, -(double)j / half);
+  double s, c, ds, dc;
+  sincos((double)p0 * freq, &s, &c);
+  sincos(freq, &ds, &dc);
+  for (int p = p0; p < p1; ++p) {
+    out[(int64_t)p * 2 * half + j] = (float)c;
+    out[(int64_t)p * 2 * half + half + j] = (float)s;
+    const double t = c * dc - s * ds;
+    s = s * dc + c * ds;
+    c = t;
   }
 }
 
@@ -330,10 +337,8 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if (e == cudaSuccess) e = cudaHostGetDevicePointer(&c->err_dev, c->err, 0);
   if (e == cudaSuccess) {
     for (int i = 0; i < kCacheErrWords; ++i) c->err[i] = 0;
-    const int64_t n = (int64_t)s.max_pos * (s.head_dim / 2);
-    const int64_t blocks = (n + 255) / 256;
-    rope_table_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256>>>(c->rope, s.max_pos, s.head_dim / 2,
-                                                                          (double)s.rope_theta);
+    rope_table_kernel<<<(s.max_pos + kRopeRun - 1) / kRopeRun, s.head_dim / 2>>>(c->rope, s.max_pos, s.head_dim / 2,
+                                                                                 (double)s.rope_theta);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();

@@ -46,15 +46,12 @@ __device__ __forceinline__ unsigned atom_cluster_add(uint32_t addr, unsigned v) 
   return old;
 }
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 4 * kSelThreads;  // 2^11
 constexpr int kBinBits = 11;
+constexpr int kBins = 1 << kBinBits;
 constexpr int kList = 256;              // keys that are ranked by comparing all pairs
 constexpr int kSelLoads = 8;            // keys a thread handles together
 constexpr int kSelWords = 4;            // words of a bitmap a warp handles together
 constexpr int kSelCap = 32768;          // weights a block holds at most
-static_assert(kSelCap / 32 <= 2 * kSelThreads, "two words of a bitmap a thread");
 
 // First cut: 2^20 keys a bin from that of 0.0 on, eight bins for every factor
 // of two; smaller keys count as the lowest bin.
@@ -76,8 +73,13 @@ static_assert((0xff800000u - kFirstKey) >> kFirstShift < (uint32_t)kBins, "bins 
 // The choice is two bitmaps, positions certainly kept and positions at the
 // threshold, of which the first `ties` are kept; a scan of their populations
 // gives every kept position its place.
-__global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __grid_constant__ CacheEvictArgs a, int cl,
-                                                                      int cap) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_kernel(
+    const __grid_constant__ CacheEvictArgs a, int cl, int cap) {
+  constexpr int kSelWarps = kSelThreads / 32;
+  constexpr int BT = kBins / kSelThreads;          // bins of a thread
+  constexpr int WT = kSelCap / 32 / kSelThreads;   // words of a bitmap of a thread
+  static_assert(BT * kSelThreads == kBins && WT * kSelThreads * 32 == kSelCap && kList <= kSelThreads, "shares");
   extern __shared__ __align__(16) unsigned keys[];    // [cap] of this block's positions
   unsigned* sure = keys + cap;                        // [cap / 32] kept; later the final choice
   unsigned* tied = sure + cap / 32;                   // [cap / 32] at the threshold; later places
@@ -99,7 +101,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   };
   auto remote = [&](const void* p, int r) { return tc::map_to_rank(tc::smem_u32(p), r); };
   auto of_rank = [&](const unsigned* p, int r) { return r == rank ? *p : ld_cluster_u32(remote(p, r)); };
-  reinterpret_cast<uint4*>(hist)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < BT; ++i) hist[threadIdx.x + i * kSelThreads] = 0u;
   if (threadIdx.x == 0) n_all = n_mine = s_ties = 0u;
   pdl_wait();
   pdl_trigger();
@@ -150,24 +153,28 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   bool rank_list = false;
   while (need > 0) {
     __syncthreads();
-    // thread t holds bins kBins - 1 - 4 t and the three below it
-    uint4* mine = reinterpret_cast<uint4*>(hist) + (kSelThreads - 1 - threadIdx.x);
-    uint4 h = *mine;
-    if (rank != 0) {
-      const unsigned v[4] = {h.x, h.y, h.z, h.w};
-      const uint32_t to = remote(mine, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (v[i]) red_cluster_add(to + 4 * i, v[i]);
-      *mine = make_uint4(0, 0, 0, 0);
-    }
+    // thread t holds bins kBins - 1 - BT t and those below it
+    unsigned* mine = hist + kBins - 1 - BT * threadIdx.x;
+    unsigned v[BT], mass = 0;
     if (cl > 1) {
+      if (rank != 0) {
+#pragma unroll
+        for (int i = 0; i < BT; ++i) {
+          v[i] = mine[-i];
+          if (v[i]) red_cluster_add(remote(mine - i, 0), v[i]);
+          mine[-i] = 0u;
+        }
+      }
       meet();
-      h = *mine;
     }
     if (rank == 0) {
-      *mine = make_uint4(0, 0, 0, 0);
-      unsigned sum = h.x + h.y + h.z + h.w;
+#pragma unroll
+      for (int i = 0; i < BT; ++i) {
+        v[i] = mine[-i];
+        mine[-i] = 0u;
+        mass += v[i];
+      }
+      unsigned sum = mass;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_up_sync(kFull, sum, o);
@@ -176,13 +183,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
       if (lane == 31) red[warp] = sum;
       __syncthreads();
       const unsigned others = lane < kSelWarps ? red[lane] : 0u;
-      unsigned at = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - (h.x + h.y + h.z + h.w);
+      unsigned at = __reduce_add_sync(kFull, lane < warp ? others : 0u) + sum - mass;
       const unsigned total = __reduce_add_sync(kFull, others);
-      const unsigned v[4] = {h.w, h.z, h.y, h.x};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < BT; ++i) {
         if (at < (unsigned)need && at + v[i] >= (unsigned)need) {
-          found[0] = kBins - 1 - 4 * threadIdx.x - i;
+          found[0] = kBins - 1 - BT * threadIdx.x - i;
           found[1] = at;
           found[2] = v[i];
         }
@@ -315,11 +321,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
   }
   __syncthreads();
   if (rank_list) ties = s_ties;  // 0 where this block has no tied key; the cluster's largest below
-  // places: thread t takes words 2 t and 2 t + 1
-  unsigned ws[2], we[2], pop = 0;  // populations, kept in the low half, tied in the high one (each <= 2^15)
+  // places: thread t takes words WT t ...
+  unsigned ws[WT], we[WT], pop = 0;  // populations, kept in the low half, tied in the high one (each <= 2^15)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = 2 * threadIdx.x + i;
+  for (int i = 0; i < WT; ++i) {
+    const int x = WT * threadIdx.x + i;
     ws[i] = x < words ? sure[x] : 0u;
     we[i] = x < words ? tied[x] : 0u;
     pop += __popc(ws[i]) + (__popc(we[i]) << 16);
@@ -352,8 +358,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = 2 * threadIdx.x + i;
+  for (int i = 0; i < WT; ++i) {
+    const int x = WT * threadIdx.x + i;
     const unsigned pe = __popc(we[i]);
     unsigned take = at_tied >= (unsigned)ties ? 0u : min(pe, (unsigned)ties - at_tied), some = 0u;
     if (take == pe) {
@@ -394,13 +400,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_select_kernel(const __gr
 
 // ---- keys and values -----------------------------------------------------------
 
-constexpr int kMoveItems = 4;
+constexpr int kCopyItems = 2;
 constexpr int kCopyThreads = 128;
 constexpr int kCopyWarps = 16;  // per SM
 
 // To other pages.  A warp takes `rows` output positions of one (sequence, KV
 // head): a lane finds where one of them comes from and goes to, then the warp
-// moves their keys and values with kMoveItems pieces of each in flight a lane,
+// moves their keys and values with kCopyItems pieces of each in flight a lane,
 // LANES lanes on a row.
 template <int LANES>
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CacheEvictArgs a, int rows) {
@@ -431,11 +437,11 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
   const uint4* vs = static_cast<const uint4*>(a.v) + c * LANES + lane % LANES;
   uint4* kd = static_cast<uint4*>(a.k_out) + c * LANES + lane % LANES;
   uint4* vd = static_cast<uint4*>(a.v_out) + c * LANES + lane % LANES;
-  for (int r0 = 0; r0 < n; r0 += RPI * kMoveItems) {
-    uint4 k[kMoveItems], v[kMoveItems];
-    uint32_t dst[kMoveItems];
+  for (int r0 = 0; r0 < n; r0 += RPI * kCopyItems) {
+    uint4 k[kCopyItems], v[kCopyItems];
+    uint32_t dst[kCopyItems];
 #pragma unroll
-    for (int u = 0; u < kMoveItems; ++u) {
+    for (int u = 0; u < kCopyItems; ++u) {
       const int r = r0 + u * RPI + lane / LANES;  // rows <= 32; behind n: lanes without a slot
       const uint32_t f = __shfl_sync(kFull, from, r & 31);
       dst[u] = __shfl_sync(kFull, to, r & 31);
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
       }
     }
 #pragma unroll
-    for (int u = 0; u < kMoveItems; ++u)
+    for (int u = 0; u < kCopyItems; ++u)
       if (dst[u] != ~0u) {
         kd[(int64_t)dst[u] * stride] = k[u];
         vd[(int64_t)dst[u] * stride] = v[u];
@@ -454,6 +460,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
   }
 }
 
+constexpr int kMoveItems = 4;
 constexpr int kShiftThreads = 512;
 
 // In place.  kept[i] >= i, so a chunk of rows [i0, i1) only overwrites rows
@@ -514,6 +521,10 @@ int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   return cl;
 }
 
+// Weights of a block from which twice the threads pay, while there is an SM for
+// every block.
+constexpr int kSelWide = 4096;
+
 template <int LANES>
 cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
   // 32 positions a warp, or 8 where that leaves too few warps to hide the latency of their loads
@@ -526,15 +537,21 @@ cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
 }  // namespace
 
 cudaError_t prepare_cache_evict() {
-  return cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kSelCap * 4 + kSelCap / 4);
+  const int bytes = kSelCap * 4 + kSelCap / 4;
+  cudaError_t e = cudaFuncSetAttribute(cache_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(cache_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
 }
 
 cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf16, int sm_count) {
-  const int cl = select_cluster(a.limit, (int64_t)a.S * a.nkv, sm_count);
+  const int64_t heads = (int64_t)a.S * a.nkv;
+  const int cl = select_cluster(a.limit, heads, sm_count);
   const int cap = (int)((a.limit + cl - 1) / cl + 31) / 32 * 32;
-  cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(kSelThreads), (size_t)cap * 4 + cap / 4, dim3(cl),
-                                     cache_select_kernel, a, cl, cap);
+  const bool wide = cap > kSelWide && heads * cl <= sm_count;
+  const int threads = wide ? 1024 : 512;
+  cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(threads), (size_t)cap * 4 + cap / 4, dim3(cl),
+                                     wide ? cache_select_kernel<1024> : cache_select_kernel<512>, a, cl, cap);
   if (e != cudaSuccess) return e;
   const int row16 = a.hd * (bf16 ? 2 : 4) / 16;
   if (a.in_place) {
