@@ -74,6 +74,7 @@ struct CacheAttendArgs {
   unsigned* arrived;  // [blocks] arrivals at a cut segment, by its first block; 0 between calls
   CacheJoin* joins;   // [blocks]
   bool join;          // a join kernel follows
+  int blocks;         // of the attention kernel
   int least;          // units a block takes at least
   int group, nsub, heads;  // query heads of a KV head, parts they are taken in, nkv * nsub
   unsigned* err;

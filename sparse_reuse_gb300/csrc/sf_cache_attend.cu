@@ -118,26 +118,25 @@ struct Ring {
 
   // Copy the tile at key0 into the next stage.
   __device__ __forceinline__ void push(const CacheAttendArgs& a, const Segment& g, int key0, int32_t page, int lane) {
-    int64_t slot = -1;
+    uint32_t sl = ~0u;
     const int j = key0 + lane % KEYS;
     if (j < g.len) {
-      slot = entry_slot(a.table, page, j);
-      if (slot < 0) cache_error(a.err, kCacheBadPage);
+      sl = entry_slot32(a.table, page, j);
+      if (sl == ~0u) cache_error(a.err, kCacheBadPage);
     }
-    const uint32_t sl = (uint32_t)slot;
     live |= (uint64_t)(__ballot_sync(kFull, sl != ~0u) & (uint32_t)((1ull << KEYS) - 1)) << (KEYS * in_ring);
     ++in_ring;
     const int ch = lane % CH, r0 = lane / CH;
     const char* kb = static_cast<const char*>(a.k) + (int64_t)g.kvh * kRowBytes + ch * 16;
     const char* vb = static_cast<const char*>(a.v) + (int64_t)g.kvh * kRowBytes + ch * 16;
-    const int64_t stride = (int64_t)a.nkv * kRowBytes;
+    const uint32_t stride = a.nkv * kRowBytes;
     const uint32_t dst = base + fill * kStageBytes;
 #pragma unroll
     for (int i = 0; i < KEYS / RPC; ++i) {
       const int r = i * RPC + r0;
       const uint32_t x = __shfl_sync(kFull, sl, r);
       const bool on = x != ~0u;
-      const int64_t off = on ? (int64_t)x * stride : 0;
+      const uint64_t off = (uint64_t)(on ? x : 0u) * stride;
       const uint32_t to = dst + r * kRowBytes + ((ch ^ turn(r)) << 4);
       cp_async16(to, kb + off, on);
       cp_async16(to + KEYS * kRowBytes, vb + off, on);
@@ -639,7 +638,7 @@ struct PartSum {
 };
 
 constexpr int kShort = 4;        // tiles of a segment that one warp takes alone
-constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself
+constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself (at most 32)
 constexpr int kWaste = 24;       // tiles a block may take beyond an even share to keep to one segment
 
 // The work is cut over the blocks in one of two ways, by the batch's lengths.
@@ -897,8 +896,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   }
 }
 
-// Joins a segment cut over more than kInlineParts blocks: a block per (its
-// first block, head), the parts dealt over groups of HD / 4 threads.
+// Joins a segment cut over more than kInlineParts blocks: a block per (segment,
+// head), the parts dealt over groups of HD / 4 threads.
 constexpr int kJoinThreads = 256;
 constexpr int kMaxBlocks = 512;  // of the attention kernel
 
@@ -909,15 +908,20 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   __shared__ float2 ml[GROUPS];
   pdl_wait();
   pdl_trigger();
-  const CacheJoin j = a.joins[blockIdx.x];
+  // a joined segment spans more than kInlineParts blocks: at most one starts among kInlineParts neighbours
+  const int lane = threadIdx.x & 31, b = blockIdx.x * kInlineParts + lane;
+  const unsigned hit = __ballot_sync(kFull, lane < kInlineParts && b < a.blocks && a.joins[b].n > 0);
+  if (hit == 0u) return;
+  const int b0 = blockIdx.x * kInlineParts + __ffs(hit) - 1;
+  const CacheJoin j = a.joins[b0];
   const int h = blockIdx.y;
-  if (h >= j.nh || j.n == 0) return;
+  if (h >= j.nh) return;
   const int g = threadIdx.x / COLS, col = threadIdx.x % COLS;
   PartSum sum;
   for (int x0 = g; x0 < j.n; x0 += GROUPS * kPartLoads)
     sum.add<NH, HD, kPartLoads>(a, h, 4 * col, (j.n - x0 + GROUPS - 1) / GROUPS, [&](int x) {
       const int p = x0 + x * GROUPS;
-      return p ? 2 * ((int)blockIdx.x + p) : j.first;
+      return p ? 2 * (b0 + p) : j.first;
     });
   acc[g][col] = sum.o;
   if (col == 0) ml[g] = make_float2(sum.top, sum.l);
@@ -994,12 +998,14 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   const int blocks = (int)(want < most_blocks ? want : most_blocks);
   // a segment of t tiles has at least 1 / heads of all units: it lies in at most blocks / heads + 2 blocks, and in
   // (t - 1) / least + 2
+  a.blocks = blocks;
   a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks / a.heads + 2 > kInlineParts;
   const size_t table = (2 * (size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
   cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
                              a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);
   if (e == cudaSuccess && a.join)
-    e = launch_pdl(st, dim3(blocks, NH < G ? NH : G), dim3(kJoinThreads), 0, 1, cache_join_kernel<T, HD, NH>, a);
+    e = launch_pdl(st, dim3((blocks + kInlineParts - 1) / kInlineParts, NH < G ? NH : G), dim3(kJoinThreads), 0, 1,
+                   cache_join_kernel<T, HD, NH>, a);
   if (e == cudaSuccess && a.w_out) {
     const int64_t most = (int64_t)a.S * a.nkv * ((a.limit + kWeightKeys - 1) / kWeightKeys);
     e = launch_pdl(st, dim3((unsigned)(most < 8 * sm_count ? most : 8 * sm_count)), dim3(kWeightThreads), table, 1,

@@ -51,6 +51,13 @@ SF_HD int64_t entry_slot(const PageTable& t, int32_t page, int j) {
   return (int64_t)page * t.page_size + (j - page_of(t, j) * t.page_size);
 }
 
+// The same in 32 bits, ~0 for none: pools have fewer than 2^32 - 1 slots.
+SF_HD uint32_t entry_slot32(const PageTable& t, int32_t page, int j) {
+  const uint32_t pages = t.n_pages > 0x7fffffff ? 0x80000000u : (uint32_t)t.n_pages;
+  if ((uint32_t)page >= pages) return ~0u;
+  return (uint32_t)page * (uint32_t)t.page_size + (uint32_t)(j - page_of(t, j) * t.page_size);
+}
+
 // Both: -1 when j lies outside the table or on a page outside the pool.
 SF_HD int64_t page_slot(const PageTable& t, int s, int j) { return entry_slot(t, page_entry(t, s, j), j); }
 

@@ -70,6 +70,10 @@ extern "C" {
 long long slot(const int* pages, long long ld, int cols, int page, long long n_pages, int s, int j) {
   return sf::page_slot(sf::make_page_table(pages, ld, cols, page, n_pages), s, j);
 }
+unsigned slot32(const int* pages, long long ld, int cols, int page, long long n_pages, int s, int j) {
+  const sf::PageTable t = sf::make_page_table(pages, ld, cols, page, n_pages);
+  return sf::entry_slot32(t, sf::page_entry(t, s, j), j);
+}
 int quotients(int page) {  // positions whose page is not their quotient
   const sf::PageTable t = sf::make_page_table(nullptr, 0, 0, page, 0);
   int wrong = 0;
@@ -94,6 +98,8 @@ int len(int n, long long lim, int* bad) { bool b; int r = sf::checked_len(n, lim
     lib.slot.restype = ctypes.c_longlong
     lib.slot.argtypes = [ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong,
                          ctypes.c_int, ctypes.c_int]
+    lib.slot32.argtypes = lib.slot.argtypes
+    lib.slot32.restype = ctypes.c_uint
     lib.limit.restype = lib.per.restype = ctypes.c_longlong
     return lib
 
@@ -111,6 +117,8 @@ def test_slots_and_bad_pages(index_lib, page):
             c = j // page
             ok = 0 <= j < 9 * page and 0 <= table[s, c] < 50
             assert got == (int(table[s, c]) * page + j % page if ok else -1), (s, j)
+            if j >= 0:
+                assert index_lib.slot32(wide.ctypes.data, 12, 9, page, 50, s, j) == got % 2 ** 32
 
 
 def test_page_of_every_position(index_lib):
@@ -122,6 +130,9 @@ def test_page_of_every_position(index_lib):
 def test_slots_beyond_32_bits(index_lib):
     table = np.array([[2 ** 31 - 1]], np.int32)
     assert index_lib.slot(table.ctypes.data, 1, 1, 65536, 2 ** 31, 0, 65535) == (2 ** 31 - 1) * 65536 + 65535
+    assert index_lib.slot32(table.ctypes.data, 1, 1, 1, 2 ** 32 - 2, 0, 0) == 2 ** 31 - 1
+    table[0, 0] = -1
+    assert index_lib.slot32(table.ctypes.data, 1, 1, 1, 2 ** 32 - 2, 0, 0) == 2 ** 32 - 1
 
 
 def test_length_limits(index_lib):
