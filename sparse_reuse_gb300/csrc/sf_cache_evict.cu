@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
   constexpr int kSelWarps = kSelThreads / 32;
   constexpr int BT = kBins / kSelThreads;          // bins of a thread
   constexpr int WT = kSelCap / 32 / kSelThreads;   // words of a bitmap of a thread
-  static_assert(BT * kSelThreads == kBins && WT * kSelThreads * 32 == kSelCap && kList <= kSelThreads, "shares");
+  static_assert(BT * kSelThreads == kBins && WT * kSelThreads * 32 == kSelCap, "shares");
   extern __shared__ __align__(16) unsigned keys[];    // [cap] of this block's positions
   unsigned* sure = keys + cap;                        // [cap / 32] kept; later the final choice
   unsigned* tied = sure + cap / 32;                   // [cap / 32] at the threshold; later places
@@ -150,8 +150,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
   int shift = kFirstShift;                       // of 2^shift keys
   uint32_t thr = ~0u;                            // keys above it are kept (none is above ~0),
   int ties = 0;                                  // and the first `ties` equal to it
-  bool rank_list = false;
-  while (need > 0) {
+  // few candidates: all of them are ranked, nothing is narrowed
+  bool rank_list = need > 0 && len - a.n_first - a.n_recent <= kList;
+  if (rank_list) thr = hi;
+  while (need > 0 && !rank_list) {
     __syncthreads();
     // thread t holds bins kBins - 1 - BT t and those below it
     unsigned* mine = hist + kBins - 1 - BT * threadIdx.x;
@@ -244,7 +246,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
       }
     }
   }
-  if (need == 0) meet();  // every key is in place (the passes met otherwise); a.w is read by everybody: w_out may be w
+  // every key is in place and a.w is read by everybody (w_out may be w); the passes have met for that otherwise
+  if (need == 0 || rank_list) meet();
   // bitmaps; the keys still to be ranked into the lists.  kSelWords words at a time, so that their latencies overlap
   for (int x0 = warp * kSelWords; x0 < words; x0 += kSelWarps * kSelWords) {
     uint32_t k[kSelWords];
@@ -295,11 +298,11 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
     meet();
     const int m = cl > 1 ? (int)of_rank(&n_all, 0) : (int)n_mine, mine = (int)n_mine;
     if (rank != 0) {
-      if (threadIdx.x < m) all_key[threadIdx.x] = ld_cluster_u32(remote(all_key + threadIdx.x, 0));
+      for (int x = threadIdx.x; x < m; x += kSelThreads) all_key[x] = ld_cluster_u32(remote(all_key + x, 0));
       __syncthreads();
     }
-    if (threadIdx.x < mine) {
-      const unsigned me = my_key[threadIdx.x];
+    for (int t = threadIdx.x; t < mine; t += kSelThreads) {
+      const unsigned me = my_key[t];
       int greater = 0, equal = 0, x = 0;
       for (; x + 4 <= m; x += 4) {
         const uint4 k = *reinterpret_cast<const uint4*>(all_key + x);
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
         greater += all_key[x] > me;
         equal += all_key[x] == me;
       }
-      const int i = my_pos[threadIdx.x];
+      const int i = my_pos[t];
       if (greater + equal <= need) {
         atomicOr(&sure[i >> 5], 1u << (i & 31));
       } else if (greater < need) {
@@ -521,9 +524,12 @@ int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   return cl;
 }
 
-// Weights of a block from which twice the threads pay, while there is an SM for
-// every block.
-constexpr int kSelWide = 4096;
+// Threads of a selection block: 512, but 1,024 for more than kSelWide weights
+// while there is an SM for every block (66 heads of up to 5,001 weights: 14.2
+// against 15.9 us), and 128 for up to kSelNarrow weights where 512 would not
+// all be resident at once (488 heads of 32 weights: 7.3 against 9.6 us; with
+// few heads 512 are 0.3 us faster).
+constexpr int kSelWide = 4096, kSelNarrow = 512;
 
 template <int LANES>
 cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
@@ -548,10 +554,12 @@ cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf1
   const int64_t heads = (int64_t)a.S * a.nkv;
   const int cl = select_cluster(a.limit, heads, sm_count);
   const int cap = (int)((a.limit + cl - 1) / cl + 31) / 32 * 32;
-  const bool wide = cap > kSelWide && heads * cl <= sm_count;
-  const int threads = wide ? 1024 : 512;
+  const bool wide = cap > kSelWide && heads * cl <= sm_count, narrow = cap <= kSelNarrow && heads > 2 * sm_count;
+  const int threads = wide ? 1024 : narrow ? 128 : 512;
   cudaError_t e = launch_pdl_cluster(st, dim3(cl * a.nkv, a.S), dim3(threads), (size_t)cap * 4 + cap / 4, dim3(cl),
-                                     wide ? cache_select_kernel<1024> : cache_select_kernel<512>, a, cl, cap);
+                                     wide ? cache_select_kernel<1024>
+                                          : narrow ? cache_select_kernel<128> : cache_select_kernel<512>,
+                                     a, cl, cap);
   if (e != cudaSuccess) return e;
   const int row16 = a.hd * (bf16 ? 2 : 4) / 16;
   if (a.in_place) {
