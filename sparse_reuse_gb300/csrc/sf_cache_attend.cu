@@ -529,7 +529,7 @@ __device__ __forceinline__ int scan_lens(const CacheAttendArgs& a, int* first, i
     int x = 0;
     if (s < a.S) {
       bool bad;
-      const int len = checked_len(a.lens[s], a.limit, &bad);
+      const int len = checked_len(__ldcg(a.lens + s), a.limit, &bad);
       lens[s] = len;
       x = units_of(len);
       if (bad && blockIdx.x == 0) cache_error(a.err, kCacheBadLength);
@@ -947,27 +947,33 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __g
   extern __shared__ int first[];
   __shared__ int sums[kWeightThreads / 32];
   int* lens = first + a.S + 1;
-  pdl_wait();
-  pdl_trigger();
-  const int G = a.nq / a.nkv;
+  // Behind the attention kernel, which has waited for everything before it: the lengths, and the weights so far, are
+  // there and stay as they are.  Read through L2.
+  const int G = a.group;
   scan_lens<kWeightThreads>(a, first, lens, sums, [](int len) { return (len + kWeightKeys - 1) / kWeightKeys; });
   const int64_t units = (int64_t)first[a.S] * a.nkv;
+  bool waited = false;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int s = find_sequence(first, a.S, u, a.nkv), n = first[s + 1] - first[s];
     const int in_s = (int)(u - (int64_t)first[s] * a.nkv), c = in_s / n;
     const int j = in_s % n * kWeightKeys + 4 * (int)threadIdx.x, len = lens[s];
-    if (j >= len) continue;
     // the rows of scores are padded to 4 floats: behind the length there is something to read, if nothing to use
     const int64_t at = ((int64_t)s * a.nkv + c) * a.ld_w + j;
     const int64_t h = (int64_t)s * a.nq + c * G;
     const float4* sc = reinterpret_cast<const float4*>(a.scores + h * a.ld_scores + j);
     float before[4], w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) before[i] = a.w_in && j + i < len ? a.w_in[at + i] : 0.f;
+    for (int i = 0; i < 4; ++i) before[i] = a.w_in && j + i < len ? __ldcg(a.w_in + at + i) : 0.f;
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+    if (j >= len) continue;
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
       const float lse = a.lse[h + g];
-      const float4 x = sc[g * (a.ld_scores / 4)];
+      const float4 x = __ldcs(sc + g * (a.ld_scores / 4));
       w[0] += x.x == -INFINITY ? 0.f : ex2(x.x - lse);
       w[1] += x.y == -INFINITY ? 0.f : ex2(x.y - lse);
       w[2] += x.z == -INFINITY ? 0.f : ex2(x.z - lse);
@@ -977,6 +983,7 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __g
     for (int i = 0; i < 4; ++i)
       if (j + i < len) a.w_out[at + i] = before[i] + w[i];
   }
+  if (!waited) pdl_wait();
 }
 
 template <typename T, int HD, int NT>

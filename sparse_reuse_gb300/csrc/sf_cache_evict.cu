@@ -414,25 +414,29 @@ constexpr int kCopyWarps = 16;  // per SM
 template <int LANES>
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_constant__ CacheEvictArgs a, int rows) {
   constexpr int RPI = 32 / LANES;  // rows of one load
-  pdl_wait();
-  pdl_trigger();
   const int s = blockIdx.z, c = blockIdx.y, lane = threadIdx.x & 31;
   const int i0 = (blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5)) * rows;
+  // Behind the selection kernel, which has waited for everything before it and writes neither lengths nor tables:
+  // they can be read, through L2, before it is done.
   bool bad;
-  const int n_keep = min(checked_len(a.lens[s], a.limit, &bad), a.budget);
-  // lens_out may be lens: the blocks that read it later find n_keep, which gives n_keep again
-  if (blockIdx.x == 0 && c == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;
+  const int n_keep = min(checked_len(__ldcg(a.lens + s), a.limit, &bad), a.budget);
   const int n = min(rows, n_keep - i0);
-  if (n <= 0) return;
   uint32_t from = ~0u, to = ~0u;
   if (lane < n) {
-    const int64_t f = page_slot(a.table, s, a.kept[((int64_t)s * a.nkv + c) * a.budget + i0 + lane]);
-    const int64_t t = page_slot(a.table_out, s, i0 + lane);
-    if (f < 0 || t < 0) {
+    const int i = i0 + lane, col = page_of(a.table_out, i);
+    to = entry_slot32(a.table_out, col < a.table_out.cols ? __ldcg(a.table_out.pages + s * a.table_out.ld + col) : -1, i);
+  }
+  pdl_wait();
+  pdl_trigger();
+  // lens_out may be lens: the blocks that read it later find n_keep, which gives n_keep again
+  if (blockIdx.x == 0 && c == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;
+  if (n <= 0) return;
+  if (lane < n) {
+    const int j = a.kept[((int64_t)s * a.nkv + c) * a.budget + i0 + lane];
+    from = entry_slot32(a.table, page_entry(a.table, s, j), j);
+    if (from == ~0u || to == ~0u) {
       cache_error(a.err, kCacheBadPage);
-    } else {
-      from = (uint32_t)f;
-      to = (uint32_t)t;
+      to = ~0u;
     }
   }
   const int64_t stride = (int64_t)a.nkv * LANES;  // pieces from one position to the next
@@ -463,50 +467,54 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const __grid_c
   }
 }
 
-constexpr int kMoveItems = 4;
-constexpr int kShiftThreads = 512;
+constexpr int kMoveItems = 2;
+constexpr int kShiftThreads = 1024;
 
 // In place.  kept[i] >= i, so a chunk of rows [i0, i1) only overwrites rows
 // that this chunk or an earlier one reads: a block reads the chunk into
 // registers, meets, and writes it.  Different bytes of a row never meet, so
 // the rows of a (sequence, KV head, keys or values) are cut into slices of
-// `pieces` times 16 bytes, a block each.
+// 2^log_pieces times 16 bytes, a block each.
 __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid_constant__ CacheEvictArgs a, int row16,
-                                                                    int pieces) {
-  pdl_wait();
-  pdl_trigger();
-  const int s = blockIdx.y, slices = row16 / pieces;
+                                                                    int log_pieces) {
+  const int s = blockIdx.y, slices = row16 >> log_pieces;
   const int slice = blockIdx.x % slices, part = blockIdx.x / slices % 2, c = blockIdx.x / slices / 2;
   bool bad;
-  const int n_keep = min(checked_len(a.lens[s], a.limit, &bad), a.budget);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;  // lens_out may be lens: n_keep reads back as itself
+  const int n_keep = min(checked_len(__ldcg(a.lens + s), a.limit, &bad), a.budget);  // as in cache_copy_kernel
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[s] = n_keep;
   const int32_t* kept = a.kept + ((int64_t)s * a.nkv + c) * a.budget;
-  uint4* pool = static_cast<uint4*>(part ? a.v_out : a.k_out);
-  const int rows = kShiftThreads / pieces, piece = threadIdx.x % pieces + slice * pieces;
+  const int piece = (threadIdx.x & ((1 << log_pieces) - 1)) + (slice << log_pieces);
+  uint4* pool = static_cast<uint4*>(part ? a.v_out : a.k_out) + c * row16 + piece;
+  const int64_t stride = (int64_t)a.nkv * row16;
+  const int rows = kShiftThreads >> log_pieces, row = threadIdx.x >> log_pieces;
   for (int i0 = 0; i0 < n_keep; i0 += rows * kMoveItems) {
     uint4 x[kMoveItems];
-    int64_t to[kMoveItems];
+    uint32_t from[kMoveItems], to[kMoveItems];
 #pragma unroll
     for (int u = 0; u < kMoveItems; ++u) {
-      const int i = i0 + u * rows + (int)threadIdx.x / pieces;
-      to[u] = -1;
+      const int i = i0 + u * rows + row;
+      from[u] = to[u] = ~0u;
       if (i < n_keep) {
         const int j = kept[i];
         if (j != i) {
-          const int64_t from = page_slot(a.table, s, j), dst = page_slot(a.table_out, s, i);
-          if (from < 0 || dst < 0) {
+          from[u] = entry_slot32(a.table, page_entry(a.table, s, j), j);
+          to[u] = entry_slot32(a.table_out, page_entry(a.table_out, s, i), i);
+          if (from[u] == ~0u || to[u] == ~0u) {
             cache_error(a.err, kCacheBadPage);
-          } else {
-            to[u] = (dst * a.nkv + c) * row16 + piece;
-            x[u] = pool[(from * a.nkv + c) * row16 + piece];
+            to[u] = ~0u;
           }
         }
       }
     }
+#pragma unroll
+    for (int u = 0; u < kMoveItems; ++u)
+      if (to[u] != ~0u) x[u] = pool[from[u] * stride];
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMoveItems; ++u)
-      if (to[u] >= 0) pool[to[u]] = x[u];
+      if (to[u] != ~0u) pool[to[u] * stride] = x[u];
   }
 }
 
@@ -563,9 +571,11 @@ cudaError_t launch_cache_evict(cudaStream_t st, const CacheEvictArgs& a, int bf1
   if (e != cudaSuccess) return e;
   const int row16 = a.hd * (bf16 ? 2 : 4) / 16;
   if (a.in_place) {
-    const int pieces = 2;
-    return launch_pdl(st, dim3(a.nkv * 2 * (row16 / pieces), a.S), dim3(kShiftThreads), 0, 1, cache_shift_kernel, a,
-                      row16, pieces);
+    // slices of 16 bytes at least, until there is a block for every SM
+    int log_pieces = row16 == 8 ? 3 : row16 == 16 ? 4 : 5;
+    while (log_pieces > 0 && 2 * heads * (row16 >> log_pieces) < sm_count) --log_pieces;
+    return launch_pdl(st, dim3(2 * a.nkv * (row16 >> log_pieces), a.S), dim3(kShiftThreads), 0, 1, cache_shift_kernel,
+                      a, row16, log_pieces);
   }
   if (row16 == 8) return copy_rows<8>(st, a, sm_count);
   return row16 == 16 ? copy_rows<16>(st, a, sm_count) : copy_rows<32>(st, a, sm_count);
