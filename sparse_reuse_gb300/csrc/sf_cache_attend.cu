@@ -159,7 +159,7 @@ struct Ring {
 // the rows, the group's query heads the columns, so a group of up to 8 heads
 // wastes nothing but columns.  (tcgen05 tiles have 128 rows and one issuing
 // thread per block; here 8 warps each stream their own tiles with no barrier
-// between them, and the tensor pipe is busy under a tenth of the time.)
+// between them, and the tensor pipe is busy a tenth of the time at 5.7 TB/s.)
 //
 // P enters as the sum of two bf16 numbers (16 bits of it), twice the PV steps,
 // so that the result is as good as fp32 weights.
