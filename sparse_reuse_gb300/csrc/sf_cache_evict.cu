@@ -34,6 +34,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+// The two halves of a cluster barrier: what a thread did before arriving is seen by those that have waited.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -125,7 +134,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
   // candidates, in this block's indexes
   const int lo_j = min(max(a.n_first - j0, 0), n), hi_j = max(min(len - a.n_recent - j0, n), lo_j);
   const int words = (n + 31) / 32;
-  meet();  // every histogram and counter of the cluster is empty
+  __syncthreads();  // this block's histogram and counters are empty;
+  if (cl > 1) cluster_arrive();
   for (int i0 = threadIdx.x; i0 < n; i0 += kSelThreads * kSelLoads) {
     float x[kSelLoads];
 #pragma unroll
@@ -144,6 +154,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
       }
     }
   }
+  if (cl > 1) cluster_wait();  // so are the cluster's
   int need = a.budget - a.n_first - a.n_recent;  // below the number of candidates, since budget < len
   uint32_t lo = 0u, hi = 0xff800000u;            // the need-th largest key lies in [lo, hi]
   uint32_t base = kFirstKey;                     // bins start here,
@@ -301,24 +312,33 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
       for (int x = threadIdx.x; x < m; x += kSelThreads) all_key[x] = ld_cluster_u32(remote(all_key + x, 0));
       __syncthreads();
     }
-    for (int t = threadIdx.x; t < mine; t += kSelThreads) {
-      const unsigned me = my_key[t];
-      int greater = 0, equal = 0, x = 0;
-      for (; x + 4 <= m; x += 4) {
+    // four lanes a key, each a quarter of the list (all of a warp stay for the shuffles)
+    const int q = lane & 3;
+    for (int t0 = warp * 8; t0 < mine; t0 += kSelWarps * 8) {
+      const int t = t0 + (lane >> 2);
+      const unsigned me = t < mine ? my_key[t] : 0u;
+      int greater = 0, equal = 0, x = 4 * q;
+      for (; x + 4 <= m; x += 16) {
         const uint4 k = *reinterpret_cast<const uint4*>(all_key + x);
         greater += (k.x > me) + (k.y > me) + (k.z > me) + (k.w > me);
         equal += (k.x == me) + (k.y == me) + (k.z == me) + (k.w == me);
       }
-      for (; x < m; ++x) {
+      for (const int end = min(x + 4, m); x < end; ++x) {  // the list's last, short quarter
         greater += all_key[x] > me;
         equal += all_key[x] == me;
       }
-      const int i = my_pos[t];
-      if (greater + equal <= need) {
-        atomicOr(&sure[i >> 5], 1u << (i & 31));
-      } else if (greater < need) {
-        atomicOr(&tied[i >> 5], 1u << (i & 31));
-        s_ties = need - greater;  // the same from all of them
+      greater += __shfl_xor_sync(kFull, greater, 1);
+      equal += __shfl_xor_sync(kFull, equal, 1);
+      greater += __shfl_xor_sync(kFull, greater, 2);
+      equal += __shfl_xor_sync(kFull, equal, 2);
+      if (t < mine && q == 0) {
+        const int i = my_pos[t];
+        if (greater + equal <= need) {
+          atomicOr(&sure[i >> 5], 1u << (i & 31));
+        } else if (greater < need) {
+          atomicOr(&tied[i >> 5], 1u << (i & 31));
+          s_ties = need - greater;  // the same from all of them
+        }
       }
     }
   }
@@ -359,6 +379,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
         at_tied += of_rank(&pub[1], r);
       }
     }
+    cluster_arrive();  // the last reads of other blocks' shared memory are done
   }
 #pragma unroll
   for (int i = 0; i < WT; ++i) {
@@ -398,7 +419,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
     }
   }
   for (int i = a.budget + all; i < len; i += stride) w_out[i] = 0.f;
-  if (cl > 1) tc::cluster_sync_all();  // nobody leaves while its shared memory may be read
+  if (cl > 1) cluster_wait();  // nobody leaves while its shared memory may be read
 }
 
 // ---- keys and values -----------------------------------------------------------
