@@ -655,19 +655,20 @@ struct PartSum {
   }
 };
 
-constexpr int kShort = 4;        // tiles of a segment that one warp takes alone
+constexpr int kShort = 8;        // tiles of a segment that one warp takes alone
 constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself (at most 32)
-constexpr int kWaste = 24;       // tiles a block may take beyond an even share to keep to one segment
+constexpr int kWaste = 64;       // tiles a block may take beyond an even share to keep to one segment
 
 // The work is cut over the blocks in one of two ways, by the batch's lengths.
 //
 // Chunks: where there is a block for every segment, every segment is cut into
-// chunks of the same number of tiles, the smallest that gives at most one chunk
-// per block.  A block has one segment, loads one query, joins once.
+// equal chunks, as many as give at most one chunk per block.  A block has one
+// segment, loads one query, joins once (3 x 4,096 keys of 8 heads: 13.7 against
+// 16.9 us on a line).
 //
-// Line: otherwise, or where chunks would leave blocks idle for more than
-// kWaste tiles' time (what a second segment in a block costs, about 5,000
-// cycles), blocks walk equal parts of the line of units (sf_cache_index.h).
+// Line: otherwise, or where a chunk would be more than kWaste tiles longer than
+// an even share, blocks walk equal parts of the line of units
+// (sf_cache_index.h).  Up to there chunks do no worse: 80 blocks saturate DRAM.
 //
 // The 8 warps of a block take the tiles of a segment in turn, or, where the
 // next segments of a line are whole and short, one segment each.  A segment cut
@@ -807,17 +808,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
 
   // ---- chunks.  Every warp works the plan out for itself (no barrier).
   if ((int64_t)filled * H <= gridDim.x && a.S <= kThreads) {
-    int size = (int)share, chunks = 0;
+    int size = (int)share, chunks = 0, longest = 0;
     for (int i = 0; i < 4; ++i) {
-      chunks = 0;
+      chunks = longest = 0;
       for (int s0 = 0; s0 < a.S; s0 += 32) {
-        const int s = s0 + lane, t = s < a.S ? first[s + 1] - first[s] : 0;
-        chunks += __reduce_add_sync(kFull, ((unsigned)t + size - 1) / (unsigned)size);
+        const int s = s0 + lane;
+        const unsigned t = s < a.S ? first[s + 1] - first[s] : 0;
+        const unsigned n = (t + size - 1) / (unsigned)size, c = n ? (t + n - 1) / n : 0u;
+        chunks += __reduce_add_sync(kFull, n);
+        longest = max(longest, (int)__reduce_max_sync(kFull, c));
       }
       if (chunks * H <= (int)gridDim.x) break;
       size += (int)quotient((int64_t)size * (chunks * H - (int)gridDim.x), gridDim.x) + 1;
     }
-    if (chunks * H <= (int)gridDim.x && size <= share + kWaste) {
+    if (chunks * H <= (int)gridDim.x && longest <= share + kWaste) {
       if (blk >= chunks * H) return;
       int before = 0;  // chunks of the sequences in front
       for (int s0 = 0;; s0 += 32) {
@@ -834,7 +838,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           const int l = __ffs(hit) - 1, n = __shfl_sync(kFull, c, l);
           const int r = blk - (before + __shfl_sync(kFull, incl, l) - n) * H;
           const int hs = (unsigned)r / (unsigned)n, x = r - hs * n, tiles = __shfl_sync(kFull, t, l);
-          take(segment(s0 + l, hs), x * size, min(tiles, (x + 1) * size), n, blk - x, 2 * (blk - x), 2 * blk);
+          const int each = (unsigned)(tiles + n - 1) / (unsigned)n;  // the last chunk may be short or empty
+          take(segment(s0 + l, hs), min(tiles, x * each), min(tiles, (x + 1) * each), n, blk - x, 2 * (blk - x),
+               2 * blk);
           return;
         }
         before += __shfl_sync(kFull, incl, 31);

@@ -562,7 +562,8 @@ constexpr int kSelWide = 4096, kSelNarrow = 512;
 
 template <int LANES>
 cudaError_t copy_rows(cudaStream_t st, const CacheEvictArgs& a, int sm_count) {
-  // 32 positions a warp, or 8 where that leaves too few warps to hide the latency of their loads
+  // 32 positions a warp, or 8 where that leaves too few warps to hide the latency of their loads (8 heads of 2,048 ->
+  // 1,024 positions: 10.3 against 16.5 us for four sequences, 20.3 against 22.1 for eight, 31.0 against 30.3 for 16)
   const int rows = (int64_t)a.S * a.nkv * ((a.budget + 31) / 32) < kCopyWarps * sm_count ? 8 : 32;
   const int per_block = rows * (kCopyThreads / 32);
   return launch_pdl(st, dim3((a.budget + per_block - 1) / per_block, a.nkv, a.S), dim3(kCopyThreads), 0, 1,
