@@ -540,16 +540,15 @@ __global__ void __launch_bounds__(kShiftThreads) cache_shift_kernel(const __grid
 }
 
 // Blocks of a cluster for `heads` (sequence, KV head) pairs of up to `limit`
-// weights: as few as hold them, but four or eight, of at least 2,048 weights
-// each, where the launch leaves SMs free (32 heads of 16,384 weights: the whole
-// eviction takes 37.8 us with eight, 42 with one; two blocks of 2,500 weights
-// are slower than one of 5,000, 19.1 against 18.4 us: a pass meets the cluster
-// twice, at about 1,500 cycles).
+// weights: as few as hold them, but four, of at least 2,048 weights each, where
+// the launch leaves SMs free (32 heads of 16,384 weights: the whole eviction
+// takes 35.9 us with four, 37.6 with two or eight, 39.6 with one; two blocks of
+// 2,500 weights are slower than one of 5,000, 19.1 against 18.4 us: a pass meets
+// the cluster twice, at about 1,500 cycles).
 int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   int cl = 1;
   while (cl < 8 && limit > (int64_t)cl * kSelCap) cl *= 2;
   if (cl < 4 && limit >= 4 * 2048 && 4 * heads <= sm_count) cl = 4;
-  if (cl < 8 && limit >= 8 * 2048 && 8 * heads <= 2 * sm_count) cl = 8;
   return cl;
 }
 
