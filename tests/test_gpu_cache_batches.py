@@ -250,7 +250,8 @@ def test_evict_random_batches(sf, seed):
 @pytest.mark.parametrize("kind", WEIGHTS)
 @pytest.mark.parametrize("lens,budget,max_len", [([32768], 5000, None), ([32769, 100], 32768, None),
                                                  ([70001], 65536, None), ([262144], 100000, None),
-                                                 ([9000, 8999, 300], 4000, 262144), ([16384] * 40, 257, None)])
+                                                 ([9000, 8999, 300], 4000, 262144), ([16384] * 40, 257, None),
+                                                 ([300, 40, 271, 269, 270], 20, 262144), ([16384] * 3, 14, None)])
 def test_evict_long_rows(sf, lens, budget, max_len, kind):
     """Rows at the limits of one block and of a cluster, and short rows of an object for long ones."""
     run_evict(sf, 5, (1, 1, 64), "bf16", 64, lens, budget, 3, 11, kind, max_len)
