@@ -444,6 +444,8 @@ class PagedCache:
     def __init__(self, *, n_q_heads, n_kv_heads, head_dim, dtype, page_size, max_seqs, max_len, max_pos=None,
                  rms_eps=1e-6, rope_theta=10000.0, track_weights=False):
         import torch
+        if dtype not in ("bf16", "f32", SF_BF16, SF_F32):
+            raise ValueError(f"dtype must be 'bf16' or 'f32': got {dtype!r}")
         bf16 = dtype in ("bf16", SF_BF16)
         self.shapes = SfCacheShapes(n_q_heads, n_kv_heads, head_dim, SF_BF16 if bf16 else SF_F32, page_size,
                                     max_seqs, max_len, max_len if max_pos is None else max_pos, rms_eps, rope_theta,

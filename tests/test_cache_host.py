@@ -255,6 +255,12 @@ def test_weights_need_an_object_that_tracks_them(sf):
     assert "track_weights" in sf.lib.sf_cache_last_error(obj).decode()
 
 
+def test_binding_refuses_unknown_types(sf):
+    for dtype in ("fp16", torch.float16, None, 2):
+        with pytest.raises(ValueError):
+            sf.PagedCache(n_q_heads=4, n_kv_heads=2, head_dim=64, dtype=dtype, page_size=16, max_seqs=1, max_len=16)
+
+
 def test_null_objects(sf):
     assert sf.lib.sf_cache_sync_status(None, None) == sf.SF_ERR_INVALID_ARG
     assert sf.lib.sf_cache_destroy(None) == sf.SF_ERR_INVALID_ARG
