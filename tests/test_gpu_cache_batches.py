@@ -261,3 +261,60 @@ def test_evict_crowd_of_short_rows(sf):
     """More (sequence, head) pairs than resident blocks."""
     rng = np.random.default_rng(1)
     run_evict(sf, 6, (8, 8, 64), "f32", 4, random_lens(rng, "short", 120, 64), 20, 2, 3, "few values")
+
+
+# ---------------------------------------------------------------- pools beyond 32-bit offsets
+
+def test_pools_beyond_32_bit_offsets(sf):
+    """Pools of 2.2 * 10^9 elements (4.3 GB each): a sequence on their last pages
+    gets the bits that it gets on a small pool's."""
+    nq, nkv, hd, page, n_pages = 8, 8, 128, 64, 33000
+    assert n_pages * page * nkv * hd > 2 ** 31
+    rng = np.random.default_rng(3)
+    lens, new = [500, 90], [40, 3]
+    need = [-(-n // page) for n in lens]
+    small = np.full((2, max(need)), 2 ** 30, np.int32)
+    big = small.copy()
+    small[0, :need[0]], small[1, :need[1]] = np.arange(need[0]), need[0] + np.arange(need[1])
+    big[0, :need[0]] = n_pages - 1 - np.arange(need[0]) * 2
+    big[1, :need[1]] = n_pages - 40 - np.arange(need[1])
+    c = sf.PagedCache(n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype="bf16", page_size=page, max_seqs=2, max_len=500,
+                      track_weights=True)
+    index = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, new)])
+    seq = i32(np.repeat([0, 1], new))
+    g = torch.Generator("cuda").manual_seed(1)
+    rows = torch.randn((sum(new), nq + 2 * nkv, hd), generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn((2, nq, hd), generator=g, device="cuda").to(torch.bfloat16)
+    k0, v0 = (torch.randn((sum(need), page, nkv, hd), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    got = []
+    for table, total in ((small, sum(need)), (big, n_pages)):
+        k, v = (torch.zeros((total, page, nkv, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        for s in range(2):
+            where = torch.from_numpy(table[s, :need[s]].astype(np.int64)).cuda()
+            first = torch.from_numpy(small[s, :need[s]].astype(np.int64)).cuda()
+            k[where], v[where] = k0[first], v0[first]
+        t, w = i32(table), torch.zeros((2, nkv, 512), device="cuda")
+        qr = c.append(rows, i32(index), t, k, v, seq=seq)
+        out = c.attend(q, k, v, t, i32(lens), weights=w)
+        w2 = torch.zeros_like(w)
+        # to a small pool, then in place
+        t_out = i32(np.array([[0, 1], [2, 3]]))
+        k2, v2 = (torch.zeros((4, page, nkv, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ln, kept = c.evict(k, v, t, i32(lens), w, 100, n_recent=7, k_out=k2, v_out=v2, table_out=t_out, weights_out=w2)
+        ln2, kept2 = c.evict(k, v, t, i32(lens), w, 100, n_recent=7)
+        c.sync()
+        rows_k = [gather(k, table[s], int(ln2[s]), page) for s in range(2)]
+        got.append([qr, out, w, w2, ln, kept, kept2, k2, v2, *rows_k])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # the other way round: out to the last pages of the large pools
+    k, v = (torch.zeros((n_pages, page, nkv, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    t_out = np.array([[n_pages - 1, n_pages - 2], [n_pages - 3, n_pages - 4]], np.int32)
+    ln, kept3 = c.evict(k0.clone(), v0.clone(), i32(small), i32(lens), torch.rand((2, nkv, 512), generator=g, device="cuda"),
+                        100, k_out=k, v_out=v, table_out=i32(t_out))
+    c.sync()
+    for s in range(2):
+        src, dst = gather(k0, small[s], lens[s], page), gather(k, t_out[s], int(ln[s]), page)
+        for h in range(nkv):
+            assert torch.equal(dst[:, h], src[kept3[s, h, :int(ln[s])].long(), h])
+    c.close()
