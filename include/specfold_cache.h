@@ -119,16 +119,17 @@ sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_
  *   out[s,h] = sum_j p_h[j] v[s,j,kv(h)],   kv(h) = h / (n_q_heads / n_kv_heads)
  * and, where weights_out is given, for every kv head c and j < lens[s]
  *   weights_out[s,c,j] = weights_in[s,c,j] + sum over h with kv(h) = c of p_h[j]
- * A sequence of length 0 gets zeros and no weights.
+ * A sequence of length 0 gets zeros and no weights; so does a head of which
+ * every score is -infinity (a sequence with all its pages out of range, for
+ * one) where its values are finite.
  *   q        device [S] rows of n_q_heads * head_dim elements, ld_q apart.
  *   out      device [S] rows likewise, ld_out apart; not overlapping q.
  *   weights_in   device fp32 [S, n_kv_heads, ld_w] or NULL (counted as 0).
  *   weights_out  the same or NULL (none wanted); may be weights_in.  Entries at
  *            j >= lens[s] are not touched.  ld_w >= min(max_len, table_cols *
  *            page_size).
- * Results do not depend on what else is in the batch only up to rounding (the
- * sums are split by the batch's total length); the same call gives the same
- * bits.  Values: keys, values and queries as stored; products and sums fp32.
+ * What else is in the batch changes results by rounding only (the sums are
+ * split by the batch's total length); the same call gives the same bits.  Values: keys, values and queries as stored; products and sums fp32.
  * NaN and infinite values, and NaN and +infinite scores, among the live
  * positions make the outputs that they enter non-finite; a score of -infinity
  * weighs nothing.  What pools hold behind a sequence's length is never read.

@@ -588,6 +588,10 @@ __device__ __forceinline__ int find_sequence(const int* first, int S, int64_t u,
   return lo;
 }
 
+// Reciprocal of a denominator; 0 for the denominator 0 of a row without a score above -infinity, which gets zeros
+// (its sums are 0, and 0 times the reciprocal's infinity would be NaN).  NaN stays NaN.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 // o times the reciprocal of the denominator: one quotient where there were four, for one more rounding of fp32.
 template <typename T>
 __device__ __forceinline__ void write_out(const CacheAttendArgs& a, int s, int h, int hd, int d, float4 o, float inv) {
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       if (n > 1)
         *reinterpret_cast<float4*>(part + h * HD + d) = o;
       else
-        write_out<T>(a, g.s, g.h0 + h, HD, d, o, 1.f / l);
+        write_out<T>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
     }
     if (n > kInlineParts) {
       if (blk == b0 && threadIdx.x == 0) a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, slot0};
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
               sum.add<NH, HD, kPartLoads>(a, h, d, n - x0, [&](int x) { return x0 + x ? 2 * (b0 + x0 + x) : slot0; });
           const float4 o = sum.o;
           const float top = sum.top, l = sum.l;
-          write_out<T>(a, g.s, g.h0 + h, HD, d, o, 1.f / l);
+          write_out<T>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
           if (TRACK && d == 0) write_lse(a, g.s, g.h0 + h, top, l);
         }
       }
@@ -909,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           __syncwarp();
           w.store(my_out, sml[warp], lane);
           __syncwarp();
-          if (lane < g.nh) sfac[warp][lane] = 1.f / sml[warp][lane].y;
+          if (lane < g.nh) sfac[warp][lane] = inverse(sml[warp][lane].y);
           __syncwarp();
           for (int i = lane; i < g.nh * HD / 4; i += 32) {
             const int h = i / (HD / 4), d = i % (HD / 4) * 4;
@@ -973,7 +977,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     sum.scale(to);
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i) sum.add_one(acc[i][col], ml[i].x, ml[i].y);
-    write_out<T>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, 1.f / sum.l);
+    write_out<T>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, inverse(sum.l));
     if (a.w_out && col == 0) write_lse(a, j.s, j.h0 + h, sum.top, sum.l);
   }
 }
