@@ -168,6 +168,23 @@ def _stream_handle(stream) -> Optional[int]:
     return h or None
 
 
+def _empty(stream, device, shape, dtype):
+    """A new output of a call on `stream` (a torch stream, its handle, or None for the current one), in memory of
+    that stream's own pool: what was there before is done with in stream order when the call writes it, whatever the
+    current stream still has to do.  It counts as used by the current stream too, so that a reader there need not
+    record it."""
+    import torch
+    current = torch.cuda.current_stream(device)
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream is None or stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 # ---------------------------------------------------------------- C-ABI mirrors
 
 def sf_create(shapes: SfShapes, layers: Sequence[SfLayerWeights]) -> int:
@@ -439,7 +456,9 @@ class PagedCache:
     Tensors must be on the object's device, of the documented type and shape
     with contiguous rows (ValueError otherwise).  Work runs on `stream` (a
     torch stream or its handle; default: the current one of the device); the
-    caller orders the tensors it passes with that stream."""
+    caller orders the tensors it passes with that stream, and waits for it
+    before another stream reads the results.  Outputs that a call makes belong
+    to `stream`, as if made under torch.cuda.stream(stream)."""
 
     def __init__(self, *, n_q_heads, n_kv_heads, head_dim, dtype, page_size, max_seqs, max_len, max_pos=None,
                  rms_eps=1e-6, rope_theta=10000.0, track_weights=False):
@@ -475,14 +494,7 @@ class PagedCache:
             pass
 
     def _empty(self, stream, *shape, dtype):
-        """A new output, kept by the allocator until `stream` is done with it."""
-        import torch
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-            t.record_stream(stream)
-        return t
+        return _empty(stream, self.device, shape, dtype)
 
     def append(self, qkv, index, table, k_pages, v_pages, *, pos=None, seq=None, q_gain=None, k_gain=None, q=None,
                stream=None):

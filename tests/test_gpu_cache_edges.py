@@ -65,3 +65,57 @@ def test_attend_without_a_score_gives_zeros(sf, heads, page, lens, gone, dtype, 
     check_attend(heads, dtype, page, a, calls[0], w_out, w_in=a["w"], seqs=rest)
     check_attend(heads, dtype, page, a, calls[1], None, seqs=rest)
     a["c"].close()
+
+
+# ---------------------------------------------------------------- outputs made by a call on another stream
+
+def _current_stream_is_late(numel, dtype):
+    """The current stream, asleep for some 100 ms, will then copy a block that is already free again: its copy, the
+    block's address and its bytes."""
+    block = torch.full((numel,), 7, dtype=dtype, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    return block.clone(), block.data_ptr(), block.numel() * block.element_size()
+
+
+def _apart(t, address, size):
+    assert t.data_ptr() + t.numel() * t.element_size() <= address or t.data_ptr() >= address + size
+
+
+def test_outputs_on_a_side_stream_wait_for_nobody_and_spoil_nothing(sf):
+    """A call on a stream makes its outputs in that stream's memory: never in a
+    block that the current stream has freed but has still to read."""
+    heads, page, n = (40, 8, 128), 32, 400
+    lens = [40 + i % 9 for i in range(n)]
+    a = attend_inputs(sf, heads, "bf16", page, lens, seed=31)
+    c, table, ln, last = a["c"], i32(a["table"]), i32(lens), i32([x - 1 for x in lens])
+    qkv = torch.randn((n, 56, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    st = torch.cuda.Stream()
+
+    def calls(stream):
+        k, v, w = a["k"].clone(), a["v"].clone(), a["w"].clone()
+        torch.cuda.synchronize()
+        blocks, got = [], []
+        if stream is not None:
+            blocks.append(_current_stream_is_late(n * 40 * 128, torch.bfloat16))
+        got.append(c.append(qkv, last, table, k, v, stream=stream))
+        if stream is not None:
+            blocks.append(_current_stream_is_late(n * 40 * 128, torch.bfloat16))
+        got.append(c.attend(got[0], k, v, table, ln, weights=w, stream=stream))
+        if stream is not None:
+            blocks.append(_current_stream_is_late(n * 8 * 30, torch.int32))
+        got += c.evict(k, v, table, ln, w, 30, n_recent=4, stream=stream)
+        for t in got:
+            for copy, address, size in blocks:
+                if t.dtype == copy.dtype:
+                    _apart(t, address, size)
+        c.sync(stream)
+        torch.cuda.synchronize()
+        assert all(bool((copy == 7).all()) for copy, _, _ in blocks)
+        return got + [k, v, w]
+
+    want = calls(None)
+    for stream in (st, st.cuda_stream):
+        for x, y in zip(calls(stream), want):
+            assert torch.equal(x.view(torch.int8), y.view(torch.int8))    # bits: there is NaN behind the lengths
+    c.close()
