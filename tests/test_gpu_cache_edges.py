@@ -119,3 +119,42 @@ def test_outputs_on_a_side_stream_wait_for_nobody_and_spoil_nothing(sf):
         for x, y in zip(calls(stream), want):
             assert torch.equal(x.view(torch.int8), y.view(torch.int8))    # bits: there is NaN behind the lengths
     c.close()
+
+
+def test_decode_on_a_side_stream_with_ordered_inputs(sf):
+    """Steps on a side stream, their inputs made before it waits for the current
+    stream and kept until it is done, give the bits of the same steps on the
+    current stream; and so does a graph of them replayed twice."""
+    from test_gpu_cache import _decode_inputs
+
+    def loop(c, t, rows, index, lens, stream):
+        outs = []
+        for i in range(30):
+            q = c.append(rows[i], index[i], t["table"], t["k"], t["v"], q_gain=t["g"], k_gain=t["g"], stream=stream)
+            outs.append(c.attend(q, t["k"], t["v"], t["table"], lens[i], weights=t["w"], stream=stream))
+        return outs, c.evict(t["k"], t["v"], t["table"], lens[29], t["w"], 16, n_first=1, n_recent=4, stream=stream)
+
+    res = []
+    for mode in ("current", "side", "graph"):
+        _, _, _, c, t, rows = _decode_inputs(sf, "bf16", 2)
+        index, lens = [i32([i] * 3) for i in range(30)], [i32([i + 1] * 3) for i in range(30)]
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        if mode == "graph":
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                outs, (n, kept) = loop(c, t, rows, index, lens, None)
+            for _ in range(2):
+                for x in ("k", "v", "w"):
+                    t[x].zero_()
+                g.replay()
+                torch.cuda.synchronize()
+                c.sync()
+        else:
+            outs, (n, kept) = loop(c, t, rows, index, lens, st if mode == "side" else None)
+            c.sync(st if mode == "side" else None)
+        res.append([x.clone() for x in (*outs, n, kept, t["k"], t["v"], t["w"])])
+        torch.cuda.synchronize()
+        c.close()
+    for other in res[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(res[0], other))
