@@ -174,10 +174,12 @@ def _empty(stream, device, shape, dtype):
     current stream still has to do.  It counts as used by the current stream too, so that a reader there need not
     record it."""
     import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     current = torch.cuda.current_stream(device)
-    if stream is not None and not hasattr(stream, "cuda_stream"):
+    if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream is None or stream.cuda_stream == current.cuda_stream:
+    if stream.cuda_stream == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
