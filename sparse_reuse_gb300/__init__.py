@@ -365,7 +365,8 @@ class SpecFold:
 
     def verify(self, hidden, parent, prefix_k, prefix_v, delta, *, out=None, fold=None, src=None,
                rc_count=None, stream=None, want_masks=True):
-        """Enqueue one pass; returns (out, fold_mask, src, rc_count) tensors."""
+        """Enqueue one pass; returns (out, fold_mask, src, rc_count) tensors.  Those that the call makes belong to
+        `stream`, as if made under torch.cuda.stream(stream)."""
         import torch
         parent = np.asarray(parent, dtype=np.int32)
         R, Bp = parent.shape
@@ -373,14 +374,14 @@ class SpecFold:
         P = 0 if prefix_k is None else int(prefix_k.shape[2])
         dev = hidden.device
         if out is None:
-            out = torch.empty_like(hidden)
+            out = _empty(stream, dev, hidden.shape, hidden.dtype)
         if want_masks:
             if fold is None:
-                fold = torch.empty((nl, R, Bp, L), dtype=torch.uint8, device=dev)
+                fold = _empty(stream, dev, (nl, R, Bp, L), torch.uint8)
             if src is None:
-                src = torch.empty((nl, R, Bp, L), dtype=torch.int32, device=dev)
+                src = _empty(stream, dev, (nl, R, Bp, L), torch.int32)
             if rc_count is None:
-                rc_count = torch.empty((nl,), dtype=torch.int32, device=dev)
+                rc_count = _empty(stream, dev, (nl,), torch.int32)
         sf_verify(self.ctx, _stream_handle(stream), _ptr(hidden), parent, _ptr(prefix_k), _ptr(prefix_v), R,
                   Bp - 1, P, delta, _ptr(out), _ptr(fold), _ptr(src), _ptr(rc_count))
         return out, fold, src, rc_count
@@ -431,18 +432,19 @@ class Head:
             pass
 
     def verify(self, hidden, tokens, parent, *, pred=None, accepted=None, chosen=None, stream=None):
-        """Enqueue the head for one pass output; returns (pred, accepted, chosen)."""
+        """Enqueue the head for one pass output; returns (pred, accepted, chosen).  Those that the call makes belong
+        to `stream`, as if made under torch.cuda.stream(stream)."""
         import torch
         parent = np.asarray(parent, dtype=np.int32)
         R, Bp = parent.shape
         L = int(hidden.shape[2])
         dev = hidden.device
         if pred is None:
-            pred = torch.empty((R, Bp, L), dtype=torch.int32, device=dev)
+            pred = _empty(stream, dev, (R, Bp, L), torch.int32)
         if accepted is None:
-            accepted = torch.empty((R, Bp), dtype=torch.uint8, device=dev)
+            accepted = _empty(stream, dev, (R, Bp), torch.uint8)
         if chosen is None:
-            chosen = torch.empty((R,), dtype=torch.int32, device=dev)
+            chosen = _empty(stream, dev, (R,), torch.int32)
         sf_head_verify(self.head, _stream_handle(stream), _ptr(hidden), _ptr(tokens), parent, R, Bp - 1, L,
                        _ptr(pred), _ptr(accepted), _ptr(chosen))
         return pred, accepted, chosen
