@@ -1,6 +1,6 @@
 /*
- * specfold_cache.h — the committed context as a paged key-value cache: what
- * writes it, reads it for one new token, and keeps it inside its capacity.
+ * specfold_cache.h — committed context as a paged key-value cache: what writes
+ * it, reads it for one new token, and keeps it inside its capacity.
  *
  * sf_verify (specfold.h) reads the committed context of every request as
  * prefix keys (already rotary-encoded) and values, shared by all branches
@@ -17,7 +17,16 @@
  *
  * A layer's prefix buffer [R, P, n_kv_heads, head_dim] with P a multiple of
  * page_size is such a pool with page_table[r][c] = r * (P / page_size) + c, so
- * the calls below can write, read and compact the pass's own prefix in place.
+ * sf_cache_append can write the prefix that sf_verify reads: P rows a request,
+ * at positions 0..P-1.
+ *
+ * sf_cache_attend and sf_cache_evict are a decode loop of their own beside
+ * that pass.  The rows that append takes and the queries come from the
+ * caller's own projections; the weights that evict goes by come from attend.
+ * What an eviction leaves is read by attend, not by sf_verify: the kept keys
+ * stay rotated at their original positions, lie at the front of buffers of the
+ * old length and may differ in number from sequence to sequence, while
+ * sf_verify takes dense keys of positions 0..P-1 with one P for all requests.
  *
  * Any page size >= 1 works.  Entries of page_table past a sequence's length
  * are never read.  A page may appear in several sequences (a shared prefix)

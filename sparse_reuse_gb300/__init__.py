@@ -467,7 +467,9 @@ class PagedCache:
     Keys and values live in pools [n_pages, page_size, n_kv_heads, head_dim]
     that the caller owns, one pair per layer; table is int32 [S, columns],
     lens int32 [S].  A layer's prefix buffer of SpecFold.verify, viewed as
-    [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool.
+    [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool, so
+    that append can write the prefix of a pass; what evict leaves is read by
+    attend only (its keys keep their original positions).
     Tensors must be on the object's device, of the documented type and shape
     with contiguous rows (ValueError otherwise).  Work runs on `stream` (a
     torch stream or its handle; default: the current one of the device); the
