@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) cache_select_
   if (len <= a.budget) {  // the same for the whole cluster
     for (int i = all; i < a.budget; i += stride) {
       kept[i] = i < len ? i : -1;
-      if (i < len) w_out[i] = w[i];
+      if (i < len) w_out[i] = key_weight(weight_key(w[i]));  // -0 as 0, as for chosen positions
     }
     return;
   }

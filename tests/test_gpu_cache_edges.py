@@ -158,3 +158,29 @@ def test_decode_on_a_side_stream_with_ordered_inputs(sf):
         c.close()
     for other in res[1:]:
         assert all(torch.equal(x, y) for x, y in zip(res[0], other))
+
+
+# ---------------------------------------------------------------- signed zeros
+
+@pytest.mark.parametrize("budget", [50, 49, 12])
+def test_evict_turns_minus_zero_into_zero(sf, budget):
+    """Weights of -0 come out as 0 whether the sequence moves whole or in part,
+    in place or elsewhere; NaN stays NaN."""
+    heads, page, lens = (4, 2, 64), 16, [50, 7, 0]
+    a = attend_inputs(sf, heads, "f32", page, lens, seed=32, track=False)
+    w = torch.zeros_like(a["w"])
+    w[:, :, ::2] = -0.0
+    w[:, :, 3] = float("nan")
+    for place in ("elsewhere", "in place"):
+        w_in = w.clone()
+        w_out = torch.full_like(w, -3.0) if place == "elsewhere" else w_in
+        n, kept = a["c"].evict(a["k"].clone(), a["v"].clone(), i32(a["table"]), i32(lens), w_in, budget, n_first=4,
+                               weights_out=w_out)
+        a["c"].sync()
+        assert n.tolist() == [min(x, budget) for x in lens]
+        for s in range(2):
+            got = w_out[s, :, :int(n[s])]
+            assert torch.isnan(got[:, 3]).all()
+            got = torch.cat([got[:, :3], got[:, 4:]], 1)
+            assert not got.view(torch.int32).any()          # +0, bit for bit
+    a["c"].close()
