@@ -244,7 +244,7 @@ void free_cache(sf_cache* c) {
   if (!c) return;
   cudaFree(c->rope);
   cudaFree(c->scores);
-  cudaFree(c->lse);
+  cudaFree(c->stats);
   cudaFree(c->parts);
   cudaFree(c->arrived);
   cudaFree(c->joins);
@@ -331,7 +331,8 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * s.head_dim * sizeof(float));
   if (e == cudaSuccess && s.track_weights)
     e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * scores_ld(s) * sizeof(float));
-  if (e == cudaSuccess && s.track_weights) e = cudaMalloc(&c->lse, (size_t)s.max_seqs * s.n_q_heads * sizeof(float));
+  if (e == cudaSuccess && s.track_weights)
+    e = cudaMalloc(&c->stats, (size_t)s.max_seqs * s.n_q_heads * sizeof(float2));
   if (e == cudaSuccess) e = cudaMalloc(&c->parts, (size_t)(blocks * cache_attend_part_floats(s)) * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&c->joins, (size_t)blocks * sizeof(CacheJoin));
   if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)blocks * sizeof(unsigned));
@@ -443,7 +444,7 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.ld_w = ld_w;
   a.scores = c->scores;
   a.ld_scores = scores_ld(s);
-  a.lse = c->lse;
+  a.stats = c->stats;
   a.parts = c->parts;
   a.arrived = c->arrived;
   a.joins = c->joins;

@@ -23,7 +23,7 @@ struct sf_cache {
   int sm_count = 148;
   float* rope = nullptr;      // [max_pos][cos half | sin half]
   float* scores = nullptr;    // [max_seqs][n_q_heads][max_len, padded to 4] scaled scores in log2 units (track_weights)
-  float* lse = nullptr;       // [max_seqs][n_q_heads] log2 of each softmax denominator (track_weights)
+  float2* stats = nullptr;    // [max_seqs][n_q_heads] reference and factor of each softmax (track_weights)
   float* parts = nullptr;     // partial results of sf_cache_attend, two per block
   unsigned* arrived = nullptr;  // [blocks] arrival counters, 0 between calls
   sf::CacheJoin* joins = nullptr;  // [blocks]
@@ -69,7 +69,7 @@ struct CacheAttendArgs {
   void* out; int64_t ld_out;
   const float* w_in; float* w_out; int64_t ld_w;
   float* scores; int64_t ld_scores;
-  float* lse;
+  float2* stats;
   float* parts;       // two partial results per block: output [heads][hd], max [heads], denominator [heads]
   unsigned* arrived;  // [blocks] arrivals at a cut segment, by its first block; 0 between calls
   CacheJoin* joins;   // [blocks]

@@ -3,8 +3,7 @@
 //
 //   score_j = scale log2(e) q . k_j,  m = max_j score_j,  p_j = 2^(score_j - m)
 //   out = (sum_j p_j v_j) / (sum_j p_j)
-//   weights_j += sum over the KV head's query heads of 2^(score_j - lse),
-//   lse = m + log2(sum_j p_j)
+//   weights_j += sum over the KV head's query heads of p_j / (sum_j p_j)
 //
 // m is not kept exact: a tile whose scores stay below m + kSlack uses the old
 // m, so the maximum is reduced and sums are rescaled only while it still grows
@@ -32,6 +31,8 @@ constexpr int kBlocksPerSM = 1;
 constexpr int kLeast = 8;  // units a block takes at least
 constexpr float kSlack = 8.f;
 constexpr float kRoom = 19.f + kSlack;
+constexpr float kUnroom = 1.f / (1 << 27);  // 2^-kRoom
+static_assert(kRoom == 27.f, "kUnroom");
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -599,8 +600,11 @@ __device__ __forceinline__ void write_out(const CacheAttendArgs& a, int s, int h
   store4<T>(p, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
-__device__ __forceinline__ void write_lse(const CacheAttendArgs& a, int s, int h, float m, float l) {
-  a.lse[(int64_t)s * a.nq + h] = (m == -INFINITY ? 0.f : m) + (kRoom + log2f(l));
+// What the weights kernel needs of a row's softmax: the reference m, and the factor that makes 2^(score - m) a weight.
+// Not log2 of the denominator added to m: the sum would be rounded at the size of m (scores around 500 then cost a
+// weight 3e-5, with the pair none of that).
+__device__ __forceinline__ void write_stats(const CacheAttendArgs& a, int s, int h, float m, float l) {
+  a.stats[(int64_t)s * a.nq + h] = make_float2(m == -INFINITY ? 0.f : m, inverse(l) * kUnroom);
 }
 
 // ex2(m - top) with an empty part (m = -inf) weighing 0 even where all are.
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
         part[NH * HD + h] = top;
         part[NH * HD + NH + h] = l;
       } else {
-        write_lse(a, g.s, g.h0 + h, top, l);
+        write_stats(a, g.s, g.h0 + h, top, l);
       }
     }
     for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           const float4 o = sum.o;
           const float top = sum.top, l = sum.l;
           write_out<T>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
-          if (TRACK && d == 0) write_lse(a, g.s, g.h0 + h, top, l);
+          if (TRACK && d == 0) write_stats(a, g.s, g.h0 + h, top, l);
         }
       }
     }
@@ -920,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
             write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
                          sfac[warp][h]);
           }
-          if (TRACK && lane < g.nh) write_lse(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
+          if (TRACK && lane < g.nh) write_stats(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
         }
         __syncthreads();  // the warps' memory is free again
         u += taken;
@@ -978,7 +982,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i) sum.add_one(acc[i][col], ml[i].x, ml[i].y);
     write_out<T>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, inverse(sum.l));
-    if (a.w_out && col == 0) write_lse(a, j.s, j.h0 + h, sum.top, sum.l);
+    if (a.w_out && col == 0) write_stats(a, j.s, j.h0 + h, sum.top, sum.l);
   }
 }
 
@@ -1016,12 +1020,12 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __g
     if (j >= len) continue;
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
-      const float lse = a.lse[h + g];
+      const float2 st = a.stats[h + g];  // its first is finite or +infinity: a score of -infinity weighs 0
       const float4 x = __ldcs(sc + g * (a.ld_scores / 4));
-      w[0] += x.x == -INFINITY ? 0.f : ex2(x.x - lse);
-      w[1] += x.y == -INFINITY ? 0.f : ex2(x.y - lse);
-      w[2] += x.z == -INFINITY ? 0.f : ex2(x.z - lse);
-      w[3] += x.w == -INFINITY ? 0.f : ex2(x.w - lse);
+      w[0] += ex2(x.x - st.x) * st.y;
+      w[1] += ex2(x.y - st.x) * st.y;
+      w[2] += ex2(x.z - st.x) * st.y;
+      w[3] += ex2(x.w - st.x) * st.y;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)

@@ -184,3 +184,37 @@ def test_evict_turns_minus_zero_into_zero(sf, budget):
             got = torch.cat([got[:, :3], got[:, 4:]], 1)
             assert not got.view(torch.int32).any()          # +0, bit for bit
     a["c"].close()
+
+
+# ---------------------------------------------------------------- weights of large scores
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,page,lens", [((12, 2, 128), 16, [100, 37]), ((14, 2, 64), 16, [20003]),
+                                             ((4, 4, 64), 16, [3 + i % 60 for i in range(300)])])
+def test_weights_of_equal_large_scores(sf, heads, page, lens, dtype):
+    """All keys of a sequence the same, scores around 500 (whose fp32 step is
+    6e-5 in log2): every position gets 1 / len of each head.
+
+    Equal scores are computed alike, so that every exponential is 2^0 = 1 and
+    the denominator a count: exact.  What rounds is the reciprocal (1 u), the
+    product (1 u) and the sum over the group's heads (G u at most)."""
+    nq, nkv, hd = heads
+    a = attend_inputs(sf, heads, dtype, page, lens, seed=33)
+    rng = np.random.default_rng(34)
+    for s, n in enumerate(lens):
+        key = torch.from_numpy(rng.standard_normal((nkv, hd)).astype(np.float32)).cuda().to(a["k"].dtype)
+        for c in range(-(-n // page)):
+            a["k"][a["table"][s, c], :min(page, n - c * page)] = key
+        reach = torch.from_numpy(rng.uniform(400, 600, (nkv, nq // nkv, 1))).cuda() * hd ** 0.5
+        unit = key.double() / (key.double() ** 2).sum(-1, keepdim=True)
+        a["q"][s] = (reach * unit[:, None]).reshape(nq, hd).to(a["q"].dtype)
+    w = torch.zeros_like(a["w"])
+    out = a["c"].attend(a["q"], a["k"], a["v"], i32(a["table"]), i32(lens), weights_out=w)
+    a["c"].sync()
+    G = nq // nkv
+    for s, n in enumerate(lens):
+        want = G / n
+        assert ((w[s, :, :n].double() - want).abs() <= (G + 2) * 2.0 ** -24 * want).all()
+        assert not w[s, :, n:].any()
+    assert torch.isfinite(out).all()
+    a["c"].close()
