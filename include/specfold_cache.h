@@ -145,9 +145,10 @@ sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_
  * A sequence whose length is negative or beyond max_len or table_cols *
  * page_size counts as empty, a position on a page out of range as one of score
  * -infinity (device check).
- * Errors: as above; SF_ERR_INVALID_ARG for a scale that is not finite, for
- * weights on an object without track_weights or weights_in without
- * weights_out; SF_ERR_SHAPE for an ld_w too small. */
+ * Errors: as above; SF_ERR_INVALID_ARG for a scale that is not finite or that
+ * is not once it is multiplied by log2(e) (above 2.35e38), for weights on an
+ * object without track_weights or weights_in without weights_out;
+ * SF_ERR_SHAPE for an ld_w too small. */
 sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t ld_q, const void* k_pages,
                           const void* v_pages, int64_t n_pages, const int32_t* page_table, int S, int table_cols,
                           int64_t ld_table, const int32_t* lens, float scale, void* out, int64_t ld_out,

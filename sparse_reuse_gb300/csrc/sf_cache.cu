@@ -415,7 +415,9 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   const int64_t wq = (int64_t)s.n_q_heads * s.head_dim;
   if (bad_row(c, q, ld_q, wq, S) || bad_row(c, out, ld_out, wq, S))
     return fail(c, SF_ERR_INVALID_ARG, "q/out null, misaligned, or rows closer than their width");
-  if (!std::isfinite(scale)) return fail(c, SF_ERR_INVALID_ARG, "scale must be finite");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2))
+    return fail(c, SF_ERR_INVALID_ARG, "scale must be finite, and so must scale * log2(e)");
   if (weights_in && !weights_out) return fail(c, SF_ERR_INVALID_ARG, "weights_in without weights_out");
   if (weights_out && !s.track_weights)
     return fail(c, SF_ERR_INVALID_ARG, "the object was created without track_weights");
@@ -436,7 +438,7 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.nkv = s.n_kv_heads;
   a.hd = s.head_dim;
   a.limit = limit;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.out = out;
   a.ld_out = ld_out;
   a.w_in = weights_in;
