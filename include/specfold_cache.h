@@ -113,8 +113,9 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out);
  * it writes no query either.
  * qkv, the pools and q_out are 16-byte aligned, ld_qkv and ld_q multiples of
  * 16 bytes, the gains 16-byte aligned, the int32 arrays 4-byte.
- * Errors (before anything is enqueued): SF_ERR_INVALID_ARG (null, misaligned
- * or overlapping-by-stride argument, another device is current), SF_ERR_SHAPE
+ * Errors (before anything is enqueued): SF_ERR_INVALID_ARG (null or misaligned
+ * argument, rows closer than their width, q_out overlapping qkv otherwise than
+ * as said, another device is current), SF_ERR_SHAPE
  * (S beyond max_seqs, T above 1048576, T > S without seq),
  * SF_ERR_DEVICE_ASSERT (an earlier check fired), SF_ERR_CUDA. */
 sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_t ld_qkv, int T, const float* q_gain,
@@ -146,7 +147,8 @@ sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_
  * page_size counts as empty, a position on a page out of range as one of score
  * -infinity (device check).
  * Errors: as above; SF_ERR_INVALID_ARG for a scale that is not finite or that
- * is not once it is multiplied by log2(e) (above 2.35e38), for weights on an
+ * is not once it is multiplied by log2(e) (above 2.35e38), for out overlapping
+ * q, for weights_out overlapping weights_in in part, for weights on an
  * object without track_weights or weights_in without weights_out;
  * SF_ERR_SHAPE for an ld_w too small. */
 sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t ld_q, const void* k_pages,
@@ -176,8 +178,9 @@ sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t 
  * A sequence whose length is out of range counts as empty (lens_out 0); rows
  * from or to a page out of range are not moved (device check).
  * Errors: as above; SF_ERR_INVALID_ARG for budget < 1, a negative n_first or
- * n_recent, n_first + n_recent > budget, or k_out/v_out/table_out of which
- * only some are the input's; SF_ERR_SHAPE for ld_w too small, budget beyond
+ * n_recent, n_first + n_recent > budget, weights_out or lens_out overlapping
+ * its input in part, or k_out/v_out/table_out of which only some are the
+ * input's; SF_ERR_SHAPE for ld_w too small, budget beyond
  * max_len or beyond table_out_cols * page_size. */
 sf_status sf_cache_evict(sf_cache* cache, void* stream, const void* k_pages, const void* v_pages, int64_t n_pages,
                          const int32_t* page_table, int S, int table_cols, int64_t ld_table, const int32_t* lens,

@@ -287,6 +287,22 @@ bool bad_row(const sf_cache* c, const void* p, int64_t ld, int64_t width, int ro
   return !p || misaligned(p, 16) || (rows > 1 && (ld < width || ld * es % 16 != 0));
 }
 
+// Do two arrays of `rows` rows, of wa and wb bytes, lda and ldb bytes apart,
+// share memory?  Rows the same distance apart (columns of one wide array) are
+// compared column by column, others by the arrays' ends.
+bool rows_overlap(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, int rows) {
+  const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a), pb = (int64_t)reinterpret_cast<uintptr_t>(b);
+  if (pa + (rows - 1) * lda + wa <= pb || pb + (rows - 1) * ldb + wb <= pa) return false;
+  if (rows == 1 || lda != ldb) return true;
+  const int64_t d = ((pb - pa) % lda + lda) % lda;
+  return d < wa || d + wb > lda;
+}
+
+// Two arrays of n elements of 4 bytes that are neither the same nor apart.
+bool half_the_same(const void* a, const void* b, int64_t n) {
+  return a && b && a != b && rows_overlap(a, 0, 4 * n, b, 0, 4 * n, 1);
+}
+
 PageTable page_table(const sf_cache* c, const int32_t* table, int cols, int64_t ld, int64_t n_pages) {
   return make_page_table(table, ld, cols, c->s.page_size, n_pages);
 }
@@ -374,6 +390,9 @@ sf_status sf_cache_append(sf_cache* c, void* stream, const void* qkv, int64_t ld
   if (bad_row(c, qkv, ld_qkv, w, T) || bad_row(c, q_out, ld_q, wq, T))
     return fail(c, SF_ERR_INVALID_ARG, "qkv/q_out null, misaligned, or rows closer than their width");
   if (T > 1048576 || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
+  const int es = s.dtype == SF_BF16 ? 2 : 4;
+  if ((q_out != qkv || (T > 1 && ld_q != ld_qkv)) && rows_overlap(qkv, ld_qkv * es, w * es, q_out, ld_q * es, wq * es, T))
+    return fail(c, SF_ERR_INVALID_ARG, "q_out overlaps qkv and is not its query part");
   if ((st = check_object(c)) != SF_OK) return st;
   CacheAppendArgs a{};
   a.qkv = qkv;
@@ -425,6 +444,11 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   if (weights_out && ld_w < limit)
     return fail(c, SF_ERR_SHAPE, "ld_w=%lld below the %lld positions of a sequence", (long long)ld_w,
                 (long long)limit);
+  const int es = s.dtype == SF_BF16 ? 2 : 4;
+  if (rows_overlap(q, ld_q * es, wq * es, out, ld_out * es, wq * es, S))
+    return fail(c, SF_ERR_INVALID_ARG, "out overlaps q");
+  if (half_the_same(weights_in, weights_out, (int64_t)S * s.n_kv_heads * ld_w))
+    return fail(c, SF_ERR_INVALID_ARG, "weights_out overlaps weights_in without being the same");
   if ((st = check_object(c)) != SF_OK) return st;
   CacheAttendArgs a{};
   a.q = q;
@@ -482,6 +506,8 @@ sf_status sf_cache_evict(sf_cache* c, void* stream, const void* k_pages, const v
                 (long long)limit);
   if (budget > s.max_len || budget > (int64_t)table_out_cols * s.page_size)
     return fail(c, SF_ERR_SHAPE, "budget=%d beyond max_len=%d or the output table", budget, s.max_len);
+  if (half_the_same(weights, weights_out, (int64_t)S * s.n_kv_heads * ld_w) || half_the_same(lens, lens_out, S))
+    return fail(c, SF_ERR_INVALID_ARG, "weights_out or lens_out overlaps its input without being the same");
   if ((st = check_object(c)) != SF_OK) return st;
   CacheEvictArgs a{};
   a.k = k_pages;
