@@ -140,7 +140,8 @@ def _marshal():
     """The compiled marshalling of the paged-cache calls (csrc/sf_torch.cpp); ImportError if it is not built."""
     import torch  # noqa: F401  (the module links against torch's libraries)
     if not os.path.exists(os.path.join(_PKG, "_sf_torch.so")):
-        raise ImportError("_sf_torch.so is not built; run sparse_reuse_gb300/build.py")
+        raise ImportError("_sf_torch.so is not built; run sparse_reuse_gb300/build.py with torch and Python's headers "
+                          "installed")
     from . import _sf_torch
     return _sf_torch
 

@@ -1,9 +1,11 @@
 """Build libspecfold.so in-tree with nvcc for sm_103a (GB300).
 
 Translation units compile in parallel into sparse_reuse_gb300/_build/ and
-link into sparse_reuse_gb300/libspecfold.so; the CPython module that marshals
-torch tensors for the paged-cache calls links against it.  A rebuild is
-skipped when both are newer than every source and header.
+link into sparse_reuse_gb300/libspecfold.so, for which nvcc is enough.  Where
+torch and Python's headers are installed, the CPython module that marshals
+torch tensors for the paged-cache calls (PagedCache) is built against it.  A
+rebuild is skipped when what there is to build is newer than every source and
+header, and the module was built for the installed torch.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecfold.so")
 TORCH_EXT = os.path.join(PKG, "_sf_torch.so")  # torch argument marshalling of the paged-cache calls
+TORCH_STAMP = os.path.join(BUILD, "sf_torch.version")  # the torch it was built for
 
 SOURCES = ["sf_api.cu", "sf_gate.cu", "sf_gemm.cu", "sf_gemm_tc.cu", "sf_attn.cu", "sf_head.cu",
            "sf_cache.cu", "sf_cache_attend.cu", "sf_cache_evict.cu"]
@@ -43,10 +46,35 @@ def _inputs():
     return files
 
 
+def _torch_version():
+    """The installed torch, which the marshalling module is compiled against; None without torch or Python's headers."""
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return None
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"{torch.__version__} {sys.implementation.cache_tag}"
+
+
+def _built_for():
+    try:
+        with open(TORCH_STAMP) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TORCH_EXT):
+    outputs = [LIB]
+    version = _torch_version()
+    if version is not None:
+        if _built_for() != version:
+            return False
+        outputs.append(TORCH_EXT)
+    if not all(os.path.exists(f) for f in outputs):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -94,8 +122,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
+    version = _torch_version()
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        torch_obj = ex.submit(_compile_torch_ext)
+        torch_obj = ex.submit(_compile_torch_ext) if version is not None else None
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
@@ -103,9 +132,13 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_torch_ext(torch_obj.result())
+    if torch_obj is not None:
+        _link_torch_ext(torch_obj.result())
+        with open(TORCH_STAMP, "w") as f:
+            f.write(version)
     if verbose:
-        print(f"built {LIB}", file=sys.stderr)
+        print(f"built {LIB}" + ("" if torch_obj is not None else " (no torch: without PagedCache's marshalling)"),
+              file=sys.stderr)
     return LIB
 
 
