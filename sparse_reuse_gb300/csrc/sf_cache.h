@@ -75,7 +75,6 @@ struct CacheAttendArgs {
   CacheJoin* joins;   // [blocks]
   bool join;          // a join kernel follows
   int blocks;         // of the attention kernel
-  int least;          // units a block takes at least
   int group, nsub, heads;  // query heads of a KV head, parts they are taken in, nkv * nsub
   unsigned* err;
 };

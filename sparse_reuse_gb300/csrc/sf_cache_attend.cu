@@ -28,7 +28,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlocksPerSM = 1;
-constexpr int kLeast = 8;  // units a block takes at least
 constexpr float kSlack = 8.f;
 constexpr float kRoom = 19.f + kSlack;
 constexpr float kUnroom = 1.f / (1 << 27);  // 2^-kRoom
@@ -664,12 +663,6 @@ struct PartSum {
   }
 };
 
-// Tiles of a segment that is never cut, and that one warp takes alone where several follow one another.  300 sequences
-// of up to 250 keys, 4 heads: 26 us with 16, 39 with 4; of up to 1,000 keys: 60 with 16, 83 with 64.
-constexpr int kShort = 16;
-constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself (at most 32)
-constexpr int kWaste = 64;       // tiles a block may take beyond an even share to keep to one segment
-
 // The work is cut over the blocks in one of two ways, by the batch's lengths.
 //
 // Chunks: where there is a block for every segment, every segment is cut into
@@ -715,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           store4<T>(static_cast<T*>(a.out) + (int64_t)s * a.ld_out + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   const int64_t units = (int64_t)first[a.S] * H;
   if (units == 0) return;
-  const int64_t share = units_per_block(units, gridDim.x, a.least);
+  const int64_t share = units_per_block(units, gridDim.x, kLeast);
 
   auto segment = [&](int s, int hs) {
     Segment g;
@@ -821,24 +814,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   // ---- chunks.  Every warp works the plan out for itself (no barrier).
   if ((int64_t)filled * H <= gridDim.x && a.S <= kThreads) {
     int size = (int)share, chunks = 0, longest = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPlanTries; ++i) {
       chunks = longest = 0;
       for (int s0 = 0; s0 < a.S; s0 += 32) {
         const int s = s0 + lane;
-        const unsigned t = s < a.S ? first[s + 1] - first[s] : 0;
-        const unsigned n = (t + size - 1) / (unsigned)size, c = n ? (t + n - 1) / n : 0u;
-        chunks += __reduce_add_sync(kFull, n);
-        longest = max(longest, (int)__reduce_max_sync(kFull, c));
+        const int t = s < a.S ? first[s + 1] - first[s] : 0;
+        const int n = chunks_of(t, size), c = n ? chunk_tiles(t, n) : 0;
+        chunks += (int)__reduce_add_sync(kFull, (unsigned)n);
+        longest = max(longest, (int)__reduce_max_sync(kFull, (unsigned)c));
       }
       if (chunks * H <= (int)gridDim.x) break;
-      size += (int)quotient((int64_t)size * (chunks * H - (int)gridDim.x), gridDim.x) + 1;
+      size = wider_chunks(size, chunks * H, gridDim.x);
     }
-    if (chunks * H <= (int)gridDim.x && longest <= share + kWaste) {
+    if (plan_fits(chunks * H, longest, share, gridDim.x)) {
       if (blk >= chunks * H) return;
       int before = 0;  // chunks of the sequences in front
       for (int s0 = 0;; s0 += 32) {
         const int s = s0 + lane, t = s < a.S ? first[s + 1] - first[s] : 0;
-        const int c = ((unsigned)t + size - 1) / (unsigned)size;
+        const int c = chunks_of(t, size);
         int incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -850,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           const int l = __ffs(hit) - 1, n = __shfl_sync(kFull, c, l);
           const int r = blk - (before + __shfl_sync(kFull, incl, l) - n) * H;
           const int hs = (unsigned)r / (unsigned)n, x = r - hs * n, tiles = __shfl_sync(kFull, t, l);
-          const int each = (unsigned)(tiles + n - 1) / (unsigned)n;  // the last chunk may be short or empty
+          const int each = chunk_tiles(tiles, n);
           take(segment(s0 + l, hs), min(tiles, x * each), min(tiles, (x + 1) * each), n, blk - x, 2 * (blk - x),
                2 * blk);
           return;
@@ -877,9 +870,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       while (s < a.S && first[s + 1] == first[s]);
     }
   };
-  // A short segment is whole in the block that it starts in.
-  if (t0 > 0 && first[s + 1] - first[s] <= kShort) {
-    u += first[s + 1] - first[s] - t0;
+  if (const int skip = skipped(t0, first[s + 1] - first[s])) {
+    u += skip;
     t0 = 0;
     advance(s, hs);
   }
@@ -934,11 +926,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       }
     }
     const int64_t seg0 = u - t0;
-    const int end = !whole && u_end - u < tiles - t0 ? t0 + (int)(u_end - u) : tiles;
-    const int b0 = t0 == 0 ? blk : first_block(seg0, share), b1 = end == tiles ? blk : last_block(seg0, tiles, share);
-    take(segment(s, hs), t0, end, b1 - b0 + 1, b0, part_slot(b0, seg0, share), part_slot(blk, seg0, share));
+    const LineTake x = take_of_line(blk, u, u_end, t0, tiles, share);
+    take(segment(s, hs), t0, x.end, x.b1 - x.b0 + 1, x.b0, part_slot(x.b0, seg0, share), part_slot(blk, seg0, share));
     __syncthreads();  // the warps' memory and tables are free for the next segment
-    u += end - t0;
+    u += x.end - t0;
     t0 = 0;
     advance(s, hs);
   }
@@ -1044,17 +1035,12 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   const int most_blocks = cache_attend_blocks(sm_count);
   constexpr int NH = WarpOf<T, HD, NT>::type::kHeads;
   const int G = a.nq / a.nkv, longest = tiles_of((int)a.limit);
-  a.least = kLeast;
   a.group = G;
   a.nsub = (G + NH - 1) / NH;
   a.heads = a.nkv * a.nsub;
-  // no more blocks than the longest batch of this table could keep busy
-  const int64_t want = ((int64_t)a.S * a.heads * longest + a.least - 1) / a.least;
-  const int blocks = (int)(want < most_blocks ? want : most_blocks);
-  // a segment of t tiles has at least 1 / heads of all units: it lies in at most blocks / heads + 2 blocks, and in
-  // (t - 1) / least + 2
+  const int blocks = attend_blocks((int64_t)a.S * a.heads * longest, most_blocks);
   a.blocks = blocks;
-  a.join = (longest - 1) / a.least + 2 > kInlineParts && blocks / a.heads + 2 > kInlineParts;
+  a.join = may_need_join(longest, a.heads, blocks);
   const size_t table = (2 * (size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
   cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
                              a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);

@@ -76,13 +76,20 @@ SF_HD int checked_len(int len, int64_t limit, bool* bad) {
 
 // ---- the split of a batch's attention over thread blocks ---------------------
 //
-// The work is a line of units: sequence after sequence, head group after head
-// group, tile of kTileKeys keys after tile.  Block k takes units
-// [k * per, (k + 1) * per).  A segment (one sequence and head group) that lies
-// in one block is finished there.  One that is cut leaves a partial result per
-// block; a block is the inside or the end of at most one cut segment (its
-// first) and the start of at most one (its last), so two partial slots and one
-// arrival counter per block are enough for any batch.
+// A segment is one sequence and head group, cut into tiles of kTileKeys keys.
+// A batch is split in one of two ways:
+//
+//   chunks  every segment into equal runs of tiles, at most one per block
+//           (plan_fits below);
+//   line    sequence after sequence, head group after head group, tile after
+//           tile: block k takes units [k * per, (k + 1) * per) of that line,
+//           but a segment of up to kShort tiles whole, in the block that it
+//           starts in.
+//
+// A segment that lies in one block is finished there.  One that is cut leaves
+// a partial result per block; a block is the inside or the end of at most one
+// cut segment (its first) and the start of at most one (its last), so two
+// partial slots and one arrival counter per block are enough for any batch.
 
 constexpr int kTileKeys = 16;
 
@@ -107,5 +114,55 @@ SF_HD int last_block(int64_t first, int tiles, int64_t per) { return (int)quotie
 
 // Partial slot of block `block` for the cut segment starting at `first`.
 SF_HD int part_slot(int block, int64_t first, int64_t per) { return 2 * block + (first > block * per ? 1 : 0); }
+
+// Tiles of a segment that a line does not cut, and that one warp takes alone where several follow one another.  300
+// sequences of up to 250 keys, 4 heads: 26 us with 16, 39 with 4; of up to 1,000 keys: 60 with 16, 83 with 64.
+constexpr int kShort = 16;
+constexpr int kLeast = 8;         // units a block takes at least
+constexpr int kInlineParts = 24;  // partial results that the last block to arrive joins itself (at most 32)
+constexpr int kWaste = 64;        // tiles a block may take beyond an even share to keep to one segment
+constexpr int kPlanTries = 4;     // chunk sizes that are tried
+
+// Blocks of a launch that has `most`: no more than the longest batch of the table could keep busy.
+SF_HD int attend_blocks(int64_t longest_units, int most) {
+  const int64_t want = (longest_units + kLeast - 1) / kLeast;
+  return (int)(want < most ? want : most);
+}
+
+// May a segment lie in more than kInlineParts blocks?  One of t tiles lies in
+// at most (t - 1) / kLeast + 2, and, having at least 1 / heads of all units, in
+// at most blocks / heads + 2.
+SF_HD bool may_need_join(int longest_tiles, int heads, int blocks) {
+  return (longest_tiles - 1) / kLeast + 2 > kInlineParts && blocks / heads + 2 > kInlineParts;
+}
+
+// -- line
+
+// Units in front of a block's work: what is left, from tile t0 on, of a short segment of an earlier block.
+SF_HD int skipped(int t0, int tiles) { return t0 > 0 && tiles <= kShort ? tiles - t0 : 0; }
+
+// What the block at unit u, tile t0 of a segment, takes of it: tiles [t0, end), as one of the blocks b0 .. b1.
+struct LineTake {
+  int end, b0, b1;
+};
+SF_HD LineTake take_of_line(int block, int64_t u, int64_t u_end, int t0, int tiles, int64_t per) {
+  const int64_t first = u - t0;
+  const int end = tiles > kShort && u_end - u < tiles - t0 ? t0 + (int)(u_end - u) : tiles;
+  return LineTake{end, t0 == 0 ? block : first_block(first, per), end == tiles ? block : last_block(first, tiles, per)};
+}
+
+// -- chunks of at most `size` tiles
+
+SF_HD int chunks_of(int tiles, int size) { return (int)(((unsigned)tiles + size - 1) / (unsigned)size); }
+// Tiles of each of a segment's n chunks; the last may be short or empty.
+SF_HD int chunk_tiles(int tiles, int n) { return (int)((unsigned)(tiles + n - 1) / (unsigned)n); }
+// The next size to try where `chunks` are more than there are blocks.
+SF_HD int wider_chunks(int size, int chunks, int blocks) {
+  return size + (int)quotient((int64_t)size * (chunks - blocks), blocks) + 1;
+}
+// Is there a block for every chunk, and none of them much longer than an even share?
+SF_HD bool plan_fits(int chunks, int longest, int64_t share, int blocks) {
+  return chunks <= blocks && longest <= share + kWaste;
+}
 
 }  // namespace sf
