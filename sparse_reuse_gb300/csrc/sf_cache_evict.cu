@@ -74,10 +74,13 @@ static_assert((0xff800000u - kFirstKey) >> kFirstShift < (uint32_t)kBins, "bins 
 // The need-th largest candidate key is found by counting keys into bins and
 // narrowing [lo, hi] to the bin that holds it: first with bins of a fixed size,
 // counted while the weights arrive, then, while the bin holds more than kList
-// keys, in up to kBins equal parts of it (two such passes at most).  The lowest
-// bin is never counted (if the others do not reach, it is the one), which
-// keeps the usual crowd of zero weights out of the shared-memory atomics.  The
-// keys of the last bin are ranked by comparing all pairs.
+// keys, in up to kBins equal parts of it: two such passes at most (shifts 9
+// and 0), or three where the first cut's lowest bin is the one, as for a
+// threshold among zeros (21, 9, 0) or negative weights (21, 10, 0).  The lowest
+// bin is never counted (if the others do not reach, it is the one), which keeps
+// the usual crowd of zero weights out of the first cut's shared-memory atomics;
+// in later passes equal keys of a warp add once.  The keys of the last bin are
+// ranked by comparing all pairs.
 //
 // The choice is two bitmaps, positions certainly kept and positions at the
 // threshold, of which the first `ties` are kept; a scan of their populations
