@@ -218,3 +218,88 @@ def test_weights_of_equal_large_scores(sf, heads, page, lens, dtype):
         assert not w[s, :, n:].any()
     assert torch.isfinite(out).all()
     a["c"].close()
+
+
+# ---------------------------------------------------------------- sums of long sequences
+
+U = 2.0 ** -24
+SUMS = [
+    # heads, dtype, lens: chunks and the join kernel, then a line
+    ((2, 1, 64), "bf16", [262144, 5]),
+    ((12, 1, 128), "bf16", [262144]),
+    ((2, 1, 64), "f32", [262144, 5]),
+    ((10, 2, 128), "f32", [131071, 100001]),
+    ((8, 8, 64), "bf16", [30000] * 25),
+]
+
+
+def _bounds(q, k, v, heads, tiles_of_a_warp, parts):
+    """Weights, output and their bounds in float64 for one sequence, q [nkv, G, hd], k and v [n, nkv, hd].
+
+    A term of the output is added into a warp's sum with the others of its tiles (two products of 16 keys a tile, in
+    any order inside the tensor core), which is rescaled at most once a tile; then 8 warps' sums are scaled and added;
+    then the parts (at most one a block), by 8 or 16 groups, then the groups' sums, each scaled; then the quotient (3
+    roundings):
+        D = 33 tiles + 16 + 2 (parts / 8 + 1 + 16) + 3 roundings of 2u of sum p |v| (2u: tensor cores may truncate),
+    and the same for the denominator.  A score is two chains of hd / 2 products, their sum, and the scale:
+        d = (hd / 2 + 4) 2u scale sum |q k|,
+    which moves the output by d of sum p |v - out| <= sum p |v| + |out|, and a weight by 2 d of itself.  The
+    exponential is good to 4u, and two bf16 numbers for a weight to 2^-16."""
+    hd = heads[2]
+    scale = hd ** -0.5
+    s = torch.einsum("cgd,ncd->cgn", q, k) * scale
+    p = torch.softmax(s, -1)
+    out = torch.einsum("cgn,ncd->cgd", p, v)
+    mag = torch.einsum("cgn,ncd->cgd", p, v.abs())
+    d = (hd / 2 + 4) * 2 * U * scale * torch.einsum("cgd,ncd->cgn", q.abs(), k.abs()).amax(-1)
+    D = 33 * tiles_of_a_warp + 16 + 2 * (parts / 8 + 1 + 16) + 3
+    r = 2 * D * 2 * U + 4 * U + 2.0 ** -16
+    return p, out, d[..., None] * (mag + out.abs()) + r * mag, 2 * d + r
+
+
+@pytest.mark.parametrize("heads,dtype,lens", SUMS)
+def test_sums_of_long_sequences(sf, heads, dtype, lens):
+    """Outputs and weights within a bound over the real depth of the sums, which
+    does not let pass an output of zeros or one that lacks a block's keys."""
+    from test_gpu_cache import DT, E, make_pages
+    nq, nkv, hd = heads
+    page, G = 64, nq // nkv
+    table, total = make_pages(np.random.default_rng(8), lens, page)
+    g = torch.Generator("cuda").manual_seed(4)
+    k, v = (torch.randn((total, page, nkv, hd), generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    q = (2 * torch.randn((len(lens), nq, hd), generator=g, device="cuda")).to(DT[dtype])
+    c = sf.PagedCache(n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=dtype, page_size=page, max_seqs=len(lens),
+                      max_len=max(lens), max_pos=16, track_weights=True)
+    w = torch.zeros((len(lens), nkv, max(lens)), device="cuda")
+    out = c.attend(q, k, v, i32(table), i32(lens), weights=w)
+    c.sync()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    units = sum(-(-n // 16) for n in lens) * nkv
+    # a block takes at most an even share, rounded up, and 64 tiles; a warp takes every eighth tile of a segment
+    share = -(-units // sms) + 64
+    e = E[dtype]
+    for s in sorted({0, 1, len(lens) - 1} & set(range(len(lens)))):
+        n = lens[s]
+        idx = np.arange(n)
+        slot = torch.from_numpy(table[s, idx // page].astype(np.int64) * page + idx % page).cuda()
+        ks, vs = (x.view(-1, nkv, hd)[slot].double() for x in (k, v))
+        per_block = min(-(-n // 16), share)
+        p, ref, tol, rel = _bounds(q[s].double().view(nkv, G, hd), ks, vs, heads, -(-per_block // 8), sms)
+        tol = tol * (1 + e) + e * ref.abs()
+        err = (out[s].double().view(nkv, G, hd) - ref).abs()
+        assert (err <= tol).all(), (err - tol).max().item()
+        want = p.sum(1)
+        werr = (w[s, :, :n].double() - want).abs()
+        assert (werr <= (p * rel[..., None]).sum(1) + G * U * want).all()
+        assert not w[s, :, n:].any()
+        if n < 1000:
+            continue
+        # mistakes that the bound has to see, made in the reference
+        assert not (ref.abs() <= tol).all()
+        for lost in (slice(0, n // 200), slice(n // 2, n // 2 + n // 200)):
+            part = p.clone()
+            part[..., lost] = 0
+            less = torch.einsum("cgn,ncd->cgd", part / part.sum(-1, keepdim=True), vs)
+            assert not ((less - ref).abs() <= tol).all()
+            assert not ((part.sum(1) - want).abs() <= (p * rel[..., None]).sum(1) + G * U * want).all()
+    c.close()
