@@ -303,3 +303,40 @@ def test_sums_of_long_sequences(sf, heads, dtype, lens):
             assert not ((less - ref).abs() <= tol).all()
             assert not ((part.sum(1) - want).abs() <= (p * rel[..., None]).sum(1) + G * U * want).all()
     c.close()
+
+
+# ---------------------------------------------------------------- short sequences in objects for long ones
+
+@pytest.mark.parametrize("heads,dtype,lens", [((12, 2, 128), "bf16", [512]), ((40, 8, 128), "bf16", [1000, 0, 1, 2000]),
+                                              ((4, 2, 64), "f32", [700, 33]), ((8, 8, 64), "bf16", [60] * 40)])
+def test_attend_in_an_object_for_long_sequences(sf, heads, dtype, lens):
+    """An object and a table for 262,144 positions: the launch is planned for
+    those, the sequences are far shorter."""
+    page = 64
+    a = attend_inputs(sf, heads, dtype, page, lens, seed=35, cols=4096)
+    a["c"].close()
+    nq, nkv, hd = heads
+    a["c"] = c = sf.PagedCache(n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=dtype, page_size=page,
+                               max_seqs=len(lens), max_len=262144, max_pos=16, track_weights=True)
+    w = torch.zeros((len(lens), nkv, 262144), device="cuda")
+    out = c.attend(a["q"], a["k"], a["v"], i32(a["table"]), i32(lens), weights=w)
+    # a table cut to the columns that the batch needs plans the call for those, whatever the object holds
+    cols = -(-max(lens) // page)
+    less = c.attend(a["q"], a["k"], a["v"], i32(a["table"])[:, :cols], i32(lens))
+    c.sync()
+    check_attend(heads, dtype, page, a, out, w, w_in=torch.zeros_like(w))
+    check_attend(heads, dtype, page, a, less, None)
+    assert not out[[s for s, n in enumerate(lens) if n == 0]].any()
+    c.close()
+
+
+@pytest.mark.parametrize("kind", ["spread", "few values", "equal", "any"])
+@pytest.mark.parametrize("heads,lens,budget", [((1, 1, 64), [9000, 8999, 300], 4000), ((1, 1, 64), [300, 40, 269], 20),
+                                               ((2, 2, 64), [5, 9, 0, 33], 4), ((2, 2, 64), [2047] * 6, 1000)])
+def test_evict_in_an_object_for_long_sequences(sf, monkeypatch, heads, lens, budget, kind):
+    """Clusters of eight blocks with tables for 262,144 positions: few weights a
+    block, or none in most of them."""
+    import test_gpu_cache_batches as batches
+    make = batches.make_pages
+    monkeypatch.setattr(batches, "make_pages", lambda rng, lens, page, cols=None: make(rng, lens, page, cols=cols or 4096))
+    batches.run_evict(sf, 7, heads, "bf16", 64, lens, budget, 1, 2, kind, max_len=262144)
