@@ -470,7 +470,9 @@ class PagedCache:
     lens int32 [S].  A layer's prefix buffer of SpecFold.verify, viewed as
     [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool, so
     that append can write the prefix of a pass; what evict leaves is read by
-    attend only (its keys keep their original positions).
+    attend only (its keys keep their original positions).  attend and evict
+    plan for the longest sequence that the table's columns could hold: pass
+    table[:, :columns in use] where the sequences are far shorter.
     Tensors must be on the object's device, of the documented type and shape
     with contiguous rows (ValueError otherwise).  Work runs on `stream` (a
     torch stream or its handle; default: the current one of the device); the

@@ -675,7 +675,7 @@ struct PartSum {
 //
 // Line: otherwise, or where a chunk would be more than kWaste tiles longer than
 // an even share, blocks walk equal parts of the line of units
-// (sf_cache_index.h).  Up to there chunks do no worse: 80 blocks saturate DRAM.
+// (sf_cache_index.h).  kWaste has measurements on both sides there.
 //
 // The 8 warps of a block take the tiles of a segment in turn, or, where short
 // segments follow one another on a line, one segment each (300 sequences of up

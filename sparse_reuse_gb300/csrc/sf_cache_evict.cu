@@ -555,11 +555,15 @@ int select_cluster(int64_t limit, int64_t heads, int sm_count) {
   return cl;
 }
 
-// Threads of a selection block: 512, but 1,024 for more than kSelWide weights
-// while there is an SM for every block (66 heads of up to 5,001 weights: 14.2
-// against 15.9 us), and 128 for up to kSelNarrow weights where 512 would not
-// all be resident at once (488 heads of 32 weights: 7.3 against 9.6 us; with
-// few heads 512 are 0.3 us faster).
+// Threads of a selection block: 512, but 1,024 for more than kSelWide weights a
+// block while there is an SM for every block: with 66 (sequence, head) pairs the
+// whole eviction to 64 positions takes, with 1,024 and 512 threads, 8.9 and 8.9 us
+// for 5,001 weights, 9.8 and 10.1 for 8,000, 11.7 and 12.1 for 12,000, 13.1 and
+// 14.0 for 16,384, 19.5 and 21.8 for 32,768; with 128 pairs 9.7 and 9.2, 10.6 and
+// 10.4, 12.4 and 12.3, 14.0 and 14.3, 23.2 and 27.1; up to 3,500 weights 512 are
+// 0.2 to 1 us faster.  And 128 for up to kSelNarrow weights where 512 would not
+// all be resident at once (488 heads of 32 weights: 7.3 against 9.6 us; with few
+// heads 512 are 0.3 us faster).
 constexpr int kSelWide = 4096, kSelNarrow = 512;
 
 template <int LANES>
