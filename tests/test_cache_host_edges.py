@@ -30,8 +30,8 @@ OVERLAPS = [
     ("append", APPEND, dict(qkv=FAR, q_out=FAR), "q_out"),                             # packed over the rows it reads
     ("append", APPEND, dict(qkv=FAR, q_out=FAR + 512, ld_q=512), "q_out"),             # over the keys
     ("append", APPEND, dict(qkv=FAR, ld_qkv=768, q_out=FAR + 1024, ld_q=768), None),   # beside the row
-    ("append", APPEND, dict(qkv=FAR, q_out=FAR + 3 * 1024), None),                     # right behind the last row
-    ("append", APPEND, dict(qkv=FAR, q_out=FAR + 3 * 1024 - 16), "q_out"),
+    ("append", APPEND, dict(qkv=FAR, q_out=FAR + 2 * 1024, T=2), None),                # right behind the last row
+    ("append", APPEND, dict(qkv=FAR, q_out=FAR + 2 * 1024 - 16, T=2), "q_out"),
     ("append", APPEND, dict(qkv=FAR, q_out=FAR - 3 * 512), None),                      # right before the first
     ("attend", ATTEND, dict(q=FAR, out=FAR), "out"),
     ("attend", ATTEND, dict(q=FAR, out=FAR, S=1), "out"),

@@ -48,3 +48,22 @@ def test_outputs_come_from_the_memory_of_their_stream(by):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     head.close()
     ctx.close()
+
+
+def test_the_default_stream_by_its_handle():
+    """Handle 0 names the default stream, whichever is current."""
+    import sparse_reuse_gb300 as sf
+    cfg = synth.CONFIGS["tiny"].with_(n_layers=2)
+    wl = synth.make_workload(cfg, 6, device="cuda")
+    ctx = sf.from_config(cfg, wl.weights)
+    want = [t.clone() for t in ctx.verify(wl.hidden, wl.parents, wl.prefix_k, wl.prefix_v, 0.1)]
+    ctx.sync()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for stream in (0, torch.cuda.default_stream()):
+            got = ctx.verify(wl.hidden, wl.parents, wl.prefix_k, wl.prefix_v, 0.1, stream=stream)
+            ctx.sync(stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ctx.close()
