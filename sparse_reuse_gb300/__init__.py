@@ -372,13 +372,17 @@ class SpecFold:
         parent = np.asarray(parent, dtype=np.int32)
         R, Bp = parent.shape
         L, nl = self.shapes.block_len, self.shapes.n_layers
-        P = int(prefix_k.shape[2]) if prefix_k is not None and prefix_k.dim() == 5 else 0
+        P = 0 if prefix_k is None else int(prefix_k.shape[2])
+        row = self.shapes.n_kv_heads * self.shapes.head_dim
         for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)):
             if t is not None and prefix_k is not None:  # without keys there is no prefix
-                want = (nl, R, P, self.shapes.n_kv_heads, self.shapes.head_dim)
-                if tuple(t.shape) != want:
-                    raise ValueError(f"{name} must be [n_layers, R, P, n_kv_heads, head_dim] = {list(want)}, with P "
-                                     f"of prefix_k: got {list(t.shape)}")
+                # the heads may be flattened; layers behind the context's own are not read, nor, of one layer, requests
+                requests = int(t.shape[1])
+                if t.shape[0] < nl or requests < R or (requests > R and nl > 1) or t.shape[2] != P \
+                        or t.shape[3:].numel() != row:
+                    raise ValueError(f"{name} must be [n_layers, R, P, n_kv_heads, head_dim] = "
+                                     f"{[nl, R, P, self.shapes.n_kv_heads, self.shapes.head_dim]} (P: prefix_k's): got "
+                                     f"{list(t.shape)}")
         for name, t in (("hidden", hidden), ("prefix_k", prefix_k), ("prefix_v", prefix_v), ("out", out),
                         ("fold", fold), ("src", src), ("rc_count", rc_count)):
             # the pass reads and writes dense arrays: a slice of a longer prefix, say, has other strides

@@ -41,13 +41,18 @@ def test_dense_prefixes_pass(sf, ctx):
     a = _args()
     short = {n: a[n][:, :, :32].contiguous() for n in ("prefix_k", "prefix_v")}
     _reaches_the_library(sf, ctx, dict(a, **short))
+    # flattened heads, and a buffer with more layers than the context
+    _reaches_the_library(sf, ctx, dict(a, prefix_k=a["prefix_k"].flatten(3)))
+    _reaches_the_library(sf, ctx, dict(a, prefix_v=torch.zeros(3, 2, 48, 2, 64)))
+    empty = torch.zeros(2, 2, 0, 2, 64)
+    _reaches_the_library(sf, ctx, dict(a, prefix_k=empty, prefix_v=empty))
 
 
 @pytest.mark.parametrize("name,change", [
     ("prefix_k", lambda t: t[:, :, :32]), ("prefix_v", lambda t: t[:, :, :32]), ("hidden", lambda t: t[..., ::2]),
     ("out", lambda t: t.transpose(1, 2)), ("prefix_k", lambda t: t[0]), ("prefix_k", lambda t: t[:1]),
     ("prefix_v", lambda t: t[:, :1].contiguous()), ("prefix_v", lambda t: t[:, :, :32].contiguous()),
-    ("prefix_k", lambda t: t.view(2, 2, 48, 4, 32))])
+    ("prefix_k", lambda t: t[..., :32].contiguous()), ("prefix_v", lambda t: t[:, :, :0].contiguous())])
 def test_other_layouts_are_refused(ctx, name, change):
     a = _args()
     a[name] = change(a[name])
