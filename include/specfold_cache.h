@@ -147,7 +147,8 @@ sf_status sf_cache_append(sf_cache* cache, void* stream, const void* qkv, int64_
  *            j >= lens[s] are not touched.  ld_w >= min(max_len, table_cols *
  *            page_size).
  * What else is in the batch changes results by rounding only (the sums are
- * split by the batch's total length); the same call gives the same bits.  Values: keys, values and queries as stored; products and sums fp32.
+ * split by the batch's total length); the same call gives the same bits.
+ * Values: keys, values and queries as stored; products and sums fp32.
  * NaN and infinite values, and NaN and +infinite scores, among the live
  * positions make the outputs that they enter non-finite; a score of -infinity
  * weighs nothing.  What pools hold behind a sequence's length is never read.

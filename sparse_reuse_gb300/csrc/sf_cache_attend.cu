@@ -177,9 +177,9 @@ struct Ring {
 //
 // P enters as the sum of two bf16 numbers, twice the PV steps: at most 2^-16 of
 // each p_j is lost (with one number 2^-8), up or down, where rounding to bf16
-// loses up to 2^-8 of the sum.  The denominator adds
-// the p_j in fp32.  At 131,071 keys 6 to 12 of 3,584 outputs are not the nearest
-// bf16 to the exact value; with fp32 weights throughout it is 2 to 8.
+// loses up to 2^-8 of the sum.  The denominator adds the p_j in fp32.  At
+// 131,071 keys 6 to 12 of 3,584 outputs are not the nearest bf16 to the exact
+// value; with fp32 weights throughout it is 2 to 8.
 template <int HD, int NT>
 struct WarpBf16 {
   template <bool FIRST>
