@@ -96,11 +96,36 @@ typedef struct sf_cache_shapes {
  * error. */
 sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out);
 
+/* What sf_cache_create leaves at its default: zeros are the defaults. */
+enum { SF_ROTARY_HALVES = 0, SF_ROTARY_NEIGHBOURS = 1 };
+typedef struct sf_cache_options {
+  int rotary_layout;       /* pairs (j, j + rotary_dim/2), or SF_ROTARY_NEIGHBOURS: (2j, 2j + 1) */
+  int rotary_dim;          /* the first dimensions of a head that positions turn; a multiple of 16, 0 = head_dim */
+  const double* inv_freq;  /* host [rotary_dim / 2]: angle of one position for every pair; NULL:
+                              rope_theta^(-2j/rotary_dim).  Copied. */
+  double rotary_magnitude; /* sine and cosine are multiplied by it (queries and keys alike); 0 = 1 */
+  int max_rows;            /* rows of a call of sf_cache_attend_rows, sequences of one of sf_cache_attend_shared, up to
+                              1048576; 0: neither is called.  A workspace of 2 * SMs * 256 * (head_dim + 2) * 4 bytes
+                              (bf16; a quarter of it for fp32), and min(max_rows, max_seqs) * n_q_heads *
+                              (head_dim + 2) * 4 bytes. */
+} sf_cache_options;
+
+/* The same with options (NULL: none).
+ * Errors: also SF_ERR_INVALID_ARG for an unknown layout, a magnitude that is
+ * negative or not finite (nor may 1 / magnitude in fp32 be infinite), a
+ * frequency that is not finite, a negative size; SF_ERR_UNSUPPORTED for a
+ * rotary_dim that is not a multiple of 16 up to head_dim, max_rows beyond its
+ * limit. */
+sf_status sf_cache_create_with(const sf_cache_shapes* shapes, const sf_cache_options* options, sf_cache** out);
+
 /* Norm, rotate and store the T new rows of a layer: for every row t
  *   q, k of each head:  x / sqrt(mean(x^2) + rms_eps) * gain  (where the gain is
- *                       given), then the rotate-half rotation at position
- *                       pos[t] (pairs (j, j + head_dim/2), angle
- *                       pos * rope_theta^(-2j/head_dim));
+ *                       given; the mean is the whole head's), then the
+ *                       rotation at position pos[t]: pairs (a, b) =
+ *                       (j, j + head_dim/2) become (a cos - b sin, b cos +
+ *                       a sin) of the angle pos * rope_theta^(-2j/head_dim);
+ *                       or as the options say, dimensions past rotary_dim as
+ *                       they are;
  *   q -> q_out[t]; k and v -> position index[t] of sequence seq[t].
  * Computed in fp32, rounded once to dtype.
  *   qkv      device [T] rows of dtype, ld_qkv elements apart: the row's
@@ -164,6 +189,72 @@ sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t 
                           const void* v_pages, int64_t n_pages, const int32_t* page_table, int S, int table_cols,
                           int64_t ld_table, const int32_t* lens, float scale, void* out, int64_t ld_out,
                           const float* weights_in, float* weights_out, int64_t ld_w);
+
+/* Attention of blocks of rows: each sequence's rows over all of its cached
+ * positions, with no mask among the rows (a denoising block over its prefix, a
+ * decoder's rows over an encoder's states):
+ *   rows of sequence s = starts[s] .. starts[s+1] - 1;  for each of them, t,
+ *   p_h[j] = softmax over j < lens[s] of scale * q[t,h] . k[s,j,kv(h)]
+ *   out[t,h] = sum_j p_h[j] v[s,j,kv(h)],   kv(h) = h / (n_q_heads / n_kv_heads)
+ *   lse[t,h] = ln sum_j exp(scale * q[t,h] . k[s,j,kv(h)])
+ * Rows of a sequence of length 0 get zeros and an lse of -infinity; so does a
+ * head of which every score is -infinity where its values are finite.  Rows in
+ * front of starts[0] and from starts[S] on are left as they were.
+ *   q        device [T] rows of n_q_heads * head_dim elements, ld_q apart.
+ *   starts   device int32 [S + 1], 0 <= starts[0] <= starts[1] ... <= T.  Where
+ *            they do not ascend so, nothing is written (device check).
+ *   out      device [T] rows likewise, ld_out apart; not overlapping q.
+ *   lse      device fp32 [T, n_q_heads] or NULL; not overlapping q or out.
+ * Products and sums are fp32.
+ * The rest as for sf_cache_attend: what else is in the batch changes results
+ * by rounding only, the same call gives the same bits; NaN and infinities;
+ * lengths and pages out of range.  The workspace is the object's.
+ * Errors: as above; SF_ERR_INVALID_ARG for an object without max_rows, a scale
+ * as for sf_cache_attend, overlapping outputs; SF_ERR_SHAPE for T beyond
+ * max_rows. */
+sf_status sf_cache_attend_rows(sf_cache* cache, void* stream, const void* q, int64_t ld_q, int T, const void* k_pages,
+                               const void* v_pages, int64_t n_pages, const int32_t* page_table, int S, int table_cols,
+                               int64_t ld_table, const int32_t* lens, const int32_t* starts, float scale, void* out,
+                               int64_t ld_out, float* lse);
+
+/* Attention of one new token per sequence where groups of sequences share a
+ * prefix: sequences starts[g] .. starts[g+1] - 1 see the prefix_lens[g]
+ * positions of prefix g, then the lens[s] positions of their own, as if these
+ * lay in one table.  A prefix is read once for its group (per 256 query
+ * vectors), not once per sequence.  Sequences in front of starts[0] and from
+ * starts[G] on have no prefix.
+ *   q, out   device [S] rows as for sf_cache_attend; lse [S, n_q_heads] or NULL.
+ *   page_table, lens            the sequences' own positions, [S].
+ *   prefix_table, prefix_lens   device int32 [G, prefix_cols], rows ld_prefix
+ *            apart, and [G]; pages of the same pools.
+ *   starts   device int32 [G + 1], 0 <= starts[0] <= ... <= S.  Where they do
+ *            not ascend so, nothing is written (device check).
+ * A prefix and a sequence's own positions may hold up to max_len each.
+ * Arithmetic, checks and workspace as for sf_cache_attend (own positions) and
+ * sf_cache_attend_rows (prefixes); the two are joined in fp32.
+ * Errors: as for sf_cache_attend_rows, S taking the place of T; G < 1. */
+sf_status sf_cache_attend_shared(sf_cache* cache, void* stream, const void* q, int64_t ld_q, const void* k_pages,
+                                 const void* v_pages, int64_t n_pages, const int32_t* page_table, int S,
+                                 int table_cols, int64_t ld_table, const int32_t* lens, const int32_t* prefix_table,
+                                 int G, int prefix_cols, int64_t ld_prefix, const int32_t* prefix_lens,
+                                 const int32_t* starts, float scale, void* out, int64_t ld_out, float* lse);
+
+/* Turn keys in the cache to other positions: the key at place i < lens[s] of
+ * sequence s and KV head c, which append rotated at position pos_from[s,c,i],
+ * becomes the one of position pos_to[s,c,i] (rotation by the difference, in the
+ * object's layout, dimensions and frequencies; rotary_magnitude is in the key
+ * already).  Computed in fp32, rounded once to dtype.
+ *   pos_from, pos_to   device int32 [S, n_kv_heads, ld_pos]; pos_to NULL = the
+ *            place i.  evict's `kept` is a pos_from where positions are
+ *            places.  Where either is negative the key stays as it is.
+ * What an eviction left in dense pages becomes so a prefix for sf_verify.
+ * A sequence longer than ld_pos counts as out of range (nothing of it is
+ * turned, device check), so does a position from max_pos on (that key stays).
+ * Pages are distinct: a key that two entries reach would be turned twice.
+ * Errors: as above; ld_pos < 1. */
+sf_status sf_cache_reposition(sf_cache* cache, void* stream, void* k_pages, int64_t n_pages, const int32_t* page_table,
+                              int S, int table_cols, int64_t ld_table, const int32_t* lens, const int32_t* pos_from,
+                              const int32_t* pos_to, int64_t ld_pos);
 
 /* Keep at most `budget` positions of every sequence, chosen per KV head by
  * accumulated attention weight, and move them to the front:

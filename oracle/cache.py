@@ -61,3 +61,43 @@ def choose(weights, n, budget, n_first, n_recent):
     rest.sort(key=lambda j: (1, 0.0, j) if np.isnan(weights[j]) else (0, -float(weights[j]) + 0.0, j))
     kept |= set(rest[:budget - n_first - n_recent])
     return sorted(kept)
+
+
+def frequencies(dim, theta, factor=1.0):
+    """theta^(-2j/dim) / factor of every pair j."""
+    return float(theta) ** (-2.0 * np.arange(dim // 2) / dim) / factor
+
+
+def turn(x, steps, freq, layout="half", magnitude=1.0):
+    """[..., heads, hd] turned by steps [..., 1 or heads] positions: the first
+    2 len(freq) dimensions as complex numbers times magnitude e^{i steps freq},
+    the others as they are.  layout "half": pairs (j, j + len(freq)),
+    "interleaved": (2j, 2j + 1)."""
+    x, freq = np.asarray(x, F64), np.asarray(freq, F64)
+    half = len(freq)
+    z = magnitude * np.exp(1j * np.asarray(steps, F64)[..., None] * freq)
+    out = x.copy()
+    if layout == "half":
+        z = z * (x[..., :half] + 1j * x[..., half:2 * half])
+        out[..., :half], out[..., half:2 * half] = z.real, z.imag
+    else:
+        z = z * (x[..., 0:2 * half:2] + 1j * x[..., 1:2 * half:2])
+        out[..., 0:2 * half:2], out[..., 1:2 * half:2] = z.real, z.imag
+    return out
+
+
+def attend_rows(q, k, v, scale):
+    """q [R, nq, hd], k and v [n, nkv, hd] -> out [R, nq, hd], lse [R, nq],
+    weights [R, nq, n]; without keys zeros and -infinity."""
+    q, k, v = (np.asarray(t, F64) for t in (q, k, v))
+    R, nq, n = q.shape[0], q.shape[1], k.shape[0]
+    out, lse, w = np.zeros_like(q), np.full((R, nq), -np.inf), np.zeros((R, nq, n))
+    for h in range(nq if n else 0):
+        c = h // (nq // k.shape[1])
+        s = q[:, h] @ k[:, c].T * scale
+        top = s.max(1, keepdims=True)
+        e = np.exp(s - top)
+        w[:, h] = e / e.sum(1, keepdims=True)
+        lse[:, h] = top[:, 0] + np.log(e.sum(1))
+        out[:, h] = w[:, h] @ v[:, c]
+    return out, lse, w

@@ -10,6 +10,7 @@ streams only.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import List, Optional, Sequence
 
@@ -32,7 +33,9 @@ EXPORTS = ["sf_create", "sf_verify", "sf_set_debug", "sf_set_rho_dump", "sf_set_
            "sfk_gemm_bf16", "sfk_gate_noalloc", "sf_inject_stall",
            "sf_head_create", "sf_head_verify", "sf_head_last_error", "sf_head_destroy",
            "sf_cache_create", "sf_cache_append", "sf_cache_attend", "sf_cache_evict", "sf_cache_sync_status",
-           "sf_cache_last_error", "sf_cache_destroy"]
+           "sf_cache_last_error", "sf_cache_destroy", "sf_cache_create_with", "sf_cache_reposition",
+           "sf_cache_attend_rows", "sf_cache_attend_shared"]
+SF_ROTARY_HALVES, SF_ROTARY_NEIGHBOURS = 0, 1
 
 
 class SfShapes(ctypes.Structure):
@@ -58,6 +61,12 @@ class SfCacheShapes(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("page_size", ctypes.c_int), ("max_seqs", ctypes.c_int),
                 ("max_len", ctypes.c_int), ("max_pos", ctypes.c_int), ("rms_eps", ctypes.c_float),
                 ("rope_theta", ctypes.c_float), ("track_weights", ctypes.c_int)]
+
+
+class SfCacheOptions(ctypes.Structure):
+    _fields_ = [("rotary_layout", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("rotary_magnitude", ctypes.c_double),
+                ("max_rows", ctypes.c_int)]
 
 
 class SfStats(ctypes.Structure):
@@ -109,6 +118,13 @@ def _load() -> ctypes.CDLL:
                                     i64]
     lib.sf_cache_evict.argtypes = [vp, vp, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, i64, c_int, c_int, c_int, vp,
                                    vp, i64, vp, c_int, i64, vp, vp, vp]
+    lib.sf_cache_create_with.argtypes = [ctypes.POINTER(SfCacheShapes), ctypes.POINTER(SfCacheOptions),
+                                         ctypes.POINTER(vp)]
+    lib.sf_cache_reposition.argtypes = [vp, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, vp, i64]
+    lib.sf_cache_attend_rows.argtypes = [vp, vp, vp, i64, c_int, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, c_float,
+                                         vp, i64, vp]
+    lib.sf_cache_attend_shared.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, c_int, c_int,
+                                           i64, vp, vp, c_float, vp, i64, vp]
     lib.sf_cache_sync_status.argtypes = [vp, vp]
     lib.sf_cache_last_error.argtypes = [vp]
     lib.sf_cache_last_error.restype = ctypes.c_char_p
@@ -298,6 +314,35 @@ def sf_cache_create(shapes: SfCacheShapes) -> int:
     return c.value
 
 
+def sf_cache_create_with(shapes: SfCacheShapes, options: SfCacheOptions) -> int:
+    c = ctypes.c_void_p()
+    _check(lib.sf_cache_create_with(ctypes.byref(shapes), ctypes.byref(options), ctypes.byref(c)), None,
+           "sf_cache_create_with")
+    return c.value
+
+
+def sf_cache_reposition(cache, stream, k_pages, n_pages, page_table, S, table_cols, ld_table, lens, pos_from, pos_to,
+                        ld_pos) -> None:
+    _check(lib.sf_cache_reposition(cache, stream, k_pages, n_pages, page_table, S, table_cols, ld_table, lens,
+                                   pos_from, pos_to, ld_pos), None, "sf_cache_reposition", cache=cache)
+
+
+def sf_cache_attend_rows(cache, stream, q, ld_q, T, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table,
+                         lens, starts, scale, out, ld_out, lse=None) -> None:
+    _check(lib.sf_cache_attend_rows(cache, stream, q, ld_q, T, k_pages, v_pages, n_pages, page_table, S, table_cols,
+                                    ld_table, lens, starts, scale, out, ld_out, lse),
+           None, "sf_cache_attend_rows", cache=cache)
+
+
+def sf_cache_attend_shared(cache, stream, q, ld_q, k_pages, v_pages, n_pages, page_table, S, table_cols, ld_table,
+                           lens, prefix_table, G, prefix_cols, ld_prefix, prefix_lens, starts, scale, out, ld_out,
+                           lse=None) -> None:
+    _check(lib.sf_cache_attend_shared(cache, stream, q, ld_q, k_pages, v_pages, n_pages, page_table, S, table_cols,
+                                      ld_table, lens, prefix_table, G, prefix_cols, ld_prefix, prefix_lens, starts,
+                                      scale, out, ld_out, lse),
+           None, "sf_cache_attend_shared", cache=cache)
+
+
 def sf_cache_append(cache, stream, qkv, ld_qkv, T, q_gain, k_gain, index, pos, seq, page_table, S, table_cols,
                     ld_table, k_pages, v_pages, n_pages, q_out, ld_q) -> None:
     _check(lib.sf_cache_append(cache, stream, qkv, ld_qkv, T, q_gain, k_gain, index, pos, seq, page_table, S,
@@ -466,6 +511,54 @@ class Head:
         return pred, accepted, chosen
 
 
+def rotary_frequencies(dim, theta=10000.0, *, scaling="none", factor=1.0, original_len=None, fast=32.0, slow=1.0,
+                       low=1.0, high=4.0):
+    """Frequencies of the dim / 2 rotated pairs, scaled for contexts `factor` times longer than the original_len
+    positions that a model was made for, and the magnitude that goes with them: PagedCache's inv_freq and
+    rotary_magnitude.  With f_j = theta^(-2j/dim):
+
+      "none"    f_j
+      "linear"  f_j / factor
+      "ntk"     f_j of theta * factor^(dim / (dim - 2)): the slowest pair is stretched by factor, the fastest stays
+      "yarn"    f_j / factor * g + f_j * (1 - g), where g rises from 0 to 1 over the pairs j from floor(j(fast)) to
+                ceil(j(slow)), kept within 0 .. dim - 1, and j(r) = dim ln(original_len / (2 pi r)) / (2 ln theta) is
+                the pair that turns r times in original_len; magnitude 0.1 ln(factor) + 1 (1 for a factor up to 1)
+      "bands"   the same with g = 1 for pairs that turn up to `low` times in original_len, 0 from `high` times on, and
+                linear in the turns between; magnitude 1
+
+    Returns (tuple of dim / 2 floats, magnitude)."""
+    if dim < 2 or dim % 2:
+        raise ValueError(f"dim must be even and positive: got {dim}")
+    if not (math.isfinite(theta) and theta > 0) or not (math.isfinite(factor) and factor > 0):
+        raise ValueError(f"theta and factor must be positive: got {theta}, {factor}")
+    if scaling in ("yarn", "bands") and not (original_len and original_len > 0):
+        raise ValueError(f"{scaling} needs original_len")
+    if scaling == "ntk":
+        if dim == 2:
+            raise ValueError("ntk needs more than one pair")
+        theta *= factor ** (dim / (dim - 2))
+    freq = [theta ** (-2.0 * j / dim) for j in range(dim // 2)]
+    magnitude = 1.0
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if not 0 < slow < fast or theta == 1:
+            raise ValueError(f"yarn needs 0 < slow < fast and a theta other than 1: got {slow}, {fast}, {theta}")
+        a, b = (dim * math.log(original_len / (2 * math.pi * r)) / (2 * math.log(theta)) for r in (fast, slow))
+        a, b = max(math.floor(a), 0), min(math.ceil(b), dim - 1)
+        mix = [min(max((j - a) / max(b - a, 0.001), 0.0), 1.0) for j in range(dim // 2)]
+        freq = [f / factor * g + f * (1 - g) for f, g in zip(freq, mix)]
+        magnitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling == "bands":
+        if not 0 < low < high:
+            raise ValueError(f"bands need 0 < low < high: got {low}, {high}")
+        mix = [min(max((original_len * f / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for f in freq]
+        freq = [f / factor * (1 - g) + f * g for f, g in zip(freq, mix)]
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling must be 'none', 'linear', 'ntk', 'yarn' or 'bands': got {scaling!r}")
+    return tuple(freq), magnitude
+
+
 class PagedCache:
     """Operators on a paged key-value cache over torch tensors (include/specfold_cache.h).
 
@@ -473,9 +566,14 @@ class PagedCache:
     that the caller owns, one pair per layer; table is int32 [S, columns],
     lens int32 [S].  A layer's prefix buffer of SpecFold.verify, viewed as
     [R * P / page_size, page_size, n_kv_heads, head_dim], is such a pool, so
-    that append can write the prefix of a pass; what evict leaves is read by
-    attend only (its keys keep their original positions).  attend and evict
-    plan for the longest sequence that the table's columns could hold: pass
+    that append can write the prefix of a pass; what evict leaves keeps its
+    keys' original positions, until reposition turns them to new ones.
+    Rotation: the first rotary_dim dimensions of a head (default: all), in
+    pairs (j, j + rotary_dim / 2), or (2j, 2j + 1) with
+    rotary_layout="interleaved"; inv_freq and rotary_magnitude as
+    rotary_frequencies returns them (default: rope_theta^(-2j / rotary_dim),
+    1).  attend_rows and attend_shared take up to max_rows rows a call.  attend
+    and evict plan for the longest sequence that the table's columns could hold: pass
     table[:, :columns in use] where the sequences are far shorter.
     Tensors must be on the object's device, of the documented type and shape
     with contiguous rows (ValueError otherwise).  Work runs on `stream` (a
@@ -485,8 +583,19 @@ class PagedCache:
     to `stream`, as if made under torch.cuda.stream(stream)."""
 
     def __init__(self, *, n_q_heads, n_kv_heads, head_dim, dtype, page_size, max_seqs, max_len, max_pos=None,
-                 rms_eps=1e-6, rope_theta=10000.0, track_weights=False):
+                 rms_eps=1e-6, rope_theta=10000.0, track_weights=False, rotary_dim=None, rotary_layout="half",
+                 inv_freq=None, rotary_magnitude=1.0, max_rows=0):
         import torch
+        if rotary_layout not in ("half", "interleaved"):
+            raise ValueError(f"rotary_layout must be 'half' or 'interleaved': got {rotary_layout!r}")
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if rotary_dim < 1 and head_dim > 0 or not rotary_magnitude > 0:  # the library's 0 is its default
+            raise ValueError(f"rotary_dim and rotary_magnitude must be positive: got {rotary_dim}, {rotary_magnitude}")
+        if inv_freq is not None:
+            inv_freq = [float(f) for f in inv_freq]
+            if len(inv_freq) != rotary_dim // 2:
+                raise ValueError(f"inv_freq must hold rotary_dim / 2 = {rotary_dim // 2} numbers: got {len(inv_freq)}")
+            inv_freq = (ctypes.c_double * len(inv_freq))(*inv_freq)
         if dtype not in ("bf16", "f32", SF_BF16, SF_F32):
             raise ValueError(f"dtype must be 'bf16' or 'f32': got {dtype!r}")
         bf16 = dtype in ("bf16", SF_BF16)
@@ -494,7 +603,9 @@ class PagedCache:
                                     max_seqs, max_len, max_len if max_pos is None else max_pos, rms_eps, rope_theta,
                                     int(bool(track_weights)))
         self.dtype = torch.bfloat16 if bf16 else torch.float32
-        self.cache = sf_cache_create(self.shapes)
+        self.cache = sf_cache_create_with(self.shapes, SfCacheOptions(
+            SF_ROTARY_NEIGHBOURS if rotary_layout == "interleaved" else SF_ROTARY_HALVES, rotary_dim, inv_freq,
+            rotary_magnitude, max_rows))
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._bind(self.cache, self.device.index)
 
@@ -543,6 +654,41 @@ class PagedCache:
         if st:
             _check(st, None, "sf_cache_attend", cache=self.cache)
         return out
+
+    def attend_rows(self, q, k_pages, v_pages, table, lens, starts, *, scale=None, out=None, lse=None, stream=None):
+        """Attention of blocks of rows, q [T, n_q_heads, head_dim]: rows starts[s] .. starts[s + 1] - 1 (int32
+        [S + 1]) over all lens[s] positions of sequence s, with no mask among them; returns [T, n_q_heads, head_dim].
+        lse (fp32 [T, n_q_heads]) gets the logarithm of every softmax's sum.  Rows of no sequence are left as they
+        were in out and lse (undefined in an out that the call makes)."""
+        if out is None:
+            out = self._empty(stream, q.shape[0], self.shapes.n_q_heads, self.shapes.head_dim, dtype=self.dtype)
+        st = self._call.attend_rows(self._state, q, k_pages, v_pages, table, lens, starts,
+                                    self._scale if scale is None else scale, out, lse, stream)
+        if st:
+            _check(st, None, "sf_cache_attend_rows", cache=self.cache)
+        return out
+
+    def attend_shared(self, q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, starts, *, scale=None,
+                      out=None, lse=None, stream=None):
+        """Attention of one new token per sequence, q [S, n_q_heads, head_dim], where sequences starts[g] ..
+        starts[g + 1] - 1 (int32 [G + 1]) see the prefix_lens[g] positions of prefix g (prefix_table [G, columns])
+        and then their own lens[s] positions (table); returns [S, n_q_heads, head_dim].  A group's prefix is read
+        once.  lse (fp32 [S, n_q_heads]) gets the logarithm of every softmax's sum."""
+        if out is None:
+            out = self._empty(stream, q.shape[0], self.shapes.n_q_heads, self.shapes.head_dim, dtype=self.dtype)
+        st = self._call.attend_shared(self._state, q, k_pages, v_pages, table, lens, prefix_table, prefix_lens,
+                                      starts, self._scale if scale is None else scale, out, lse, stream)
+        if st:
+            _check(st, None, "sf_cache_attend_shared", cache=self.cache)
+        return out
+
+    def reposition(self, k_pages, table, lens, pos_from, *, pos_to=None, stream=None):
+        """Turn the cached keys, in place, from the positions pos_from (int32 [S, n_kv_heads, n], n at least the
+        longest length; evict's `kept` where positions were places) to pos_to (the same shape; default: their
+        places).  Keys with a negative position stay as they are."""
+        st = self._call.reposition(self._state, k_pages, table, lens, pos_from, pos_to, stream)
+        if st:
+            _check(st, None, "sf_cache_reposition", cache=self.cache)
 
     def evict(self, k_pages, v_pages, table, lens, weights, budget, *, n_first=0, n_recent=0, k_out=None, v_out=None,
               table_out=None, weights_out=None, lens_out=None, kept=None, stream=None):

@@ -6,6 +6,8 @@
 #include <new>
 
 #include "sf_cache.h"
+#include "sf_pairs.cuh"
+#include "sf_rotary.cuh"
 
 namespace sf {
 namespace {
@@ -17,89 +19,24 @@ namespace {
 // step, far below fp32's half step); FP64 rates make a sine per entry slow.
 constexpr int kRopeRun = 64;
 
-__global__ void rope_table_kernel(float* out, int max_pos, int half, double theta) {
+// The frequencies are theta^(-j / half), or the caller's; `magnitude` scales
+// every entry.
+struct RopeFreqs {
+  double f[64];
+};
+__global__ void rope_table_kernel(float* out, int max_pos, int half, double theta, bool given,
+                                  const __grid_constant__ RopeFreqs freqs, double magnitude) {
   const int j = threadIdx.x, p0 = blockIdx.x * kRopeRun, p1 = min(p0 + kRopeRun, max_pos);
-  const double freq = pow(theta, -(double)j / half);
+  const double freq = given ? freqs.f[j] : pow(theta, -(double)j / half);
   double s, c, ds, dc;
   sincos((double)p0 * freq, &s, &c);
   sincos(freq, &ds, &dc);
   for (int p = p0; p < p1; ++p) {
-    out[(int64_t)p * 2 * half + j] = (float)c;
-    out[(int64_t)p * 2 * half + half + j] = (float)s;
+    out[(int64_t)p * 2 * half + j] = (float)(c * magnitude);
+    out[(int64_t)p * 2 * half + half + j] = (float)(s * magnitude);
     const double t = c * dc - s * ds;
     s = s * dc + c * ds;
     c = t;
-  }
-}
-
-// Two fp32 values in a register pair: sm_100's packed arithmetic does both in
-// one instruction, each rounded as the scalar one.
-struct Two {
-  unsigned long long v;
-};
-__device__ __forceinline__ Two two(float a, float b) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 both(Two a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-// 16 bytes of a row as pairs of fp32, and back.
-template <typename T>
-struct Piece;
-template <>
-struct Piece<float> {
-  static constexpr int PAIRS = 2;
-  static __device__ __forceinline__ void load(const uint4& u, Two (&x)[2]) {
-    x[0] = two(__uint_as_float(u.x), __uint_as_float(u.y));
-    x[1] = two(__uint_as_float(u.z), __uint_as_float(u.w));
-  }
-  static __device__ __forceinline__ uint4 store(const Two (&x)[2]) {
-    const float2 a = both(x[0]), b = both(x[1]);
-    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
-  }
-};
-template <>
-struct Piece<__nv_bfloat16> {
-  static constexpr int PAIRS = 4;
-  static __device__ __forceinline__ void load(const uint4& u, Two (&x)[4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  }
-  static __device__ __forceinline__ uint4 store(const Two (&x)[4]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = both(x[i]);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-
-template <int PAIRS>
-__device__ __forceinline__ void load_pairs(const float* p, Two (&x)[PAIRS]) {
-#pragma unroll
-  for (int i = 0; i < PAIRS / 2; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
-    x[2 * i] = two(v.x, v.y);
-    x[2 * i + 1] = two(v.z, v.w);
   }
 }
 
@@ -112,12 +49,21 @@ constexpr int kAppendBlocks = 18;
 // 4.2 us with one, 4.9 with two; 1,024 rows: 8.6 and 7.8; 4,096 rows: 31.4 and 24.2.
 constexpr int kAppendWide = 2048;
 
-// Norm, rotation and store of HPT heads of one row by a group of lanes: a lane
-// holds 16 bytes of a head's lower half and the same 16 of its upper half, so
-// both members of its rotation pairs are in its registers and the norm needs
-// log2(lanes) shuffles.  Bytes bound it (each row in and out once); HPT heads
-// keep 2 HPT loads in flight and share the row's angles and its page lookup.
-template <typename T, int HD, int HPT>
+// Which two 16-byte pieces of a head a lane holds: both members of its rotation
+// pairs are in its registers.
+//   kHalves      the whole head in halves: piece `lane` of the lower half and
+//                the same of the upper
+//   kPart        the first rotary.dim dimensions in halves: the lanes of these
+//                likewise, the others two neighbouring pieces as they are
+//   kNeighbours  pairs of neighbours lie inside a piece: pieces as for kHalves,
+//                of which those within the first rotary.dim dimensions turn
+enum Form { kHalves, kPart, kNeighbours };
+
+// Norm, rotation and store of HPT heads of one row by a group of lanes, two
+// pieces a lane; the norm needs log2(lanes) shuffles.  Bytes bound it (each row
+// in and out once); HPT heads keep 2 HPT loads in flight and share the row's
+// angles and its page lookup.
+template <typename T, int HD, int HPT, Form FORM>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
   using P = Piece<T>;
   constexpr int N = P::PAIRS, VEC = 2 * N, LANES = HD / 2 / VEC, GROUPS = kAppendThreads / LANES;
@@ -130,14 +76,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_ke
   const int t = item / NB, h0 = (item - t * NB) * HPT;
   if (t >= a.T) return;  // whole groups: the shuffles below stay inside a group
   const unsigned mask = (LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u)) << ((threadIdx.x & 31) / LANES * LANES);
+  const int turned = FORM == kPart ? a.rotary.dim / (2 * VEC) : LANES;  // lanes of the rotated part
+  const bool pairs = FORM != kPart || lane < turned;
+  const int c0 = pairs ? lane : 2 * lane, c1 = pairs ? lane + turned : 2 * lane + 1;
   // the row itself first: it waits for nothing, its place and angles arrive meanwhile
-  const T* src = static_cast<const T*>(a.qkv) + t * a.ld_qkv + h0 * HD + lane * VEC;
+  const T* src = static_cast<const T*>(a.qkv) + t * a.ld_qkv + h0 * HD;
   uint4 lo[HPT], hi[HPT];
 #pragma unroll
   for (int i = 0; i < HPT; ++i)
     if (h0 + i < NH) {
-      lo[i] = *reinterpret_cast<const uint4*>(src + i * HD);
-      hi[i] = *reinterpret_cast<const uint4*>(src + i * HD + HD / 2);
+      lo[i] = *reinterpret_cast<const uint4*>(src + i * HD + c0 * VEC);
+      hi[i] = *reinterpret_cast<const uint4*>(src + i * HD + c1 * VEC);
     }
   const int idx = a.index[t];
   const int pos = a.pos ? a.pos[t] : idx;
@@ -146,12 +95,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_ke
     if (lane == 0) cache_error(a.err, kCacheBadRow);
     return;
   }
-  Two cs[N], sn[N];
-  if (h0 < a.nq + a.nkv) {
-    const float* p = a.rope + (int64_t)pos * HD + lane * VEC;
-    load_pairs(p, cs);
-    load_pairs(p + HD / 2, sn);
-  }
+  const int dim = FORM == kHalves ? HD : a.rotary.dim;
+  Angles<T, FORM == kNeighbours> angles;
+  if (h0 < a.nq + a.nkv && pairs) angles.load(a.rope + (int64_t)pos * dim, dim / 2, c0, c1);
   int64_t slot = -1;
   if (h0 + HPT > a.nq && idx >= 0) {
     const int s = a.seq ? a.seq[t] : t;
@@ -173,7 +119,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_ke
       dst = static_cast<T*>(a.k) + (slot * a.nkv + (head - a.nq)) * HD;
     else
       dst = static_cast<T*>(a.v) + (slot * a.nkv + (head - a.nq - a.nkv)) * HD;
-    dst += lane * VEC;
     if (head < a.nq + a.nkv) {
       const float* gain = head < a.nq ? a.q_gain : a.k_gain;
       Two x[N], y[N];
@@ -191,42 +136,43 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_ke
         const float r = rsqrtf(ss * (1.f / HD) + a.eps);
         const Two rr = two(r, r);
         Two gl[N], gh[N];
-        load_pairs(gain + lane * VEC, gl);
-        load_pairs(gain + HD / 2 + lane * VEC, gh);
+        load_pairs(gain + c0 * VEC, gl);
+        load_pairs(gain + c1 * VEC, gh);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           x[e] = x[e] * rr * gl[e];
           y[e] = y[e] * rr * gh[e];
         }
       }
-      const Two minus = two(-1.f, -1.f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const Two u = x[e], w = y[e];
-        x[e] = fma2(w * minus, sn[e], u * cs[e]);
-        y[e] = fma2(u, sn[e], w * cs[e]);
-      }
+      if (pairs) angles.turn(x, y);
       lo[i] = P::store(x);
       hi[i] = P::store(y);
     }
-    *reinterpret_cast<uint4*>(dst) = lo[i];
-    *reinterpret_cast<uint4*>(dst + HD / 2) = hi[i];
+    *reinterpret_cast<uint4*>(dst + c0 * VEC) = lo[i];
+    *reinterpret_cast<uint4*>(dst + c1 * VEC) = hi[i];
   }
 }
 
-template <typename T, int HD, int HPT>
+template <typename T, int HD, int HPT, Form FORM>
 cudaError_t append_n(cudaStream_t st, const CacheAppendArgs& a) {
   constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
   const int64_t threads = (int64_t)a.T * ((a.nq + 2 * a.nkv + HPT - 1) / HPT) * LANES;
   return launch_pdl(st, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0, 1,
-                    cache_append_kernel<T, HD, HPT>, a);
+                    cache_append_kernel<T, HD, HPT, FORM>, a);
+}
+
+template <typename T, int HD, Form FORM>
+cudaError_t append_f(cudaStream_t st, const CacheAppendArgs& a, int sm_count) {
+  constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
+  const int64_t threads = (int64_t)a.T * (a.nq + 2 * a.nkv) * LANES;
+  return threads <= (int64_t)sm_count * kAppendWide ? append_n<T, HD, 1, FORM>(st, a)
+                                                       : append_n<T, HD, kAppendHeads, FORM>(st, a);
 }
 
 template <typename T, int HD>
 cudaError_t append_t(cudaStream_t st, const CacheAppendArgs& a, int sm_count) {
-  constexpr int LANES = HD / 2 / (16 / (int)sizeof(T));
-  const int64_t threads = (int64_t)a.T * (a.nq + 2 * a.nkv) * LANES;
-  return threads <= (int64_t)sm_count * kAppendWide ? append_n<T, HD, 1>(st, a) : append_n<T, HD, kAppendHeads>(st, a);
+  if (a.rotary.neighbours) return append_f<T, HD, kNeighbours>(st, a, sm_count);
+  return a.rotary.dim == HD ? append_f<T, HD, kHalves>(st, a, sm_count) : append_f<T, HD, kPart>(st, a, sm_count);
 }
 
 bool misaligned(const void* p, uintptr_t align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)); }
@@ -248,6 +194,11 @@ void free_cache(sf_cache* c) {
   cudaFree(c->parts);
   cudaFree(c->arrived);
   cudaFree(c->joins);
+  cudaFree(c->row_parts);
+  cudaFree(c->row_ml);
+  cudaFree(c->row_joins);
+  cudaFree(c->tail_o);
+  cudaFree(c->tail_ml);
   if (c->err) cudaFreeHost(c->err);
   delete c;
 }
@@ -307,6 +258,49 @@ PageTable page_table(const sf_cache* c, const int32_t* table, int cols, int64_t 
   return make_page_table(table, ld, cols, c->s.page_size, n_pages);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What attend_rows and attend_shared check of their rows.
+sf_status check_rows(sf_cache* c, const void* q, int64_t ld_q, int T, float scale, const void* out, int64_t ld_out,
+                     const float* lse) {
+  const sf_cache_shapes& s = c->s;
+  if (c->o.max_rows < 1) return fail(c, SF_ERR_INVALID_ARG, "the object was created without max_rows");
+  if (T < 0) return fail(c, SF_ERR_INVALID_ARG, "%d rows", T);
+  if (T > c->o.max_rows) return fail(c, SF_ERR_SHAPE, "%d rows beyond the object's %d", T, c->o.max_rows);
+  const int64_t wq = (int64_t)s.n_q_heads * s.head_dim, es = s.dtype == SF_BF16 ? 2 : 4, w = wq * es;
+  const int64_t wl = 4 * (int64_t)s.n_q_heads;
+  if (bad_row(c, q, ld_q, wq, T) || bad_row(c, out, ld_out, wq, T))
+    return fail(c, SF_ERR_INVALID_ARG, "q/out null, misaligned, or rows closer than their width");
+  if (misaligned(lse, 4)) return fail(c, SF_ERR_INVALID_ARG, "lse misaligned");
+  if (!std::isfinite(scale * kLog2e))
+    return fail(c, SF_ERR_INVALID_ARG, "scale must be finite, and so must scale * log2(e)");
+  if (rows_overlap(q, ld_q * es, w, out, ld_out * es, w, T)) return fail(c, SF_ERR_INVALID_ARG, "out overlaps q");
+  if (lse && (rows_overlap(q, ld_q * es, w, lse, wl, wl, T) || rows_overlap(out, ld_out * es, w, lse, wl, wl, T)))
+    return fail(c, SF_ERR_INVALID_ARG, "lse overlaps q or out");
+  return SF_OK;
+}
+
+CacheRowsArgs rows_args(const sf_cache* c, const void* q, int64_t ld_q, int T, float scale, void* out, int64_t ld_out,
+                        float* lse) {
+  CacheRowsArgs a{};
+  a.q = q;
+  a.ld_q = ld_q;
+  a.T = T;
+  a.nq = c->s.n_q_heads;
+  a.nkv = c->s.n_kv_heads;
+  a.group = a.nq / a.nkv;
+  a.scale_log2 = scale * kLog2e;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.lse = lse;
+  a.parts = c->row_parts;
+  a.part_ml = c->row_ml;
+  a.joins = c->row_joins;
+  a.ctas = cache_rows_ctas(c->sm_count);
+  a.err = c->err_dev;
+  return a;
+}
+
 sf_status launched(sf_cache* c, cudaError_t e) {
   if (e == cudaSuccess) return SF_OK;
   cudaGetLastError();
@@ -327,6 +321,10 @@ using namespace sf;
 extern "C" {
 
 sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
+  return sf_cache_create_with(shapes, nullptr, out);
+}
+
+sf_status sf_cache_create_with(const sf_cache_shapes* shapes, const sf_cache_options* options, sf_cache** out) {
   if (!out) return SF_ERR_INVALID_ARG;
   *out = nullptr;
   if (!shapes) return SF_ERR_INVALID_ARG;
@@ -338,13 +336,31 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if ((s.head_dim != 64 && s.head_dim != 128) || s.n_q_heads % s.n_kv_heads != 0 || s.n_q_heads > 1024 ||
       s.page_size > kMaxPageSize || s.max_seqs > 4096 || s.max_len > kMaxLen || s.max_pos > 4194304)
     return SF_ERR_UNSUPPORTED;
+  sf_cache_options o = options ? *options : sf_cache_options{};
+  if (o.rotary_dim == 0) o.rotary_dim = s.head_dim;
+  if (o.rotary_magnitude == 0.) o.rotary_magnitude = 1.;
+  if (o.max_rows < 0 || o.rotary_dim < 0 || !(o.rotary_magnitude > 0.) || !std::isfinite((float)o.rotary_magnitude) ||
+      !std::isfinite((float)(1. / o.rotary_magnitude)) ||
+      (o.rotary_layout != SF_ROTARY_HALVES && o.rotary_layout != SF_ROTARY_NEIGHBOURS))
+    return SF_ERR_INVALID_ARG;
+  if (o.max_rows > kMaxCallRows || o.rotary_dim % 16 != 0 || o.rotary_dim > s.head_dim) return SF_ERR_UNSUPPORTED;
+  const int half = o.rotary_dim / 2;
+  RopeFreqs freqs{};
+  const bool given = o.inv_freq != nullptr;
+  for (int j = 0; given && j < half; ++j) {
+    freqs.f[j] = o.inv_freq[j];
+    if (!std::isfinite(freqs.f[j])) return SF_ERR_INVALID_ARG;
+  }
+  o.inv_freq = nullptr;  // the caller's array is not kept
   sf_cache* c = new (std::nothrow) sf_cache();
   if (!c) return SF_ERR_OOM;
   c->s = s;
+  c->o = o;
+  c->rotary = Rotary{o.rotary_dim, o.rotary_layout == SF_ROTARY_NEIGHBOURS};
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
   const int blocks = cache_attend_blocks(c->sm_count);
-  if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * s.head_dim * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->rope, (size_t)s.max_pos * o.rotary_dim * sizeof(float));
   if (e == cudaSuccess && s.track_weights)
     e = cudaMalloc(&c->scores, (size_t)s.max_seqs * s.n_q_heads * scores_ld(s) * sizeof(float));
   if (e == cudaSuccess && s.track_weights)
@@ -353,14 +369,24 @@ sf_status sf_cache_create(const sf_cache_shapes* shapes, sf_cache** out) {
   if (e == cudaSuccess) e = cudaMalloc(&c->joins, (size_t)blocks * sizeof(CacheJoin));
   if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)blocks * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)blocks * sizeof(unsigned));
+  if (o.max_rows > 0) {
+    const size_t ctas = (size_t)cache_rows_ctas(c->sm_count), rows = 2 * ctas * cache_rows_slot_rows(s.dtype == SF_BF16);
+    const size_t tails = (size_t)(o.max_rows < s.max_seqs ? o.max_rows : s.max_seqs) * s.n_q_heads;
+    if (e == cudaSuccess) e = cudaMalloc(&c->row_parts, rows * s.head_dim * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&c->row_ml, rows * sizeof(float2));
+    if (e == cudaSuccess) e = cudaMalloc(&c->row_joins, ctas * sizeof(RowsJoin));
+    if (e == cudaSuccess) e = cudaMalloc(&c->tail_o, tails * s.head_dim * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&c->tail_ml, tails * sizeof(float2));
+    if (e == cudaSuccess) e = prepare_cache_rows();
+  }
   if (e == cudaSuccess) e = prepare_cache_attend();
   if (e == cudaSuccess) e = prepare_cache_evict();
   if (e == cudaSuccess) e = cudaHostAlloc(&c->err, kCacheErrWords * sizeof(unsigned), cudaHostAllocMapped);
   if (e == cudaSuccess) e = cudaHostGetDevicePointer(&c->err_dev, c->err, 0);
   if (e == cudaSuccess) {
     for (int i = 0; i < kCacheErrWords; ++i) c->err[i] = 0;
-    rope_table_kernel<<<(s.max_pos + kRopeRun - 1) / kRopeRun, s.head_dim / 2>>>(c->rope, s.max_pos, s.head_dim / 2,
-                                                                                 (double)s.rope_theta);
+    rope_table_kernel<<<(s.max_pos + kRopeRun - 1) / kRopeRun, half>>>(c->rope, s.max_pos, half, (double)s.rope_theta,
+                                                                       given, freqs, o.rotary_magnitude);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
@@ -389,7 +415,7 @@ sf_status sf_cache_append(sf_cache* c, void* stream, const void* qkv, int64_t ld
   const int64_t wq = (int64_t)s.n_q_heads * s.head_dim, w = wq + 2 * (int64_t)s.n_kv_heads * s.head_dim;
   if (bad_row(c, qkv, ld_qkv, w, T) || bad_row(c, q_out, ld_q, wq, T))
     return fail(c, SF_ERR_INVALID_ARG, "qkv/q_out null, misaligned, or rows closer than their width");
-  if (T > 1048576 || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
+  if (T > kMaxCallRows || (!seq && T > S)) return fail(c, SF_ERR_SHAPE, "T=%d rows for S=%d sequences", T, S);
   const int es = s.dtype == SF_BF16 ? 2 : 4;
   if ((q_out != qkv || (T > 1 && ld_q != ld_qkv)) && rows_overlap(qkv, ld_qkv * es, w * es, q_out, ld_q * es, wq * es, T))
     return fail(c, SF_ERR_INVALID_ARG, "q_out overlaps qkv and is not its query part");
@@ -408,6 +434,7 @@ sf_status sf_cache_append(sf_cache* c, void* stream, const void* qkv, int64_t ld
   a.k = k_pages;
   a.v = v_pages;
   a.rope = c->rope;
+  a.rotary = c->rotary;
   a.T = T;
   a.S = S;
   a.nq = s.n_q_heads;
@@ -476,6 +503,112 @@ sf_status sf_cache_attend(sf_cache* c, void* stream, const void* q, int64_t ld_q
   a.joins = c->joins;
   a.err = c->err_dev;
   return launched(c, launch_cache_attend((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
+}
+
+sf_status sf_cache_reposition(sf_cache* c, void* stream, void* k_pages, int64_t n_pages, const int32_t* page_table_, int S,
+                              int table_cols, int64_t ld_table, const int32_t* lens, const int32_t* pos_from,
+                              const int32_t* pos_to, int64_t ld_pos) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes& s = c->s;
+  sf_status st = SF_OK;
+  if (S == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_table(c, k_pages, k_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if (!lens || !pos_from || misaligned(lens, 4) || misaligned(pos_from, 4) || misaligned(pos_to, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "null lens or pos_from, or lens/pos_from/pos_to misaligned");
+  if (ld_pos < 1) return fail(c, SF_ERR_INVALID_ARG, "ld_pos=%lld", (long long)ld_pos);
+  if ((st = check_object(c)) != SF_OK) return st;
+  CacheTurnArgs a{};
+  a.k = k_pages;
+  a.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  a.lens = lens;
+  a.from = pos_from;
+  a.to = pos_to;
+  a.ld_pos = ld_pos;
+  a.rope = c->rope;
+  a.rotary = c->rotary;
+  a.unscale = (float)(1. / c->o.rotary_magnitude);
+  a.S = S;
+  a.nkv = s.n_kv_heads;
+  a.hd = s.head_dim;
+  a.max_pos = s.max_pos;
+  a.limit = length_limit(s.max_len, table_cols, s.page_size);
+  if (ld_pos < a.limit) a.limit = ld_pos;
+  a.err = c->err_dev;
+  return launched(c, launch_cache_turn((cudaStream_t)stream, a, s.dtype == SF_BF16, c->sm_count));
+}
+
+sf_status sf_cache_attend_rows(sf_cache* c, void* stream, const void* q, int64_t ld_q, int T, const void* k_pages,
+                               const void* v_pages, int64_t n_pages, const int32_t* page_table_, int S, int table_cols,
+                               int64_t ld_table, const int32_t* lens, const int32_t* starts, float scale, void* out,
+                               int64_t ld_out, float* lse) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  sf_status st = SF_OK;
+  if (S == 0 || T == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_rows(c, q, ld_q, T, scale, out, ld_out, lse)) != SF_OK) return st;
+  if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if (!lens || !starts || misaligned(lens, 4) || misaligned(starts, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "lens or starts null or misaligned");
+  if ((st = check_object(c)) != SF_OK) return st;
+  CacheRowsArgs a = rows_args(c, q, ld_q, T, scale, out, ld_out, lse);
+  a.k = k_pages;
+  a.v = v_pages;
+  a.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  a.lens = lens;
+  a.starts = starts;
+  a.S = S;
+  a.limit = length_limit(c->s.max_len, table_cols, c->s.page_size);
+  return launched(c, launch_cache_rows((cudaStream_t)stream, a, c->s.dtype == SF_BF16, c->s.head_dim, c->sm_count));
+}
+
+sf_status sf_cache_attend_shared(sf_cache* c, void* stream, const void* q, int64_t ld_q, const void* k_pages,
+                                 const void* v_pages, int64_t n_pages, const int32_t* page_table_, int S,
+                                 int table_cols, int64_t ld_table, const int32_t* lens, const int32_t* prefix_table,
+                                 int G, int prefix_cols, int64_t ld_prefix, const int32_t* prefix_lens,
+                                 const int32_t* starts, float scale, void* out, int64_t ld_out, float* lse) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  const sf_cache_shapes& s = c->s;
+  sf_status st = SF_OK;
+  if (S == 0) return check_object(c);  // nothing to do, whatever the pointers
+  if ((st = check_rows(c, q, ld_q, S, scale, out, ld_out, lse)) != SF_OK) return st;
+  if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if (G < 1) return fail(c, SF_ERR_INVALID_ARG, "G=%d groups", G);
+  if ((st = check_table(c, k_pages, v_pages, n_pages, prefix_table, G, prefix_cols, ld_prefix)) != SF_OK) return st;
+  if (!lens || !prefix_lens || !starts || misaligned(lens, 4) || misaligned(prefix_lens, 4) || misaligned(starts, 4))
+    return fail(c, SF_ERR_INVALID_ARG, "lens, prefix_lens or starts null or misaligned");
+  if ((st = check_object(c)) != SF_OK) return st;
+  // the sequences' own positions first, then the prefixes, which join them
+  CacheAttendArgs t{};
+  t.q = q;
+  t.ld_q = ld_q;
+  t.k = k_pages;
+  t.v = v_pages;
+  t.table = page_table(c, page_table_, table_cols, ld_table, n_pages);
+  t.lens = lens;
+  t.S = S;
+  t.nq = s.n_q_heads;
+  t.nkv = s.n_kv_heads;
+  t.hd = s.head_dim;
+  t.limit = length_limit(s.max_len, table_cols, s.page_size);
+  t.scale_log2 = scale * kLog2e;
+  t.state_o = c->tail_o;
+  t.stats = c->tail_ml;
+  t.parts = c->parts;
+  t.arrived = c->arrived;
+  t.joins = c->joins;
+  t.err = c->err_dev;
+  if ((st = launched(c, launch_cache_attend((cudaStream_t)stream, t, s.dtype == SF_BF16, c->sm_count))) != SF_OK)
+    return st;
+  CacheRowsArgs a = rows_args(c, q, ld_q, S, scale, out, ld_out, lse);
+  a.k = k_pages;
+  a.v = v_pages;
+  a.table = page_table(c, prefix_table, prefix_cols, ld_prefix, n_pages);
+  a.lens = prefix_lens;
+  a.starts = starts;
+  a.S = G;
+  a.limit = length_limit(s.max_len, prefix_cols, s.page_size);
+  a.tail_o = c->tail_o;
+  a.tail_ml = c->tail_ml;
+  return launched(c, launch_cache_rows((cudaStream_t)stream, a, s.dtype == SF_BF16, s.head_dim, c->sm_count));
 }
 
 sf_status sf_cache_evict(sf_cache* c, void* stream, const void* k_pages, const void* v_pages, int64_t n_pages,

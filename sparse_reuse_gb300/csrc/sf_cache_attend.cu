@@ -596,8 +596,14 @@ __device__ __forceinline__ int find_sequence(const int* first, int S, int64_t u,
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // o times the reciprocal of the denominator: one quotient where there were four, for one more rounding of fp32.
-template <typename T>
+// STATE: in fp32, for a later join with what other keys gave.
+template <typename T, bool STATE>
 __device__ __forceinline__ void write_out(const CacheAttendArgs& a, int s, int h, int hd, int d, float4 o, float inv) {
+  if constexpr (STATE) {
+    *reinterpret_cast<float4*>(a.state_o + ((int64_t)s * a.nq + h) * hd + d) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    return;
+  }
   T* p = static_cast<T*>(a.out) + (int64_t)s * a.ld_out + (int64_t)h * hd + d;
   store4<T>(p, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
@@ -605,8 +611,9 @@ __device__ __forceinline__ void write_out(const CacheAttendArgs& a, int s, int h
 // What the weights kernel needs of a row's softmax: the reference m, and the factor that makes 2^(score - m) a weight.
 // Not log2 of the denominator added to m: the sum would be rounded at the size of m (scores around 500 then cost a
 // weight 3e-5, with the pair none of that).
+template <bool STATE>
 __device__ __forceinline__ void write_stats(const CacheAttendArgs& a, int s, int h, float m, float l) {
-  a.stats[(int64_t)s * a.nq + h] = make_float2(m == -INFINITY ? 0.f : m, inverse(l) * kUnroom);
+  a.stats[(int64_t)s * a.nq + h] = STATE ? make_float2(m, l) : make_float2(m == -INFINITY ? 0.f : m, inverse(l) * kUnroom);
 }
 
 // ex2(m - top) with an empty part (m = -inf) weighing 0 even where all are.
@@ -682,7 +689,10 @@ struct PartSum {
 // to 62 keys, 4 heads: 12.6 us; every segment by a block: 43.8).  A segment cut
 // over few blocks is joined by the last of them to finish, one cut over many by
 // the join kernel.
-template <typename T, int HD, int NT, bool TRACK>
+//
+// TRACK: scores are written for the weights kernel.  STATE: outputs go out in
+// fp32, with the maximum and denominator of their softmax.
+template <typename T, int HD, int NT, bool TRACK, bool STATE>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(const __grid_constant__ CacheAttendArgs a) {
   using Warp = typename WarpOf<T, HD, NT>::type;
   constexpr int NH = Warp::kHeads, ROW = Warp::kRow;
@@ -707,8 +717,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
   if (filled < a.S)
     for (int s = blk; s < a.S; s += gridDim.x)
       if (first[s + 1] == first[s])
-        for (int i = threadIdx.x; i < a.nq * HD / 4; i += kThreads)
-          store4<T>(static_cast<T*>(a.out) + (int64_t)s * a.ld_out + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int i = threadIdx.x; i < a.nq * HD / 4; i += kThreads) {
+          if constexpr (STATE) {
+            const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+            write_out<T, true>(a, s, h, HD, d, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+            if (d == 0) write_stats<true>(a, s, h, -INFINITY, 0.f);
+          } else {
+            store4<T>(static_cast<T*>(a.out) + (int64_t)s * a.ld_out + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+          }
+        }
   const int64_t units = (int64_t)first[a.S] * H;
   if (units == 0) return;
   const int64_t share = units_per_block(units, gridDim.x, kLeast);
@@ -751,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       sfac[x][h] = part_factor(sml[x][h].x, top);
     }
     __syncthreads();
-    if (threadIdx.x < g.nh && (n > 1 || TRACK)) {
+    if (threadIdx.x < g.nh && (n > 1 || TRACK || STATE)) {
       const int h = threadIdx.x;
       float top = -INFINITY, l = 0.f;
 #pragma unroll
@@ -763,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
         part[NH * HD + h] = top;
         part[NH * HD + NH + h] = l;
       } else {
-        write_stats(a, g.s, g.h0 + h, top, l);
+        write_stats<STATE>(a, g.s, g.h0 + h, top, l);
       }
     }
     for (int i = threadIdx.x; i < g.nh * HD / 4; i += kThreads) {
@@ -783,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
       if (n > 1)
         *reinterpret_cast<float4*>(part + h * HD + d) = o;
       else
-        write_out<T>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
+        write_out<T, STATE>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
     }
     if (n > kInlineParts) {
       if (blk == b0 && threadIdx.x == 0) a.joins[b0] = CacheJoin{n, g.s, g.h0, g.nh, slot0};
@@ -807,8 +824,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
               sum.add<NH, HD, kPartLoads>(a, h, d, n - x0, [&](int x) { return x0 + x ? 2 * (b0 + x0 + x) : slot0; });
           const float4 o = sum.o;
           const float top = sum.top, l = sum.l;
-          write_out<T>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
-          if (TRACK && d == 0) write_stats(a, g.s, g.h0 + h, top, l);
+          write_out<T, STATE>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
+          if ((TRACK || STATE) && d == 0) write_stats<STATE>(a, g.s, g.h0 + h, top, l);
         }
       }
     }
@@ -916,10 +933,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
           __syncwarp();
           for (int i = lane; i < g.nh * HD / 4; i += 32) {
             const int h = i / (HD / 4), d = i % (HD / 4) * 4;
-            write_out<T>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
+            write_out<T, STATE>(a, g.s, g.h0 + h, HD, d, *reinterpret_cast<const float4*>(my_out + h * ROW + d),
                          sfac[warp][h]);
           }
-          if (TRACK && lane < g.nh) write_stats(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
+          if ((TRACK || STATE) && lane < g.nh)
+            write_stats<STATE>(a, g.s, g.h0 + lane, sml[warp][lane].x, sml[warp][lane].y);
         }
         __syncthreads();  // the warps' memory is free again
         u += taken;
@@ -943,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) cache_attend_kernel(co
 constexpr int kJoinThreads = 256;
 constexpr int kMaxBlocks = 512;  // of the attention kernel
 
-template <typename T, int HD, int NH>
+template <typename T, int HD, int NH, bool STATE>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttendArgs a) {
   constexpr int COLS = HD / 4, GROUPS = kJoinThreads / COLS;
   __shared__ float4 acc[GROUPS][COLS];
@@ -975,8 +993,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     sum.scale(to);
 #pragma unroll
     for (int i = 1; i < GROUPS; ++i) sum.add_one(acc[i][col], ml[i].x, ml[i].y);
-    write_out<T>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, inverse(sum.l));
-    if (a.w_out && col == 0) write_stats(a, j.s, j.h0 + h, sum.top, sum.l);
+    write_out<T, STATE>(a, j.s, j.h0 + h, HD, 4 * col, sum.o, inverse(sum.l));
+    if ((STATE || a.w_out) && col == 0) write_stats<STATE>(a, j.s, j.h0 + h, sum.top, sum.l);
   }
 }
 
@@ -1046,10 +1064,13 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   a.join = may_need_join(longest, a.heads, blocks);
   const size_t table = (2 * (size_t)a.S + 1) * sizeof(int), smem = ring_bytes<T, HD, NT>() + table;
   cudaError_t e = launch_pdl(st, dim3(blocks), dim3(kThreads), smem, 1,
-                             a.w_out ? cache_attend_kernel<T, HD, NT, true> : cache_attend_kernel<T, HD, NT, false>, a);
+                             a.state_o ? cache_attend_kernel<T, HD, NT, false, true>
+                             : a.w_out ? cache_attend_kernel<T, HD, NT, true, false>
+                                       : cache_attend_kernel<T, HD, NT, false, false>,
+                             a);
   if (e == cudaSuccess && a.join)
     e = launch_pdl(st, dim3((blocks + kInlineParts - 1) / kInlineParts, NH < G ? NH : G), dim3(kJoinThreads), 0, 1,
-                   cache_join_kernel<T, HD, NH>, a);
+                   a.state_o ? cache_join_kernel<T, HD, NH, true> : cache_join_kernel<T, HD, NH, false>, a);
   if (e == cudaSuccess && a.w_out) {
     const int64_t most = (int64_t)a.S * a.nkv * ((a.limit + kWeightKeys - 1) / kWeightKeys);
     e = launch_pdl(st, dim3((unsigned)(most < 8 * sm_count ? most : 8 * sm_count)), dim3(kWeightThreads), table, 1,
@@ -1061,10 +1082,10 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
 template <typename T, int HD, int NT>
 cudaError_t allow_smem() {
   const int bytes = ring_bytes<T, HD, NT>() + (2 * 4096 + 1) * (int)sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<T, HD, NT, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(cache_attend_kernel<T, HD, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaSuccess;
+  for (auto kernel : {cache_attend_kernel<T, HD, NT, true, false>, cache_attend_kernel<T, HD, NT, false, false>,
+                      cache_attend_kernel<T, HD, NT, false, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e;
 }
 

@@ -1,0 +1,550 @@
+// Attention of blocks of rows over the paged cache (specfold_cache.h,
+// sf_cache_attend_rows), and the shared prefixes of sf_cache_attend_shared.
+//
+//   x_j = scale log2(e) q . k_j,  m = max_j x_j,  p_j = 2^(x_j - m - kRowsRoom)
+//   out = (sum_j p_j v_j) / (sum_j p_j),  lse = ln 2 (m + kRowsRoom + log2 sum_j p_j)
+//
+// The rows of a sequence and the query heads of one KV head are query vectors
+// of one product: they see the same keys.  Keys are streamed once per tile of
+// them with the running maximum and sum of the softmax; how tiles are cut over
+// thread blocks is in sf_cache_index.h, and cut ones are joined by
+// cache_rows_join_kernel.  kRowsRoom keeps unnormalised sums from overflowing
+// where the result does not (2^18 values at most).
+#include <cmath>
+
+#include "sf_cache.h"
+#include "sf_tc.cuh"
+
+namespace sf {
+namespace {
+
+constexpr float kRowsRoom = 27.f;
+constexpr int kRowsCtasPerSM = 1;
+constexpr int kRowsMaxCtas = 512;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows and length of sequence s; bad where its offsets are not ascending within [0, T] or its length is out of range.
+struct SeqRows {
+  int s, row0, rows, len;
+};
+__device__ __forceinline__ SeqRows sequence_rows(const CacheRowsArgs& a, int s, bool* bad_rows, bool* bad_len) {
+  const int r0 = __ldcg(a.starts + s), r1 = __ldcg(a.starts + s + 1);
+  *bad_rows = r0 < 0 || r1 < r0 || r1 > a.T;
+  SeqRows q;
+  q.s = s;
+  q.row0 = r0;
+  q.rows = *bad_rows ? 0 : r1 - r0;
+  q.len = checked_len(__ldcg(a.lens + s), a.limit, bad_len);
+  return q;
+}
+
+__device__ __forceinline__ int64_t units_of(const RowsShape& sh, const SeqRows& q) {
+  return q.rows > 0 && q.len > 0 ? sh.nkv * row_units(sh, q.rows, q.len) : 0;
+}
+
+__device__ __forceinline__ int64_t shfl_up64(int64_t x, int o) {
+  return (int64_t)__shfl_up_sync(kFull, (unsigned long long)x, o);
+}
+
+// Where a thread block's share of the line starts, and the walk along it.
+// Every warp walks on its own: all 32 lanes call next() together.
+struct RowsWalk {
+  int64_t u, end, per;  // this block's units [u, end)
+  int64_t first;        // of seq
+  SeqRows seq;
+
+  __device__ __forceinline__ bool next(const CacheRowsArgs& a, const RowsShape& sh, RowsPart& p, SeqRows& q) {
+    while (u < end) {
+      p = rows_part(sh, seq.rows, seq.len, first, u, end);
+      q = seq;
+      u = rows_part_end(p);
+      const int64_t units = units_of(sh, seq);
+      if (u >= first + units && u < end) {  // the next sequence with units: 32 looked at together
+        first += units;
+        const int lane = threadIdx.x & 31;
+        for (int s0 = seq.s + 1;; s0 += 32) {
+          bool b0, b1;
+          SeqRows x{0, 0, 0, 0};
+          if (s0 + lane < a.S) x = sequence_rows(a, s0 + lane, &b0, &b1);
+          const unsigned hit = __ballot_sync(kFull, units_of(sh, x) > 0);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            seq.s = s0 + l;
+            seq.row0 = __shfl_sync(kFull, x.row0, l);
+            seq.rows = __shfl_sync(kFull, x.rows, l);
+            seq.len = __shfl_sync(kFull, x.len, l);
+            break;
+          }
+          if (s0 + 32 >= a.S) {  // not reached: units are left
+            u = end;
+            break;
+          }
+        }
+      }
+      if (p.b0 < p.b1) return true;
+    }
+    return false;
+  }
+};
+
+// By all THREADS of the block: the walk's start.  False where nothing of the
+// call may be written (offsets that do not ascend).  *empties: some sequence
+// with rows has no keys.
+template <int THREADS>
+__device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShape& sh, RowsWalk& walk, bool* empties) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int64_t sums[WARPS];
+  __shared__ RowsWalk found;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t mine = 0;
+  int flags = 0;
+  SeqRows head{0, 0, 0, 0};
+  for (int s = threadIdx.x; s < a.S; s += THREADS) {
+    bool bad_rows, bad_len;
+    const SeqRows q = sequence_rows(a, s, &bad_rows, &bad_len);
+    if (s == (int)threadIdx.x) head = q;
+    mine += units_of(sh, q);
+    flags |= (bad_rows ? 1 : 0) | (bad_len ? 2 : 0) | (q.rows > 0 && q.len == 0 ? 4 : 0);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += (int64_t)__shfl_xor_sync(kFull, (unsigned long long)mine, o);
+  if (lane == 0) sums[warp] = mine;
+  const bool bad_rows = __syncthreads_or(flags & 1), bad_len = __syncthreads_or(flags & 2);
+  *empties = __syncthreads_or(flags & 4);
+  if (threadIdx.x == 0 && blockIdx.x == 0) {
+    if (bad_rows) cache_error(a.err, kCacheBadRow);
+    if (bad_len) cache_error(a.err, kCacheBadLength);
+  }
+  if (bad_rows) return false;
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) total += sums[w];
+  const int64_t per = units_per_block(total, a.ctas, a.least);
+  const int64_t lo = per * blockIdx.x, hi = lo + per < total ? lo + per : total;
+  if (lo >= hi) {
+    walk.u = walk.end = 0;
+    walk.per = per;
+    return true;
+  }
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.S; s0 += THREADS) {
+    const int s = s0 + threadIdx.x;
+    SeqRows q = head;
+    if (s0 > 0) {
+      bool b0, b1;
+      q = SeqRows{0, 0, 0, 0};
+      if (s < a.S) q = sequence_rows(a, s, &b0, &b1);
+    }
+    const int64_t x = units_of(sh, q);
+    int64_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = shfl_up64(y, o);
+      if (lane >= o) y += z;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = y;
+    __syncthreads();
+    int64_t at = before + y - x;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
+    if (before > lo) break;
+  }
+  __syncthreads();
+  walk = found;
+  return true;
+}
+
+// One float4 of a finished row: normalised, together with the tail's state
+// where the call has one.
+template <typename T, int HD>
+__device__ __forceinline__ void rows_finish(const CacheRowsArgs& a, int64_t t, int h, int d, float4 o, float m, float l) {
+  const int64_t at = t * a.nq + h;
+  if (a.tail_ml) {
+    const float2 tail = __ldcg(a.tail_ml + at);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.tail_o + at * HD + d));
+    const float top = fmaxf(m, tail.x), base = top == -INFINITY ? 0.f : top;
+    // the tail's output is normalised: its weight is its denominator
+    const float f = ex2(m - base), g = tail.y * ex2(tail.x - base);
+    o = make_float4(o.x * f + y.x * g, o.y * f + y.y * g, o.z * f + y.z * g, o.w * f + y.w * g);
+    l = l * f + g;
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
+  store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d,
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
+}
+
+// Rows that no key belongs to: those of sequences without keys, and with a tail those of no sequence.
+template <typename T, int HD, int THREADS>
+__device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
+  auto clear = [&](int64_t t0, int64_t n) {
+    for (int64_t i = threadIdx.x; i < n * a.nq * (HD / 4); i += THREADS) {
+      const int64_t r = i / (HD / 4);
+      rows_finish<T, HD>(a, t0 + r / a.nq, (int)(r % a.nq), 4 * (int)(i % (HD / 4)), make_float4(0.f, 0.f, 0.f, 0.f),
+                         -INFINITY, 0.f);
+    }
+  };
+  if (empties)
+    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+      bool b0, b1;
+      const SeqRows q = sequence_rows(a, s, &b0, &b1);
+      if (q.len == 0 && q.rows > 0) clear(q.row0, q.rows);
+    }
+  if (a.tail_ml) {  // rows in front of the first group and behind the last
+    const int r0 = __ldcg(a.starts), r1 = __ldcg(a.starts + a.S);
+    for (int t = blockIdx.x; t < r0; t += gridDim.x) clear(t, 1);
+    for (int t = r1 + blockIdx.x; t < a.T; t += gridDim.x) clear(t, 1);
+  }
+}
+
+// ---- partial results: per slot ROWS query vectors, [HD / 4][ROWS] float4 and
+// (m, l) of each.  Neighbouring rows lie side by side: a thread has one row,
+// or a few.
+template <int HD, int ROWS>
+__device__ __forceinline__ float4* part_at(const CacheRowsArgs& a, int slot, int c4, int row) {
+  return reinterpret_cast<float4*>(a.parts) + ((int64_t)slot * (HD / 4) + c4) * ROWS + row;
+}
+template <int ROWS>
+__device__ __forceinline__ float2* part_ml(const CacheRowsArgs& a, int slot, int row) {
+  return a.part_ml + (int64_t)slot * ROWS + row;
+}
+
+// By one thread of the block that starts a cut tile.
+__device__ __forceinline__ void rows_record(const CacheRowsArgs& a, const RowsPart& p, const SeqRows& q, int first,
+                                            int last) {
+  a.joins[first] = RowsJoin{last - first + 1, p.nv, q.row0, p.kvh, p.v0};
+}
+
+constexpr int kRowsJoinThreads = 256;
+constexpr int kRowsJoinWarps = kRowsJoinThreads / 32;
+constexpr int kRowsJoinCols = 4;      // float4 columns of a block's item
+
+// Items of 32 rows x kRowsJoinCols columns of one cut tile; the warps of a
+// block take its parts in turn.
+template <typename T, int HD, int ROWS>
+__global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const __grid_constant__ CacheRowsArgs a) {
+  __shared__ short list[kRowsMaxCtas];
+  __shared__ int upto[kRowsMaxCtas + 1];  // items in front of record i of the list
+  __shared__ int sums[2][kRowsJoinWarps];
+  __shared__ float4 acc[kRowsJoinWarps][kRowsJoinCols][32];
+  __shared__ float2 ml[kRowsJoinWarps][32];
+  constexpr int GROUPS = HD / 4 / kRowsJoinCols;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  // the records in use, in order
+  int count = 0, items = 0;
+  for (int c0 = 0; c0 < a.ctas; c0 += kRowsJoinThreads) {
+    const int c = c0 + threadIdx.x;
+    const int nv = c < a.ctas && a.joins[c].n > 0 ? a.joins[c].nv : 0;
+    int x = nv > 0, y = (nv + 31) / 32 * GROUPS;
+    const int x0 = x, y0 = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) {
+        x += u;
+        y += v;
+      }
+    }
+    if (lane == 31) {
+      sums[0][warp] = x;
+      sums[1][warp] = y;
+    }
+    __syncthreads();
+    int at = count + x - x0, it = items + y - y0;
+#pragma unroll
+    for (int w = 0; w < kRowsJoinWarps; ++w) {
+      if (w < warp) {
+        at += sums[0][w];
+        it += sums[1][w];
+      }
+      count += sums[0][w];
+      items += sums[1][w];
+    }
+    if (nv > 0) {
+      list[at] = (short)c;
+      upto[at] = it;
+    }
+    __syncthreads();
+  }
+  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (upto[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int first = list[lo];
+    const RowsJoin j = a.joins[first];
+    const int in = i - upto[lo], row = in / GROUPS * 32 + lane, c0 = in % GROUPS * kRowsJoinCols;
+    const bool on = row < j.nv;
+    float m = -INFINITY, l = 0.f;
+    float4 o[kRowsJoinCols];
+#pragma unroll
+    for (int c = 0; c < kRowsJoinCols; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on)
+#pragma unroll 2
+      for (int x = warp; x < j.n; x += kRowsJoinWarps) {
+        const int slot = rows_slot(first + x, first);
+        const float2 y = __ldcg(part_ml<ROWS>(a, slot, row));
+        float4 z[kRowsJoinCols];
+#pragma unroll
+        for (int c = 0; c < kRowsJoinCols; ++c) z[c] = __ldcg(part_at<HD, ROWS>(a, slot, c0 + c, row));
+        const float to = fmaxf(m, y.x), base = to == -INFINITY ? 0.f : to;
+        const float f = ex2(m - base), g = ex2(y.x - base);
+        l = l * f + y.y * g;
+        m = to;
+#pragma unroll
+        for (int c = 0; c < kRowsJoinCols; ++c)
+          o[c] = make_float4(o[c].x * f + z[c].x * g, o[c].y * f + z[c].y * g, o[c].z * f + z[c].z * g,
+                             o[c].w * f + z[c].w * g);
+      }
+    ml[warp][lane] = make_float2(m, l);
+#pragma unroll
+    for (int c = 0; c < kRowsJoinCols; ++c) acc[warp][c][lane] = o[c];
+    __syncthreads();
+    if (warp < kRowsJoinCols && on) {  // warp c: column c of the rows
+      float top = ml[0][lane].x;
+#pragma unroll
+      for (int w = 1; w < kRowsJoinWarps; ++w) top = fmaxf(top, ml[w][lane].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRowsJoinWarps; ++w) {
+        const float f = ex2(ml[w][lane].x - base);
+        const float4 z = acc[w][warp][lane];
+        y = make_float4(y.x + z.x * f, y.y + z.y * f, y.z + z.z * f, y.w + z.w * f);
+        sum += ml[w][lane].y * f;
+      }
+      const int v = j.v0 + row, r = v / a.group;
+      rows_finish<T, HD>(a, j.row0 + r, j.kvh * a.group + (v - r * a.group), 4 * (c0 + warp), y, top, sum);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- CUDA cores --------------------------------------------------------------
+//
+// MR query vectors and blocks of 64 keys: thread (ty, tx) of 16 x 16 has
+// MR / 16 x 4 scores (vectors ty * MR / 16 .., keys tx, tx + 16, ...) and
+// MR / 16 x HD / 16 outputs (columns 4 tx .., 64 + 4 tx ..).  The scores'
+// operands come 4 dimensions at a time from rows padded by 16 bytes.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 64;
+
+template <int HD, int MR>
+struct SimtLayout {
+  static constexpr int LD = HD + 4, PLD = kSimtKeys + 4;
+  static constexpr int Q = 0, K = Q + MR * LD, V = K + kSimtKeys * LD, P = V + kSimtKeys * HD, LIVE = P + MR * PLD;
+  static constexpr int BYTES = (LIVE + kSimtKeys) * 4;
+};
+
+__device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
+  return fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, fmaf(x.x, y.x, s))));
+}
+__device__ __forceinline__ void axpy4(float (&o)[4], float p, float4 v) {
+  o[0] = fmaf(p, v.x, o[0]);
+  o[1] = fmaf(p, v.y, o[1]);
+  o[2] = fmaf(p, v.z, o[2]);
+  o[3] = fmaf(p, v.w, o[3]);
+}
+
+template <typename T, int HD, int MR>
+__global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __grid_constant__ CacheRowsArgs a) {
+  using Lay = SimtLayout<HD, MR>;
+  constexpr int RPT = MR / 16, KPT = kSimtKeys / 16, CPT = HD / 64;
+  extern __shared__ __align__(16) float sm[];
+  float *sq = sm + Lay::Q, *sk = sm + Lay::K, *sv = sm + Lay::V, *sp = sm + Lay::P;
+  int* live = reinterpret_cast<int*>(sm + Lay::LIVE);
+  const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys};
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  pdl_wait();
+  pdl_trigger();
+  RowsWalk walk;
+  bool empties;
+  const bool ok = rows_plan<kSimtThreads>(a, sh, walk, &empties);
+  if (tid == 0) a.joins[blockIdx.x].n = 0;
+  if (!ok) return;
+  rows_empties<T, HD, kSimtThreads>(a, empties);
+  RowsPart p;
+  SeqRows q;
+  while (walk.next(a, sh, p, q)) {
+    __syncthreads();  // the last part's queries are read
+    for (int i = tid; i < MR * HD / 4; i += kSimtThreads) {
+      const int r = i / (HD / 4), d = i % (HD / 4) * 4, v = p.v0 + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < p.nv)
+        x = load4<T>(static_cast<const T*>(a.q) + (int64_t)(q.row0 + v / a.group) * a.ld_q +
+                     (int64_t)(p.kvh * a.group + v % a.group) * HD + d);
+      *reinterpret_cast<float4*>(sq + r * Lay::LD + d) = x;
+    }
+    float o[RPT][CPT][4], m[RPT], l[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
+    }
+#pragma unroll 1
+    for (int b = p.b0; b < p.b1; ++b) {
+      __syncthreads();  // the last block's keys, values and weights are read
+      for (int i = tid; i < kSimtKeys * HD / 4; i += kSimtThreads) {
+        const int r = i / (HD / 4), d = i % (HD / 4) * 4, j = b * kSimtKeys + r;
+        uint32_t slot = ~0u;
+        if (j < q.len) {
+          slot = entry_slot32(a.table, page_entry(a.table, q.s, j), j);
+          if (slot == ~0u) cache_error(a.err, kCacheBadPage);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (slot != ~0u) {
+          const int64_t at = ((int64_t)slot * a.nkv + p.kvh) * HD + d;
+          x = load4<T>(static_cast<const T*>(a.k) + at);
+          y = load4<T>(static_cast<const T*>(a.v) + at);
+        }
+        *reinterpret_cast<float4*>(sk + r * Lay::LD + d) = x;
+        *reinterpret_cast<float4*>(sv + r * HD + d) = y;
+        if (d == 0) live[r] = slot != ~0u;
+      }
+      __syncthreads();
+      float s[RPT][KPT];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) s[i][k] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 4) {
+        float4 x[RPT], y[KPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) x[i] = *reinterpret_cast<const float4*>(sq + (ty * RPT + i) * Lay::LD + d);
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) y[k] = *reinterpret_cast<const float4*>(sk + (tx + 16 * k) * Lay::LD + d);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+          for (int k = 0; k < KPT; ++k) s[i][k] = dot4(x[i], y[k], s[i][k]);
+      }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+          s[i][k] = live[tx + 16 * k] ? s[i][k] * a.scale_log2 : -INFINITY;
+          top = fmaxf(top, s[i][k]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+        const float base = top == -INFINITY ? 0.f : top, f = ex2(m[i] - base);
+        m[i] = top;
+        l[i] *= f;
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+          const float w = ex2((s[i][k] - base) - kRowsRoom);
+          l[i] += w;
+          sp[(ty * RPT + i) * Lay::PLD + tx + 16 * k] = w;
+        }
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
+      }
+      __syncwarp();  // a warp's two ty read only their own weights
+#pragma unroll 2
+      for (int j = 0; j < kSimtKeys; j += 4) {
+        float4 w[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (ty * RPT + i) * Lay::PLD + j);
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+          float4 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float4*>(sv + (j + e) * HD + 64 * c + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) {
+            axpy4(o[i][c], w[i].x, v[0]);
+            axpy4(o[i][c], w[i].y, v[1]);
+            axpy4(o[i][c], w[i].z, v[2]);
+            axpy4(o[i][c], w[i].w, v[3]);
+          }
+        }
+      }
+    }
+    const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per);
+    const int slot = rows_slot(blockIdx.x, first);
+    if (last > first && first == (int)blockIdx.x && tid == 0) rows_record(a, p, q, first, last);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], x);
+      const int r = ty * RPT + i, v = p.v0 + r, t = v / a.group;
+      if (r >= p.nv) continue;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        const float4 y = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+        if (last > first)
+          *part_at<HD, MR>(a, slot, 16 * c + tx, r) = y;
+        else
+          rows_finish<T, HD>(a, q.row0 + t, p.kvh * a.group + (v - t * a.group), 64 * c + 4 * tx, y, m[i], l[i]);
+      }
+      if (last > first && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+template <typename T, int HD, int MR>
+cudaError_t simt_rows(cudaStream_t st, CacheRowsArgs a, int sm_count) {
+  a.least = 1;
+  cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD, MR>::BYTES, 1,
+                             cache_rows_simt_kernel<T, HD, MR>, a);
+  if (e == cudaSuccess)
+    e = launch_pdl(st, dim3(4 * sm_count), dim3(kRowsJoinThreads), 0, 1, cache_rows_join_kernel<T, HD, MR>, a);
+  return e;
+}
+
+template <typename T, int HD>
+cudaError_t allow_simt() {
+  return cudaFuncSetAttribute(cache_rows_simt_kernel<T, HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SimtLayout<HD, 64>::BYTES);
+}
+
+}  // namespace
+
+int cache_rows_ctas(int sm_count) {
+  return kRowsCtasPerSM * sm_count < kRowsMaxCtas ? kRowsCtasPerSM * sm_count : kRowsMaxCtas;
+}
+int cache_rows_slot_rows(int bf16) { return 64; }
+
+cudaError_t prepare_cache_rows() {
+  cudaError_t e = allow_simt<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = allow_simt<__nv_bfloat16, 64>();
+  if (e == cudaSuccess) e = allow_simt<float, 128>();
+  if (e == cudaSuccess) e = allow_simt<float, 64>();
+  return e;
+}
+
+cudaError_t launch_cache_rows(cudaStream_t st, const CacheRowsArgs& a, int bf16, int hd, int sm_count) {
+  if (!bf16) return hd == 128 ? simt_rows<float, 128, 64>(st, a, sm_count) : simt_rows<float, 64, 64>(st, a, sm_count);
+  return hd == 128 ? simt_rows<__nv_bfloat16, 128, 64>(st, a, sm_count)
+                   : simt_rows<__nv_bfloat16, 64, 64>(st, a, sm_count);
+}
+
+}  // namespace sf

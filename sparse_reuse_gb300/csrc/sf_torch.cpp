@@ -205,6 +205,66 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+double as_double(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{""};
+  return v;
+}
+
+// state, k_pages, table, lens, pos_from, pos_to, stream
+PyObject* py_reposition(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, n ? a[0] : Py_None, [&](const State& s) -> int {
+    const Table t = table(s, a[2], "table");
+    const Pools p = pools(s, a[1], a[1]);
+    const int64_t S[1] = {t.S};
+    const void* lens = fixed(s, a[3], "lens", at::kInt, S);
+    const at::Tensor& ft = tensor(a[4], "pos_from");
+    const int64_t shape[3] = {t.S, s.nkv, ft.dim() == 3 ? ft.size(2) : 0};
+    const void* from = fixed(s, a[4], "pos_from", at::kInt, shape);
+    const void* to = fixed(s, a[5], "pos_to", at::kInt, shape, true);
+    return sf_cache_reposition(s.cache, stream_of(s, a[6]), p.k, p.pages, t.p, count(t.S, "S"), count(t.cols, "columns"),
+                               t.ld, (const int32_t*)lens, (const int32_t*)from, (const int32_t*)to, shape[2]);
+  });
+}
+
+// state, q, k_pages, v_pages, table, lens, starts, scale, out, lse, stream
+PyObject* py_attend_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, n ? a[0] : Py_None, [&](const State& s) -> int {
+    const Table t = table(s, a[4], "table");
+    const Rows q = rows(s, a[1], "q", s.nq), out = rows(s, a[8], "out", s.nq);
+    if (out.n != q.n) throw Refused{"out has " + std::to_string(out.n) + " rows, q " + std::to_string(q.n)};
+    const Pools p = pools(s, a[2], a[3]);
+    const int64_t S[1] = {t.S}, S1[1] = {t.S + 1}, ls[2] = {q.n, s.nq};
+    const void* lens = fixed(s, a[5], "lens", at::kInt, S);
+    const void* starts = fixed(s, a[6], "starts", at::kInt, S1);
+    void* lse = fixed(s, a[9], "lse", at::kFloat, ls, true);
+    return sf_cache_attend_rows(s.cache, stream_of(s, a[10]), q.p, q.ld, count(q.n, "T"), p.k, p.v, p.pages, t.p,
+                                count(t.S, "S"), count(t.cols, "columns"), t.ld, (const int32_t*)lens,
+                                (const int32_t*)starts, (float)as_double(a[7]), out.p, out.ld, (float*)lse);
+  });
+}
+
+// state, q, k_pages, v_pages, table, lens, prefix_table, prefix_lens, starts, scale, out, lse, stream
+PyObject* py_attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, n ? a[0] : Py_None, [&](const State& s) -> int {
+    const Table t = table(s, a[4], "table"), pt = table(s, a[6], "prefix_table");
+    const Rows q = rows(s, a[1], "q", s.nq), out = rows(s, a[10], "out", s.nq);
+    if (q.n != t.S || out.n != t.S)
+      throw Refused{"q has " + std::to_string(q.n) + " rows, out " + std::to_string(out.n) + ", table " +
+                    std::to_string(t.S)};
+    const Pools p = pools(s, a[2], a[3]);
+    const int64_t S[1] = {t.S}, G[1] = {pt.S}, G1[1] = {pt.S + 1}, ls[2] = {q.n, s.nq};
+    const void* lens = fixed(s, a[5], "lens", at::kInt, S);
+    const void* plens = fixed(s, a[7], "prefix_lens", at::kInt, G);
+    const void* starts = fixed(s, a[8], "starts", at::kInt, G1);
+    void* lse = fixed(s, a[11], "lse", at::kFloat, ls, true);
+    return sf_cache_attend_shared(s.cache, stream_of(s, a[12]), q.p, q.ld, p.k, p.v, p.pages, t.p, count(t.S, "S"),
+                                  count(t.cols, "columns"), t.ld, (const int32_t*)lens, pt.p, count(pt.S, "G"),
+                                  count(pt.cols, "prefix columns"), pt.ld, (const int32_t*)plens,
+                                  (const int32_t*)starts, (float)as_double(a[9]), out.p, out.ld, (float*)lse);
+  });
+}
+
 // state, k_pages, v_pages, table, lens, weights, budget, n_first, n_recent, k_out, v_out, table_out, weights_out,
 // lens_out, kept, stream
 PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -246,6 +306,12 @@ PyMethodDef methods[] = {
     {"state", py_state, METH_VARARGS, "Checks' view of a cache object."},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_append)), METH_FASTCALL, "sf_cache_append"},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend)), METH_FASTCALL, "sf_cache_attend"},
+    {"reposition", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_reposition)), METH_FASTCALL,
+     "sf_cache_reposition"},
+    {"attend_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend_rows)), METH_FASTCALL,
+     "sf_cache_attend_rows"},
+    {"attend_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attend_shared)), METH_FASTCALL,
+     "sf_cache_attend_shared"},
     {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_evict)), METH_FASTCALL, "sf_cache_evict"},
     {nullptr, nullptr, 0, nullptr}};
 
