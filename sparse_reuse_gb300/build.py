@@ -26,7 +26,8 @@ TORCH_EXT = os.path.join(PKG, "_sf_torch.so")  # torch argument marshalling of t
 TORCH_STAMP = os.path.join(BUILD, "sf_torch.version")  # the torch it was built for
 
 SOURCES = ["sf_api.cu", "sf_gate.cu", "sf_gemm.cu", "sf_gemm_tc.cu", "sf_attn.cu", "sf_head.cu",
-           "sf_cache.cu", "sf_cache_attend.cu", "sf_cache_evict.cu", "sf_cache_rows.cu", "sf_cache_turn.cu"]
+           "sf_cache.cu", "sf_cache_attend.cu", "sf_cache_evict.cu", "sf_cache_rows.cu",
+           "sf_cache_rows_tc.cu", "sf_cache_turn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                 "-I", INCLUDE, "-I", CSRC]

@@ -210,9 +210,10 @@ sf_status check_object(sf_cache* c) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device)
     return fail(c, SF_ERR_INVALID_ARG, "the object lives on device %d, the current one is %d", c->device, dev);
   const volatile unsigned* e = c->err;
-  if (e[kCacheBadPage] || e[kCacheBadLength] || e[kCacheBadRow])
-    return fail(c, SF_ERR_DEVICE_ASSERT, "device check fired:%s%s%s", e[kCacheBadPage] ? " page out of range" : "",
-                e[kCacheBadLength] ? " length out of range" : "", e[kCacheBadRow] ? " row out of range" : "");
+  if (e[kCacheBadPage] || e[kCacheBadLength] || e[kCacheBadRow] || e[kCacheStall])
+    return fail(c, SF_ERR_DEVICE_ASSERT, "device check fired:%s%s%s%s", e[kCacheBadPage] ? " page out of range" : "",
+                e[kCacheBadLength] ? " length out of range" : "", e[kCacheBadRow] ? " row out of range" : "",
+                e[kCacheStall] ? " a wait inside a kernel ran out" : "");
   return SF_OK;
 }
 

@@ -61,7 +61,7 @@ namespace sf {
 // Device checks: one word each in pinned host memory, set to 1 by the kernel
 // that met the case.  A word per check needs no atomic, costs a clean call
 // nothing and no copy back.
-enum CacheErr { kCacheBadPage = 0, kCacheBadLength = 1, kCacheBadRow = 2, kCacheErrWords = 3 };
+enum CacheErr { kCacheBadPage = 0, kCacheBadLength = 1, kCacheBadRow = 2, kCacheStall = 3, kCacheErrWords = 4 };
 
 __device__ __forceinline__ void cache_error(unsigned* err, CacheErr which) {
   *reinterpret_cast<volatile unsigned*>(err + which) = 1u;
@@ -143,7 +143,11 @@ struct CacheRowsArgs {
 };
 int cache_rows_ctas(int sm_count);
 int cache_rows_slot_rows(int bf16);  // query vectors of a partial slot
+constexpr int kTcTileRows = 256;
 cudaError_t prepare_cache_rows();
+cudaError_t prepare_cache_rows_tc();
+// The bf16 tiles (cut ones as partial results).
+cudaError_t launch_cache_rows_tc(cudaStream_t st, const CacheRowsArgs& a, int hd);
 cudaError_t launch_cache_rows(cudaStream_t st, const CacheRowsArgs& a, int bf16, int hd, int sm_count);
 
 struct CacheEvictArgs {

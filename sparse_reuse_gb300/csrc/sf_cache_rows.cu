@@ -10,223 +10,12 @@
 // thread blocks is in sf_cache_index.h, and cut ones are joined by
 // cache_rows_join_kernel.  kRowsRoom keeps unnormalised sums from overflowing
 // where the result does not (2^18 values at most).
-#include <cmath>
-
-#include "sf_cache.h"
-#include "sf_tc.cuh"
+#include "sf_cache_rows.cuh"
 
 namespace sf {
 namespace {
 
-constexpr float kRowsRoom = 27.f;
-constexpr int kRowsCtasPerSM = 1;
-constexpr int kRowsMaxCtas = 512;
-constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Rows and length of sequence s; bad where its offsets are not ascending within [0, T] or its length is out of range.
-struct SeqRows {
-  int s, row0, rows, len;
-};
-__device__ __forceinline__ SeqRows sequence_rows(const CacheRowsArgs& a, int s, bool* bad_rows, bool* bad_len) {
-  const int r0 = __ldcg(a.starts + s), r1 = __ldcg(a.starts + s + 1);
-  *bad_rows = r0 < 0 || r1 < r0 || r1 > a.T;
-  SeqRows q;
-  q.s = s;
-  q.row0 = r0;
-  q.rows = *bad_rows ? 0 : r1 - r0;
-  q.len = checked_len(__ldcg(a.lens + s), a.limit, bad_len);
-  return q;
-}
-
-__device__ __forceinline__ int64_t units_of(const RowsShape& sh, const SeqRows& q) {
-  return q.rows > 0 && q.len > 0 ? sh.nkv * row_units(sh, q.rows, q.len) : 0;
-}
-
-__device__ __forceinline__ int64_t shfl_up64(int64_t x, int o) {
-  return (int64_t)__shfl_up_sync(kFull, (unsigned long long)x, o);
-}
-
-// Where a thread block's share of the line starts, and the walk along it.
-// Every warp walks on its own: all 32 lanes call next() together.
-struct RowsWalk {
-  int64_t u, end, per;  // this block's units [u, end)
-  int64_t first;        // of seq
-  SeqRows seq;
-
-  __device__ __forceinline__ bool next(const CacheRowsArgs& a, const RowsShape& sh, RowsPart& p, SeqRows& q) {
-    while (u < end) {
-      p = rows_part(sh, seq.rows, seq.len, first, u, end);
-      q = seq;
-      u = rows_part_end(p);
-      const int64_t units = units_of(sh, seq);
-      if (u >= first + units && u < end) {  // the next sequence with units: 32 looked at together
-        first += units;
-        const int lane = threadIdx.x & 31;
-        for (int s0 = seq.s + 1;; s0 += 32) {
-          bool b0, b1;
-          SeqRows x{0, 0, 0, 0};
-          if (s0 + lane < a.S) x = sequence_rows(a, s0 + lane, &b0, &b1);
-          const unsigned hit = __ballot_sync(kFull, units_of(sh, x) > 0);
-          if (hit) {
-            const int l = __ffs(hit) - 1;
-            seq.s = s0 + l;
-            seq.row0 = __shfl_sync(kFull, x.row0, l);
-            seq.rows = __shfl_sync(kFull, x.rows, l);
-            seq.len = __shfl_sync(kFull, x.len, l);
-            break;
-          }
-          if (s0 + 32 >= a.S) {  // not reached: units are left
-            u = end;
-            break;
-          }
-        }
-      }
-      if (p.b0 < p.b1) return true;
-    }
-    return false;
-  }
-};
-
-// By all THREADS of the block: the walk's start.  False where nothing of the
-// call may be written (offsets that do not ascend).  *empties: some sequence
-// with rows has no keys.
-template <int THREADS>
-__device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShape& sh, RowsWalk& walk, bool* empties) {
-  constexpr int WARPS = THREADS / 32;
-  __shared__ int64_t sums[WARPS];
-  __shared__ RowsWalk found;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t mine = 0;
-  int flags = 0;
-  SeqRows head{0, 0, 0, 0};
-  for (int s = threadIdx.x; s < a.S; s += THREADS) {
-    bool bad_rows, bad_len;
-    const SeqRows q = sequence_rows(a, s, &bad_rows, &bad_len);
-    if (s == (int)threadIdx.x) head = q;
-    mine += units_of(sh, q);
-    flags |= (bad_rows ? 1 : 0) | (bad_len ? 2 : 0) | (q.rows > 0 && q.len == 0 ? 4 : 0);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += (int64_t)__shfl_xor_sync(kFull, (unsigned long long)mine, o);
-  if (lane == 0) sums[warp] = mine;
-  const bool bad_rows = __syncthreads_or(flags & 1), bad_len = __syncthreads_or(flags & 2);
-  *empties = __syncthreads_or(flags & 4);
-  if (threadIdx.x == 0 && blockIdx.x == 0) {
-    if (bad_rows) cache_error(a.err, kCacheBadRow);
-    if (bad_len) cache_error(a.err, kCacheBadLength);
-  }
-  if (bad_rows) return false;
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += sums[w];
-  const int64_t per = units_per_block(total, a.ctas, a.least);
-  const int64_t lo = per * blockIdx.x, hi = lo + per < total ? lo + per : total;
-  if (lo >= hi) {
-    walk.u = walk.end = 0;
-    walk.per = per;
-    return true;
-  }
-  int64_t before = 0;
-  for (int s0 = 0; s0 < a.S; s0 += THREADS) {
-    const int s = s0 + threadIdx.x;
-    SeqRows q = head;
-    if (s0 > 0) {
-      bool b0, b1;
-      q = SeqRows{0, 0, 0, 0};
-      if (s < a.S) q = sequence_rows(a, s, &b0, &b1);
-    }
-    const int64_t x = units_of(sh, q);
-    int64_t y = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = shfl_up64(y, o);
-      if (lane >= o) y += z;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = y;
-    __syncthreads();
-    int64_t at = before + y - x;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) at += sums[w];
-      before += sums[w];
-    }
-    if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
-    if (before > lo) break;
-  }
-  __syncthreads();
-  walk = found;
-  return true;
-}
-
-// One float4 of a finished row: normalised, together with the tail's state
-// where the call has one.
-template <typename T, int HD>
-__device__ __forceinline__ void rows_finish(const CacheRowsArgs& a, int64_t t, int h, int d, float4 o, float m, float l) {
-  const int64_t at = t * a.nq + h;
-  if (a.tail_ml) {
-    const float2 tail = __ldcg(a.tail_ml + at);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.tail_o + at * HD + d));
-    const float top = fmaxf(m, tail.x), base = top == -INFINITY ? 0.f : top;
-    // the tail's output is normalised: its weight is its denominator
-    const float f = ex2(m - base), g = tail.y * ex2(tail.x - base);
-    o = make_float4(o.x * f + y.x * g, o.y * f + y.y * g, o.z * f + y.z * g, o.w * f + y.w * g);
-    l = l * f + g;
-    m = top;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
-  store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d,
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
-}
-
-// Rows that no key belongs to: those of sequences without keys, and with a tail those of no sequence.
-template <typename T, int HD, int THREADS>
-__device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
-  auto clear = [&](int64_t t0, int64_t n) {
-    for (int64_t i = threadIdx.x; i < n * a.nq * (HD / 4); i += THREADS) {
-      const int64_t r = i / (HD / 4);
-      rows_finish<T, HD>(a, t0 + r / a.nq, (int)(r % a.nq), 4 * (int)(i % (HD / 4)), make_float4(0.f, 0.f, 0.f, 0.f),
-                         -INFINITY, 0.f);
-    }
-  };
-  if (empties)
-    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
-      bool b0, b1;
-      const SeqRows q = sequence_rows(a, s, &b0, &b1);
-      if (q.len == 0 && q.rows > 0) clear(q.row0, q.rows);
-    }
-  if (a.tail_ml) {  // rows in front of the first group and behind the last
-    const int r0 = __ldcg(a.starts), r1 = __ldcg(a.starts + a.S);
-    for (int t = blockIdx.x; t < r0; t += gridDim.x) clear(t, 1);
-    for (int t = r1 + blockIdx.x; t < a.T; t += gridDim.x) clear(t, 1);
-  }
-}
-
-// ---- partial results: per slot ROWS query vectors, [HD / 4][ROWS] float4 and
-// (m, l) of each.  Neighbouring rows lie side by side: a thread has one row,
-// or a few.
-template <int HD, int ROWS>
-__device__ __forceinline__ float4* part_at(const CacheRowsArgs& a, int slot, int c4, int row) {
-  return reinterpret_cast<float4*>(a.parts) + ((int64_t)slot * (HD / 4) + c4) * ROWS + row;
-}
-template <int ROWS>
-__device__ __forceinline__ float2* part_ml(const CacheRowsArgs& a, int slot, int row) {
-  return a.part_ml + (int64_t)slot * ROWS + row;
-}
-
-// By one thread of the block that starts a cut tile.
-__device__ __forceinline__ void rows_record(const CacheRowsArgs& a, const RowsPart& p, const SeqRows& q, int first,
-                                            int last) {
-  a.joins[first] = RowsJoin{last - first + 1, p.nv, q.row0, p.kvh, p.v0};
-}
+using namespace rows;
 
 constexpr int kRowsJoinThreads = 256;
 constexpr int kRowsJoinWarps = kRowsJoinThreads / 32;
@@ -510,19 +299,22 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
   }
 }
 
+template <typename T, int HD, int ROWS>
+cudaError_t join_rows(cudaStream_t st, const CacheRowsArgs& a, int sm_count) {
+  return launch_pdl(st, dim3(4 * sm_count), dim3(kRowsJoinThreads), 0, 1, cache_rows_join_kernel<T, HD, ROWS>, a);
+}
+
 template <typename T, int HD, int MR>
 cudaError_t simt_rows(cudaStream_t st, CacheRowsArgs a, int sm_count) {
   a.least = 1;
   cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD, MR>::BYTES, 1,
                              cache_rows_simt_kernel<T, HD, MR>, a);
-  if (e == cudaSuccess)
-    e = launch_pdl(st, dim3(4 * sm_count), dim3(kRowsJoinThreads), 0, 1, cache_rows_join_kernel<T, HD, MR>, a);
-  return e;
+  return e == cudaSuccess ? join_rows<T, HD, MR>(st, a, sm_count) : e;
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t allow_simt() {
-  return cudaFuncSetAttribute(cache_rows_simt_kernel<T, HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(cache_rows_simt_kernel<float, HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               SimtLayout<HD, 64>::BYTES);
 }
 
@@ -531,20 +323,21 @@ cudaError_t allow_simt() {
 int cache_rows_ctas(int sm_count) {
   return kRowsCtasPerSM * sm_count < kRowsMaxCtas ? kRowsCtasPerSM * sm_count : kRowsMaxCtas;
 }
-int cache_rows_slot_rows(int bf16) { return 64; }
+int cache_rows_slot_rows(int bf16) { return bf16 ? kTcTileRows : 64; }
 
 cudaError_t prepare_cache_rows() {
-  cudaError_t e = allow_simt<__nv_bfloat16, 128>();
-  if (e == cudaSuccess) e = allow_simt<__nv_bfloat16, 64>();
-  if (e == cudaSuccess) e = allow_simt<float, 128>();
-  if (e == cudaSuccess) e = allow_simt<float, 64>();
+  cudaError_t e = allow_simt<128>();
+  if (e == cudaSuccess) e = allow_simt<64>();
+  if (e == cudaSuccess) e = prepare_cache_rows_tc();
   return e;
 }
 
 cudaError_t launch_cache_rows(cudaStream_t st, const CacheRowsArgs& a, int bf16, int hd, int sm_count) {
   if (!bf16) return hd == 128 ? simt_rows<float, 128, 64>(st, a, sm_count) : simt_rows<float, 64, 64>(st, a, sm_count);
-  return hd == 128 ? simt_rows<__nv_bfloat16, 128, 64>(st, a, sm_count)
-                   : simt_rows<__nv_bfloat16, 64, 64>(st, a, sm_count);
+  const cudaError_t e = launch_cache_rows_tc(st, a, hd);
+  if (e != cudaSuccess) return e;
+  return hd == 128 ? join_rows<__nv_bfloat16, 128, kTcTileRows>(st, a, sm_count)
+                   : join_rows<__nv_bfloat16, 64, kTcTileRows>(st, a, sm_count);
 }
 
 }  // namespace sf

@@ -1,0 +1,236 @@
+// What the kernels of sf_cache_attend_rows share: the walk over a batch's
+// tiles, the end of a row, partial results.
+#pragma once
+
+#include "sf_cache.h"
+
+namespace sf {
+namespace rows {
+
+constexpr float kRowsRoom = 27.f;
+constexpr int kRowsCtasPerSM = 1;
+constexpr int kRowsMaxCtas = 512;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows and length of sequence s; bad where its offsets are not ascending within [0, T] or its length is out of range.
+struct SeqRows {
+  int s, row0, rows, len;
+};
+__device__ __forceinline__ SeqRows sequence_rows(const CacheRowsArgs& a, int s, bool* bad_rows, bool* bad_len) {
+  const int r0 = __ldcg(a.starts + s), r1 = __ldcg(a.starts + s + 1);
+  *bad_rows = r0 < 0 || r1 < r0 || r1 > a.T;
+  SeqRows q;
+  q.s = s;
+  q.row0 = r0;
+  q.rows = *bad_rows ? 0 : r1 - r0;
+  q.len = checked_len(__ldcg(a.lens + s), a.limit, bad_len);
+  return q;
+}
+
+__device__ __forceinline__ int64_t units_of(const RowsShape& sh, const SeqRows& q) {
+  return q.rows > 0 && q.len > 0 ? sh.nkv * row_units(sh, q.rows, q.len) : 0;
+}
+
+__device__ __forceinline__ int64_t shfl_up64(int64_t x, int o) {
+  return (int64_t)__shfl_up_sync(kFull, (unsigned long long)x, o);
+}
+
+// Where a thread block's share of the line starts, and the walk along it.
+// Every warp walks on its own: all 32 lanes call next() together.
+struct RowsWalk {
+  int64_t u, end, per;  // this block's units [u, end)
+  int64_t first;        // of seq
+  SeqRows seq;
+
+  __device__ __forceinline__ bool next(const CacheRowsArgs& a, const RowsShape& sh, RowsPart& p, SeqRows& q) {
+    while (u < end) {
+      p = rows_part(sh, seq.rows, seq.len, first, u, end);
+      q = seq;
+      u = rows_part_end(p);
+      const int64_t units = units_of(sh, seq);
+      if (u >= first + units && u < end) {  // the next sequence with units: 32 looked at together
+        first += units;
+        const int lane = threadIdx.x & 31;
+        for (int s0 = seq.s + 1;; s0 += 32) {
+          bool b0, b1;
+          SeqRows x{0, 0, 0, 0};
+          if (s0 + lane < a.S) x = sequence_rows(a, s0 + lane, &b0, &b1);
+          const unsigned hit = __ballot_sync(kFull, units_of(sh, x) > 0);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            seq.s = s0 + l;
+            seq.row0 = __shfl_sync(kFull, x.row0, l);
+            seq.rows = __shfl_sync(kFull, x.rows, l);
+            seq.len = __shfl_sync(kFull, x.len, l);
+            break;
+          }
+          if (s0 + 32 >= a.S) {  // not reached: units are left
+            u = end;
+            break;
+          }
+        }
+      }
+      if (p.b0 < p.b1) return true;
+    }
+    return false;
+  }
+};
+
+// By all THREADS of the block: the walk's start.  False where nothing of the
+// call may be written (offsets that do not ascend).  *empties: some sequence
+// with rows has no keys.
+template <int THREADS>
+__device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShape& sh, RowsWalk& walk, bool* empties) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int64_t sums[WARPS];
+  __shared__ RowsWalk found;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t mine = 0;
+  int flags = 0;
+  SeqRows head{0, 0, 0, 0};
+  for (int s = threadIdx.x; s < a.S; s += THREADS) {
+    bool bad_rows, bad_len;
+    const SeqRows q = sequence_rows(a, s, &bad_rows, &bad_len);
+    if (s == (int)threadIdx.x) head = q;
+    mine += units_of(sh, q);
+    flags |= (bad_rows ? 1 : 0) | (bad_len ? 2 : 0) | (q.rows > 0 && q.len == 0 ? 4 : 0);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += (int64_t)__shfl_xor_sync(kFull, (unsigned long long)mine, o);
+  if (lane == 0) sums[warp] = mine;
+  const bool bad_rows = __syncthreads_or(flags & 1), bad_len = __syncthreads_or(flags & 2);
+  *empties = __syncthreads_or(flags & 4);
+  if (threadIdx.x == 0 && blockIdx.x == 0) {
+    if (bad_rows) cache_error(a.err, kCacheBadRow);
+    if (bad_len) cache_error(a.err, kCacheBadLength);
+  }
+  if (bad_rows) return false;
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) total += sums[w];
+  const int64_t per = units_per_block(total, a.ctas, a.least);
+  const int64_t lo = per * blockIdx.x, hi = lo + per < total ? lo + per : total;
+  if (lo >= hi) {
+    walk.u = walk.end = 0;
+    walk.per = per;
+    return true;
+  }
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.S; s0 += THREADS) {
+    const int s = s0 + threadIdx.x;
+    SeqRows q = head;
+    if (s0 > 0) {
+      bool b0, b1;
+      q = SeqRows{0, 0, 0, 0};
+      if (s < a.S) q = sequence_rows(a, s, &b0, &b1);
+    }
+    const int64_t x = units_of(sh, q);
+    int64_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = shfl_up64(y, o);
+      if (lane >= o) y += z;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = y;
+    __syncthreads();
+    int64_t at = before + y - x;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
+    if (before > lo) break;
+  }
+  __syncthreads();
+  walk = found;
+  return true;
+}
+
+// What makes a finished row of its unnormalised sums (m, l): with the tail's
+// state, where the call has one, out = (o f + tail g) inv.
+struct RowEnd {
+  float f, g, inv;
+};
+__device__ __forceinline__ RowEnd rows_end(const CacheRowsArgs& a, int64_t at, float m, float l, bool lse) {
+  RowEnd e{1.f, 0.f, 0.f};
+  if (a.tail_ml) {
+    const float2 tail = __ldcg(a.tail_ml + at);
+    const float top = fmaxf(m, tail.x), base = top == -INFINITY ? 0.f : top;
+    // the tail's output is normalised: its weight is its denominator
+    e.f = ex2(m - base);
+    e.g = tail.y * ex2(tail.x - base);
+    l = l * e.f + e.g;
+    m = top;
+  }
+  e.inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
+  if (lse && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
+  return e;
+}
+template <int HD>
+__device__ __forceinline__ float4 rows_value(const CacheRowsArgs& a, int64_t at, int d, float4 o, const RowEnd& e) {
+  if (a.tail_ml) {
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.tail_o + at * HD + d));
+    o = make_float4(o.x * e.f + y.x * e.g, o.y * e.f + y.y * e.g, o.z * e.f + y.z * e.g, o.w * e.f + y.w * e.g);
+  }
+  return make_float4(o.x * e.inv, o.y * e.inv, o.z * e.inv, o.w * e.inv);
+}
+// One float4 of a finished row.
+template <typename T, int HD>
+__device__ __forceinline__ void rows_finish(const CacheRowsArgs& a, int64_t t, int h, int d, float4 o, float m, float l) {
+  const int64_t at = t * a.nq + h;
+  const RowEnd e = rows_end(a, at, m, l, d == 0);
+  store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d, rows_value<HD>(a, at, d, o, e));
+}
+
+// Rows that no key belongs to: those of sequences without keys, and with a tail those of no sequence.
+template <typename T, int HD, int THREADS>
+__device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
+  auto clear = [&](int64_t t0, int64_t n) {
+    for (int64_t i = threadIdx.x; i < n * a.nq * (HD / 4); i += THREADS) {
+      const int64_t r = i / (HD / 4);
+      rows_finish<T, HD>(a, t0 + r / a.nq, (int)(r % a.nq), 4 * (int)(i % (HD / 4)), make_float4(0.f, 0.f, 0.f, 0.f),
+                         -INFINITY, 0.f);
+    }
+  };
+  if (empties)
+    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+      bool b0, b1;
+      const SeqRows q = sequence_rows(a, s, &b0, &b1);
+      if (q.len == 0 && q.rows > 0) clear(q.row0, q.rows);
+    }
+  if (a.tail_ml) {  // rows in front of the first group and behind the last
+    const int r0 = __ldcg(a.starts), r1 = __ldcg(a.starts + a.S);
+    for (int t = blockIdx.x; t < r0; t += gridDim.x) clear(t, 1);
+    for (int t = r1 + blockIdx.x; t < a.T; t += gridDim.x) clear(t, 1);
+  }
+}
+
+// ---- partial results: per slot ROWS query vectors, [HD / 4][ROWS] float4 and
+// (m, l) of each.  Neighbouring rows lie side by side: a thread has one row,
+// or a few.
+template <int HD, int ROWS>
+__device__ __forceinline__ float4* part_at(const CacheRowsArgs& a, int slot, int c4, int row) {
+  return reinterpret_cast<float4*>(a.parts) + ((int64_t)slot * (HD / 4) + c4) * ROWS + row;
+}
+template <int ROWS>
+__device__ __forceinline__ float2* part_ml(const CacheRowsArgs& a, int slot, int row) {
+  return a.part_ml + (int64_t)slot * ROWS + row;
+}
+
+// By one thread of the block that starts a cut tile.
+__device__ __forceinline__ void rows_record(const CacheRowsArgs& a, const RowsPart& p, const SeqRows& q, int first,
+                                            int last) {
+  a.joins[first] = RowsJoin{last - first + 1, p.nv, q.row0, p.kvh, p.v0};
+}
+
+}  // namespace rows
+}  // namespace sf

@@ -1,0 +1,489 @@
+// Attention of blocks of rows over the paged cache, bf16: 5th-generation
+// tensor cores (the operator is described in sf_cache_rows.cu).
+//
+// A tile is up to 256 query vectors, two halves of 128 (a half's vectors are
+// the 128 TMEM lanes), over blocks of 128 keys.  Per half and block
+//   S = Q K^T   tcgen05.mma, Q and K from shared memory, S in TMEM
+//   P = 2^(x - m - kRowsRoom) by one thread per vector, written over S as bf16
+//   O += P V    tcgen05.mma, P from TMEM, V MN-major from shared memory, O in
+//               TMEM
+// and the two halves take turns: one's softmax runs while the tensor core works
+// for the other.  A tile of one half alone ("narrow") gives both softmax groups
+// the same vectors and every other block each; their two results meet in
+// registers at the end.  Its bound is the keys' bandwidth, not the tensor core,
+// so P enters there as the sum of two bf16 numbers.
+//
+// Order on the tensor core.  One thread issues every MMA, and they execute in
+// that order; a commit covers all before it.  S of a half's next block follows
+// its O += P V, so when the softmax sees the new S, O is at rest: a row whose
+// maximum grows by more than kSlack rescales it there (rarely: the maximum is
+// kept only to within 2^kSlack).
+//
+// Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 MMA (owns TMEM),
+// 9 keys, 10 values: pages are gathered by 16-byte cp.async into 128-byte
+// swizzled tiles, whatever the page size, with zeros for positions that are not
+// there.
+#include <cmath>
+
+#include "sf_cache_rows.cuh"
+#include "sf_pairs.cuh"
+#include "sf_tc.cuh"
+
+namespace sf {
+namespace {
+
+using namespace rows;
+
+constexpr int kTcThreads = 384;
+constexpr int kTcHalf = 128;   // query vectors of a half
+constexpr int kTcKeys = 128;   // keys of a block
+constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
+constexpr float kSlack = 8.f;
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
+
+template <int HD>
+struct TcLayout {
+  static constexpr int ST = HD == 128 ? 2 : 4;       // stages of the key ring, and of the value ring
+  static constexpr int TILE = 128 * 128;             // 128 rows of 64 dimensions
+  static constexpr int STAGE = HD / 64 * TILE;
+  static constexpr int Q = 0;                        // two halves
+  static constexpr int K = Q + 2 * STAGE;
+  static constexpr int V = K + ST * STAGE;
+  static constexpr int BYTES = V + ST * STAGE + 1024;  // + alignment of the dynamic window
+  static constexpr int O_COL = 256;                  // TMEM: S of half w at 128 w, O at 256 + HD w
+  static_assert(BYTES <= 224 * 1024, "shared memory");
+};
+
+struct Barriers {
+  uint64_t qfull[2], sfull[2], pfull[2], odone[2];
+  uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
+};
+
+// Bounded wait: after 2 s without the phase, or once another wait of the block
+// has given up, it returns; the call is reported as stalled.
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
+  if (tc::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*dead) return;
+    if (tc::globaltimer_ns() - t0 > 2000000000ull) {
+      *dead = 1;
+      cache_error(err, kCacheStall);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+// This thread arrives on `bar` once its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Which of a part's blocks softmax group w takes: `n` of them, the i-th being
+// block first + step * i of the part.
+struct Share {
+  int n, first, step;
+};
+__device__ __forceinline__ Share share_of(const RowsPart& p, int w) {
+  const int nb = p.b1 - p.b0;
+  return p.w == 2 ? Share{nb, 0, 1} : Share{(nb + 1 - w) >> 1, w, 2};
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __grid_constant__ CacheRowsArgs a,
+                                                                      const int q_sign) {
+  using Lay = TcLayout<HD>;
+  constexpr int ST = Lay::ST, CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy instruction
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Barriers bar;
+  __shared__ __align__(16) uint32_t live[kLiveRing][4];
+  __shared__ float2 sml[2][kTcHalf];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int dead_;
+  volatile int* dead = &dead_;
+  unsigned char* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const RowsShape sh{a.group, a.nkv, kTcHalf, 2, kTcKeys};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.qfull[i], kTcHalf);
+      tc::mbar_init(&bar.sfull[i], 1);
+      tc::mbar_init(&bar.pfull[i], kTcHalf);
+      tc::mbar_init(&bar.odone[i], 1);
+    }
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(&bar.kfull[i], 33);  // every lane's copies, and the mask of live keys
+      tc::mbar_init(&bar.kempty[i], 1);
+      tc::mbar_init(&bar.vfull[i], 32);
+      tc::mbar_init(&bar.vempty[i], 1);
+    }
+    dead_ = 0;
+    tc::fence_barrier_init();
+  }
+  // before the next kernel may start: it could take the TMEM that this one would wait for
+  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_slot, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  RowsWalk walk;
+  bool empties;
+  const bool ok = rows_plan<kTcThreads>(a, sh, walk, &empties);
+  if (tid == 0) a.joins[blockIdx.x].n = 0;
+  if (ok) rows_empties<__nv_bfloat16, HD, kTcThreads>(a, empties);
+  else walk.u = walk.end = 0;
+  RowsPart p;
+  SeqRows q;
+
+  if (warp == kMmaWarp) {
+    const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
+    const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
+    const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::Q));
+    const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::K));
+    const uint64_t dv = tc::sw128_mnmajor_desc(tc::smem_u32(base + Lay::V), Lay::TILE);
+    uint32_t blocks = 0, parts[2] = {0, 0}, steps[2] = {0, 0};  // so far: of the rings, of each group
+    while (walk.next(a, sh, p, q)) {
+      if (lane == 0) {
+        const Share share[2] = {share_of(p, 0), share_of(p, 1)};
+        const bool wide = p.w == 2;
+        auto scores = [&](int w, int i) {
+          const uint32_t b = blocks + share[w].first + share[w].step * i, st = b % ST;
+          wait_for(&bar.kfull[st], (b / ST) & 1, dead, a.err);
+          tc::fence_proxy_async_smem();  // the copies are the generic proxy's
+          tc::fence_after_sync();
+          const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4), qa = dq + (uint64_t)((w * Lay::STAGE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * Lay::TILE + (kk & 3) * 32) >> 4);
+            tc::mma_bf16(tmem + w * kTcKeys, qa + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&bar.sfull[w]);
+          if (!wide || w == 1) tc::mma_commit(&bar.kempty[st]);
+        };
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (share[w].n > 0) {
+            wait_for(&bar.qfull[w], parts[w] & 1, dead, a.err);
+            tc::fence_proxy_async_smem();
+            scores(w, 0);
+            ++parts[w];
+          }
+        for (int i = 0; i < share[0].n; ++i)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (i >= share[w].n) continue;
+            const uint32_t b = blocks + share[w].first + share[w].step * i, st = b % ST;
+            wait_for(&bar.vfull[st], (b / ST) & 1, dead, a.err);
+            wait_for(&bar.pfull[w], steps[w] & 1, dead, a.err);
+            ++steps[w];
+            tc::fence_proxy_async_smem();
+            tc::fence_after_sync();
+            const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
+            const uint32_t o = tmem + Lay::O_COL + w * HD, pa = tmem + w * kTcKeys;
+#pragma unroll
+            for (int kk = 0; kk < kTcKeys / 16; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
+              tc::mma_bf16_ts(o, pa + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, i > 0 || kk > 0 ? 1u : 0u);
+            if (!wide)
+#pragma unroll
+              for (int kk = 0; kk < kTcKeys / 16; ++kk)  // what rounding P left
+                tc::mma_bf16_ts(o, pa + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
+            if (!wide || w == 1) tc::mma_commit(&bar.vempty[st]);
+            if (i + 1 < share[w].n)
+              scores(w, i + 1);
+            else
+              tc::mma_commit(&bar.odone[w]);
+          }
+        blocks += p.b1 - p.b0;
+      }
+      __syncwarp();
+    }
+  } else if (warp == kKeyWarp || warp == kValueWarp) {
+    const bool keys = warp == kKeyWarp;
+    const uint32_t ring = tc::smem_u32(base + (keys ? Lay::K : Lay::V));
+    uint64_t* full = keys ? bar.kfull : bar.vfull;
+    uint64_t* empty = keys ? bar.kempty : bar.vempty;
+    const char* pool = static_cast<const char*>(keys ? a.k : a.v);
+    const int ch = lane % CH, r0 = lane / CH;
+    const uint32_t stride = a.nkv * HD * 2;
+    uint32_t blocks = 0;
+    while (walk.next(a, sh, p, q)) {
+      const char* from = pool + (int64_t)p.kvh * HD * 2 + ch * 16;
+      int32_t page[4];
+      auto look = [&](int b) {  // page entries of this lane's keys of block b
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int j = b * kTcKeys + 32 * t + lane;
+          page[t] = j < q.len ? page_entry(a.table, q.s, j) : -1;
+        }
+      };
+      look(p.b0);
+      for (int b = p.b0; b < p.b1; ++b, ++blocks) {
+        uint32_t slot[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int j = b * kTcKeys + 32 * t + lane;
+          slot[t] = ~0u;
+          if (j < q.len) {
+            slot[t] = entry_slot32(a.table, page[t], j);
+            if (slot[t] == ~0u) cache_error(a.err, kCacheBadPage);
+          }
+        }
+        if (b + 1 < p.b1) look(b + 1);
+        const uint32_t st = blocks % ST;
+        if (blocks >= ST) wait_for(&empty[st], (blocks / ST - 1) & 1, dead, a.err);
+        if (keys) {
+          uint32_t m[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) m[t] = __ballot_sync(kFull, slot[t] != ~0u);
+          if (lane == 0) {
+            *reinterpret_cast<uint4*>(live[blocks % kLiveRing]) = make_uint4(m[0], m[1], m[2], m[3]);
+            tc::mbar_arrive(&full[st]);
+          }
+        }
+        const uint32_t to = ring + st * Lay::STAGE + (ch >> 3) * Lay::TILE;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll 4
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int r = i * RPI + r0;
+            const uint32_t x = __shfl_sync(kFull, slot[t], r);
+            cp_async16(to + (32 * t + r) * 128 + (((ch ^ r) & 7) << 4), from + (uint64_t)(x != ~0u ? x : 0u) * stride,
+                       x != ~0u);
+          }
+        cp_async_arrive(&full[st]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kMmaWarp) {
+    const int w = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_at = lanes + w * kTcKeys, o_at = lanes + Lay::O_COL + w * HD;
+    unsigned char* sq = base + Lay::Q + w * Lay::STAGE;
+    const float scale = a.scale_log2;
+    uint32_t blocks = 0, steps = 0, parts = 0;
+    while (walk.next(a, sh, p, q)) {
+      const Share share = share_of(p, w);
+      const bool wide = p.w == 2, both = !wide && p.b1 - p.b0 > 1;  // both: the two groups' results meet
+      const int v0 = p.v0 + (wide ? w * kTcHalf : 0), nv = p.v0 + p.nv - v0;  // this group's vectors
+      if (share.n > 0) {
+        // queries: the last part's S products have read theirs
+#pragma unroll 1
+        for (int k0 = 0; k0 < CH; k0 += 8) {
+          uint4 u[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = r + (k0 + k) * 128, row = i / CH, c = i % CH, v = v0 + row;
+            u[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < nv && q_sign != 0) {
+              const int t = v / a.group;
+              u[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                     (int64_t)(q.row0 + t) * a.ld_q +
+                                                     (int64_t)(p.kvh * a.group + (v - t * a.group)) * HD + c * 8);
+              if (q_sign < 0) {
+                u[k].x ^= 0x80008000u;
+                u[k].y ^= 0x80008000u;
+                u[k].z ^= 0x80008000u;
+                u[k].w ^= 0x80008000u;
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = r + (k0 + k) * 128, row = i / CH, c = i % CH;
+            *reinterpret_cast<uint4*>(sq + (c >> 3) * Lay::TILE + row * 128 + (((c ^ row) & 7) << 4)) = u[k];
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&bar.qfull[w]);
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < share.n; ++i, ++steps) {
+        wait_for(&bar.sfull[w], steps & 1, dead, a.err);
+        __syncwarp();  // tensor-memory accesses are the whole warp's
+        tc::fence_after_sync();
+        float s[128];
+        tc::tmem_ld128(s_at, s);
+        const uint4 on = *reinterpret_cast<const uint4*>(live[(blocks + share.first + share.step * i) % kLiveRing]);
+        if ((on.x & on.y & on.z & on.w) != kFull) {
+          const uint32_t word[4] = {on.x, on.y, on.z, on.w};
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (!(word[k >> 5] >> (k & 31) & 1)) s[k] = -INFINITY;
+        }
+        float t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = s[k];
+#pragma unroll
+        for (int k = 8; k < 128; ++k) t[k & 7] = fmaxf(t[k & 7], s[k]);
+        const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7]))) * scale;
+        const bool grew = top > m + kSlack;
+        if (__any_sync(kFull, grew)) {  // the whole warp: TMEM accesses are collective
+          const float to = grew ? top : m;
+          if (i > 0) {
+            const float f = grew ? ex2(m - to) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              tc::tmem_ld32(o_at + c, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= f;
+              tc::tmem_st32(o_at + c, o);
+            }
+          }
+          m = to;
+        }
+        const float bias = (m == -INFINITY ? 0.f : -m) - kRowsRoom;
+        const Two scale2 = two(scale, scale), bias2 = two(bias, bias);
+        Two sum[4] = {two(0.f, 0.f), two(0.f, 0.f), two(0.f, 0.f), two(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t hi[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = ::sf::both(fma2(two(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]), scale2, bias2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            sum[k & 3] = sum[k & 3] + two(p0, p1);
+            hi[k] = pack_bf16(p0, p1);
+            if (!wide) {
+              s[32 * c + 2 * k] = p0 - __uint_as_float(hi[k] << 16);
+              s[32 * c + 2 * k + 1] = p1 - __uint_as_float(hi[k] & 0xffff0000u);
+            }
+          }
+          tc::tmem_st_u32<16>(s_at + 16 * c, hi);
+        }
+        if (!wide) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) lo[k] = pack_bf16(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]);
+            tc::tmem_st_u32<16>(s_at + 64 + 16 * c, lo);
+          }
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bar.pfull[w]);
+        const float2 x = ::sf::both((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        l += x.x + x.y;
+      }
+      blocks += p.b1 - p.b0;
+      if (share.n > 0) {
+        wait_for(&bar.odone[w], parts & 1, dead, a.err);
+        __syncwarp();
+        ++parts;
+        tc::fence_after_sync();
+      }
+      if (share.n > 0 || both) {
+        // columns [c0, c1) of the rows are this group's to finish
+        int c0 = 0, c1 = HD;
+        float f0 = 1.f, f1 = 0.f;
+        if (both) {
+          sml[w][r] = make_float2(m, l);
+          tc::fence_before_sync();
+          tc::named_bar_sync(1, 256);
+          tc::fence_after_sync();
+          const float2 x = sml[0][r], y = sml[1][r];
+          const float top = fmaxf(x.x, y.x), b = top == -INFINITY ? 0.f : top;
+          f0 = ex2(x.x - b);
+          f1 = ex2(y.x - b);
+          m = top;
+          l = x.y * f0 + y.y * f1;
+          c0 = w * (HD / 2);
+          c1 = c0 + HD / 2;
+        }
+        const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per);
+        const bool cut = last > first, mine = r < nv;
+        const int slot = rows_slot(blockIdx.x, first), row = wide ? w * kTcHalf + r : r;
+        const int v = v0 + r, t = v / a.group, h = p.kvh * a.group + (v - t * a.group);
+        const int64_t at = (int64_t)(q.row0 + t) * a.nq + h;
+        RowEnd end{1.f, 0.f, 0.f};
+        if (cut) {
+          if (tid == 0 && first == (int)blockIdx.x) rows_record(a, p, q, first, last);
+          if (mine && c0 == 0) *part_ml<kTcTileRows>(a, slot, row) = make_float2(m, l);
+        } else if (mine) {
+          end = rows_end(a, at, m, l, c0 == 0);
+        }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(q.row0 + t) * a.ld_out + (int64_t)h * HD;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          float o[32];
+          if (both) {
+            float y[32];
+            tc::tmem_ld32(lanes + Lay::O_COL + c, o);
+            tc::tmem_ld32(lanes + Lay::O_COL + HD + c, y);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + y[k] * f1;
+          } else {
+            tc::tmem_ld32(o_at + c, o);
+          }
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              const float4 x = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              const float4 y = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+              if (cut) {
+                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4, row) = x;
+                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4 + 1, row) = y;
+              } else {
+                const float4 u = rows_value<HD>(a, at, c + k, x, end), z = rows_value<HD>(a, at, c + k + 4, y, end);
+                *reinterpret_cast<uint4*>(out + c + k) =
+                    make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(z.x, z.y), pack_bf16(z.z, z.w));
+              }
+            }
+          }
+          __syncwarp();  // the next loads are the whole warp's
+        }
+        if (both) {  // both O are read before either group lets the next part begin
+          tc::fence_before_sync();
+          tc::named_bar_sync(1, 256);
+          tc::fence_after_sync();
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+cudaError_t rows_tc(cudaStream_t st, CacheRowsArgs a) {
+  // a negative scale turns the queries' signs, 0 makes them 0: the maximum of
+  // the scaled scores is then that of the scores
+  const int sign = a.scale_log2 > 0.f ? 1 : a.scale_log2 < 0.f ? -1 : 0;
+  a.scale_log2 = sign == 0 ? 1.f : fabsf(a.scale_log2);
+  a.least = 4;
+  return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, sign);
+}
+
+}  // namespace
+
+cudaError_t prepare_cache_rows_tc() {
+  cudaError_t e = cudaFuncSetAttribute(cache_rows_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TcLayout<128>::BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(cache_rows_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLayout<64>::BYTES);
+  return e;
+}
+
+cudaError_t launch_cache_rows_tc(cudaStream_t st, const CacheRowsArgs& a, int hd) {
+  return hd == 128 ? rows_tc<128>(st, a) : rows_tc<64>(st, a);
+}
+
+}  // namespace sf
