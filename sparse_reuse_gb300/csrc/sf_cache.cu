@@ -281,6 +281,13 @@ sf_status check_rows(sf_cache* c, const void* q, int64_t ld_q, int T, float scal
   return SF_OK;
 }
 
+// TMA takes the pool's positions as 31-bit row numbers (and one that is outside).
+sf_status check_gather(sf_cache* c, int64_t n_pages) {
+  if (c->s.dtype == SF_BF16 && n_pages > 2147483646ll / c->s.page_size)
+    return fail(c, SF_ERR_SHAPE, "n_pages=%lld pages of %d positions", (long long)n_pages, c->s.page_size);
+  return SF_OK;
+}
+
 CacheRowsArgs rows_args(const sf_cache* c, const void* q, int64_t ld_q, int T, float scale, void* out, int64_t ld_out,
                         float* lse) {
   CacheRowsArgs a{};
@@ -547,6 +554,7 @@ sf_status sf_cache_attend_rows(sf_cache* c, void* stream, const void* q, int64_t
   if (S == 0 || T == 0) return check_object(c);  // nothing to do, whatever the pointers
   if ((st = check_rows(c, q, ld_q, T, scale, out, ld_out, lse)) != SF_OK) return st;
   if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
+  if ((st = check_gather(c, n_pages)) != SF_OK) return st;
   if (!lens || !starts || misaligned(lens, 4) || misaligned(starts, 4))
     return fail(c, SF_ERR_INVALID_ARG, "lens or starts null or misaligned");
   if ((st = check_object(c)) != SF_OK) return st;
@@ -574,6 +582,7 @@ sf_status sf_cache_attend_shared(sf_cache* c, void* stream, const void* q, int64
   if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
   if (G < 1) return fail(c, SF_ERR_INVALID_ARG, "G=%d groups", G);
   if ((st = check_table(c, k_pages, v_pages, n_pages, prefix_table, G, prefix_cols, ld_prefix)) != SF_OK) return st;
+  if ((st = check_gather(c, n_pages)) != SF_OK) return st;
   if (!lens || !prefix_lens || !starts || misaligned(lens, 4) || misaligned(prefix_lens, 4) || misaligned(starts, 4))
     return fail(c, SF_ERR_INVALID_ARG, "lens, prefix_lens or starts null or misaligned");
   if ((st = check_object(c)) != SF_OK) return st;

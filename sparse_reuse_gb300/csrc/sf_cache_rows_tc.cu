@@ -20,12 +20,13 @@
 // kept only to within 2^kSlack).
 //
 // Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 MMA (owns TMEM),
-// 9 keys, 10 values: pages are gathered by 16-byte cp.async into 128-byte
-// swizzled tiles, whatever the page size, with zeros for positions that are not
-// there.
+// 9 keys, 10 values: four rows an instruction are gathered by TMA, whatever the
+// page size, with zeros for positions that are not there.  (By 16-byte cp.async
+// of one warp each they took 9,800 cycles a block.)
 #include <cmath>
 
 #include "sf_cache_rows.cuh"
+#include "sf_internal.h"
 #include "sf_pairs.cuh"
 #include "sf_tc.cuh"
 
@@ -74,14 +75,6 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-// This thread arrives on `bar` once its copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -99,12 +92,14 @@ __device__ __forceinline__ Share share_of(const RowsPart& p, int w) {
 
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __grid_constant__ CacheRowsArgs a,
+                                                                      const __grid_constant__ CUtensorMap map_k,
+                                                                      const __grid_constant__ CUtensorMap map_v,
                                                                       const int q_sign) {
   using Lay = TcLayout<HD>;
-  constexpr int ST = Lay::ST, CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a copy instruction
+  constexpr int ST = Lay::ST, CH = HD / 8;  // 16-byte chunks of a row
   extern __shared__ unsigned char smem_raw[];
   __shared__ Barriers bar;
-  __shared__ __align__(16) uint32_t live[kLiveRing][4];
+  __shared__ __align__(32) uint32_t live[kLiveRing][8];  // byte x: keys 4 x .. 4 x + 3
   __shared__ float2 sml[2][kTcHalf];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_;
@@ -121,9 +116,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       tc::mbar_init(&bar.odone[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
-      tc::mbar_init(&bar.kfull[i], 33);  // every lane's copies, and the mask of live keys
+      tc::mbar_init(&bar.kfull[i], 1);
       tc::mbar_init(&bar.kempty[i], 1);
-      tc::mbar_init(&bar.vfull[i], 32);
+      tc::mbar_init(&bar.vfull[i], 1);
       tc::mbar_init(&bar.vempty[i], 1);
     }
     dead_ = 0;
@@ -160,7 +155,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         auto scores = [&](int w, int i) {
           const uint32_t b = blocks + share[w].first + share[w].step * i, st = b % ST;
           wait_for(&bar.kfull[st], (b / ST) & 1, dead, a.err);
-          tc::fence_proxy_async_smem();  // the copies are the generic proxy's
           tc::fence_after_sync();
           const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4), qa = dq + (uint64_t)((w * Lay::STAGE) >> 4);
 #pragma unroll
@@ -175,7 +169,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         for (int w = 0; w < 2; ++w)
           if (share[w].n > 0) {
             wait_for(&bar.qfull[w], parts[w] & 1, dead, a.err);
-            tc::fence_proxy_async_smem();
             scores(w, 0);
             ++parts[w];
           }
@@ -187,7 +180,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
             wait_for(&bar.vfull[st], (b / ST) & 1, dead, a.err);
             wait_for(&bar.pfull[w], steps[w] & 1, dead, a.err);
             ++steps[w];
-            tc::fence_proxy_async_smem();
             tc::fence_after_sync();
             const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
             const uint32_t o = tmem + Lay::O_COL + w * HD, pa = tmem + w * kTcKeys;
@@ -209,62 +201,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       __syncwarp();
     }
   } else if (warp == kKeyWarp || warp == kValueWarp) {
+    // lane x takes keys 4 x .. 4 x + 3 of a block
     const bool keys = warp == kKeyWarp;
-    const uint32_t ring = tc::smem_u32(base + (keys ? Lay::K : Lay::V));
+    const uint32_t ring = tc::smem_u32(base + (keys ? Lay::K : Lay::V)) + lane * 512;
     uint64_t* full = keys ? bar.kfull : bar.vfull;
     uint64_t* empty = keys ? bar.kempty : bar.vempty;
-    const char* pool = static_cast<const char*>(keys ? a.k : a.v);
-    const int ch = lane % CH, r0 = lane / CH;
-    const uint32_t stride = a.nkv * HD * 2;
+    const CUtensorMap* map = keys ? &map_k : &map_v;
+    const int none = (int)(a.table.n_pages * a.table.page_size);  // a row outside the pool
     uint32_t blocks = 0;
     while (walk.next(a, sh, p, q)) {
-      const char* from = pool + (int64_t)p.kvh * HD * 2 + ch * 16;
       int32_t page[4];
       auto look = [&](int b) {  // page entries of this lane's keys of block b
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int j = b * kTcKeys + 32 * t + lane;
+          const int j = b * kTcKeys + 4 * lane + t;
           page[t] = j < q.len ? page_entry(a.table, q.s, j) : -1;
         }
       };
       look(p.b0);
       for (int b = p.b0; b < p.b1; ++b, ++blocks) {
-        uint32_t slot[4];
+        int slot[4];
+        uint32_t there = 0;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int j = b * kTcKeys + 32 * t + lane;
-          slot[t] = ~0u;
+          const int j = b * kTcKeys + 4 * lane + t;
+          slot[t] = none;
           if (j < q.len) {
-            slot[t] = entry_slot32(a.table, page[t], j);
-            if (slot[t] == ~0u) cache_error(a.err, kCacheBadPage);
+            const uint32_t x = entry_slot32(a.table, page[t], j);
+            if (x == ~0u)
+              cache_error(a.err, kCacheBadPage);
+            else
+              slot[t] = (int)x, there |= 1u << t;
           }
         }
         if (b + 1 < p.b1) look(b + 1);
         const uint32_t st = blocks % ST;
         if (blocks >= ST) wait_for(&empty[st], (blocks / ST - 1) & 1, dead, a.err);
-        if (keys) {
-          uint32_t m[4];
+        if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
+        __syncwarp();
+        if (lane == 0) tc::mbar_expect_tx(&full[st], Lay::STAGE);
+        __syncwarp();
 #pragma unroll
-          for (int t = 0; t < 4; ++t) m[t] = __ballot_sync(kFull, slot[t] != ~0u);
-          if (lane == 0) {
-            *reinterpret_cast<uint4*>(live[blocks % kLiveRing]) = make_uint4(m[0], m[1], m[2], m[3]);
-            tc::mbar_arrive(&full[st]);
-          }
-        }
-        const uint32_t to = ring + st * Lay::STAGE + (ch >> 3) * Lay::TILE;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll 4
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int r = i * RPI + r0;
-            const uint32_t x = __shfl_sync(kFull, slot[t], r);
-            cp_async16(to + (32 * t + r) * 128 + (((ch ^ r) & 7) << 4), from + (uint64_t)(x != ~0u ? x : 0u) * stride,
-                       x != ~0u);
-          }
-        cp_async_arrive(&full[st]);
+        for (int x = 0; x < HD / 64; ++x)
+          tc::tma_gather4(ring + st * Lay::STAGE + x * Lay::TILE, map, p.kvh * HD + 64 * x, slot[0], slot[1], slot[2],
+                          slot[3], &full[st]);
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    // after a stall nothing waits for the last copies: they land before the block ends
+    if (*dead)
+      for (uint32_t b = blocks > ST ? blocks - ST : 0; b < blocks; ++b) {
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!tc::mbar_try_wait(&full[b % ST], (b / ST) & 1) && tc::globaltimer_ns() - t0 < 2000000000ull) {
+        }
+      }
   } else if (warp < kMmaWarp) {
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -315,12 +304,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         tc::fence_after_sync();
         float s[128];
         tc::tmem_ld128(s_at, s);
-        const uint4 on = *reinterpret_cast<const uint4*>(live[(blocks + share.first + share.step * i) % kLiveRing]);
-        if ((on.x & on.y & on.z & on.w) != kFull) {
-          const uint32_t word[4] = {on.x, on.y, on.z, on.w};
+        const uint32_t* on = live[(blocks + share.first + share.step * i) % kLiveRing];
+        if (__any_sync(kFull, on[lane >> 2] != 0x0f0f0f0fu)) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (!(word[k >> 5] >> (k & 31) & 1)) s[k] = -INFINITY;
+          for (int x = 0; x < 8; ++x) {
+            const uint32_t word = on[x];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (!(word >> (8 * (k >> 2) + (k & 3)) & 1)) s[16 * x + k] = -INFINITY;
+          }
         }
         float t[8];
 #pragma unroll
@@ -464,12 +456,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 
 template <int HD>
 cudaError_t rows_tc(cudaStream_t st, CacheRowsArgs a) {
+  alignas(64) CUtensorMap map_k, map_v;
+  const uint64_t slots = (uint64_t)a.table.n_pages * a.table.page_size;
+  if (!make_tmap_pool(&map_k, a.k, HD, a.nkv, slots) || !make_tmap_pool(&map_v, a.v, HD, a.nkv, slots))
+    return cudaErrorInvalidValue;
   // a negative scale turns the queries' signs, 0 makes them 0: the maximum of
   // the scaled scores is then that of the scores
   const int sign = a.scale_log2 > 0.f ? 1 : a.scale_log2 < 0.f ? -1 : 0;
   a.scale_log2 = sign == 0 ? 1.f : fabsf(a.scale_log2);
   a.least = 4;
-  return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, sign);
+  return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, map_k,
+                    map_v, sign);
 }
 
 }  // namespace

@@ -424,6 +424,20 @@ bool make_tmap_kv(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of a pool of pages, [slots][nkv * hd] bf16, gathered four at a time as
+// 64 columns each (tile::gather4: the box is one row high).
+bool make_tmap_pool(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t slots) {
+  auto fn = encode_fn();
+  if (!fn || hd % 64 != 0 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)nkv * hd, slots};
+  cuuint64_t strides[1] = {(cuuint64_t)nkv * hd * 2};
+  cuuint32_t box[2] = {64u, 1u};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // K splits for an M x K weight over n_tiles row tiles: the largest cluster
 // size that keeps every (m, n) tile resident in one wave and gives each CTA
 // at least one K block.
