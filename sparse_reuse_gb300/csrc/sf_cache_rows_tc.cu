@@ -20,10 +20,13 @@
 // kept only to within 2^kSlack).
 //
 // Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 MMA (owns TMEM),
-// 9 keys, 10 values: four rows an instruction are gathered by TMA, whatever the
-// page size, with zeros for positions that are not there.  (By 16-byte cp.async
-// of one warp each they took 9,800 cycles a block.)
+// 9 keys, 10 values, by TMA: runs of rows that lie within a page as boxes, rows
+// of odd pages and of runs that are not all there four at a time (gather4),
+// with zeros for positions that are not there.  A gather4 of 512 bytes takes the
+// TMA unit some 38 cycles (a block's keys and values 4,900), a box of 16 rows
+// little more.
 #include <cmath>
+#include <type_traits>
 
 #include "sf_cache_rows.cuh"
 #include "sf_internal.h"
@@ -90,11 +93,16 @@ __device__ __forceinline__ Share share_of(const RowsPart& p, int w) {
   return p.w == 2 ? Share{nb, 0, 1} : Share{(nb + 1 - w) >> 1, w, 2};
 }
 
+// Keys and values as rows for gather4, and as boxes of `run` rows: the largest
+// power of two up to 128 that divides the page size.
+struct PoolMaps {
+  CUtensorMap gather[2], box[2];
+};
+
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __grid_constant__ CacheRowsArgs a,
-                                                                      const __grid_constant__ CUtensorMap map_k,
-                                                                      const __grid_constant__ CUtensorMap map_v,
-                                                                      const int q_sign) {
+                                                                      const __grid_constant__ PoolMaps maps,
+                                                                      const int run, const int q_sign) {
   using Lay = TcLayout<HD>;
   constexpr int ST = Lay::ST, CH = HD / 8;  // 16-byte chunks of a row
   extern __shared__ unsigned char smem_raw[];
@@ -201,13 +209,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       __syncwarp();
     }
   } else if (warp == kKeyWarp || warp == kValueWarp) {
-    // lane x takes keys 4 x .. 4 x + 3 of a block
+    // lane x takes keys 4 x .. 4 x + 3 of a block, and the runs that start there
     const bool keys = warp == kKeyWarp;
     const uint32_t ring = tc::smem_u32(base + (keys ? Lay::K : Lay::V)) + lane * 512;
     uint64_t* full = keys ? bar.kfull : bar.vfull;
     uint64_t* empty = keys ? bar.kempty : bar.vempty;
-    const CUtensorMap* map = keys ? &map_k : &map_v;
+    const CUtensorMap *gather = &maps.gather[keys ? 0 : 1], *box = &maps.box[keys ? 0 : 1];
     const int none = (int)(a.table.n_pages * a.table.page_size);  // a row outside the pool
+    const unsigned peers = run >= 128 ? kFull : run >= 8 ? ((1u << (run / 4)) - 1u) << (lane / (run / 4) * (run / 4)) : 1u << lane;
+    const bool leads = run >= 4 && (4 * lane) % run == 0;
     uint32_t blocks = 0;
     while (walk.next(a, sh, p, q)) {
       int32_t page[4];
@@ -240,11 +250,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
         __syncwarp();
         if (lane == 0) tc::mbar_expect_tx(&full[st], Lay::STAGE);
-        __syncwarp();
+        const bool whole = run >= 4 && (__ballot_sync(kFull, there == 15u) & peers) == peers;
+        if (!whole) {
 #pragma unroll
-        for (int x = 0; x < HD / 64; ++x)
-          tc::tma_gather4(ring + st * Lay::STAGE + x * Lay::TILE, map, p.kvh * HD + 64 * x, slot[0], slot[1], slot[2],
-                          slot[3], &full[st]);
+          for (int x = 0; x < HD / 64; ++x)
+            tc::tma_gather4(ring + st * Lay::STAGE + x * Lay::TILE, gather, p.kvh * HD + 64 * x, slot[0], slot[1],
+                            slot[2], slot[3], &full[st]);
+        } else if (leads) {
+#pragma unroll
+          for (int x = 0; x < HD / 64; ++x)
+            tc::tma_load_3d(ring + st * Lay::STAGE + x * Lay::TILE, box, 64 * x, p.kvh, slot[0], &full[st]);
+        }
+        __syncwarp();
       }
     }
     // after a stall nothing waits for the last copies: they land before the block ends
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     uint32_t blocks = 0, steps = 0, parts = 0;
     while (walk.next(a, sh, p, q)) {
       const Share share = share_of(p, w);
-      const bool wide = p.w == 2, both = !wide && p.b1 - p.b0 > 1;  // both: the two groups' results meet
+      const bool wide = p.w == 2, meet = !wide && p.b1 - p.b0 > 1;  // meet: the two groups' results do
       const int v0 = p.v0 + (wide ? w * kTcHalf : 0), nv = p.v0 + p.nv - v0;  // this group's vectors
       if (share.n > 0) {
         // queries: the last part's S products have read theirs
@@ -297,8 +314,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         tc::mbar_arrive(&bar.qfull[w]);
       }
       float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (int i = 0; i < share.n; ++i, ++steps) {
+      auto step = [&](int i, auto split) {
+        constexpr bool SPLIT = decltype(split)::value;  // P as two bf16 numbers
         wait_for(&bar.sfull[w], steps & 1, dead, a.err);
         __syncwarp();  // tensor-memory accesses are the whole warp's
         tc::fence_after_sync();
@@ -314,12 +331,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
               if (!(word >> (8 * (k >> 2) + (k & 3)) & 1)) s[16 * x + k] = -INFINITY;
           }
         }
-        float t[8];
+        float t[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = s[k];
+        for (int k = 0; k < 4; ++k) t[k] = s[k];
 #pragma unroll
-        for (int k = 8; k < 128; ++k) t[k & 7] = fmaxf(t[k & 7], s[k]);
-        const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7]))) * scale;
+        for (int k = 4; k < 124; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), s[k + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = fmaxf(t[e], s[124 + e]);
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
         const bool grew = top > m + kSlack;
         if (__any_sync(kFull, grew)) {  // the whole warp: TMEM accesses are collective
           const float to = grew ? top : m;
@@ -339,26 +360,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         }
         const float bias = (m == -INFINITY ? 0.f : -m) - kRowsRoom;
         const Two scale2 = two(scale, scale), bias2 = two(bias, bias);
-        Two sum[4] = {two(0.f, 0.f), two(0.f, 0.f), two(0.f, 0.f), two(0.f, 0.f)};
+        Two sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t hi[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float2 x = ::sf::both(fma2(two(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]), scale2, bias2));
+            const float2 x = both(fma2(two(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]), scale2, bias2));
             const float p0 = ex2(x.x), p1 = ex2(x.y);
-            sum[k & 3] = sum[k & 3] + two(p0, p1);
+            sum[k & 1] = sum[k & 1] + two(p0, p1);
             hi[k] = pack_bf16(p0, p1);
-            if (!wide) {
+            if constexpr (SPLIT) {
               s[32 * c + 2 * k] = p0 - __uint_as_float(hi[k] << 16);
               s[32 * c + 2 * k + 1] = p1 - __uint_as_float(hi[k] & 0xffff0000u);
             }
           }
           tc::tmem_st_u32<16>(s_at + 16 * c, hi);
-        }
-        if (!wide) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          if constexpr (SPLIT) {
             uint32_t lo[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) lo[k] = pack_bf16(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]);
@@ -368,8 +386,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(&bar.pfull[w]);
-        const float2 x = ::sf::both((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        const float2 x = both(sum[0] + sum[1]);
         l += x.x + x.y;
+        ++steps;
+      };
+      if (wide) {
+#pragma unroll 1
+        for (int i = 0; i < share.n; ++i) step(i, std::false_type());
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < share.n; ++i) step(i, std::true_type());
       }
       blocks += p.b1 - p.b0;
       if (share.n > 0) {
@@ -377,12 +403,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         __syncwarp();
         ++parts;
         tc::fence_after_sync();
-      }
-      if (share.n > 0 || both) {
         // columns [c0, c1) of the rows are this group's to finish
         int c0 = 0, c1 = HD;
         float f0 = 1.f, f1 = 0.f;
-        if (both) {
+        if (meet) {
           sml[w][r] = make_float2(m, l);
           tc::fence_before_sync();
           tc::named_bar_sync(1, 256);
@@ -412,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float o[32];
-          if (both) {
+          if (meet) {
             float y[32];
             tc::tmem_ld32(lanes + Lay::O_COL + c, o);
             tc::tmem_ld32(lanes + Lay::O_COL + HD + c, y);
@@ -438,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           }
           __syncwarp();  // the next loads are the whole warp's
         }
-        if (both) {  // both O are read before either group lets the next part begin
+        if (meet) {  // both O are read before either group lets the next part begin
           tc::fence_before_sync();
           tc::named_bar_sync(1, 256);
           tc::fence_after_sync();
@@ -456,17 +480,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 
 template <int HD>
 cudaError_t rows_tc(cudaStream_t st, CacheRowsArgs a) {
-  alignas(64) CUtensorMap map_k, map_v;
+  PoolMaps maps;
   const uint64_t slots = (uint64_t)a.table.n_pages * a.table.page_size;
-  if (!make_tmap_pool(&map_k, a.k, HD, a.nkv, slots) || !make_tmap_pool(&map_v, a.v, HD, a.nkv, slots))
-    return cudaErrorInvalidValue;
+  int run = 1;
+  while (run < kTcKeys && a.table.page_size % (2 * run) == 0) run *= 2;
+  for (int i = 0; i < 2; ++i) {
+    const void* pool = i ? a.v : a.k;
+    if (!make_tmap_pool(&maps.gather[i], pool, HD, a.nkv, slots) ||
+        !make_tmap_kv(&maps.box[i], pool, HD, a.nkv, slots, run))
+      return cudaErrorInvalidValue;
+  }
   // a negative scale turns the queries' signs, 0 makes them 0: the maximum of
   // the scaled scores is then that of the scores
   const int sign = a.scale_log2 > 0.f ? 1 : a.scale_log2 < 0.f ? -1 : 0;
   a.scale_log2 = sign == 0 ? 1.f : fabsf(a.scale_log2);
   a.least = 4;
-  return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, map_k,
-                    map_v, sign);
+  return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, maps, run,
+                    sign);
 }
 
 }  // namespace
