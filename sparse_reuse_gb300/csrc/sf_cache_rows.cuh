@@ -85,16 +85,26 @@ struct RowsWalk {
 
 // By all THREADS of the block: the walk's start.  False where nothing of the
 // call may be written (offsets that do not ascend).  *empties: some sequence
-// with rows has no keys.
+// with rows has no keys.  Batches of up to THREADS sequences are scanned once,
+// between two barriers.
 template <int THREADS>
 __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShape& sh, RowsWalk& walk, bool* empties) {
   constexpr int WARPS = THREADS / 32;
   __shared__ int64_t sums[WARPS];
+  __shared__ int flags_of[WARPS];
   __shared__ RowsWalk found;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto upto_lane = [&](int64_t y) {  // inclusive sum over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = shfl_up64(y, o);
+      if (lane >= o) y += z;
+    }
+    return y;
+  };
+  SeqRows head{0, 0, 0, 0};
   int64_t mine = 0;
   int flags = 0;
-  SeqRows head{0, 0, 0, 0};
   for (int s = threadIdx.x; s < a.S; s += THREADS) {
     bool bad_rows, bad_len;
     const SeqRows q = sequence_rows(a, s, &bad_rows, &bad_len);
@@ -102,53 +112,55 @@ __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShap
     mine += units_of(sh, q);
     flags |= (bad_rows ? 1 : 0) | (bad_len ? 2 : 0) | (q.rows > 0 && q.len == 0 ? 4 : 0);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += (int64_t)__shfl_xor_sync(kFull, (unsigned long long)mine, o);
-  if (lane == 0) sums[warp] = mine;
-  const bool bad_rows = __syncthreads_or(flags & 1), bad_len = __syncthreads_or(flags & 2);
-  *empties = __syncthreads_or(flags & 4);
-  if (threadIdx.x == 0 && blockIdx.x == 0) {
-    if (bad_rows) cache_error(a.err, kCacheBadRow);
-    if (bad_len) cache_error(a.err, kCacheBadLength);
+  const int64_t incl = upto_lane(mine);
+  flags = __reduce_or_sync(kFull, flags);
+  if (lane == 31) {
+    sums[warp] = incl;
+    flags_of[warp] = flags;
   }
-  if (bad_rows) return false;
-  int64_t total = 0;
+  __syncthreads();
+  int64_t total = 0, before = 0;
+  flags = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += sums[w];
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+    flags |= flags_of[w];
+  }
+  *empties = flags & 4;
+  if (threadIdx.x == 0 && blockIdx.x == 0) {
+    if (flags & 1) cache_error(a.err, kCacheBadRow);
+    if (flags & 2) cache_error(a.err, kCacheBadLength);
+  }
   const int64_t per = units_per_block(total, a.ctas, a.least);
   const int64_t lo = per * blockIdx.x, hi = lo + per < total ? lo + per : total;
-  if (lo >= hi) {
-    walk.u = walk.end = 0;
-    walk.per = per;
-    return true;
-  }
-  int64_t before = 0;
-  for (int s0 = 0; s0 < a.S; s0 += THREADS) {
-    const int s = s0 + threadIdx.x;
-    SeqRows q = head;
-    if (s0 > 0) {
+  walk.u = walk.end = 0;
+  walk.per = per;
+  if (flags & 1) return false;
+  if (lo >= hi) return true;
+  if (a.S <= THREADS) {
+    const int64_t at = before + incl - mine;
+    if (at <= lo && lo < at + mine) found = RowsWalk{lo, hi, per, at, head};
+  } else {
+    before = 0;
+    for (int s0 = 0; s0 < a.S; s0 += THREADS) {
+      const int s = s0 + threadIdx.x;
       bool b0, b1;
-      q = SeqRows{0, 0, 0, 0};
+      SeqRows q{0, 0, 0, 0};
       if (s < a.S) q = sequence_rows(a, s, &b0, &b1);
-    }
-    const int64_t x = units_of(sh, q);
-    int64_t y = x;
+      const int64_t x = units_of(sh, q), y = upto_lane(x);
+      __syncthreads();
+      if (lane == 31) sums[warp] = y;
+      __syncthreads();
+      int64_t at = before + y - x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = shfl_up64(y, o);
-      if (lane >= o) y += z;
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) at += sums[w];
+        before += sums[w];
+      }
+      if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
+      if (before > lo) break;
     }
-    __syncthreads();
-    if (lane == 31) sums[warp] = y;
-    __syncthreads();
-    int64_t at = before + y - x;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) at += sums[w];
-      before += sums[w];
-    }
-    if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
-    if (before > lo) break;
   }
   __syncthreads();
   walk = found;

@@ -13,18 +13,22 @@
 // registers at the end.  Its bound is the keys' bandwidth, not the tensor core,
 // so P enters there as the sum of two bf16 numbers.
 //
-// Order on the tensor core.  One thread issues every MMA, and they execute in
-// that order; a commit covers all before it.  S of a half's next block follows
-// its O += P V, so when the softmax sees the new S, O is at rest: a row whose
-// maximum grows by more than kSlack rescales it there (rarely: the maximum is
-// kept only to within 2^kSlack).
+// Order on the tensor core.  One thread issues all of a half's MMAs, and they
+// execute in that order; a commit covers all before it.  S of a half's next
+// block follows its O += P V (whose P it overwrites), so when the softmax sees
+// the new S, O is at rest: a row whose maximum grows by more than kSlack
+// rescales it there (rarely: the maximum is kept only to within 2^kSlack).
+// Each half has an issuing warp of its own: a wait costs 110 cycles even where
+// there is nothing to wait for, and the tensor core's queue is short (one warp
+// for both took 3,700 cycles for a block of two halves).
 //
-// Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 MMA (owns TMEM),
-// 9 keys, 10 values, by TMA: runs of rows that lie within a page as boxes, rows
-// of odd pages and of runs that are not all there four at a time (gather4),
-// with zeros for positions that are not there.  A gather4 of 512 bytes takes the
-// TMA unit some 38 cycles (a block's keys and values 4,900), a box of 16 rows
-// little more.
+// Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 and 9 the MMAs of
+// the halves (8 owns TMEM), 10 keys, 11 values.  Warp 10 also walks along the
+// block's share of the batch and hands the parts to the others through a ring.
+// Loads are TMA: runs of rows that lie within a page as boxes, rows of odd pages
+// and of runs that are not all there four at a time (gather4), with zeros for
+// positions that are not there.  A gather4 of 512 bytes takes the TMA unit some
+// 38 cycles (a block's keys and values 4,900), a box of 16 rows little more.
 #include <cmath>
 #include <type_traits>
 
@@ -43,7 +47,8 @@ constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
-constexpr int kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10;
+constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
+constexpr int kPartRing = 4;
 
 template <int HD>
 struct TcLayout {
@@ -59,8 +64,21 @@ struct TcLayout {
 };
 
 struct Barriers {
-  uint64_t qfull[2], sfull[2], pfull[2], odone[2];
+  uint64_t qfull[2], sfull[2], pfull[2][2], odone[2];  // of each half; P's in two parts of 64 keys
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
+  uint64_t part_full[kPartRing], part_empty[kPartRing];
+  uint64_t meet;  // of both softmax groups
+};
+
+// What a thread block does next: blocks b0 .. b0 + nb - 1 of a tile.
+struct TcPart {
+  int nb;        // 0: nothing more
+  int wide;      // two halves
+  int nv;        // query vectors
+  int kvh;
+  int t0, rem;   // row and head (within the KV head) of its first vector
+  int slot;      // of the partial result; -1: the tile is whole
+  int s, len, b0;
 };
 
 // Bounded wait: after 2 s without the phase, or once another wait of the block
@@ -88,9 +106,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 struct Share {
   int n, first, step;
 };
-__device__ __forceinline__ Share share_of(const RowsPart& p, int w) {
-  const int nb = p.b1 - p.b0;
-  return p.w == 2 ? Share{nb, 0, 1} : Share{(nb + 1 - w) >> 1, w, 2};
+__device__ __forceinline__ Share share_of(int nb, int wide, int w) {
+  return wide ? Share{nb, 0, 1} : Share{(nb + 1 - w) >> 1, w, 2};
 }
 
 // Keys and values as rows for gather4, and as boxes of `run` rows: the largest
@@ -107,6 +124,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   constexpr int ST = Lay::ST, CH = HD / 8;  // 16-byte chunks of a row
   extern __shared__ unsigned char smem_raw[];
   __shared__ Barriers bar;
+  __shared__ TcPart ring_of_parts[kPartRing];
   __shared__ __align__(32) uint32_t live[kLiveRing][8];  // byte x: keys 4 x .. 4 x + 3
   __shared__ float2 sml[2][kTcHalf];
   __shared__ uint32_t tmem_slot;
@@ -120,15 +138,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar.qfull[i], kTcHalf);
       tc::mbar_init(&bar.sfull[i], 1);
-      tc::mbar_init(&bar.pfull[i], kTcHalf);
+      tc::mbar_init(&bar.pfull[i][0], kTcHalf);
+      tc::mbar_init(&bar.pfull[i][1], kTcHalf);
       tc::mbar_init(&bar.odone[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&bar.kfull[i], 1);
-      tc::mbar_init(&bar.kempty[i], 1);
+      tc::mbar_init(&bar.kempty[i], 2);  // both halves, or one of them twice
       tc::mbar_init(&bar.vfull[i], 1);
-      tc::mbar_init(&bar.vempty[i], 1);
+      tc::mbar_init(&bar.vempty[i], 2);
     }
+    for (int i = 0; i < kPartRing; ++i) {
+      tc::mbar_init(&bar.part_full[i], 1);
+      tc::mbar_init(&bar.part_empty[i], 11);  // 8 softmax warps, 2 issuers, values
+    }
+    tc::mbar_init(&bar.meet, 2 * kTcHalf);
     dead_ = 0;
     tc::fence_barrier_init();
   }
@@ -143,71 +167,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   RowsWalk walk;
   bool empties;
   const bool ok = rows_plan<kTcThreads>(a, sh, walk, &empties);
-  if (tid == 0) a.joins[blockIdx.x].n = 0;
-  if (ok) rows_empties<__nv_bfloat16, HD, kTcThreads>(a, empties);
-  else walk.u = walk.end = 0;
-  RowsPart p;
-  SeqRows q;
+  if (ok && (empties || a.tail_ml)) rows_empties<__nv_bfloat16, HD, kTcThreads>(a, empties);
 
-  if (warp == kMmaWarp) {
-    const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
-    const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
-    const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::Q));
-    const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::K));
-    const uint64_t dv = tc::sw128_mnmajor_desc(tc::smem_u32(base + Lay::V), Lay::TILE);
-    uint32_t blocks = 0, parts[2] = {0, 0}, steps[2] = {0, 0};  // so far: of the rings, of each group
-    while (walk.next(a, sh, p, q)) {
-      if (lane == 0) {
-        const Share share[2] = {share_of(p, 0), share_of(p, 1)};
-        const bool wide = p.w == 2;
-        auto scores = [&](int w, int i) {
-          const uint32_t b = blocks + share[w].first + share[w].step * i, st = b % ST;
+  if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    if (lane == 0) {
+      const int w = warp - kMmaWarp;
+      const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
+      const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
+      const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::Q + w * Lay::STAGE));
+      const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::K));
+      const uint64_t dv = tc::sw128_mnmajor_desc(tc::smem_u32(base + Lay::V), Lay::TILE);
+      const uint32_t o_at = tmem + Lay::O_COL + w * HD, s_at = tmem + w * kTcKeys;
+      uint32_t blocks = 0, parts = 0, steps = 0;  // so far: of the rings, of this half
+      for (uint32_t x = 0;; ++x) {
+        wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+        const TcPart& p = ring_of_parts[x % kPartRing];
+        const int nb = *dead ? 0 : p.nb, wide = p.wide;
+        tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
+        if (nb == 0) break;
+        const Share share = share_of(nb, wide, w);
+        auto scores = [&](int i) {
+          const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
           wait_for(&bar.kfull[st], (b / ST) & 1, dead, a.err);
           tc::fence_after_sync();
-          const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4), qa = dq + (uint64_t)((w * Lay::STAGE) >> 4);
+          const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint64_t off = (uint64_t)(((kk >> 2) * Lay::TILE + (kk & 3) * 32) >> 4);
-            tc::mma_bf16(tmem + w * kTcKeys, qa + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
+            tc::mma_bf16(s_at, dq + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
           }
           tc::mma_commit(&bar.sfull[w]);
-          if (!wide || w == 1) tc::mma_commit(&bar.kempty[st]);
+          tc::mma_commit(&bar.kempty[st]);
+          if (!wide) tc::mma_commit(&bar.kempty[st]);
         };
+        if (share.n > 0) {
+          wait_for(&bar.qfull[w], parts & 1, dead, a.err);
+          ++parts;
+          scores(0);
+        }
+        for (int i = 0; i < share.n; ++i, ++steps) {
+          const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
+          wait_for(&bar.vfull[st], (b / ST) & 1, dead, a.err);
+          const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (share[w].n > 0) {
-            wait_for(&bar.qfull[w], parts[w] & 1, dead, a.err);
-            scores(w, 0);
-            ++parts[w];
-          }
-        for (int i = 0; i < share[0].n; ++i)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (i >= share[w].n) continue;
-            const uint32_t b = blocks + share[w].first + share[w].step * i, st = b % ST;
-            wait_for(&bar.vfull[st], (b / ST) & 1, dead, a.err);
-            wait_for(&bar.pfull[w], steps[w] & 1, dead, a.err);
-            ++steps[w];
+          for (int half = 0; half < 2; ++half) {
+            wait_for(&bar.pfull[w][half], steps & 1, dead, a.err);
             tc::fence_after_sync();
-            const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
-            const uint32_t o = tmem + Lay::O_COL + w * HD, pa = tmem + w * kTcKeys;
 #pragma unroll
-            for (int kk = 0; kk < kTcKeys / 16; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
-              tc::mma_bf16_ts(o, pa + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, i > 0 || kk > 0 ? 1u : 0u);
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
+              tc::mma_bf16_ts(o_at, s_at + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, i > 0 || kk > 0 ? 1u : 0u);
             if (!wide)
 #pragma unroll
-              for (int kk = 0; kk < kTcKeys / 16; ++kk)  // what rounding P left
-                tc::mma_bf16_ts(o, pa + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
-            if (!wide || w == 1) tc::mma_commit(&bar.vempty[st]);
-            if (i + 1 < share[w].n)
-              scores(w, i + 1);
-            else
-              tc::mma_commit(&bar.odone[w]);
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
+                tc::mma_bf16_ts(o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
           }
-        blocks += p.b1 - p.b0;
+          tc::mma_commit(&bar.vempty[st]);
+          if (!wide) tc::mma_commit(&bar.vempty[st]);
+          if (i + 1 < share.n)
+            scores(i + 1);
+          else
+            tc::mma_commit(&bar.odone[w]);
+        }
+        blocks += nb;
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp == kKeyWarp || warp == kValueWarp) {
     // lane x takes keys 4 x .. 4 x + 3 of a block, and the runs that start there
     const bool keys = warp == kKeyWarp;
@@ -216,35 +240,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     uint64_t* empty = keys ? bar.kempty : bar.vempty;
     const CUtensorMap *gather = &maps.gather[keys ? 0 : 1], *box = &maps.box[keys ? 0 : 1];
     const int none = (int)(a.table.n_pages * a.table.page_size);  // a row outside the pool
-    const unsigned peers = run >= 128 ? kFull : run >= 8 ? ((1u << (run / 4)) - 1u) << (lane / (run / 4) * (run / 4)) : 1u << lane;
+    const unsigned peers =
+        run >= 128 ? kFull : run >= 8 ? ((1u << (run / 4)) - 1u) << (lane / (run / 4) * (run / 4)) : 1u << lane;
     const bool leads = run >= 4 && (4 * lane) % run == 0;
     uint32_t blocks = 0;
-    while (walk.next(a, sh, p, q)) {
+    if (keys && lane == 0) a.joins[blockIdx.x].n = 0;
+    for (uint32_t x = 0;; ++x) {
+      TcPart& slot_of = ring_of_parts[x % kPartRing];
+      if (keys) {  // the walk
+        RowsPart p;
+        SeqRows q;
+        const bool more = walk.next(a, sh, p, q) && !*dead;
+        if (x >= kPartRing) wait_for(&bar.part_empty[x % kPartRing], (x / kPartRing - 1) & 1, dead, a.err);
+        if (lane == 0) {
+          TcPart n{};
+          if (more) {
+            const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per), r = p.v0 / a.group;
+            n = TcPart{p.b1 - p.b0, p.w == 2, p.nv, p.kvh, q.row0 + r, p.v0 - r * a.group,
+                       last > first ? rows_slot(blockIdx.x, first) : -1, q.s, q.len, p.b0};
+            if (last > first && first == (int)blockIdx.x) rows_record(a, p, q, first, last);
+          }
+          slot_of = n;
+          tc::mbar_arrive(&bar.part_full[x % kPartRing]);
+        }
+        __syncwarp();
+      } else {
+        wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+      }
+      const int nb = *dead ? 0 : slot_of.nb, s = slot_of.s, len = slot_of.len, kvh = slot_of.kvh, b0 = slot_of.b0;
+      __syncwarp();
+      if (!keys && lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
+      if (__any_sync(kFull, nb == 0)) break;
       int32_t page[4];
       auto look = [&](int b) {  // page entries of this lane's keys of block b
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int j = b * kTcKeys + 4 * lane + t;
-          page[t] = j < q.len ? page_entry(a.table, q.s, j) : -1;
+          page[t] = j < len ? page_entry(a.table, s, j) : -1;
         }
       };
-      look(p.b0);
-      for (int b = p.b0; b < p.b1; ++b, ++blocks) {
+      look(b0);
+      for (int b = b0; b < b0 + nb; ++b, ++blocks) {
         int slot[4];
         uint32_t there = 0;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int j = b * kTcKeys + 4 * lane + t;
           slot[t] = none;
-          if (j < q.len) {
-            const uint32_t x = entry_slot32(a.table, page[t], j);
-            if (x == ~0u)
+          if (j < len) {
+            const uint32_t y = entry_slot32(a.table, page[t], j);
+            if (y == ~0u)
               cache_error(a.err, kCacheBadPage);
             else
-              slot[t] = (int)x, there |= 1u << t;
+              slot[t] = (int)y, there |= 1u << t;
           }
         }
-        if (b + 1 < p.b1) look(b + 1);
+        if (b + 1 < b0 + nb) look(b + 1);
         const uint32_t st = blocks % ST;
         if (blocks >= ST) wait_for(&empty[st], (blocks / ST - 1) & 1, dead, a.err);
         if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
@@ -253,13 +304,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         const bool whole = run >= 4 && (__ballot_sync(kFull, there == 15u) & peers) == peers;
         if (!whole) {
 #pragma unroll
-          for (int x = 0; x < HD / 64; ++x)
-            tc::tma_gather4(ring + st * Lay::STAGE + x * Lay::TILE, gather, p.kvh * HD + 64 * x, slot[0], slot[1],
+          for (int y = 0; y < HD / 64; ++y)
+            tc::tma_gather4(ring + st * Lay::STAGE + y * Lay::TILE, gather, kvh * HD + 64 * y, slot[0], slot[1],
                             slot[2], slot[3], &full[st]);
         } else if (leads) {
 #pragma unroll
-          for (int x = 0; x < HD / 64; ++x)
-            tc::tma_load_3d(ring + st * Lay::STAGE + x * Lay::TILE, box, 64 * x, p.kvh, slot[0], &full[st]);
+          for (int y = 0; y < HD / 64; ++y)
+            tc::tma_load_3d(ring + st * Lay::STAGE + y * Lay::TILE, box, 64 * y, kvh, slot[0], &full[st]);
         }
         __syncwarp();
       }
@@ -271,48 +322,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         while (!tc::mbar_try_wait(&full[b % ST], (b / ST) & 1) && tc::globaltimer_ns() - t0 < 2000000000ull) {
         }
       }
-  } else if (warp < kMmaWarp) {
+  } else {
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_at = lanes + w * kTcKeys, o_at = lanes + Lay::O_COL + w * HD;
-    unsigned char* sq = base + Lay::Q + w * Lay::STAGE;
     const float scale = a.scale_log2;
-    uint32_t blocks = 0, steps = 0, parts = 0;
-    while (walk.next(a, sh, p, q)) {
-      const Share share = share_of(p, w);
-      const bool wide = p.w == 2, meet = !wide && p.b1 - p.b0 > 1;  // meet: the two groups' results do
-      const int v0 = p.v0 + (wide ? w * kTcHalf : 0), nv = p.v0 + p.nv - v0;  // this group's vectors
-      if (share.n > 0) {
-        // queries: the last part's S products have read theirs
-#pragma unroll 1
-        for (int k0 = 0; k0 < CH; k0 += 8) {
-          uint4 u[8];
+    const unsigned inverse = 0xffffffffu / (unsigned)a.group + 1u;  // (x inverse) >> 32 = x / group for x < 2^16, group > 1
+    auto rows_in = [&](unsigned x) { return a.group == 1 ? x : __umulhi(x, inverse); };
+    // Queries of part x, rows of 16-byte chunks, towards shared memory: this group's half (the S products of the part
+    // before have read theirs).  A thread's chunks: column r % CH of rows r / CH, r / CH + 128 / CH, ...
+    const uint32_t sq = tc::smem_u32(base + Lay::Q + w * Lay::STAGE);
+    const int qc = r % CH, qr = r / CH;
+    auto fetch_queries = [&](uint32_t x) {
+      wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+      const TcPart& p = ring_of_parts[x % kPartRing];
+      const int wide = p.wide, nv = p.nv - (wide ? w * kTcHalf : 0), t0 = p.t0, rem = p.rem + (wide ? w * kTcHalf : 0);
+      if (*dead || share_of(p.nb, wide, w).n == 0) return false;
+      const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)p.kvh * a.group * HD + qc * 8;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int i = r + (k0 + k) * 128, row = i / CH, c = i % CH, v = v0 + row;
-            u[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < nv && q_sign != 0) {
-              const int t = v / a.group;
-              u[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                     (int64_t)(q.row0 + t) * a.ld_q +
-                                                     (int64_t)(p.kvh * a.group + (v - t * a.group)) * HD + c * 8);
-              if (q_sign < 0) {
-                u[k].x ^= 0x80008000u;
-                u[k].y ^= 0x80008000u;
-                u[k].z ^= 0x80008000u;
-                u[k].w ^= 0x80008000u;
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int i = r + (k0 + k) * 128, row = i / CH, c = i % CH;
-            *reinterpret_cast<uint4*>(sq + (c >> 3) * Lay::TILE + row * 128 + (((c ^ row) & 7) << 4)) = u[k];
-          }
-        }
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(&bar.qfull[w]);
+      for (int k = 0; k < CH; ++k) {
+        const int row = qr + k * (128 / CH), v = rem + (row < nv ? row : 0), t = rows_in(v);
+        const uint32_t to = sq + (qc >> 3) * Lay::TILE + row * 128 + (((qc ^ row) & 7) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                     "l"(from + (int64_t)(t0 + t) * a.ld_q + (v - t * a.group) * HD),
+                     "r"(row < nv && q_sign != 0 ? 16 : 0)
+                     : "memory");
       }
+      return true;
+    };
+    auto queries_there = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (q_sign < 0) {
+#pragma unroll 1
+        for (int k = 0; k < CH; ++k) {
+          const int row = qr + k * (128 / CH);
+          uint4* u = reinterpret_cast<uint4*>(base + Lay::Q + w * Lay::STAGE + (qc >> 3) * Lay::TILE + row * 128 +
+                                              (((qc ^ row) & 7) << 4));
+          *u = make_uint4(u->x ^ 0x80008000u, u->y ^ 0x80008000u, u->z ^ 0x80008000u, u->w ^ 0x80008000u);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(&bar.qfull[w]);
+    };
+    uint32_t blocks = 0, steps = 0, parts = 0, meetings = 0;
+    auto groups_meet = [&]() {  // not a bar.sync: a wait that ends
+      tc::fence_before_sync();
+      tc::mbar_arrive(&bar.meet);
+      wait_for(&bar.meet, meetings & 1, dead, a.err);
+      ++meetings;
+      __syncwarp();
+      tc::fence_after_sync();
+    };
+    if (fetch_queries(0)) queries_there();
+    for (uint32_t x = 0;; ++x) {
+      wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+      const TcPart& p = ring_of_parts[x % kPartRing];
+      const int nb = *dead ? 0 : p.nb, wide = p.wide;
+      if (__any_sync(kFull, nb == 0)) break;
+      const Share share = share_of(nb, wide, w);
       float m = -INFINITY, l = 0.f;
       auto step = [&](int i, auto split) {
         constexpr bool SPLIT = decltype(split)::value;  // P as two bf16 numbers
@@ -382,10 +449,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
             for (int k = 0; k < 16; ++k) lo[k] = pack_bf16(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]);
             tc::tmem_st_u32<16>(s_at + 64 + 16 * c, lo);
           }
+          if (c & 1) {  // 64 keys: their product may begin
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            tc::mbar_arrive(&bar.pfull[w][c >> 1]);
+          }
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        tc::mbar_arrive(&bar.pfull[w]);
         const float2 x = both(sum[0] + sum[1]);
         l += x.x + x.y;
         ++steps;
@@ -397,42 +466,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 #pragma unroll 1
         for (int i = 0; i < share.n; ++i) step(i, std::true_type());
       }
-      blocks += p.b1 - p.b0;
+      blocks += nb;
+      // the next part's queries on their way, then on the tensor core while this part's results go out
+      const bool next = fetch_queries(x + 1);
       if (share.n > 0) {
         wait_for(&bar.odone[w], parts & 1, dead, a.err);
         __syncwarp();
         ++parts;
         tc::fence_after_sync();
+      }
+      if (next) queries_there();
+      if (share.n > 0) {
         // columns [c0, c1) of the rows are this group's to finish
+        const bool meet = !wide && nb > 1;  // the two groups' results do
         int c0 = 0, c1 = HD;
         float f0 = 1.f, f1 = 0.f;
         if (meet) {
           sml[w][r] = make_float2(m, l);
-          tc::fence_before_sync();
-          tc::named_bar_sync(1, 256);
-          tc::fence_after_sync();
-          const float2 x = sml[0][r], y = sml[1][r];
-          const float top = fmaxf(x.x, y.x), b = top == -INFINITY ? 0.f : top;
-          f0 = ex2(x.x - b);
-          f1 = ex2(y.x - b);
+          groups_meet();
+          const float2 y = sml[0][r], z = sml[1][r];
+          const float top = fmaxf(y.x, z.x), b = top == -INFINITY ? 0.f : top;
+          f0 = ex2(y.x - b);
+          f1 = ex2(z.x - b);
           m = top;
-          l = x.y * f0 + y.y * f1;
+          l = y.y * f0 + z.y * f1;
           c0 = w * (HD / 2);
           c1 = c0 + HD / 2;
         }
-        const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per);
-        const bool cut = last > first, mine = r < nv;
-        const int slot = rows_slot(blockIdx.x, first), row = wide ? w * kTcHalf + r : r;
-        const int v = v0 + r, t = v / a.group, h = p.kvh * a.group + (v - t * a.group);
-        const int64_t at = (int64_t)(q.row0 + t) * a.nq + h;
+        const int row = wide ? w * kTcHalf + r : r, slot = p.slot;
+        const bool cut = slot >= 0, mine = row < p.nv;
+        const unsigned v = p.rem + row, t = rows_in(v);
+        const int64_t tr = p.t0 + (int64_t)t, h = p.kvh * a.group + (int)(v - t * a.group), at = tr * a.nq + h;
         RowEnd end{1.f, 0.f, 0.f};
         if (cut) {
-          if (tid == 0 && first == (int)blockIdx.x) rows_record(a, p, q, first, last);
           if (mine && c0 == 0) *part_ml<kTcTileRows>(a, slot, row) = make_float2(m, l);
         } else if (mine) {
           end = rows_end(a, at, m, l, c0 == 0);
         }
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (int64_t)(q.row0 + t) * a.ld_out + (int64_t)h * HD;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tr * a.ld_out + h * HD;
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float o[32];
@@ -448,27 +519,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           if (mine) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
-              const float4 x = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-              const float4 y = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+              const float4 y = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              const float4 z = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
               if (cut) {
-                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4, row) = x;
-                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4 + 1, row) = y;
+                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4, row) = y;
+                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4 + 1, row) = z;
               } else {
-                const float4 u = rows_value<HD>(a, at, c + k, x, end), z = rows_value<HD>(a, at, c + k + 4, y, end);
+                const float4 y1 = rows_value<HD>(a, at, c + k, y, end), z1 = rows_value<HD>(a, at, c + k + 4, z, end);
                 *reinterpret_cast<uint4*>(out + c + k) =
-                    make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(z.x, z.y), pack_bf16(z.z, z.w));
+                    make_uint4(pack_bf16(y1.x, y1.y), pack_bf16(y1.z, y1.w), pack_bf16(z1.x, z1.y), pack_bf16(z1.z, z1.w));
               }
             }
           }
           __syncwarp();  // the next loads are the whole warp's
         }
         if (meet) {  // both O are read before either group lets the next part begin
-          tc::fence_before_sync();
-          tc::named_bar_sync(1, 256);
-          tc::fence_after_sync();
+          groups_meet();
         }
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc::fence_before_sync();
   __syncthreads();
