@@ -203,26 +203,32 @@ __device__ __forceinline__ void rows_finish(const CacheRowsArgs& a, int64_t t, i
   store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d, rows_value<HD>(a, at, d, o, e));
 }
 
-// Rows that no key belongs to: those of sequences without keys, and with a tail those of no sequence.
+// Rows that no key belongs to: those of sequences without keys, and with a tail
+// those of no sequence.  By THREADS threads of every block, each block every
+// gridDim.x-th row.
 template <typename T, int HD, int THREADS>
 __device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
-  auto clear = [&](int64_t t0, int64_t n) {
-    for (int64_t i = threadIdx.x; i < n * a.nq * (HD / 4); i += THREADS) {
-      const int64_t r = i / (HD / 4);
-      rows_finish<T, HD>(a, t0 + r / a.nq, (int)(r % a.nq), 4 * (int)(i % (HD / 4)), make_float4(0.f, 0.f, 0.f, 0.f),
-                         -INFINITY, 0.f);
-    }
+  const int thread = threadIdx.x % THREADS, lane = threadIdx.x & 31;
+  auto clear = [&](int t0, int t1) {
+    for (int t = t0 + blockIdx.x; t < t1; t += gridDim.x)
+      for (int i = thread; i < a.nq * (HD / 4); i += THREADS)
+        rows_finish<T, HD>(a, t, i / (HD / 4), i % (HD / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
   };
   if (empties)
-    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+    for (int s0 = 0; s0 < a.S; s0 += 32) {  // every warp finds them for itself, 32 sequences at once
       bool b0, b1;
-      const SeqRows q = sequence_rows(a, s, &b0, &b1);
-      if (q.len == 0 && q.rows > 0) clear(q.row0, q.rows);
+      SeqRows q{0, 0, 0, 1};
+      if (s0 + lane < a.S) q = sequence_rows(a, s0 + lane, &b0, &b1);
+      unsigned hits = __ballot_sync(kFull, q.len == 0 && q.rows > 0);
+      for (; hits; hits &= hits - 1) {
+        const int l = __ffs(hits) - 1, t0 = __shfl_sync(kFull, q.row0, l), n = __shfl_sync(kFull, q.rows, l);
+        clear(t0, t0 + n);
+        __syncwarp();
+      }
     }
   if (a.tail_ml) {  // rows in front of the first group and behind the last
-    const int r0 = __ldcg(a.starts), r1 = __ldcg(a.starts + a.S);
-    for (int t = blockIdx.x; t < r0; t += gridDim.x) clear(t, 1);
-    for (int t = r1 + blockIdx.x; t < a.T; t += gridDim.x) clear(t, 1);
+    clear(0, __ldcg(a.starts));
+    clear(__ldcg(a.starts + a.S), a.T);
   }
 }
 

@@ -20,7 +20,9 @@
 // rescales it there (rarely: the maximum is kept only to within 2^kSlack).
 // Each half has an issuing warp of its own: a wait costs 110 cycles even where
 // there is nothing to wait for, and the tensor core's queue is short (one warp
-// for both took 3,700 cycles for a block of two halves).
+// for both took 3,700 cycles for a block of two halves).  The two issue in turns:
+// left alone they fall into step, both softmaxes and then both products at once
+// (4,200 cycles).
 //
 // Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 and 9 the MMAs of
 // the halves (8 owns TMEM), 10 keys, 11 values.  Warp 10 also walks along the
@@ -68,6 +70,7 @@ struct Barriers {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t part_full[kPartRing], part_empty[kPartRing];
   uint64_t meet;  // of both softmax groups
+  uint64_t turn[2];  // whose MMAs come next
 };
 
 // What a thread block does next: blocks b0 .. b0 + nb - 1 of a tile.
@@ -141,6 +144,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       tc::mbar_init(&bar.pfull[i][0], kTcHalf);
       tc::mbar_init(&bar.pfull[i][1], kTcHalf);
       tc::mbar_init(&bar.odone[i], 1);
+      tc::mbar_init(&bar.turn[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&bar.kfull[i], 1);
@@ -167,71 +171,81 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   RowsWalk walk;
   bool empties;
   const bool ok = rows_plan<kTcThreads>(a, sh, walk, &empties);
-  if (ok && (empties || a.tail_ml)) rows_empties<__nv_bfloat16, HD, kTcThreads>(a, empties);
 
   if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-    if (lane == 0) {
-      const int w = warp - kMmaWarp;
-      const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
-      const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
-      const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::Q + w * Lay::STAGE));
-      const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(base + Lay::K));
-      const uint64_t dv = tc::sw128_mnmajor_desc(tc::smem_u32(base + Lay::V), Lay::TILE);
-      const uint32_t o_at = tmem + Lay::O_COL + w * HD, s_at = tmem + w * kTcKeys;
-      uint32_t blocks = 0, parts = 0, steps = 0;  // so far: of the rings, of this half
-      for (uint32_t x = 0;; ++x) {
-        wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
-        const TcPart& p = ring_of_parts[x % kPartRing];
-        const int nb = *dead ? 0 : p.nb, wide = p.wide;
-        tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
-        if (nb == 0) break;
-        const Share share = share_of(nb, wide, w);
-        auto scores = [&](int i) {
-          const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
-          wait_for(&bar.kfull[st], (b / ST) & 1, dead, a.err);
-          tc::fence_after_sync();
-          const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
+    // the whole warp walks along, one lane issues: descriptors stay in uniform registers
+    const bool leader = tc::elect_one();
+    const int w = __shfl_sync(kFull, warp, 0) - kMmaWarp;
+    const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
+    const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
+    const uint32_t base_u = __shfl_sync(kFull, tc::smem_u32(base), 0), tmem_u = __shfl_sync(kFull, tmem, 0);
+    const uint64_t dq = tc::sw128_kmajor_desc(base_u + Lay::Q + w * Lay::STAGE);
+    const uint64_t dk = tc::sw128_kmajor_desc(base_u + Lay::K);
+    const uint64_t dv = tc::sw128_mnmajor_desc(base_u + Lay::V, Lay::TILE);
+    const uint32_t o_at = tmem_u + Lay::O_COL + w * HD, s_at = tmem_u + w * kTcKeys;
+    auto waits_for = [&](uint64_t* b, uint32_t parity) {
+      wait_for(b, parity, dead, a.err);
+      __syncwarp();
+    };
+    uint32_t blocks = 0, parts = 0, steps = 0, turns = 0;  // so far: of the rings, of this half
+    for (uint32_t x = 0;; ++x) {
+      waits_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1);
+      const TcPart& p = ring_of_parts[x % kPartRing];
+      const int nb = __shfl_sync(kFull, *dead ? 0 : p.nb, 0), wide = __shfl_sync(kFull, p.wide, 0);
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
+      if (nb == 0) break;
+      const Share share = share_of(nb, wide, w);
+      auto scores = [&](int i) {
+        const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
+        waits_for(&bar.kfull[st], (b / ST) & 1);
+        tc::fence_after_sync();
+        const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk >> 2) * Lay::TILE + (kk & 3) * 32) >> 4);
-            tc::mma_bf16(s_at, dq + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&bar.sfull[w]);
-          tc::mma_commit(&bar.kempty[st]);
-          if (!wide) tc::mma_commit(&bar.kempty[st]);
-        };
-        if (share.n > 0) {
-          wait_for(&bar.qfull[w], parts & 1, dead, a.err);
-          ++parts;
-          scores(0);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * Lay::TILE + (kk & 3) * 32) >> 4);
+          tc::mma_bf16_by(leader, s_at, dq + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
         }
-        for (int i = 0; i < share.n; ++i, ++steps) {
-          const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
-          wait_for(&bar.vfull[st], (b / ST) & 1, dead, a.err);
-          const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            wait_for(&bar.pfull[w][half], steps & 1, dead, a.err);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
-              tc::mma_bf16_ts(o_at, s_at + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, i > 0 || kk > 0 ? 1u : 0u);
-            if (!wide)
-#pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
-                tc::mma_bf16_ts(o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
-          }
-          tc::mma_commit(&bar.vempty[st]);
-          if (!wide) tc::mma_commit(&bar.vempty[st]);
-          if (i + 1 < share.n)
-            scores(i + 1);
-          else
-            tc::mma_commit(&bar.odone[w]);
-        }
-        blocks += nb;
+        tc::mma_commit_by(leader, &bar.sfull[w]);
+        tc::mma_commit_by(leader, &bar.kempty[st]);
+        if (!wide) tc::mma_commit_by(leader, &bar.kempty[st]);
+      };
+      if (share.n > 0) {
+        waits_for(&bar.qfull[w], parts & 1);
+        ++parts;
+        scores(0);
       }
+      for (int i = 0; i < share.n; ++i, ++steps) {
+        const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
+        waits_for(&bar.vfull[st], (b / ST) & 1);
+        const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
+        waits_for(&bar.pfull[w][0], steps & 1);
+        if (wide) waits_for(&bar.turn[w], (turns & 1) ^ (w == 0 ? 1 : 0));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half) waits_for(&bar.pfull[w][1], steps & 1);
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
+            tc::mma_bf16_ts_by(leader, o_at, s_at + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o,
+                               i > 0 || kk > 0 ? 1u : 0u);
+          if (!wide)
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
+              tc::mma_bf16_ts_by(leader, o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
+        }
+        tc::mma_commit_by(leader, &bar.vempty[st]);
+        if (!wide) tc::mma_commit_by(leader, &bar.vempty[st]);
+        if (i + 1 < share.n)
+          scores(i + 1);
+        else
+          tc::mma_commit_by(leader, &bar.odone[w]);
+        if (wide) {
+          if (lane == 0) tc::mbar_arrive(&bar.turn[w ^ 1]);
+          ++turns;
+        }
+      }
+      blocks += nb;
     }
-    __syncwarp();
   } else if (warp == kKeyWarp || warp == kValueWarp) {
     // lane x takes keys 4 x .. 4 x + 3 of a block, and the runs that start there
     const bool keys = warp == kKeyWarp;
@@ -541,6 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok && (empties || a.tail_ml)) rows_empties<__nv_bfloat16, HD, 2 * kTcHalf>(a, empties);
   }
   tc::fence_before_sync();
   __syncthreads();
