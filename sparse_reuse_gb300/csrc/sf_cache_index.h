@@ -173,12 +173,12 @@ SF_HD bool plan_fits(int chunks, int longest, int64_t share, int blocks) {
 //
 // The rows of a sequence and one KV head are `rows * group` query vectors,
 // vector v being row v / group, head v % group of the KV head.  They are taken
-// in halves of `half` vectors, `pair` of them together as a tile (its last one
-// may have fewer), over the sequence's keys in blocks of `block`.  A tile's
-// block costs as many units as it has halves.  Sequence after sequence, KV head
-// after KV head, tile after tile, block after block, the batch is a line of
-// units; thread block k takes the blocks that start in units
-// [k * per, (k + 1) * per) of it.
+// in halves of `half` vectors, `pair` (1 or 2) of them together as a tile (its
+// last one may have fewer), over the sequence's keys in blocks of `block`.  The
+// batch is a line of units, about equal times: sequence after sequence, KV head
+// after KV head, tile after tile, a tile being `fixed` units and then one run of
+// cost[halves - 1] for each of its blocks.  Thread block k takes the blocks that
+// start in units [k * per, (k + 1) * per) of it.
 //
 // A tile whose blocks all belong to one thread block is finished there.  One
 // that is cut leaves a partial result in each; a thread block is the inside or
@@ -189,14 +189,23 @@ struct RowsShape {
   int group;  // query heads of a KV head
   int nkv;
   int half, pair, block;
+  int fixed, cost[2];
 };
 
 SF_HD int row_halves(const RowsShape& a, int rows) {
   return (int)(((unsigned)rows * (unsigned)a.group + a.half - 1) / (unsigned)a.half);
 }
 SF_HD int row_blocks(const RowsShape& a, int len) { return (int)((unsigned)(len + a.block - 1) / (unsigned)a.block); }
+SF_HD int64_t tile_units(const RowsShape& a, int halves, int blocks) {
+  return a.fixed + (int64_t)a.cost[halves - 1] * blocks;
+}
 // Units of one KV head of a sequence.
-SF_HD int64_t row_units(const RowsShape& a, int rows, int len) { return (int64_t)row_halves(a, rows) * row_blocks(a, len); }
+SF_HD int64_t row_units(const RowsShape& a, int rows, int len) {
+  const int halves = row_halves(a, rows), blocks = row_blocks(a, len);
+  if (halves == 0 || blocks == 0) return 0;
+  const int tiles = a.pair == 2 ? halves >> 1 : halves;
+  return tiles * tile_units(a, a.pair, blocks) + (tiles * a.pair < halves ? tile_units(a, 1, blocks) : 0);
+}
 
 // What a thread block takes of one tile: blocks [b0, b1) of nb; none where b0 >= b1.
 struct RowsPart {
@@ -204,34 +213,36 @@ struct RowsPart {
   int v0, nv;    // the tile's query vectors
   int w;         // its halves
   int nb, b0, b1;
-  int64_t u0;    // the tile's first unit
+  int cost;
+  int64_t u0;    // where its first block starts
 };
 
 // The part that starts at unit u of a sequence whose own units start at
 // `first`, for a thread block whose units end at `end`.
 SF_HD RowsPart rows_part(const RowsShape& a, int rows, int len, int64_t first, int64_t u, int64_t end) {
   RowsPart p;
-  const int halves = row_halves(a, rows);
+  const int halves = row_halves(a, rows), tiles = a.pair == 2 ? halves >> 1 : halves;
   p.nb = row_blocks(a, len);
-  const int64_t head = (int64_t)halves * p.nb, tile = (int64_t)a.pair * p.nb;
+  const int64_t head = row_units(a, rows, len), tile = tile_units(a, a.pair, p.nb);
   p.kvh = (int)quotient(u - first, head);
   const int64_t in_head = u - first - p.kvh * head;
-  const int x = (int)quotient(in_head, tile);
-  p.w = halves - x * a.pair < a.pair ? halves - x * a.pair : a.pair;
+  int x = (int)quotient(in_head, tile);
+  if (x > tiles) x = tiles;
+  p.w = x < tiles ? a.pair : 1;
+  p.cost = a.cost[p.w - 1];
   p.v0 = x * a.pair * a.half;
   p.nv = rows * a.group - p.v0 < p.w * a.half ? rows * a.group - p.v0 : p.w * a.half;
-  const int64_t in_tile = in_head - x * tile;
-  p.u0 = u - in_tile;
-  p.b0 = (int)quotient(in_tile + p.w - 1, p.w);
-  const int64_t b1 = quotient(end - p.u0 + p.w - 1, p.w);
+  p.u0 = u - (in_head - x * tile) + a.fixed;
+  p.b0 = u <= p.u0 ? 0 : (int)quotient(u - p.u0 + p.cost - 1, p.cost);
+  const int64_t b1 = end <= p.u0 ? 0 : quotient(end - p.u0 + p.cost - 1, p.cost);
   p.b1 = b1 < p.nb ? (int)b1 : p.nb;
   return p;
 }
-SF_HD int64_t rows_part_end(const RowsPart& p) { return p.u0 + (int64_t)p.w * p.nb; }
+SF_HD int64_t rows_part_end(const RowsPart& p) { return p.u0 + (int64_t)p.cost * p.nb; }
 
 // The thread blocks that share a tile: those in which its first and last blocks start.
 SF_HD int rows_first_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0, per); }
-SF_HD int rows_last_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0 + (int64_t)p.w * (p.nb - 1), per); }
+SF_HD int rows_last_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0 + (int64_t)p.cost * (p.nb - 1), per); }
 // The partial slot of thread block `cta` for a cut tile that starts in thread block `first`.
 SF_HD int rows_slot(int cta, int first) { return 2 * cta + (cta == first ? 1 : 0); }
 

@@ -19,10 +19,13 @@ using namespace rows;
 
 constexpr int kRowsJoinThreads = 256;
 constexpr int kRowsJoinWarps = kRowsJoinThreads / 32;
-constexpr int kRowsJoinCols = 4;      // float4 columns of a block's item
+constexpr int kRowsJoinFew = 8;       // parts that one thread joins
+constexpr int kRowsJoinCols = 4;      // float4 columns of a block's item of more parts
 
-// Items of 32 rows x kRowsJoinCols columns of one cut tile; the warps of a
-// block take its parts in turn.
+// A block takes items of 32 rows of one cut tile: of few parts, 8 columns (one
+// a warp, all parts in flight together); of more, kRowsJoinCols columns, the
+// warps taking the parts in turn.  (All items by the second way: 32 us where
+// most tiles have two parts, 4 requests of 1,440 query vectors over 4,096 keys.)
 template <typename T, int HD, int ROWS>
 __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const __grid_constant__ CacheRowsArgs a) {
   __shared__ short list[kRowsMaxCtas];
@@ -30,7 +33,7 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
   __shared__ int sums[2][kRowsJoinWarps];
   __shared__ float4 acc[kRowsJoinWarps][kRowsJoinCols][32];
   __shared__ float2 ml[kRowsJoinWarps][32];
-  constexpr int GROUPS = HD / 4 / kRowsJoinCols;
+  auto groups = [](int n) { return n <= kRowsJoinFew ? HD / 4 / kRowsJoinWarps : HD / 4 / kRowsJoinCols; };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
@@ -38,8 +41,8 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
   int count = 0, items = 0;
   for (int c0 = 0; c0 < a.ctas; c0 += kRowsJoinThreads) {
     const int c = c0 + threadIdx.x;
-    const int nv = c < a.ctas && a.joins[c].n > 0 ? a.joins[c].nv : 0;
-    int x = nv > 0, y = (nv + 31) / 32 * GROUPS;
+    const int n = c < a.ctas ? a.joins[c].n : 0, nv = n > 0 ? a.joins[c].nv : 0;
+    int x = nv > 0, y = (nv + 31) / 32 * groups(n);
     const int x0 = x, y0 = y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -81,8 +84,39 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
     }
     const int first = list[lo];
     const RowsJoin j = a.joins[first];
-    const int in = i - upto[lo], row = in / GROUPS * 32 + lane, c0 = in % GROUPS * kRowsJoinCols;
+    const int in = i - upto[lo], g = groups(j.n), row = in / g * 32 + lane;
     const bool on = row < j.nv;
+    if (j.n <= kRowsJoinFew) {
+      if (!on) continue;
+      const int c = in % g * kRowsJoinWarps + warp;
+      float2 y[kRowsJoinFew];
+      float4 z[kRowsJoinFew];
+#pragma unroll
+      for (int x = 0; x < kRowsJoinFew; ++x) {
+        y[x] = make_float2(-INFINITY, 0.f);
+        z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < j.n) {
+          const int slot = rows_slot(first + x, first);
+          y[x] = __ldcg(part_ml<ROWS>(a, slot, row));
+          z[x] = __ldcg(part_at<HD, ROWS>(a, slot, c, row));
+        }
+      }
+      float top = y[0].x, l = 0.f;
+#pragma unroll
+      for (int x = 1; x < kRowsJoinFew; ++x) top = fmaxf(top, y[x].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kRowsJoinFew; ++x) {
+        const float f = ex2(y[x].x - base);
+        l += y[x].y * f;
+        o = make_float4(o.x + z[x].x * f, o.y + z[x].y * f, o.z + z[x].z * f, o.w + z[x].w * f);
+      }
+      const int v = j.v0 + row, r = v / a.group;
+      rows_finish<T, HD>(a, j.row0 + r, j.kvh * a.group + (v - r * a.group), 4 * c, o, top, l);
+      continue;
+    }
+    const int c0 = in % g * kRowsJoinCols;
     float m = -INFINITY, l = 0.f;
     float4 o[kRowsJoinCols];
 #pragma unroll
@@ -162,7 +196,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
   extern __shared__ __align__(16) float sm[];
   float *sq = sm + Lay::Q, *sk = sm + Lay::K, *sv = sm + Lay::V, *sp = sm + Lay::P;
   int* live = reinterpret_cast<int*>(sm + Lay::LIVE);
-  const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys};
+  const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys, 1, {1, 1}};
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_wait();
   pdl_trigger();

@@ -27,10 +27,12 @@
 // Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 and 9 the MMAs of
 // the halves (8 owns TMEM), 10 keys, 11 values.  Warp 10 also walks along the
 // block's share of the batch and hands the parts to the others through a ring.
-// Loads are TMA: runs of rows that lie within a page as boxes, rows of odd pages
-// and of runs that are not all there four at a time (gather4), with zeros for
-// positions that are not there.  A gather4 of 512 bytes takes the TMA unit some
-// 38 cycles (a block's keys and values 4,900), a box of 16 rows little more.
+// Loads are TMA.  An instruction costs the unit some 46 cycles and 2.6 for each
+// 128 bytes (4, 8, 16, 32, 64, 128 rows of 64 dimensions: 8.5, 14.5, 22.5, 31,
+// 38, 43 bytes a cycle and SM), so rows that follow one another in a page come
+// in as large boxes as its size allows, whole heads at a time; rows at the seams
+// of odd pages and behind the end four at a time (gather4), with zeros for
+// positions that are not there.
 #include <cmath>
 #include <type_traits>
 
@@ -47,6 +49,8 @@ using namespace rows;
 constexpr int kTcThreads = 384;
 constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
+// Units of a tile, and of a block of it with one half and with two.
+constexpr int kTcFixed = 8, kTcNarrow = 2, kTcWide = 3, kTcLeast = 12;
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
 constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
@@ -55,8 +59,8 @@ constexpr int kPartRing = 4;
 template <int HD>
 struct TcLayout {
   static constexpr int ST = HD == 128 ? 2 : 4;       // stages of the key ring, and of the value ring
-  static constexpr int TILE = 128 * 128;             // 128 rows of 64 dimensions
-  static constexpr int STAGE = HD / 64 * TILE;
+  // a stage: 128 rows in groups of eight, each 64 dimensions (1,024 bytes) after 64 dimensions
+  static constexpr int HALVES = HD / 64, GROUP = HALVES * 1024, STAGE = 16 * GROUP;
   static constexpr int Q = 0;                        // two halves
   static constexpr int K = Q + 2 * STAGE;
   static constexpr int V = K + ST * STAGE;
@@ -114,7 +118,8 @@ __device__ __forceinline__ Share share_of(int nb, int wide, int w) {
 }
 
 // Keys and values as rows for gather4, and as boxes of `run` rows: the largest
-// power of two up to 128 that divides the page size.
+// power of two up to 128 that divides the page size, or 8 where that is less
+// than 16 (any eight rows that follow one another then).
 struct PoolMaps {
   CUtensorMap gather[2], box[2];
 };
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   volatile int* dead = &dead_;
   unsigned char* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const RowsShape sh{a.group, a.nkv, kTcHalf, 2, kTcKeys};
+  const RowsShape sh{a.group, a.nkv, kTcHalf, 2, kTcKeys, kTcFixed, {kTcNarrow, kTcWide}};
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -179,9 +184,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     const uint32_t idesc_s = tc::idesc_bf16_f32(kTcHalf, kTcKeys);
     const uint32_t idesc_o = tc::idesc_bf16_f32(kTcHalf, HD) | (1u << 16);  // V is MN-major
     const uint32_t base_u = __shfl_sync(kFull, tc::smem_u32(base), 0), tmem_u = __shfl_sync(kFull, tmem, 0);
-    const uint64_t dq = tc::sw128_kmajor_desc(base_u + Lay::Q + w * Lay::STAGE);
-    const uint64_t dk = tc::sw128_kmajor_desc(base_u + Lay::K);
-    const uint64_t dv = tc::sw128_mnmajor_desc(base_u + Lay::V, Lay::TILE);
+    const uint64_t dq = tc::sw128_kmajor_desc(base_u + Lay::Q + w * Lay::STAGE, Lay::GROUP);
+    const uint64_t dk = tc::sw128_kmajor_desc(base_u + Lay::K, Lay::GROUP);
+    const uint64_t dv = tc::sw128_mnmajor_desc(base_u + Lay::V, 1024, Lay::GROUP);
     const uint32_t o_at = tmem_u + Lay::O_COL + w * HD, s_at = tmem_u + w * kTcKeys;
     auto waits_for = [&](uint64_t* b, uint32_t parity) {
       wait_for(b, parity, dead, a.err);
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * Lay::TILE + (kk & 3) * 32) >> 4);
+          const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
           tc::mma_bf16_by(leader, s_at, dq + off, ka + off, idesc_s, kk > 0 ? 1u : 0u);
         }
         tc::mma_commit_by(leader, &bar.sfull[w]);
@@ -225,13 +230,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           if (half) waits_for(&bar.pfull[w][1], steps & 1);
           tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: 2048 bytes of V, 8 columns of P
-            tc::mma_bf16_ts_by(leader, o_at, s_at + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o,
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: two groups of V, 8 columns of P
+            tc::mma_bf16_ts_by(leader, o_at, s_at + kk * 8, va + (uint64_t)((kk * 2 * Lay::GROUP) >> 4), idesc_o,
                                i > 0 || kk > 0 ? 1u : 0u);
           if (!wide)
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
-              tc::mma_bf16_ts_by(leader, o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2048) >> 4), idesc_o, 1u);
+              tc::mma_bf16_ts_by(leader, o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2 * Lay::GROUP) >> 4), idesc_o, 1u);
         }
         tc::mma_commit_by(leader, &bar.vempty[st]);
         if (!wide) tc::mma_commit_by(leader, &bar.vempty[st]);
@@ -247,16 +252,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       blocks += nb;
     }
   } else if (warp == kKeyWarp || warp == kValueWarp) {
-    // lane x takes keys 4 x .. 4 x + 3 of a block, and the runs that start there
+    // lane x takes keys 4 x .. 4 x + 3 of a block, and the box that starts there
     const bool keys = warp == kKeyWarp;
-    const uint32_t ring = tc::smem_u32(base + (keys ? Lay::K : Lay::V)) + lane * 512;
+    const uint32_t ring =
+        tc::smem_u32(base + (keys ? Lay::K : Lay::V)) + (lane >> 1) * Lay::GROUP + (lane & 1) * 512;
     uint64_t* full = keys ? bar.kfull : bar.vfull;
     uint64_t* empty = keys ? bar.kempty : bar.vempty;
     const CUtensorMap *gather = &maps.gather[keys ? 0 : 1], *box = &maps.box[keys ? 0 : 1];
     const int none = (int)(a.table.n_pages * a.table.page_size);  // a row outside the pool
-    const unsigned peers =
-        run >= 128 ? kFull : run >= 8 ? ((1u << (run / 4)) - 1u) << (lane / (run / 4) * (run / 4)) : 1u << lane;
-    const bool leads = run >= 4 && (4 * lane) % run == 0;
+    const int of_run = run / 4;                                   // lanes
+    const unsigned peers = of_run == 32 ? kFull : ((1u << of_run) - 1u) << (lane / of_run * of_run);
+    const bool leads = lane % of_run == 0;
     uint32_t blocks = 0;
     if (keys && lane == 0) a.joins[blockIdx.x].n = 0;
     for (uint32_t x = 0;; ++x) {
@@ -315,16 +321,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
         __syncwarp();
         if (lane == 0) tc::mbar_expect_tx(&full[st], Lay::STAGE);
-        const bool whole = run >= 4 && (__ballot_sync(kFull, there == 15u) & peers) == peers;
+        // the lane's run is there and in one piece (runs from 16 on lie within a page)
+        const int after = __shfl_down_sync(kFull, slot[0], 1);
+        const bool joined = there == 15u && slot[3] == slot[0] + 3 && (run > 8 || (lane & 1) || after == slot[0] + 4);
+        const bool whole = (__ballot_sync(kFull, joined) & peers) == peers;
         if (!whole) {
 #pragma unroll
           for (int y = 0; y < HD / 64; ++y)
-            tc::tma_gather4(ring + st * Lay::STAGE + y * Lay::TILE, gather, kvh * HD + 64 * y, slot[0], slot[1],
-                            slot[2], slot[3], &full[st]);
+            tc::tma_gather4(ring + st * Lay::STAGE + y * 1024, gather, kvh * HD + 64 * y, slot[0], slot[1], slot[2],
+                            slot[3], &full[st]);
         } else if (leads) {
-#pragma unroll
-          for (int y = 0; y < HD / 64; ++y)
-            tc::tma_load_3d(ring + st * Lay::STAGE + y * Lay::TILE, box, 64 * y, kvh, slot[0], &full[st]);
+          if (run == 8)
+            tc::tma_load_4d(ring + st * Lay::STAGE, box, 0, slot[0], 0, kvh, &full[st]);
+          else
+            tc::tma_load_5d(ring + st * Lay::STAGE, box, 0, 0, 0, slot[0] >> 3, kvh, &full[st]);
         }
         __syncwarp();
       }
@@ -347,6 +357,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     // before have read theirs).  A thread's chunks: column r % CH of rows r / CH, r / CH + 128 / CH, ...
     const uint32_t sq = tc::smem_u32(base + Lay::Q + w * Lay::STAGE);
     const int qc = r % CH, qr = r / CH;
+    auto q_place = [&](int row) {
+      return (row >> 3) * Lay::GROUP + (qc >> 3) * 1024 + (row & 7) * 128 + (((qc ^ row) & 7) << 4);
+    };
     auto fetch_queries = [&](uint32_t x) {
       wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
       const TcPart& p = ring_of_parts[x % kPartRing];
@@ -356,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int row = qr + k * (128 / CH), v = rem + (row < nv ? row : 0), t = rows_in(v);
-        const uint32_t to = sq + (qc >> 3) * Lay::TILE + row * 128 + (((qc ^ row) & 7) << 4);
+        const uint32_t to = sq + q_place(row);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
                      "l"(from + (int64_t)(t0 + t) * a.ld_q + (v - t * a.group) * HD),
                      "r"(row < nv && q_sign != 0 ? 16 : 0)
@@ -370,8 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 #pragma unroll 1
         for (int k = 0; k < CH; ++k) {
           const int row = qr + k * (128 / CH);
-          uint4* u = reinterpret_cast<uint4*>(base + Lay::Q + w * Lay::STAGE + (qc >> 3) * Lay::TILE + row * 128 +
-                                              (((qc ^ row) & 7) << 4));
+          uint4* u = reinterpret_cast<uint4*>(base + Lay::Q + w * Lay::STAGE + q_place(row));
           *u = make_uint4(u->x ^ 0x80008000u, u->y ^ 0x80008000u, u->z ^ 0x80008000u, u->w ^ 0x80008000u);
         }
       }
@@ -569,19 +581,20 @@ template <int HD>
 cudaError_t rows_tc(cudaStream_t st, CacheRowsArgs a) {
   PoolMaps maps;
   const uint64_t slots = (uint64_t)a.table.n_pages * a.table.page_size;
-  int run = 1;
-  while (run < kTcKeys && a.table.page_size % (2 * run) == 0) run *= 2;
+  int run = 8;
+  if (a.table.page_size % 16 == 0)
+    while (run < kTcKeys && a.table.page_size % (2 * run) == 0) run *= 2;
   for (int i = 0; i < 2; ++i) {
     const void* pool = i ? a.v : a.k;
-    if (!make_tmap_pool(&maps.gather[i], pool, HD, a.nkv, slots) ||
-        !make_tmap_kv(&maps.box[i], pool, HD, a.nkv, slots, run))
+    if (!make_tmap_pool_rows(&maps.gather[i], pool, HD, a.nkv, slots) ||
+        !make_tmap_pool_run(&maps.box[i], pool, HD, a.nkv, slots, run))
       return cudaErrorInvalidValue;
   }
   // a negative scale turns the queries' signs, 0 makes them 0: the maximum of
   // the scaled scores is then that of the scores
   const int sign = a.scale_log2 > 0.f ? 1 : a.scale_log2 < 0.f ? -1 : 0;
   a.scale_log2 = sign == 0 ? 1.f : fabsf(a.scale_log2);
-  a.least = 4;
+  a.least = kTcLeast;
   return launch_pdl(st, dim3(a.ctas), dim3(kTcThreads), TcLayout<HD>::BYTES, 1, cache_rows_tc_kernel<HD>, a, maps, run,
                     sign);
 }

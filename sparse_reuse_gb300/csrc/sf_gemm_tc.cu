@@ -411,22 +411,25 @@ int max_active_clusters(int s) {
 }
 
 // Prefix keys or values of one layer, [rows = R * P][nkv][hd] bf16, as a 3-D
-// TMA source with (64 dims, 1 head, box_rows keys) boxes and 128-byte swizzling.
-bool make_tmap_kv(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t rows, uint32_t box_rows) {
+// TMA source with (64 dims, 1 head, 64 keys) boxes and 128-byte swizzling.
+bool make_tmap_kv(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t rows) {
   auto fn = encode_fn();
   if (!fn || hd % 64 != 0 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return false;
   cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)nkv, rows};
   cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)nkv * hd * 2};
-  cuuint32_t box[3] = {64u, 1u, box_rows};
+  cuuint32_t box[3] = {64u, 1u, 64u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a pool of pages, [slots][nkv * hd] bf16, gathered four at a time as
-// 64 columns each (tile::gather4: the box is one row high).
-bool make_tmap_pool(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t slots) {
+// A pool of pages, [slots][nkv][hd] bf16, in two forms.  Rows [slots][nkv * hd]
+// gathered four at a time as 64 columns each (tile::gather4: the box is one row
+// high); and boxes of `run` consecutive slots of one head, all its dimensions:
+// eight rows of dimensions 0-63, the same rows of 64-127, then the next eight.
+// (run 8: eight slots from any slot on; more: from a multiple of 8 on.)
+bool make_tmap_pool_rows(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t slots) {
   auto fn = encode_fn();
   if (!fn || hd % 64 != 0 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return false;
   cuuint64_t dims[2] = {(cuuint64_t)nkv * hd, slots};
@@ -434,6 +437,20 @@ bool make_tmap_pool(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t
   cuuint32_t box[2] = {64u, 1u};
   cuuint32_t estr[2] = {1u, 1u};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_tmap_pool_run(CUtensorMap* tm, const void* base, int hd, int nkv, uint64_t slots, int run) {
+  auto fn = encode_fn();
+  if (!fn || hd % 64 != 0 || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) return false;
+  const cuuint64_t row = (cuuint64_t)nkv * hd * 2, halves = hd / 64;
+  const bool eight = run == 8;
+  // dimension, row (of eight), half of the head, KV head; with longer runs the eights before the KV head
+  cuuint64_t dims[5] = {64, eight ? slots : 8, halves, eight ? (cuuint64_t)nkv : slots / 8, (cuuint64_t)nkv};
+  cuuint64_t strides[4] = {row, 128, eight ? (cuuint64_t)hd * 2 : 8 * row, (cuuint64_t)hd * 2};
+  cuuint32_t box[5] = {64u, 8u, (cuuint32_t)halves, eight ? 1u : (cuuint32_t)(run / 8), 1u};
+  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, eight ? 4 : 5, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -115,9 +115,9 @@ using namespace sf;
 struct Part { int cta, s, kvh, v0, nv, w, nb, b0, b1, first, last, slot; };
 extern "C" {
 // Parts that every thread block takes, in its order, as the kernels walk; ~n where out is too short.
-int walk(const int* rows, const int* lens, int S, int group, int nkv, int half, int pair, int block, int ctas, int least,
-         Part* out, int room, long long* per_out) {
-  const RowsShape sh{group, nkv, half, pair, block};
+int walk(const int* rows, const int* lens, int S, int group, int nkv, int half, int pair, int block, int fixed,
+         int cost1, int cost2, int ctas, int least, Part* out, int room, long long* per_out) {
+  const RowsShape sh{group, nkv, half, pair, block, fixed, {cost1, cost2}};
   std::vector<long long> first(S + 1, 0);
   for (int s = 0; s < S; ++s) first[s + 1] = first[s] + nkv * row_units(sh, rows[s], lens[s]);
   const long long total = first[S], per = units_per_block(total, ctas, least);
@@ -139,8 +139,8 @@ int walk(const int* rows, const int* lens, int S, int group, int nkv, int half, 
   }
   return n;
 }
-long long units(int rows, int len, int group, int nkv, int half, int pair, int block) {
-  return row_units(RowsShape{group, nkv, half, pair, block}, rows, len);
+long long units(int rows, int len, int group, int nkv, int half, int pair, int block, int fixed, int cost1, int cost2) {
+  return row_units(RowsShape{group, nkv, half, pair, block, fixed, {cost1, cost2}}, rows, len);
 }
 }
 """)
@@ -160,21 +160,22 @@ def test_split_of_rows(lib, seed):
     """Every block of every tile is taken once; a tile's vectors are all of its rows'; a cut tile's thread blocks are
     first..last, each with a part; no two cut tiles share a slot or a first thread block."""
     rng = np.random.default_rng(seed)
-    half, pair, block = [(128, 2, 128), (64, 1, 64), (16, 1, 64)][seed % 3]
+    half, pair, block, fixed, costs = [(128, 2, 128, 8, (2, 3)), (64, 1, 64, 1, (1, 1)), (16, 1, 64, 0, (1, 1)),
+                                       (128, 2, 128, 0, (1, 2))][seed % 4]
     S, nkv, group = int(rng.integers(1, 30)), int(rng.integers(1, 9)), int(rng.choice([1, 4, 5, 6, 16, 21]))
-    ctas, least = int(rng.choice([1, 7, 152])), int(rng.choice([2, 3, 8]))
+    ctas, least = int(rng.choice([1, 7, 152])), int(rng.choice([3, 8, 12]))
     rows = (rng.integers(0, int(rng.choice([2, 40, 700])), S) * (rng.random(S) < 0.8)).astype(np.int32)
     lens = (rng.integers(0, int(rng.choice([2, 300, 9000])), S) * (rng.random(S) < 0.8)).astype(np.int32)
     room = 400000
     out, per = np.zeros((room, len(FIELDS)), np.int32), ctypes.c_longlong()
     n = lib.walk(rows.ctypes.data_as(ctypes.c_void_p), lens.ctypes.data_as(ctypes.c_void_p), S, group, nkv, half, pair,
-                 block, ctas, least, out.ctypes.data_as(ctypes.c_void_p), room, ctypes.byref(per))
+                 block, fixed, *costs, ctas, least, out.ctypes.data_as(ctypes.c_void_p), room, ctypes.byref(per))
     assert n >= 0
     tiles, loads = {}, np.zeros(ctas, np.int64)
     for row in out[:n]:
         p = dict(zip(FIELDS, row.tolist()))
         tiles.setdefault((p["s"], p["kvh"], p["v0"]), []).append(p)
-        loads[p["cta"]] += (p["b1"] - p["b0"]) * p["w"]
+        loads[p["cta"]] += (p["b1"] - p["b0"]) * costs[p["w"] - 1]
     slots, firsts, seen = set(), set(), {}
     for (s, kvh, v0), parts in tiles.items():
         assert v0 % (half * pair) == 0 and 0 <= kvh < nkv
@@ -198,14 +199,18 @@ def test_split_of_rows(lib, seed):
         t.sort()
         assert t[0][0] == 0 and all(a + b == c for (a, b), (c, _) in zip(t, t[1:]))
         assert sum(b for _, b in t) == rows[s] * group
-    assert loads.sum() == sum(lib.units(int(r), int(x), group, nkv, half, pair, block) * nkv for r, x in zip(rows, lens))
-    # even shares: within a block of two halves either way
-    assert n == 0 or loads.max() <= per.value + pair - 1
+    shape = (group, nkv, half, pair, block, fixed, *costs)
+    total = sum(lib.units(int(r), int(x), *shape) * nkv for r, x in zip(rows, lens))
+    assert loads.sum() == total - fixed * len(tiles)
+    # even shares: within a block either way
+    assert n == 0 or (loads.max() <= per.value + max(costs) - 1 and per.value == max(least, -(-total // ctas)))
 
 
 def test_largest_units(lib):
-    assert lib.units(1048576, 262144, 1024, 1, 128, 2, 128) == 2 ** 30 // 128 * 2048
-    assert lib.units(0, 5, 4, 2, 128, 2, 128) == lib.units(5, 0, 4, 2, 128, 2, 128) == 0
+    assert lib.units(1048576, 262144, 1024, 1, 128, 2, 128, 8, 2, 3) == 2 ** 30 // 256 * (8 + 3 * 2048)
+    assert lib.units(0, 5, 4, 2, 128, 2, 128, 8, 2, 3) == lib.units(5, 0, 4, 2, 128, 2, 128, 8, 2, 3) == 0
+    assert lib.units(97, 300, 4, 2, 128, 2, 128, 8, 2, 3) == (8 + 9) + (8 + 9)     # 388 vectors: two tiles of two halves
+    assert lib.units(96, 300, 4, 2, 128, 2, 128, 8, 2, 3) == (8 + 9) + (8 + 6)
 
 
 # ---------------------------------------------------------------- refusals
