@@ -217,33 +217,60 @@ struct RowsPart {
   int64_t u0;    // where its first block starts
 };
 
-// The part that starts at unit u of a sequence whose own units start at
-// `first`, for a thread block whose units end at `end`.
-SF_HD RowsPart rows_part(const RowsShape& a, int rows, int len, int64_t first, int64_t u, int64_t end) {
-  RowsPart p;
-  const int halves = row_halves(a, rows), tiles = a.pair == 2 ? halves >> 1 : halves;
-  p.nb = row_blocks(a, len);
-  const int64_t head = row_units(a, rows, len), tile = tile_units(a, a.pair, p.nb);
-  p.kvh = (int)quotient(u - first, head);
-  const int64_t in_head = u - first - p.kvh * head;
-  int x = (int)quotient(in_head, tile);
-  if (x > tiles) x = tiles;
-  p.w = x < tiles ? a.pair : 1;
-  p.cost = a.cost[p.w - 1];
-  p.v0 = x * a.pair * a.half;
-  p.nv = rows * a.group - p.v0 < p.w * a.half ? rows * a.group - p.v0 : p.w * a.half;
-  p.u0 = u - (in_head - x * tile) + a.fixed;
-  p.b0 = u <= p.u0 ? 0 : (int)quotient(u - p.u0 + p.cost - 1, p.cost);
-  const int64_t b1 = end <= p.u0 ? 0 : quotient(end - p.u0 + p.cost - 1, p.cost);
-  p.b1 = b1 < p.nb ? (int)b1 : p.nb;
-  return p;
-}
-SF_HD int64_t rows_part_end(const RowsPart& p) { return p.u0 + (int64_t)p.cost * p.nb; }
+// The tiles of one sequence, one after the other (quotients only at the start:
+// they are on the critical path of a thread block's first loads).
+struct RowsTiles {
+  int rows, halves, tiles, nb;  // tiles: those of `pair` halves
+  int kvh, x, b0;               // the next tile, and the first block to take of it
+  int64_t at;                   // where it starts
+
+  // From unit u on of a sequence whose own units start at `first`.
+  SF_HD void start(const RowsShape& a, int rows_, int len, int64_t first, int64_t u) {
+    rows = rows_;
+    halves = row_halves(a, rows);
+    tiles = a.pair == 2 ? halves >> 1 : halves;
+    nb = row_blocks(a, len);
+    kvh = x = b0 = 0;
+    at = first;
+    if (u <= first) return;
+    const int64_t head = row_units(a, rows, len), tile = tile_units(a, a.pair, nb);
+    kvh = (int)quotient(u - first, head);
+    const int64_t in_head = u - first - kvh * head;
+    x = (int)quotient(in_head, tile);
+    if (x > tiles) x = tiles;
+    at = u - (in_head - x * tile);
+    const int cost = a.cost[x < tiles ? a.pair - 1 : 0];
+    const int64_t u0 = at + a.fixed;
+    b0 = u <= u0 ? 0 : (int)quotient(u - u0 + cost - 1, cost);
+  }
+  SF_HD bool more(const RowsShape& a) const { return kvh < a.nkv; }
+  // What a thread block whose units end at `end` takes of the next tile; then the one after it is next.
+  SF_HD RowsPart take(const RowsShape& a, int64_t end) {
+    RowsPart p;
+    p.kvh = kvh;
+    p.w = x < tiles ? a.pair : 1;
+    p.cost = a.cost[p.w - 1];
+    p.v0 = x * a.pair * a.half;
+    p.nv = rows * a.group - p.v0 < p.w * a.half ? rows * a.group - p.v0 : p.w * a.half;
+    p.nb = nb;
+    p.b0 = b0;
+    p.u0 = at + a.fixed;
+    at = p.u0 + (int64_t)p.cost * nb;
+    p.b1 = at <= end ? nb : end <= p.u0 ? 0 : (int)quotient(end - p.u0 + p.cost - 1, p.cost);
+    if (p.b1 > nb) p.b1 = nb;
+    b0 = 0;
+    if (++x * a.pair >= halves) {
+      x = 0;
+      ++kvh;
+    }
+    return p;
+  }
+};
 
 // The thread blocks that share a tile: those in which its first and last blocks start.
 SF_HD int rows_first_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0, per); }
 SF_HD int rows_last_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0 + (int64_t)p.cost * (p.nb - 1), per); }
-// The partial slot of thread block `cta` for a cut tile that starts in thread block `first`.
-SF_HD int rows_slot(int cta, int first) { return 2 * cta + (cta == first ? 1 : 0); }
+// (The first is the one whose part begins with block 0.)  The partial slot of thread block `cta` for a cut tile.
+SF_HD int rows_slot(int cta, bool first) { return 2 * cta + (first ? 1 : 0); }
 
 }  // namespace sf

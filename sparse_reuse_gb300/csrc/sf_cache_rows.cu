@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
         y[x] = make_float2(-INFINITY, 0.f);
         z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (x < j.n) {
-          const int slot = rows_slot(first + x, first);
+          const int slot = rows_slot(first + x, x == 0);
           y[x] = __ldcg(part_ml<ROWS>(a, slot, row));
           z[x] = __ldcg(part_at<HD, ROWS>(a, slot, c, row));
         }
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
     if (on)
 #pragma unroll 2
       for (int x = warp; x < j.n; x += kRowsJoinWarps) {
-        const int slot = rows_slot(first + x, first);
+        const int slot = rows_slot(first + x, x == 0);
         const float2 y = __ldcg(part_ml<ROWS>(a, slot, row));
         float4 z[kRowsJoinCols];
 #pragma unroll
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
   rows_empties<T, HD, kSimtThreads>(a, empties);
   RowsPart p;
   SeqRows q;
+  walk.start(sh);
   while (walk.next(a, sh, p, q)) {
     __syncthreads();  // the last part's queries are read
     for (int i = tid; i < MR * HD / 4; i += kSimtThreads) {
@@ -311,9 +312,9 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
         }
       }
     }
-    const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per);
-    const int slot = rows_slot(blockIdx.x, first);
-    if (last > first && first == (int)blockIdx.x && tid == 0) rows_record(a, p, q, first, last);
+    const bool cut = is_cut(p);
+    const int slot = rows_slot(blockIdx.x, p.b0 == 0);
+    if (cut && p.b0 == 0 && tid == 0) rows_record(a, p, q, walk.per);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
 #pragma unroll
@@ -323,12 +324,12 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
         const float4 y = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
-        if (last > first)
+        if (cut)
           *part_at<HD, MR>(a, slot, 16 * c + tx, r) = y;
         else
           rows_finish<T, HD>(a, q.row0 + t, p.kvh * a.group + (v - t * a.group), 64 * c + 4 * tx, y, m[i], l[i]);
       }
-      if (last > first && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
+      if (cut && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
     }
   }
 }

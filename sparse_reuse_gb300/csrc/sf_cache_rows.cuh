@@ -42,27 +42,27 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t x, int o) {
   return (int64_t)__shfl_up_sync(kFull, (unsigned long long)x, o);
 }
 
-// Where a thread block's share of the line starts, and the walk along it.
-// Every warp walks on its own: all 32 lanes call next() together.
+// A thread block's share of the line, and the walk along it: start() once, then
+// next() for every part, by whole warps.
 struct RowsWalk {
   int64_t u, end, per;  // this block's units [u, end)
   int64_t first;        // of seq
   SeqRows seq;
+  RowsTiles tiles;
 
+  __device__ __forceinline__ void start(const RowsShape& sh) {
+    if (u < end) tiles.start(sh, seq.rows, seq.len, first, u);
+    else tiles.at = end;
+  }
   __device__ __forceinline__ bool next(const CacheRowsArgs& a, const RowsShape& sh, RowsPart& p, SeqRows& q) {
-    while (u < end) {
-      p = rows_part(sh, seq.rows, seq.len, first, u, end);
-      q = seq;
-      u = rows_part_end(p);
-      const int64_t units = units_of(sh, seq);
-      if (u >= first + units && u < end) {  // the next sequence with units: 32 looked at together
-        first += units;
+    while (tiles.at < end) {
+      if (!tiles.more(sh)) {  // the next sequence with units: 32 looked at together
         const int lane = threadIdx.x & 31;
         for (int s0 = seq.s + 1;; s0 += 32) {
           bool b0, b1;
           SeqRows x{0, 0, 0, 0};
           if (s0 + lane < a.S) x = sequence_rows(a, s0 + lane, &b0, &b1);
-          const unsigned hit = __ballot_sync(kFull, units_of(sh, x) > 0);
+          const unsigned hit = __ballot_sync(kFull, x.rows > 0 && x.len > 0);
           if (hit) {
             const int l = __ffs(hit) - 1;
             seq.s = s0 + l;
@@ -71,12 +71,12 @@ struct RowsWalk {
             seq.len = __shfl_sync(kFull, x.len, l);
             break;
           }
-          if (s0 + 32 >= a.S) {  // not reached: units are left
-            u = end;
-            break;
-          }
+          if (s0 + 32 >= a.S) return false;  // not reached: units are left
         }
+        tiles.start(sh, seq.rows, seq.len, tiles.at, tiles.at);
       }
+      p = tiles.take(sh, end);
+      q = seq;
       if (p.b0 < p.b1) return true;
     }
     return false;
@@ -85,7 +85,7 @@ struct RowsWalk {
 
 // By all THREADS of the block: the walk's start.  False where nothing of the
 // call may be written (offsets that do not ascend).  *empties: some sequence
-// with rows has no keys.  Batches of up to THREADS sequences are scanned once,
+// with rows has no keys.  (Who walks calls walk.start() then.)  Batches of up to THREADS sequences are scanned once,
 // between two barriers.
 template <int THREADS>
 __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShape& sh, RowsWalk& walk, bool* empties) {
@@ -140,7 +140,7 @@ __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShap
   if (lo >= hi) return true;
   if (a.S <= THREADS) {
     const int64_t at = before + incl - mine;
-    if (at <= lo && lo < at + mine) found = RowsWalk{lo, hi, per, at, head};
+    if (at <= lo && lo < at + mine) found = RowsWalk{lo, hi, per, at, head, {}};
   } else {
     before = 0;
     for (int s0 = 0; s0 < a.S; s0 += THREADS) {
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShap
         if (w < warp) at += sums[w];
         before += sums[w];
       }
-      if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q};
+      if (at <= lo && lo < at + x) found = RowsWalk{lo, hi, per, at, q, {}};
       if (before > lo) break;
     }
   }
@@ -244,10 +244,10 @@ __device__ __forceinline__ float2* part_ml(const CacheRowsArgs& a, int slot, int
   return a.part_ml + (int64_t)slot * ROWS + row;
 }
 
+__device__ __forceinline__ bool is_cut(const RowsPart& p) { return p.b0 > 0 || p.b1 < p.nb; }
 // By one thread of the block that starts a cut tile.
-__device__ __forceinline__ void rows_record(const CacheRowsArgs& a, const RowsPart& p, const SeqRows& q, int first,
-                                            int last) {
-  a.joins[first] = RowsJoin{last - first + 1, p.nv, q.row0, p.kvh, p.v0};
+__device__ __forceinline__ void rows_record(const CacheRowsArgs& a, const RowsPart& p, const SeqRows& q, int64_t per) {
+  a.joins[blockIdx.x] = RowsJoin{rows_last_cta(p, per) - (int)blockIdx.x + 1, p.nv, q.row0, p.kvh, p.v0};
 }
 
 }  // namespace rows

@@ -50,7 +50,7 @@ constexpr int kTcThreads = 384;
 constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
 // Units of a tile, and of a block of it with one half and with two.
-constexpr int kTcFixed = 8, kTcNarrow = 2, kTcWide = 3, kTcLeast = 12;
+constexpr int kTcFixed = 16, kTcNarrow = 5, kTcWide = 6, kTcLeast = 24;
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
 constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
@@ -103,6 +103,22 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
+// Until the loads of block `b` of a ring have been issued.  A reader that skips
+// blocks (the other half's, in narrow tiles) may come to a stage two phases
+// early, where the phase's parity alone would let it through.
+__device__ __forceinline__ void wait_issued(volatile uint32_t* issued, uint32_t b, volatile int* dead, unsigned* err) {
+  if (*issued > b) return;
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (*issued <= b) {
+    if (*dead) return;
+    if (tc::globaltimer_ns() - t0 > 2000000000ull) {
+      *dead = 1;
+      cache_error(err, kCacheStall);
+      return;
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -137,6 +153,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   __shared__ float2 sml[2][kTcHalf];
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_;
+  __shared__ volatile uint32_t issued[2];  // blocks of keys, of values
   volatile int* dead = &dead_;
   unsigned char* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -163,6 +180,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     }
     tc::mbar_init(&bar.meet, 2 * kTcHalf);
     dead_ = 0;
+    issued[0] = issued[1] = 0;
     tc::fence_barrier_init();
   }
   // before the next kernel may start: it could take the TMEM that this one would wait for
@@ -202,6 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       const Share share = share_of(nb, wide, w);
       auto scores = [&](int i) {
         const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
+        wait_issued(&issued[0], b, dead, a.err);
         waits_for(&bar.kfull[st], (b / ST) & 1);
         tc::fence_after_sync();
         const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
@@ -221,6 +240,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       }
       for (int i = 0; i < share.n; ++i, ++steps) {
         const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
+        wait_issued(&issued[1], b, dead, a.err);
         waits_for(&bar.vfull[st], (b / ST) & 1);
         const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
         waits_for(&bar.pfull[w][0], steps & 1);
@@ -264,7 +284,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     const unsigned peers = of_run == 32 ? kFull : ((1u << of_run) - 1u) << (lane / of_run * of_run);
     const bool leads = lane % of_run == 0;
     uint32_t blocks = 0;
-    if (keys && lane == 0) a.joins[blockIdx.x].n = 0;
+    if (keys) {
+      if (lane == 0) a.joins[blockIdx.x].n = 0;
+      walk.start(sh);
+    }
     for (uint32_t x = 0;; ++x) {
       TcPart& slot_of = ring_of_parts[x % kPartRing];
       if (keys) {  // the walk
@@ -275,13 +298,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         if (lane == 0) {
           TcPart n{};
           if (more) {
-            const int first = rows_first_cta(p, walk.per), last = rows_last_cta(p, walk.per), r = p.v0 / a.group;
+            const int r = p.v0 / a.group;
             n = TcPart{p.b1 - p.b0, p.w == 2, p.nv, p.kvh, q.row0 + r, p.v0 - r * a.group,
-                       last > first ? rows_slot(blockIdx.x, first) : -1, q.s, q.len, p.b0};
-            if (last > first && first == (int)blockIdx.x) rows_record(a, p, q, first, last);
+                       is_cut(p) ? rows_slot(blockIdx.x, p.b0 == 0) : -1, q.s, q.len, p.b0};
           }
           slot_of = n;
           tc::mbar_arrive(&bar.part_full[x % kPartRing]);
+          if (more && is_cut(p) && p.b0 == 0) rows_record(a, p, q, walk.per);
         }
         __syncwarp();
       } else {
@@ -320,7 +343,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         if (blocks >= ST) wait_for(&empty[st], (blocks / ST - 1) & 1, dead, a.err);
         if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
         __syncwarp();
-        if (lane == 0) tc::mbar_expect_tx(&full[st], Lay::STAGE);
+        if (lane == 0) {
+          tc::mbar_expect_tx(&full[st], Lay::STAGE);
+          issued[keys ? 0 : 1] = blocks + 1;
+        }
         // the lane's run is there and in one piece (runs from 16 on lie within a page)
         const int after = __shfl_down_sync(kFull, slot[0], 1);
         const bool joined = there == 15u && slot[3] == slot[0] + 3 && (run > 8 || (lane & 1) || after == slot[0] + 4);

@@ -125,16 +125,22 @@ int walk(const int* rows, const int* lens, int S, int group, int nkv, int half, 
   int n = 0;
   for (int c = 0; c < ctas; ++c) {
     long long u = per * c, end = u + per < total ? u + per : total;
+    if (u >= end) continue;
     int s = 0;
-    while (u < end) {
-      while (first[s + 1] <= u) ++s;
-      const RowsPart p = rows_part(sh, rows[s], lens[s], first[s], u, end);
+    while (first[s + 1] <= u) ++s;
+    RowsTiles t;
+    t.start(sh, rows[s], lens[s], first[s], u);
+    while (t.at < end) {
+      if (!t.more(sh)) {
+        do ++s; while (first[s + 1] == first[s]);
+        t.start(sh, rows[s], lens[s], t.at, t.at);
+      }
+      const RowsPart p = t.take(sh, end);
       if (p.b0 < p.b1) {
         if (n == room) return ~n;
-        const int f = rows_first_cta(p, per);
-        out[n++] = Part{c, s, p.kvh, p.v0, p.nv, p.w, p.nb, p.b0, p.b1, f, rows_last_cta(p, per), rows_slot(c, f)};
+        out[n++] = Part{c, s, p.kvh, p.v0, p.nv, p.w, p.nb, p.b0, p.b1, rows_first_cta(p, per), rows_last_cta(p, per),
+                        rows_slot(c, p.b0 == 0)};
       }
-      u = rows_part_end(p);
     }
   }
   return n;
@@ -160,7 +166,7 @@ def test_split_of_rows(lib, seed):
     """Every block of every tile is taken once; a tile's vectors are all of its rows'; a cut tile's thread blocks are
     first..last, each with a part; no two cut tiles share a slot or a first thread block."""
     rng = np.random.default_rng(seed)
-    half, pair, block, fixed, costs = [(128, 2, 128, 8, (2, 3)), (64, 1, 64, 1, (1, 1)), (16, 1, 64, 0, (1, 1)),
+    half, pair, block, fixed, costs = [(128, 2, 128, 16, (5, 6)), (64, 1, 64, 1, (1, 1)), (16, 1, 64, 0, (1, 1)),
                                        (128, 2, 128, 0, (1, 2))][seed % 4]
     S, nkv, group = int(rng.integers(1, 30)), int(rng.integers(1, 9)), int(rng.choice([1, 4, 5, 6, 16, 21]))
     ctas, least = int(rng.choice([1, 7, 152])), int(rng.choice([3, 8, 12]))
