@@ -199,6 +199,8 @@ void free_cache(sf_cache* c) {
   cudaFree(c->row_joins);
   cudaFree(c->tail_o);
   cudaFree(c->tail_ml);
+  cudaFree(c->whole_o);
+  cudaFree(c->whole_ml);
   if (c->err) cudaFreeHost(c->err);
   delete c;
 }
@@ -385,6 +387,8 @@ sf_status sf_cache_create_with(const sf_cache_shapes* shapes, const sf_cache_opt
     if (e == cudaSuccess) e = cudaMalloc(&c->row_joins, ctas * sizeof(RowsJoin));
     if (e == cudaSuccess) e = cudaMalloc(&c->tail_o, tails * s.head_dim * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&c->tail_ml, tails * sizeof(float2));
+    if (e == cudaSuccess) e = cudaMalloc(&c->whole_o, tails * s.head_dim * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&c->whole_ml, tails * sizeof(float2));
     if (e == cudaSuccess) e = prepare_cache_rows();
   }
   if (e == cudaSuccess) e = prepare_cache_attend();
@@ -586,7 +590,7 @@ sf_status sf_cache_attend_shared(sf_cache* c, void* stream, const void* q, int64
   if (!lens || !prefix_lens || !starts || misaligned(lens, 4) || misaligned(prefix_lens, 4) || misaligned(starts, 4))
     return fail(c, SF_ERR_INVALID_ARG, "lens, prefix_lens or starts null or misaligned");
   if ((st = check_object(c)) != SF_OK) return st;
-  // the sequences' own positions first, then the prefixes, which join them
+  // the sequences' own positions, the prefixes beside them, and what joins both
   CacheAttendArgs t{};
   t.q = q;
   t.ld_q = ld_q;
@@ -618,6 +622,8 @@ sf_status sf_cache_attend_shared(sf_cache* c, void* stream, const void* q, int64
   a.limit = length_limit(s.max_len, prefix_cols, s.page_size);
   a.tail_o = c->tail_o;
   a.tail_ml = c->tail_ml;
+  a.whole_o = c->whole_o;
+  a.whole_ml = c->whole_ml;
   return launched(c, launch_cache_rows((cudaStream_t)stream, a, s.dtype == SF_BF16, s.head_dim, c->sm_count));
 }
 

@@ -51,6 +51,8 @@ struct sf_cache {
   sf::RowsJoin* row_joins = nullptr;  // [thread blocks]
   float* tail_o = nullptr;         // [max_rows][n_q_heads][head_dim] the sequences' own parts (shared)
   float2* tail_ml = nullptr;       // [max_rows][n_q_heads]
+  float* whole_o = nullptr;        // the same of the prefixes
+  float2* whole_ml = nullptr;
   unsigned* err = nullptr;    // [kCacheErrWords] pinned, written by the kernels through its device address
   unsigned* err_dev = nullptr;
   char last_error[256] = {0};
@@ -136,6 +138,8 @@ struct CacheRowsArgs {
   float* lse;              // [T][nq] or null
   const float* tail_o;     // [T][nq][hd] normalised output over other keys, to be joined to every row, or null
   const float2* tail_ml;   // [T][nq] its maximum and denominator
+  float* whole_o;          // [T][nq][hd] with a tail: what the tiles gave
+  float2* whole_ml;        // [T][nq]
   float* parts; float2* part_ml;
   RowsJoin* joins;         // [ctas]
   int ctas, least;         // thread blocks; units that each takes at least

@@ -161,6 +161,19 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
     }
     __syncthreads();
   }
+  // with a tail: rows that no cut tile holds
+  if (!a.tail_ml) return;
+  const int64_t all = (int64_t)a.T * a.nq * (HD / 4);
+  for (int64_t i = (int64_t)blockIdx.x * kRowsJoinThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kRowsJoinThreads) {
+    const int64_t at = i / (HD / 4);
+    const int d = (int)(i % (HD / 4)) * 4;
+    const float2 y = __ldcg(a.whole_ml + at);
+    if (y.y == kRowCut) continue;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (y.y != 0.f) o = __ldcg(reinterpret_cast<const float4*>(a.whole_o + at * HD + d));
+    const int64_t r = at / a.nq;
+    rows_finish<T, HD>(a, r, (int)(at - r * a.nq), d, o, y.x, y.y);
+  }
 }
 
 // ---- CUDA cores --------------------------------------------------------------
@@ -198,14 +211,14 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
   int* live = reinterpret_cast<int*>(sm + Lay::LIVE);
   const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys, 1, {1, 1}};
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  pdl_wait();
+  if (!a.tail_ml) pdl_wait();  // beside the tail's kernel, which has waited for everything before it
   pdl_trigger();
   RowsWalk walk;
   bool empties;
   const bool ok = rows_plan<kSimtThreads>(a, sh, walk, &empties);
   if (tid == 0) a.joins[blockIdx.x].n = 0;
-  if (!ok) return;
-  rows_empties<T, HD, kSimtThreads>(a, empties);
+  if (ok) rows_empties<T, HD, kSimtThreads>(a, empties);
+  else rows_refused(a);
   RowsPart p;
   SeqRows q;
   walk.start(sh);
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
         const int r = i / (HD / 4), d = i % (HD / 4) * 4, j = b * kSimtKeys + r;
         uint32_t slot = ~0u;
         if (j < q.len) {
-          slot = entry_slot32(a.table, page_entry(a.table, q.s, j), j);
+          slot = entry_slot32(a.table, entry_of(a, q.s, j), j);
           if (slot == ~0u) cache_error(a.err, kCacheBadPage);
         }
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -319,19 +332,24 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
     for (int i = 0; i < RPT; ++i) {
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], x);
-      const int r = ty * RPT + i, v = p.v0 + r, t = v / a.group;
+      const int r = ty * RPT + i, v = p.v0 + r, t = v / a.group, h = p.kvh * a.group + (v - t * a.group);
+      const int64_t at = (int64_t)(q.row0 + t) * a.nq + h;
       if (r >= p.nv) continue;
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
         const float4 y = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
         if (cut)
           *part_at<HD, MR>(a, slot, 16 * c + tx, r) = y;
+        else if (a.tail_ml)
+          *reinterpret_cast<float4*>(a.whole_o + at * HD + 64 * c + 4 * tx) = y;
         else
-          rows_finish<T, HD>(a, q.row0 + t, p.kvh * a.group + (v - t * a.group), 64 * c + 4 * tx, y, m[i], l[i]);
+          rows_finish<T, HD>(a, q.row0 + t, h, 64 * c + 4 * tx, y, m[i], l[i]);
       }
       if (cut && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
+      if (a.tail_ml && tx == 0 && p.b0 == 0) a.whole_ml[at] = make_float2(m[i], cut ? kRowCut : l[i]);
     }
   }
+  if (a.tail_ml) pdl_wait();  // the join waits for this kernel only
 }
 
 template <typename T, int HD, int ROWS>

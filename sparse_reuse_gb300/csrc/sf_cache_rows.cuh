@@ -34,6 +34,13 @@ __device__ __forceinline__ SeqRows sequence_rows(const CacheRowsArgs& a, int s, 
   return q;
 }
 
+// Page entry of position j < len of sequence s, through L2: the kernels may run
+// before their own wait.
+__device__ __forceinline__ int32_t entry_of(const CacheRowsArgs& a, int s, int j) {
+  const int c = page_of(a.table, j);
+  return c < a.table.cols ? __ldcg(a.table.pages + (int64_t)s * a.table.ld + c) : -1;
+}
+
 __device__ __forceinline__ int64_t units_of(const RowsShape& sh, const SeqRows& q) {
   return q.rows > 0 && q.len > 0 ? sh.nkv * row_units(sh, q.rows, q.len) : 0;
 }
@@ -167,41 +174,33 @@ __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShap
   return true;
 }
 
-// What makes a finished row of its unnormalised sums (m, l): with the tail's
-// state, where the call has one, out = (o f + tail g) inv.
-struct RowEnd {
-  float f, g, inv;
-};
-__device__ __forceinline__ RowEnd rows_end(const CacheRowsArgs& a, int64_t at, float m, float l, bool lse) {
-  RowEnd e{1.f, 0.f, 0.f};
-  if (a.tail_ml) {
-    const float2 tail = __ldcg(a.tail_ml + at);
-    const float top = fmaxf(m, tail.x), base = top == -INFINITY ? 0.f : top;
-    // the tail's output is normalised: its weight is its denominator
-    e.f = ex2(m - base);
-    e.g = tail.y * ex2(tail.x - base);
-    l = l * e.f + e.g;
-    m = top;
-  }
-  e.inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
-  if (lse && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
-  return e;
-}
-template <int HD>
-__device__ __forceinline__ float4 rows_value(const CacheRowsArgs& a, int64_t at, int d, float4 o, const RowEnd& e) {
-  if (a.tail_ml) {
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.tail_o + at * HD + d));
-    o = make_float4(o.x * e.f + y.x * e.g, o.y * e.f + y.y * e.g, o.z * e.f + y.z * e.g, o.w * e.f + y.w * e.g);
-  }
-  return make_float4(o.x * e.inv, o.y * e.inv, o.z * e.inv, o.w * e.inv);
-}
-// One float4 of a finished row.
+// One float4 of a finished row of its unnormalised sums (m, l), together with
+// the tail's state where the call has one.
 template <typename T, int HD>
 __device__ __forceinline__ void rows_finish(const CacheRowsArgs& a, int64_t t, int h, int d, float4 o, float m, float l) {
   const int64_t at = t * a.nq + h;
-  const RowEnd e = rows_end(a, at, m, l, d == 0);
-  store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d, rows_value<HD>(a, at, d, o, e));
+  if (a.tail_ml) {
+    const float2 tail = __ldcg(a.tail_ml + at);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.tail_o + at * HD + d));
+    const float top = fmaxf(m, tail.x), base = top == -INFINITY ? 0.f : top;
+    // the tail's output is normalised: its weight is its denominator
+    const float f = ex2(m - base), g = tail.y * ex2(tail.x - base);
+    o = make_float4(o.x * f + y.x * g, o.y * f + y.y * g, o.z * f + y.z * g, o.w * f + y.w * g);
+    l = l * f + g;
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
+  store4<T>(static_cast<T*>(a.out) + t * a.ld_out + (int64_t)h * HD + d,
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
 }
+
+// With a tail, the kernels of the tiles do not finish rows: the tail's kernel may
+// still be running.  A row's own state goes to whole_o and whole_ml; its
+// denominator is kRowCut where its tile is cut and the partial results hold it,
+// and 0, without an output, where there are no keys.  The join kernel goes
+// through all of them.
+constexpr float kRowCut = -1.f;
 
 // Rows that no key belongs to: those of sequences without keys, and with a tail
 // those of no sequence.  By THREADS threads of every block, each block every
@@ -211,8 +210,11 @@ __device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
   const int thread = threadIdx.x % THREADS, lane = threadIdx.x & 31;
   auto clear = [&](int t0, int t1) {
     for (int t = t0 + blockIdx.x; t < t1; t += gridDim.x)
-      for (int i = thread; i < a.nq * (HD / 4); i += THREADS)
-        rows_finish<T, HD>(a, t, i / (HD / 4), i % (HD / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
+      if (a.tail_ml)
+        for (int h = thread; h < a.nq; h += THREADS) a.whole_ml[(int64_t)t * a.nq + h] = make_float2(-INFINITY, 0.f);
+      else
+        for (int i = thread; i < a.nq * (HD / 4); i += THREADS)
+          rows_finish<T, HD>(a, t, i / (HD / 4), i % (HD / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f);
   };
   if (empties)
     for (int s0 = 0; s0 < a.S; s0 += 32) {  // every warp finds them for itself, 32 sequences at once
@@ -230,6 +232,14 @@ __device__ void rows_empties(const CacheRowsArgs& a, bool empties) {
     clear(0, __ldcg(a.starts));
     clear(__ldcg(a.starts + a.S), a.T);
   }
+}
+
+// Where nothing of the call may be written: with a tail, no row is the join's.
+__device__ __forceinline__ void rows_refused(const CacheRowsArgs& a) {
+  if (a.tail_ml)
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)a.T * a.nq;
+         i += (int64_t)gridDim.x * blockDim.x)
+      a.whole_ml[i] = make_float2(0.f, kRowCut);
 }
 
 // ---- partial results: per slot ROWS query vectors, [HD / 4][ROWS] float4 and

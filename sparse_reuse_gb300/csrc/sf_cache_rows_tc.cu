@@ -50,7 +50,7 @@ constexpr int kTcThreads = 384;
 constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
 // Units of a tile, and of a block of it with one half and with two.
-constexpr int kTcFixed = 16, kTcNarrow = 5, kTcWide = 6, kTcLeast = 24;
+constexpr int kTcFixed = 24, kTcNarrow = 5, kTcWide = 6, kTcLeast = 24;
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
 constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
@@ -64,7 +64,9 @@ struct TcLayout {
   static constexpr int Q = 0;                        // two halves
   static constexpr int K = Q + 2 * STAGE;
   static constexpr int V = K + ST * STAGE;
-  static constexpr int BYTES = V + ST * STAGE + 1024;  // + alignment of the dynamic window
+  // rows on their way out: 64 bytes of 32 rows a warp, padded so that both ways meet few banks twice
+  static constexpr int OUT = V + ST * STAGE, OUT_LD = 80, OUT_WARP = 32 * OUT_LD;
+  static constexpr int BYTES = OUT + 8 * OUT_WARP + 1024;  // + alignment of the dynamic window
   static constexpr int O_COL = 256;                  // TMEM: S of half w at 128 w, O at 256 + HD w
   static_assert(BYTES <= 224 * 1024, "shared memory");
 };
@@ -189,11 +191,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  pdl_wait();
+  if (!a.tail_ml) pdl_wait();  // beside the tail's kernel, which has waited for everything before it
   pdl_trigger();
   RowsWalk walk;
   bool empties;
   const bool ok = rows_plan<kTcThreads>(a, sh, walk, &empties);
+  if (!ok) rows_refused(a);
 
   if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // the whole warp walks along, one lane issues: descriptors stay in uniform registers
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int j = b * kTcKeys + 4 * lane + t;
-          page[t] = j < len ? page_entry(a.table, s, j) : -1;
+          page[t] = j < len ? entry_of(a, s, j) : -1;
         }
       };
       look(b0);
@@ -545,17 +548,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           c0 = w * (HD / 2);
           c1 = c0 + HD / 2;
         }
-        const int row = wide ? w * kTcHalf + r : r, slot = p.slot;
-        const bool cut = slot >= 0, mine = row < p.nv;
-        const unsigned v = p.rem + row, t = rows_in(v);
-        const int64_t tr = p.t0 + (int64_t)t, h = p.kvh * a.group + (int)(v - t * a.group), at = tr * a.nq + h;
-        RowEnd end{1.f, 0.f, 0.f};
-        if (cut) {
-          if (mine && c0 == 0) *part_ml<kTcTileRows>(a, slot, row) = make_float2(m, l);
-        } else if (mine) {
-          end = rows_end(a, at, m, l, c0 == 0);
+        const int row0 = wide ? w * kTcHalf : 0, row = row0 + r, slot = p.slot, nv = p.nv;
+        const bool cut = slot >= 0, mine = row < nv;
+        auto vector_at = [&](int row, int64_t* tr, int64_t* h) {  // row and head of a vector of the tile
+          const unsigned v = p.rem + row, t = rows_in(v);
+          *tr = p.t0 + (int64_t)t;
+          *h = p.kvh * a.group + (int)(v - t * a.group);
+        };
+        int64_t tr, h;
+        vector_at(row, &tr, &h);
+        const int64_t at = tr * a.nq + h;
+        float inv = 1.f;
+        if (mine && c0 == 0) {
+          if (cut) *part_ml<kTcTileRows>(a, slot, row) = make_float2(m, l);
+          if (a.tail_ml) {
+            if (!cut || p.b0 == 0) a.whole_ml[at] = make_float2(m, cut ? kRowCut : l);
+          } else if (!cut && a.lse) {
+            a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + kRowsRoom) + logf(l);
+          }
         }
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tr * a.ld_out + h * HD;
+        if (!cut && !a.tail_ml) inv = l == 0.f ? 0.f : 1.f / l;  // no score above -infinity: zeros
+        f0 *= inv;
+        f1 *= inv;
+        // 64 bytes of each row through shared memory, so that four lanes write one row (a lane a row met a line each
+        // with every store: 5,700 cycles a part)
+        unsigned char* mem = base + Lay::OUT + warp * Lay::OUT_WARP;
+        auto rows_out = [&](const uint4 (&u)[4], char* to, int64_t ld_t, int64_t ld_h) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(mem + lane * Lay::OUT_LD + 16 * k) = u[k];
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int x = (lane >> 2) + 8 * k, rx = row0 + 32 * (warp & 3) + x;
+            int64_t tx, hx;
+            vector_at(rx, &tx, &hx);
+            if (rx < nv)
+              *reinterpret_cast<uint4*>(to + tx * ld_t + hx * ld_h + (lane & 3) * 16) =
+                  *reinterpret_cast<const uint4*>(mem + x * Lay::OUT_LD + (lane & 3) * 16);
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
           float o[32];
@@ -567,23 +599,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
             for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + y[k] * f1;
           } else {
             tc::tmem_ld32(o_at + c, o);
-          }
-          if (mine) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              const float4 y = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-              const float4 z = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
-              if (cut) {
-                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4, row) = y;
-                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4 + 1, row) = z;
-              } else {
-                const float4 y1 = rows_value<HD>(a, at, c + k, y, end), z1 = rows_value<HD>(a, at, c + k + 4, z, end);
-                *reinterpret_cast<uint4*>(out + c + k) =
-                    make_uint4(pack_bf16(y1.x, y1.y), pack_bf16(y1.z, y1.w), pack_bf16(z1.x, z1.y), pack_bf16(z1.z, z1.w));
-              }
-            }
+            for (int k = 0; k < 32; ++k) o[k] *= f0;
           }
-          __syncwarp();  // the next loads are the whole warp's
+          if (cut) {
+            if (mine)
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *part_at<HD, kTcTileRows>(a, slot, (c + k) / 4, row) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            __syncwarp();  // the next loads are the whole warp's
+          } else if (a.tail_ml) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint4 u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                u[k] = make_uint4(__float_as_uint(o[e + 4 * k]), __float_as_uint(o[e + 4 * k + 1]),
+                                  __float_as_uint(o[e + 4 * k + 2]), __float_as_uint(o[e + 4 * k + 3]));
+              rows_out(u, reinterpret_cast<char*>(a.whole_o + c + e), (int64_t)a.nq * HD * 4, HD * 4);
+            }
+          } else {
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+            rows_out(u, static_cast<char*>(a.out) + c * 2, a.ld_out * 2, HD * 2);
+          }
         }
         if (meet) {  // both O are read before either group lets the next part begin
           groups_meet();
@@ -595,6 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (ok && (empties || a.tail_ml)) rows_empties<__nv_bfloat16, HD, 2 * kTcHalf>(a, empties);
   }
+  if (a.tail_ml) pdl_wait();  // the join waits for this kernel only
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) {

@@ -166,7 +166,7 @@ def test_split_of_rows(lib, seed):
     """Every block of every tile is taken once; a tile's vectors are all of its rows'; a cut tile's thread blocks are
     first..last, each with a part; no two cut tiles share a slot or a first thread block."""
     rng = np.random.default_rng(seed)
-    half, pair, block, fixed, costs = [(128, 2, 128, 16, (5, 6)), (64, 1, 64, 1, (1, 1)), (16, 1, 64, 0, (1, 1)),
+    half, pair, block, fixed, costs = [(128, 2, 128, 24, (5, 6)), (64, 1, 64, 1, (1, 1)), (16, 1, 64, 0, (1, 1)),
                                        (128, 2, 128, 0, (1, 2))][seed % 4]
     S, nkv, group = int(rng.integers(1, 30)), int(rng.integers(1, 9)), int(rng.choice([1, 4, 5, 6, 16, 21]))
     ctas, least = int(rng.choice([1, 7, 152])), int(rng.choice([3, 8, 12]))

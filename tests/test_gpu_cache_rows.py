@@ -547,3 +547,31 @@ def test_shared_in_graphs(sf):
             check_shared(dict(a, q=q, lens=[i + 1] * 9), out, lse, "bf16")
     a["c"].sync()
     a["c"].close()
+
+
+def test_many_calls_in_a_row(sf):
+    """Calls that follow one another without a wait, on inputs in turn: the same bits every time, no wait that runs
+    out (tiles of one half with odd and even numbers of blocks, cut and whole)."""
+    heads, page = (40, 8, 128), 32
+    cases = [shared_inputs(sf, heads, "bf16", page, [9] * 4, [4096, 640, 129, 1000], 0, 0, [32] * 36, seed=s) for s in range(3)]
+    more = [rows_inputs(sf, (12, 2, 128), "bf16", page, [3, 30, 1, 9], [700, 129, 3000, 257], seed=s) for s in range(3)]
+    want = [run_shared(a)[0] for a in cases] + [run_rows(a)[0] for a in more]
+    for a in cases + more:
+        a["c"].sync()
+    args = [[i32(a[x]) for x in ("table", "lens", "ptable", "plens", "starts")] for a in cases]
+    rargs = [[i32(a[x]) for x in ("table", "lens", "starts")] for a in more]
+    outs = [torch.empty_like(a["q"]) for a in cases] + [torch.full_like(a["q"], 7.0) for a in more]
+    for i in range(300):
+        j = i % 3
+        a, (t, n, pt, pn, st) = cases[j], args[j]
+        a["c"].attend_shared(a["q"], a["k"], a["v"], t, n, pt, pn, st, out=outs[j])
+        a, (t, n, st) = more[j], rargs[j]
+        a["c"].attend_rows(a["q"], a["k"], a["v"], t, n, st, out=outs[3 + j])
+        if i % 25 < 3:
+            torch.cuda.synchronize()
+            assert torch.equal(outs[j], want[j]) and torch.equal(outs[3 + j], want[3 + j])
+            outs[j].zero_()
+            outs[3 + j].fill_(7.0)
+    for a in cases + more:
+        a["c"].sync()
+        a["c"].close()
