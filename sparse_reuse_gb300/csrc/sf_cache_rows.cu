@@ -22,10 +22,12 @@ constexpr int kRowsJoinWarps = kRowsJoinThreads / 32;
 constexpr int kRowsJoinFew = 8;       // parts that one thread joins
 constexpr int kRowsJoinCols = 4;      // float4 columns of a block's item of more parts
 
-// A block takes items of 32 rows of one cut tile: of few parts, 8 columns (one
-// a warp, all parts in flight together); of more, kRowsJoinCols columns, the
-// warps taking the parts in turn.  (All items by the second way: 32 us where
-// most tiles have two parts, 4 requests of 1,440 query vectors over 4,096 keys.)
+// A block takes items of 32 rows of one cut tile: of few parts, all columns (HD
+// / 32 a warp, lanes on neighbouring rows as the parts lie, then through shared
+// memory so that whole rows go out); of more, kRowsJoinCols columns, the warps
+// taking the parts in turn.  (Lane by row to the end 20 us, all items by the
+// second way 32 us, where most tiles have two parts: 4 requests of 1,440 query
+// vectors over 4,096 keys.)
 template <typename T, int HD, int ROWS>
 __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const __grid_constant__ CacheRowsArgs a) {
   __shared__ short list[kRowsMaxCtas];
@@ -33,7 +35,9 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
   __shared__ int sums[2][kRowsJoinWarps];
   __shared__ float4 acc[kRowsJoinWarps][kRowsJoinCols][32];
   __shared__ float2 ml[kRowsJoinWarps][32];
-  auto groups = [](int n) { return n <= kRowsJoinFew ? HD / 4 / kRowsJoinWarps : HD / 4 / kRowsJoinCols; };
+  auto groups = [](int n) { return n <= kRowsJoinFew ? 1 : HD / 4 / kRowsJoinCols; };
+  __shared__ float4 rows_[32][HD / 4 + 1];
+  __shared__ float2 row_ml[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
@@ -87,33 +91,63 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
     const int in = i - upto[lo], g = groups(j.n), row = in / g * 32 + lane;
     const bool on = row < j.nv;
     if (j.n <= kRowsJoinFew) {
-      if (!on) continue;
-      const int c = in % g * kRowsJoinWarps + warp;
+      float f[kRowsJoinFew], top = -INFINITY, l = 0.f;
       float2 y[kRowsJoinFew];
-      float4 z[kRowsJoinFew];
 #pragma unroll
       for (int x = 0; x < kRowsJoinFew; ++x) {
         y[x] = make_float2(-INFINITY, 0.f);
-        z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < j.n) {
-          const int slot = rows_slot(first + x, x == 0);
-          y[x] = __ldcg(part_ml<ROWS>(a, slot, row));
-          z[x] = __ldcg(part_at<HD, ROWS>(a, slot, c, row));
-        }
+        if (on && x < j.n) y[x] = __ldcg(part_ml<ROWS>(a, rows_slot(first + x, x == 0), row));
       }
-      float top = y[0].x, l = 0.f;
+      constexpr int CW = HD / 4 / kRowsJoinWarps;  // columns of a warp
+      float4 o[CW], z[CW][2];
 #pragma unroll
-      for (int x = 1; x < kRowsJoinFew; ++x) top = fmaxf(top, y[x].x);
+      for (int c = 0; c < CW; ++c) {
+        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)  // the usual two parts at once
+          if (on && x < j.n)
+            z[c][x] = __ldcg(part_at<HD, ROWS>(a, rows_slot(first + x, x == 0), c * kRowsJoinWarps + warp, row));
+      }
+#pragma unroll
+      for (int x = 0; x < kRowsJoinFew; ++x) top = fmaxf(top, y[x].x);
       const float base = top == -INFINITY ? 0.f : top;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kRowsJoinFew; ++x) {
-        const float f = ex2(y[x].x - base);
-        l += y[x].y * f;
-        o = make_float4(o.x + z[x].x * f, o.y + z[x].y * f, o.z + z[x].z * f, o.w + z[x].w * f);
+        f[x] = ex2(y[x].x - base);
+        l += y[x].y * f[x];
       }
-      const int v = j.v0 + row, r = v / a.group;
-      rows_finish<T, HD>(a, j.row0 + r, j.kvh * a.group + (v - r * a.group), 4 * c, o, top, l);
+      auto add = [](float4& o, const float4& z, float f) {
+        o = make_float4(o.x + z.x * f, o.y + z.y * f, o.z + z.z * f, o.w + z.w * f);
+      };
+      if (on) {
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+          add(o[c], z[c][0], f[0]);
+          add(o[c], z[c][1], f[1]);
+        }
+#pragma unroll
+        for (int x = 2; x < kRowsJoinFew; ++x)
+          if (x < j.n) {
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+              z[c][0] = __ldcg(part_at<HD, ROWS>(a, rows_slot(first + x, false), c * kRowsJoinWarps + warp, row));
+#pragma unroll
+            for (int c = 0; c < CW; ++c) add(o[c], z[c][0], f[x]);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < CW; ++c) rows_[lane][c * kRowsJoinWarps + warp] = o[c];
+      if (warp == 0) row_ml[lane] = make_float2(top, l);
+      __syncthreads();
+      for (int x = threadIdx.x; x < 32 * (HD / 4); x += kRowsJoinThreads) {
+        const int r = x / (HD / 4), c = x % (HD / 4), rr = in / g * 32 + r;
+        if (rr < j.nv) {
+          const int v = j.v0 + rr, t = v / a.group;
+          rows_finish<T, HD>(a, j.row0 + t, j.kvh * a.group + (v - t * a.group), 4 * c, rows_[r][c], row_ml[r].x,
+                             row_ml[r].y);
+        }
+      }
+      __syncthreads();
       continue;
     }
     const int c0 = in % g * kRowsJoinCols;

@@ -50,7 +50,7 @@ constexpr int kTcThreads = 384;
 constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
 // Units of a tile, and of a block of it with one half and with two.
-constexpr int kTcFixed = 24, kTcNarrow = 5, kTcWide = 6, kTcLeast = 24;
+constexpr int kTcFixed = 24, kTcNarrow = 5, kTcWide = 6, kTcLeast = 6;
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
 constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
