@@ -139,7 +139,7 @@ __device__ __forceinline__ bool rows_plan(const CacheRowsArgs& a, const RowsShap
     if (flags & 1) cache_error(a.err, kCacheBadRow);
     if (flags & 2) cache_error(a.err, kCacheBadLength);
   }
-  const int64_t per = units_per_block(total, a.ctas, a.least);
+  const int64_t even = quick_quotient(total + a.ctas - 1, a.ctas), per = even < a.least ? a.least : even;
   const int64_t lo = per * blockIdx.x, hi = lo + per < total ? lo + per : total;
   walk.u = walk.end = 0;
   walk.per = per;

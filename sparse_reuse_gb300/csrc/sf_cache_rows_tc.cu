@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         if (lane == 0) {
           TcPart n{};
           if (more) {
-            const int r = p.v0 / a.group;
+            const int r = (int)quick_quotient(p.v0, a.group);
             n = TcPart{p.b1 - p.b0, p.w == 2, p.nv, p.kvh, q.row0 + r, p.v0 - r * a.group,
                        is_cut(p) ? rows_slot(blockIdx.x, p.b0 == 0) : -1, q.s, q.len, p.b0};
           }
@@ -441,10 +441,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         wait_for(&bar.sfull[w], steps & 1, dead, a.err);
         __syncwarp();  // tensor-memory accesses are the whole warp's
         tc::fence_after_sync();
+        const uint32_t* on = live[(blocks + share.first + share.step * i) % kLiveRing];
+        const bool holes = on[lane >> 2] != 0x0f0f0f0fu;
         float s[128];
         tc::tmem_ld128(s_at, s);
-        const uint32_t* on = live[(blocks + share.first + share.step * i) % kLiveRing];
-        if (__any_sync(kFull, on[lane >> 2] != 0x0f0f0f0fu)) {
+        if (__any_sync(kFull, holes)) {
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const uint32_t word = on[x];
@@ -483,33 +484,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         const float bias = (m == -INFINITY ? 0.f : -m) - kRowsRoom;
         const Two scale2 = two(scale, scale), bias2 = two(bias, bias);
         Two sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t hi[16];
+        uint32_t hi[2][16], lo[16];
+        auto weights = [&](int c) {  // keys 32 c .. of the block
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 x = both(fma2(two(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]), scale2, bias2));
             const float p0 = ex2(x.x), p1 = ex2(x.y);
             sum[k & 1] = sum[k & 1] + two(p0, p1);
-            hi[k] = pack_bf16(p0, p1);
-            if constexpr (SPLIT) {
-              s[32 * c + 2 * k] = p0 - __uint_as_float(hi[k] << 16);
-              s[32 * c + 2 * k + 1] = p1 - __uint_as_float(hi[k] & 0xffff0000u);
-            }
+            hi[c & 1][k] = pack_bf16(p0, p1);
+            if constexpr (SPLIT)
+              lo[k] = pack_bf16(p0 - __uint_as_float(hi[c & 1][k] << 16), p1 - __uint_as_float(hi[c & 1][k] & 0xffff0000u));
           }
-          tc::tmem_st_u32<16>(s_at + 16 * c, hi);
-          if constexpr (SPLIT) {
-            uint32_t lo[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) lo[k] = pack_bf16(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]);
-            tc::tmem_st_u32<16>(s_at + 64 + 16 * c, lo);
-          }
-          if (c & 1) {  // 64 keys: their product may begin
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(&bar.pfull[w][c >> 1]);
-          }
-        }
+          if constexpr (SPLIT) tc::tmem_st_u32<16>(s_at + 64 + 16 * c, lo);
+        };
+        auto store = [&](int c) { tc::tmem_st_u32<16>(s_at + 16 * c, hi[c & 1]); };
+        auto arrive = [&](int half) {  // 64 keys: their product may begin
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&bar.pfull[w][half]);
+        };
+        // stores complete behind the next keys' exponentials
+        weights(0);
+        store(0);
+        weights(1);
+        store(1);
+        weights(2);
+        arrive(0);
+        store(2);
+        weights(3);
+        store(3);
+        arrive(1);
         const float2 x = both(sum[0] + sum[1]);
         l += x.x + x.y;
         ++steps;
