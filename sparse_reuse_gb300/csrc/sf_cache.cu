@@ -45,6 +45,7 @@ __global__ void rope_table_kernel(float* out, int max_pos, int half, double thet
 constexpr int kAppendThreads = 64;
 constexpr int kAppendHeads = 2;
 constexpr int kAppendBlocks = 18;
+constexpr int kAppendBlocksForms = 16;  // of the other forms, which need more registers
 // (lane, head) pairs per SM from which a group takes several heads.  40/8 heads x 128 bf16, 512 rows (1,509 pairs):
 // 4.2 us with one, 4.9 with two; 1,024 rows: 8.6 and 7.8; 4,096 rows: 31.4 and 24.2.
 constexpr int kAppendWide = 2048;
@@ -64,7 +65,7 @@ enum Form { kHalves, kPart, kNeighbours };
 // in and out once); HPT heads keep 2 HPT loads in flight and share the row's
 // angles and its page lookup.
 template <typename T, int HD, int HPT, Form FORM>
-__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, FORM == kHalves ? kAppendBlocks : kAppendBlocksForms) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
   using P = Piece<T>;
   constexpr int N = P::PAIRS, VEC = 2 * N, LANES = HD / 2 / VEC, GROUPS = kAppendThreads / LANES;
   pdl_wait();

@@ -8,13 +8,18 @@
 namespace sf {
 namespace {
 
-constexpr int kTurnThreads = 256;
-constexpr int kTurnPlaces = 32;  // places of a sequence that a block takes at a time
+// 4 x 4,096 places of 8 heads x 128 bf16, and 1,024 of 2 heads: 16.5 and 2.5 us so; 32 places and 256 threads 17.3 and
+// 3.1, 16 and 256 17.0 and 2.4, 2 and 128 17.6 and 2.7.
+constexpr int kTurnThreads = 128;
+constexpr int kTurnPlaces = 4;  // places of a sequence that a block takes at a time
 
 // A group of dim / 2 / VEC lanes turns one key head: each lane holds two
 // 16-byte pieces, both members of its rotation pairs.  Bytes bound it: the
-// turned part of every key in and out once, and as many bytes of the table
-// from L2 as of the key.
+// turned part of every key in and out once, and twice as many bytes of the
+// table, from L2.  (Not kept, at 16.5 us and half the copy bandwidth: two or
+// four keys in flight a group 20 to 29 us, angles as sums of two rows that stay
+// in L1 17.4 and of one that stays in registers 19.2, sines and cosines of 64-bit
+// phases 16.7.)
 template <typename T, int HD, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kTurnThreads) cache_turn_kernel(const __grid_constant__ CacheTurnArgs a) {
   using P = Piece<T>;
