@@ -106,7 +106,7 @@ typedef struct sf_cache_options {
   double rotary_magnitude; /* sine and cosine are multiplied by it (queries and keys alike); 0 = 1 */
   int max_rows;            /* rows of a call of sf_cache_attend_rows, sequences of one of sf_cache_attend_shared, up to
                               1048576; 0: neither is called.  A workspace of 2 * SMs * 256 * (head_dim + 2) * 4 bytes
-                              (bf16; a quarter of it for fp32), and 2 * min(max_rows, max_seqs) * n_q_heads *
+                              (bf16; half of it for fp32), and 2 * min(max_rows, max_seqs) * n_q_heads *
                               (head_dim + 2) * 4 bytes. */
 } sf_cache_options;
 

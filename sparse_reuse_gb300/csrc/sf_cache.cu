@@ -307,7 +307,7 @@ CacheRowsArgs rows_args(const sf_cache* c, const void* q, int64_t ld_q, int T, f
   a.parts = c->row_parts;
   a.part_ml = c->row_ml;
   a.joins = c->row_joins;
-  a.ctas = cache_rows_ctas(c->sm_count);
+  a.ctas = cache_rows_ctas(c->sm_count, c->s.dtype == SF_BF16);
   a.err = c->err_dev;
   return a;
 }
@@ -381,7 +381,7 @@ sf_status sf_cache_create_with(const sf_cache_shapes* shapes, const sf_cache_opt
   if (e == cudaSuccess) e = cudaMalloc(&c->arrived, (size_t)blocks * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMemset(c->arrived, 0, (size_t)blocks * sizeof(unsigned));
   if (o.max_rows > 0) {
-    const size_t ctas = (size_t)cache_rows_ctas(c->sm_count), rows = 2 * ctas * cache_rows_slot_rows(s.dtype == SF_BF16);
+    const size_t ctas = (size_t)cache_rows_ctas(c->sm_count, s.dtype == SF_BF16), rows = 2 * ctas * cache_rows_slot_rows(s.dtype == SF_BF16);
     const size_t tails = (size_t)(o.max_rows < s.max_seqs ? o.max_rows : s.max_seqs) * s.n_q_heads;
     if (e == cudaSuccess) e = cudaMalloc(&c->row_parts, rows * s.head_dim * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&c->row_ml, rows * sizeof(float2));

@@ -145,7 +145,7 @@ struct CacheRowsArgs {
   int ctas, least;         // thread blocks; units that each takes at least
   unsigned* err;
 };
-int cache_rows_ctas(int sm_count);
+int cache_rows_ctas(int sm_count, int bf16);
 int cache_rows_slot_rows(int bf16);  // query vectors of a partial slot
 constexpr int kTcTileRows = 256;
 cudaError_t prepare_cache_rows();

@@ -11,6 +11,7 @@
 // cache_rows_join_kernel.  kRowsRoom keeps unnormalised sums from overflowing
 // where the result does not (2^18 values at most).
 #include "sf_cache_rows.cuh"
+#include "sf_pairs.cuh"
 
 namespace sf {
 namespace {
@@ -210,39 +211,34 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
   }
 }
 
-// ---- CUDA cores --------------------------------------------------------------
+// ---- fp32: CUDA cores --------------------------------------------------------
 //
 // MR query vectors and blocks of 64 keys: thread (ty, tx) of 16 x 16 has
 // MR / 16 x 4 scores (vectors ty * MR / 16 .., keys tx, tx + 16, ...) and
-// MR / 16 x HD / 16 outputs (columns 4 tx .., 64 + 4 tx ..).  The scores'
-// operands come 4 dimensions at a time from rows padded by 16 bytes.
+// MR / 16 x HD / 16 outputs (columns 4 tx .., 64 + 4 tx ..), in packed fp32.  The
+// scores' operands come 4 dimensions at a time from rows padded by 16 bytes; the
+// weights lie over the keys.  Two blocks an SM: one loads while the other
+// computes.  The products bound it.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;
+constexpr int kSimtCtasPerSM = 2;
 
 template <int HD, int MR>
 struct SimtLayout {
   static constexpr int LD = HD + 4, PLD = kSimtKeys + 4;
-  static constexpr int Q = 0, K = Q + MR * LD, V = K + kSimtKeys * LD, P = V + kSimtKeys * HD, LIVE = P + MR * PLD;
-  static constexpr int BYTES = (LIVE + kSimtKeys) * 4;
+  static constexpr int Q = 0, K = Q + MR * LD, V = K + kSimtKeys * LD, SLOTS = V + kSimtKeys * HD;
+  static constexpr int BYTES = (SLOTS + 2 * kSimtKeys) * 4;
+  static_assert(MR * PLD <= kSimtKeys * LD, "weights over the keys");
+  static_assert(kSimtCtasPerSM * (BYTES + 2048) <= 227 * 1024, "two blocks an SM");
 };
 
-__device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
-  return fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, fmaf(x.x, y.x, s))));
-}
-__device__ __forceinline__ void axpy4(float (&o)[4], float p, float4 v) {
-  o[0] = fmaf(p, v.x, o[0]);
-  o[1] = fmaf(p, v.y, o[1]);
-  o[2] = fmaf(p, v.z, o[2]);
-  o[3] = fmaf(p, v.w, o[3]);
-}
-
-template <typename T, int HD, int MR>
-__global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __grid_constant__ CacheRowsArgs a) {
+template <int HD, int MR>
+__global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSM) cache_rows_simt_kernel(const __grid_constant__ CacheRowsArgs a) {
   using Lay = SimtLayout<HD, MR>;
-  constexpr int RPT = MR / 16, KPT = kSimtKeys / 16, CPT = HD / 64;
+  constexpr int RPT = MR / 16, KPT = kSimtKeys / 16, CPT = HD / 64, COLS = HD / 4;
   extern __shared__ __align__(16) float sm[];
-  float *sq = sm + Lay::Q, *sk = sm + Lay::K, *sv = sm + Lay::V, *sp = sm + Lay::P;
-  int* live = reinterpret_cast<int*>(sm + Lay::LIVE);
+  float *sq = sm + Lay::Q, *sk = sm + Lay::K, *sv = sm + Lay::V, *sp = sk;
+  uint32_t* slots = reinterpret_cast<uint32_t*>(sm + Lay::SLOTS);  // of two blocks in turn
   const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys, 1, {1, 1}};
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (!a.tail_ml) pdl_wait();  // beside the tail's kernel, which has waited for everything before it
@@ -251,57 +247,74 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
   bool empties;
   const bool ok = rows_plan<kSimtThreads>(a, sh, walk, &empties);
   if (tid == 0) a.joins[blockIdx.x].n = 0;
-  if (ok) rows_empties<T, HD, kSimtThreads>(a, empties);
+  if (ok) rows_empties<float, HD, kSimtThreads>(a, empties);
   else rows_refused(a);
   RowsPart p;
   SeqRows q;
   walk.start(sh);
   while (walk.next(a, sh, p, q)) {
-    __syncthreads();  // the last part's queries are read
-    for (int i = tid; i < MR * HD / 4; i += kSimtThreads) {
-      const int r = i / (HD / 4), d = i % (HD / 4) * 4, v = p.v0 + r;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < p.nv)
-        x = load4<T>(static_cast<const T*>(a.q) + (int64_t)(q.row0 + v / a.group) * a.ld_q +
-                     (int64_t)(p.kvh * a.group + v % a.group) * HD + d);
-      *reinterpret_cast<float4*>(sq + r * Lay::LD + d) = x;
-    }
-    float o[RPT][CPT][4], m[RPT], l[RPT];
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int c = 0; c < CPT; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
-    }
-#pragma unroll 1
-    for (int b = p.b0; b < p.b1; ++b) {
-      __syncthreads();  // the last block's keys, values and weights are read
-      for (int i = tid; i < kSimtKeys * HD / 4; i += kSimtThreads) {
-        const int r = i / (HD / 4), d = i % (HD / 4) * 4, j = b * kSimtKeys + r;
+    auto look = [&](int b) {  // slots of block b
+      if (tid < kSimtKeys) {
+        const int j = b * kSimtKeys + tid;
         uint32_t slot = ~0u;
         if (j < q.len) {
           slot = entry_slot32(a.table, entry_of(a, q.s, j), j);
           if (slot == ~0u) cache_error(a.err, kCacheBadPage);
         }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (slot != ~0u) {
-          const int64_t at = ((int64_t)slot * a.nkv + p.kvh) * HD + d;
-          x = load4<T>(static_cast<const T*>(a.k) + at);
-          y = load4<T>(static_cast<const T*>(a.v) + at);
-        }
-        *reinterpret_cast<float4*>(sk + r * Lay::LD + d) = x;
-        *reinterpret_cast<float4*>(sv + r * HD + d) = y;
-        if (d == 0) live[r] = slot != ~0u;
+        slots[(b & 1) * kSimtKeys + tid] = slot;
       }
+    };
+    __syncthreads();  // the last part's queries and slots are read
+    look(p.b0);
+    for (int i = tid; i < MR * COLS; i += kSimtThreads) {
+      const int r = i / COLS, d = i % COLS * 4, v = p.v0 + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < p.nv)
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (int64_t)(q.row0 + v / a.group) * a.ld_q +
+                                             (int64_t)(p.kvh * a.group + v % a.group) * HD + d);
+      *reinterpret_cast<float4*>(sq + r * Lay::LD + d) = x;
+    }
+    Two o[RPT][CPT][2];
+    float m[RPT], l[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) o[i][c][0] = o[i][c][1] = two(0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int b = p.b0; b < p.b1; ++b) {
+      __syncthreads();  // the last block's values and weights are read, this one's slots written
+      const uint32_t* slot = slots + (b & 1) * kSimtKeys;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // keys, then values: so many loads in flight together
+        const float* pool = static_cast<const float*>(h ? a.v : a.k) + (int64_t)p.kvh * HD;
+        constexpr int PER = kSimtKeys * COLS / kSimtThreads;
+        float4 x[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int i = tid + k * kSimtThreads;
+          const uint32_t at = slot[i / COLS];
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (at != ~0u) x[k] = *reinterpret_cast<const float4*>(pool + (int64_t)at * a.nkv * HD + i % COLS * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int i = tid + k * kSimtThreads;
+          *reinterpret_cast<float4*>((h ? sv + i / COLS * HD : sk + i / COLS * Lay::LD) + i % COLS * 4) = x[k];
+        }
+      }
+      if (b + 1 < p.b1) look(b + 1);
+      bool live[KPT];
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) live[k] = slot[tx + 16 * k] != ~0u;
       __syncthreads();
-      float s[RPT][KPT];
+      Two s2[RPT][KPT];
 #pragma unroll
       for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int k = 0; k < KPT; ++k) s[i][k] = 0.f;
+        for (int k = 0; k < KPT; ++k) s2[i][k] = two(0.f, 0.f);
 #pragma unroll 4
       for (int d = 0; d < HD; d += 4) {
         float4 x[RPT], y[KPT];
@@ -312,15 +325,18 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-          for (int k = 0; k < KPT; ++k) s[i][k] = dot4(x[i], y[k], s[i][k]);
+          for (int k = 0; k < KPT; ++k)
+            s2[i][k] = fma2(two(x[i].z, x[i].w), two(y[k].z, y[k].w), fma2(two(x[i].x, x[i].y), two(y[k].x, y[k].y), s2[i][k]));
       }
+      __syncthreads();  // the keys are read: the weights go over them
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
-        float top = m[i];
+        float s[KPT], top = m[i];
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-          s[i][k] = live[tx + 16 * k] ? s[i][k] * a.scale_log2 : -INFINITY;
-          top = fmaxf(top, s[i][k]);
+          const float2 x = both(s2[i][k]);
+          s[k] = live[k] ? (x.x + x.y) * a.scale_log2 : -INFINITY;
+          top = fmaxf(top, s[k]);
         }
 #pragma unroll
         for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
@@ -329,14 +345,16 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
         l[i] *= f;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-          const float w = ex2((s[i][k] - base) - kRowsRoom);
+          const float w = ex2((s[k] - base) - kRowsRoom);
           l[i] += w;
           sp[(ty * RPT + i) * Lay::PLD + tx + 16 * k] = w;
         }
+        const Two ff = two(f, f);
 #pragma unroll
-        for (int c = 0; c < CPT; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
+        for (int c = 0; c < CPT; ++c) {
+          o[i][c][0] = o[i][c][0] * ff;
+          o[i][c][1] = o[i][c][1] * ff;
+        }
       }
       __syncwarp();  // a warp's two ty read only their own weights
 #pragma unroll 2
@@ -345,18 +363,18 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
 #pragma unroll
         for (int i = 0; i < RPT; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (ty * RPT + i) * Lay::PLD + j);
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) {
-          float4 v[4];
+        for (int c = 0; c < CPT; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float4*>(sv + (j + e) * HD + 64 * c + 4 * tx);
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + (j + e) * HD + 64 * c + 4 * tx);
+            const Two v0 = two(v.x, v.y), v1 = two(v.z, v.w);
 #pragma unroll
-          for (int i = 0; i < RPT; ++i) {
-            axpy4(o[i][c], w[i].x, v[0]);
-            axpy4(o[i][c], w[i].y, v[1]);
-            axpy4(o[i][c], w[i].z, v[2]);
-            axpy4(o[i][c], w[i].w, v[3]);
+            for (int i = 0; i < RPT; ++i) {
+              const float x = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+              o[i][c][0] = fma2(two(x, x), v0, o[i][c][0]);
+              o[i][c][1] = fma2(two(x, x), v1, o[i][c][1]);
+            }
           }
-        }
       }
     }
     const bool cut = is_cut(p);
@@ -371,13 +389,14 @@ __global__ void __launch_bounds__(kSimtThreads) cache_rows_simt_kernel(const __g
       if (r >= p.nv) continue;
 #pragma unroll
       for (int c = 0; c < CPT; ++c) {
-        const float4 y = make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+        const float2 y0 = both(o[i][c][0]), y1 = both(o[i][c][1]);
+        const float4 y = make_float4(y0.x, y0.y, y1.x, y1.y);
         if (cut)
           *part_at<HD, MR>(a, slot, 16 * c + tx, r) = y;
         else if (a.tail_ml)
           *reinterpret_cast<float4*>(a.whole_o + at * HD + 64 * c + 4 * tx) = y;
         else
-          rows_finish<T, HD>(a, q.row0 + t, h, 64 * c + 4 * tx, y, m[i], l[i]);
+          rows_finish<float, HD>(a, q.row0 + t, h, 64 * c + 4 * tx, y, m[i], l[i]);
       }
       if (cut && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
       if (a.tail_ml && tx == 0 && p.b0 == 0) a.whole_ml[at] = make_float2(m[i], cut ? kRowCut : l[i]);
@@ -391,24 +410,25 @@ cudaError_t join_rows(cudaStream_t st, const CacheRowsArgs& a, int sm_count) {
   return launch_pdl(st, dim3(4 * sm_count), dim3(kRowsJoinThreads), 0, 1, cache_rows_join_kernel<T, HD, ROWS>, a);
 }
 
-template <typename T, int HD, int MR>
+template <int HD, int MR>
 cudaError_t simt_rows(cudaStream_t st, CacheRowsArgs a, int sm_count) {
   a.least = 1;
-  cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD, MR>::BYTES, 1,
-                             cache_rows_simt_kernel<T, HD, MR>, a);
-  return e == cudaSuccess ? join_rows<T, HD, MR>(st, a, sm_count) : e;
+  const cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD, MR>::BYTES, 1,
+                                   cache_rows_simt_kernel<HD, MR>, a);
+  return e == cudaSuccess ? join_rows<float, HD, MR>(st, a, sm_count) : e;
 }
 
 template <int HD>
 cudaError_t allow_simt() {
-  return cudaFuncSetAttribute(cache_rows_simt_kernel<float, HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(cache_rows_simt_kernel<HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               SimtLayout<HD, 64>::BYTES);
 }
 
 }  // namespace
 
-int cache_rows_ctas(int sm_count) {
-  return kRowsCtasPerSM * sm_count < kRowsMaxCtas ? kRowsCtasPerSM * sm_count : kRowsMaxCtas;
+int cache_rows_ctas(int sm_count, int bf16) {
+  const int n = (bf16 ? 1 : kSimtCtasPerSM) * sm_count;
+  return n < kRowsMaxCtas ? n : kRowsMaxCtas;
 }
 int cache_rows_slot_rows(int bf16) { return bf16 ? kTcTileRows : 64; }
 
@@ -420,7 +440,7 @@ cudaError_t prepare_cache_rows() {
 }
 
 cudaError_t launch_cache_rows(cudaStream_t st, const CacheRowsArgs& a, int bf16, int hd, int sm_count) {
-  if (!bf16) return hd == 128 ? simt_rows<float, 128, 64>(st, a, sm_count) : simt_rows<float, 64, 64>(st, a, sm_count);
+  if (!bf16) return hd == 128 ? simt_rows<128, 64>(st, a, sm_count) : simt_rows<64, 64>(st, a, sm_count);
   const cudaError_t e = launch_cache_rows_tc(st, a, hd);
   if (e != cudaSuccess) return e;
   return hd == 128 ? join_rows<__nv_bfloat16, 128, kTcTileRows>(st, a, sm_count)

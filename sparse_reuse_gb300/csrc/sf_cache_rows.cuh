@@ -8,7 +8,6 @@ namespace sf {
 namespace rows {
 
 constexpr float kRowsRoom = 27.f;
-constexpr int kRowsCtasPerSM = 1;
 constexpr int kRowsMaxCtas = 512;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
