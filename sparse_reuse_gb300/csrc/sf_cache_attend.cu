@@ -998,6 +998,72 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
 }
 
+// The same as cache_attend_kernel's STATE form for short sequences: a segment to
+// `w` warps (1, 2 or 4), without a plan.  Blocks of four warps, two an SM.
+// (cache_attend_kernel goes through a block's segments one after another, 6 us
+// each where its 8 warps share one: 53 us for 127 sequences of up to 701 keys, 8
+// heads; with a warp a segment 39, as long as the longest takes it, with two
+// 26.)
+constexpr int kTailWarps = 4;
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(32 * kTailWarps, 2) cache_tails_kernel(const __grid_constant__ CacheAttendArgs a, const int w) {
+  using Warp = typename WarpOf<T, HD, NT>::type;
+  constexpr int NH = Warp::kHeads, ROW = Warp::kRow;
+  constexpr bool F32 = sizeof(T) == 4;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float2 sml[kTailWarps][NH];
+  __shared__ __align__(16) float sq[F32 ? kTailWarps : 1][F32 ? NH * HD : 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / w, first = team * w;  // of the team's warps
+  unsigned char* mine = smem + warp * Warp::kBytes;
+  pdl_wait();
+  pdl_trigger();
+  const int x = blockIdx.x * (kTailWarps / w) + team;
+  if (x >= a.S * a.heads) return;  // whole teams
+  Segment g;
+  g.s = x / a.heads;
+  const int hs = x - g.s * a.heads;
+  g.kvh = hs / a.nsub;
+  const int sub = hs - g.kvh * a.nsub;
+  g.h0 = g.kvh * a.group + sub * NH;
+  g.nh = min(NH, a.group - sub * NH);
+  bool bad;
+  g.len = checked_len(__ldcg(a.lens + g.s), a.limit, &bad);
+  if (bad && lane == 0) cache_error(a.err, kCacheBadLength);
+  float* q = sq[F32 ? warp : 0];
+  auto queries = [&]() {
+    if constexpr (F32) {
+      for (int i = lane; i < NH * HD; i += 32)
+        q[i] = i < g.nh * HD ? static_cast<const float*>(a.q)[(int64_t)g.s * a.ld_q + (int64_t)g.h0 * HD + i] : 0.f;
+    }
+    __syncwarp();
+  };
+  Warp one;
+  one.template run<false>(a, g, mine, q, queries, warp - first, w, tiles_of(g.len), lane);
+  __syncwarp();
+  one.store(reinterpret_cast<float*>(mine), sml[warp], lane);
+  if (w > 1)
+    tc::named_bar_sync(1 + team, 32 * w);
+  else
+    __syncwarp();
+  for (int i = (warp - first) * 32 + lane; i < g.nh * HD / 4; i += 32 * w) {
+    const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+    float top = sml[first][h].x;
+    for (int y = 1; y < w; ++y) top = fmaxf(top, sml[first + y][h].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int y = 0; y < w; ++y) {
+      const float4 z = *reinterpret_cast<const float4*>(smem + (first + y) * Warp::kBytes + (h * ROW + d) * 4);
+      const float f = part_factor(sml[first + y][h].x, top);
+      o = make_float4(o.x + z.x * f, o.y + z.y * f, o.z + z.z * f, o.w + z.w * f);
+      l += sml[first + y][h].y * f;
+    }
+    write_out<T, true>(a, g.s, g.h0 + h, HD, d, o, inverse(l));
+    if (d == 0) write_stats<true>(a, g.s, g.h0 + h, top, l);
+  }
+}
+
 // weights_out[s][c][j] = weights_in + the group's normalised weights of key j.
 // Blocks take units of kWeightKeys keys of one (sequence, KV head) in turn.
 constexpr int kWeightThreads = 256;
@@ -1046,6 +1112,10 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __g
   if (!waited) pdl_wait();
 }
 
+// Tiles of the longest sequence for each of a segment's warps, for every segment that an SM gets, up to which tails go
+// by warps: a warp takes 0.4 to 0.9 us a tile, a block some 6 us a segment.
+constexpr int kTailTiles = 16;
+
 template <typename T, int HD, int NT>
 constexpr int ring_bytes() {
   return kWarps * WarpOf<T, HD, NT>::type::kBytes;
@@ -1054,11 +1124,20 @@ constexpr int ring_bytes() {
 template <typename T, int HD, int NT>
 cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   const int most_blocks = cache_attend_blocks(sm_count);
-  constexpr int NH = WarpOf<T, HD, NT>::type::kHeads;
+  using Warp = typename WarpOf<T, HD, NT>::type;
+  constexpr int NH = Warp::kHeads;
   const int G = a.nq / a.nkv, longest = tiles_of((int)a.limit);
   a.group = G;
   a.nsub = (G + NH - 1) / NH;
   a.heads = a.nkv * a.nsub;
+  if (a.state_o) {
+    const int64_t segments = (int64_t)a.S * a.heads;
+    int w = 1;
+    while (w < kTailWarps && longest > 4 * w && segments * 2 * w <= 16 * (int64_t)sm_count) w *= 2;
+    if (longest <= kTailTiles * w * (segments > sm_count ? segments / sm_count : 1))
+      return launch_pdl(st, dim3((unsigned)((segments * w + kTailWarps - 1) / kTailWarps)), dim3(32 * kTailWarps),
+                        kTailWarps * Warp::kBytes, 1, cache_tails_kernel<T, HD, NT>, a, w);
+  }
   const int blocks = attend_blocks((int64_t)a.S * a.heads * longest, most_blocks);
   a.blocks = blocks;
   a.join = may_need_join(longest, a.heads, blocks);
@@ -1086,6 +1165,9 @@ cudaError_t allow_smem() {
   for (auto kernel : {cache_attend_kernel<T, HD, NT, true, false>, cache_attend_kernel<T, HD, NT, false, false>,
                       cache_attend_kernel<T, HD, NT, false, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(cache_tails_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTailWarps * WarpOf<T, HD, NT>::type::kBytes);
   return e;
 }
 
