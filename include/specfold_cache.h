@@ -232,7 +232,9 @@ sf_status sf_cache_attend_rows(sf_cache* cache, void* stream, const void* q, int
  * A prefix and a sequence's own positions may hold up to max_len each.
  * Arithmetic, checks and workspace as for sf_cache_attend (own positions) and
  * sf_cache_attend_rows (prefixes); the two are joined in fp32.
- * Errors: as for sf_cache_attend_rows, S taking the place of T; G < 1. */
+ * Errors: as for sf_cache_attend_rows, S taking the place of T;
+ * SF_ERR_INVALID_ARG for G < 1, SF_ERR_SHAPE for G > 65536 (there may be more
+ * groups than sequences: empty ones). */
 sf_status sf_cache_attend_shared(sf_cache* cache, void* stream, const void* q, int64_t ld_q, const void* k_pages,
                                  const void* v_pages, int64_t n_pages, const int32_t* page_table, int S,
                                  int table_cols, int64_t ld_table, const int32_t* lens, const int32_t* prefix_table,

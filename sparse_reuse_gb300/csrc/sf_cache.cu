@@ -221,7 +221,7 @@ sf_status check_object(sf_cache* c) {
 }
 
 sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages, const int32_t* table, int S,
-                      int cols, int64_t ld) {
+                      int cols, int64_t ld, int most) {
   if (!k || !v || !table) return fail(c, SF_ERR_INVALID_ARG, "null pool or page table");
   if (misaligned(k, 16) || misaligned(v, 16) || misaligned(table, 4))
     return fail(c, SF_ERR_INVALID_ARG, "pools need 16-byte alignment, page tables 4-byte");
@@ -231,8 +231,13 @@ sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages
   // slots are 32-bit in the kernels, the last value meaning none
   if (n_pages > 4294967294ll / c->s.page_size)
     return fail(c, SF_ERR_SHAPE, "n_pages=%lld pages of %d positions", (long long)n_pages, c->s.page_size);
-  if (S > c->s.max_seqs) return fail(c, SF_ERR_SHAPE, "S=%d beyond the object's %d sequences", S, c->s.max_seqs);
+  if (S > most) return fail(c, SF_ERR_SHAPE, "S=%d beyond the object's %d sequences", S, most);
   return SF_OK;
+}
+
+sf_status check_table(sf_cache* c, const void* k, const void* v, int64_t n_pages, const int32_t* table, int S,
+                      int cols, int64_t ld) {
+  return check_table(c, k, v, n_pages, table, S, cols, ld, c->s.max_seqs);
 }
 
 int64_t scores_ld(const sf_cache_shapes& s) { return ((int64_t)s.max_len + 3) / 4 * 4; }
@@ -586,7 +591,9 @@ sf_status sf_cache_attend_shared(sf_cache* c, void* stream, const void* q, int64
   if ((st = check_rows(c, q, ld_q, S, scale, out, ld_out, lse)) != SF_OK) return st;
   if ((st = check_table(c, k_pages, v_pages, n_pages, page_table_, S, table_cols, ld_table)) != SF_OK) return st;
   if (G < 1) return fail(c, SF_ERR_INVALID_ARG, "G=%d groups", G);
-  if ((st = check_table(c, k_pages, v_pages, n_pages, prefix_table, G, prefix_cols, ld_prefix)) != SF_OK) return st;
+  if (G > kMaxGroups) return fail(c, SF_ERR_SHAPE, "G=%d groups", G);
+  if ((st = check_table(c, k_pages, v_pages, n_pages, prefix_table, G, prefix_cols, ld_prefix, kMaxGroups)) != SF_OK)
+    return st;
   if ((st = check_gather(c, n_pages)) != SF_OK) return st;
   if (!lens || !prefix_lens || !starts || misaligned(lens, 4) || misaligned(prefix_lens, 4) || misaligned(starts, 4))
     return fail(c, SF_ERR_INVALID_ARG, "lens, prefix_lens or starts null or misaligned");

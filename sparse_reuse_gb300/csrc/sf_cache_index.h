@@ -16,6 +16,7 @@ namespace sf {
 constexpr int kMaxLen = 262144;      // positions of a sequence
 constexpr int kMaxPageSize = 65536;
 constexpr int kMaxCallRows = 1048576;  // rows of a call
+constexpr int kMaxGroups = 65536;      // groups of one
 
 // One page table: entry (s, c) is the page of positions c * page_size ...
 struct PageTable {

@@ -273,7 +273,7 @@ TURN = dict(k=16, n_pages=9, page_table=16, S=4, cols=4, ld_table=4, lens=16, fr
     ("attend_rows", ROWS, dict(S=-1), 1, "S=-1"), ("attend_rows", ROWS, dict(cols=0), 1, "table_cols"),
     ("attend_shared", SHARED, dict(q=8), 1, "q/out"), ("attend_shared", SHARED, dict(S=5), 2, "S=5"),
     ("attend_shared", SHARED, dict(S=-1), 1, "-1 rows"), ("attend_shared", SHARED, dict(G=0), 1, "G=0"),
-    ("attend_shared", SHARED, dict(G=5), 2, "S=5"), ("attend_shared", SHARED, dict(ptable=None), 1, "table"),
+    ("attend_shared", SHARED, dict(G=65537), 2, "G=65537"), ("attend_shared", SHARED, dict(ptable=None), 1, "table"),
     ("attend_shared", SHARED, dict(pcols=0), 1, "table_cols"), ("attend_shared", SHARED, dict(ld_ptable=3), 1, "ld_table"),
     ("attend_shared", SHARED, dict(plens=None), 1, "prefix_lens"), ("attend_shared", SHARED, dict(starts=None), 1, "starts"),
     ("attend_shared", SHARED, dict(plens=18), 1, "prefix_lens"), ("attend_shared", SHARED, dict(out=16), 1, "out overlaps q"),

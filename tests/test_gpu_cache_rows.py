@@ -363,6 +363,10 @@ SHARED = [
     ((16, 1, 128), "bf16", 48, [17, 16], [1500, 20000], 0, 1, [50] * 33 + [0]),
     ((28, 4, 128), "bf16", 16, [2, 2], [0, 0], 0, 0, [0, 9, 300, 0]),
     ((7, 7, 128), "bf16", 24, [300], [40], 0, 0, [1] * 300),
+    ((12, 2, 128), "bf16", 16, [0, 1, 0, 0, 1, 0, 0], [9, 300, 0, 4, 129, 1, 2], 0, 0, [3, 0]),
+    ((4, 2, 64), "f32", 16, [1] + [0] * 400, [70] * 401, 0, 0, [3]),
+    ((32, 8, 128), "bf16", 16, [40], [100], 0, 0, list(range(0, 1600, 40))),
+    ((4, 2, 64), "bf16", 16, [3], [50], 0, 0, [5000, 1, 300]),
 ]
 
 
@@ -376,7 +380,7 @@ def shared_inputs(sf, heads, dtype, page, members, prefixes, front, behind, tail
     blank_behind(k, both, list(tails) + list(prefixes), page, float("nan"))
     blank_behind(v, both, list(tails) + list(prefixes), page, float("inf"))
     q = (torch.from_numpy(rng.standard_normal((S, nq, hd)).astype(np.float32)) * 2).cuda().to(DT[dtype])
-    c = sf.PagedCache(n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=dtype, page_size=page, max_seqs=max(S, len(members)),
+    c = sf.PagedCache(n_q_heads=nq, n_kv_heads=nkv, head_dim=hd, dtype=dtype, page_size=page, max_seqs=S,
                       max_len=max(1, max(tails), max(prefixes)), max_rows=S)
     return dict(c=c, k=k, v=v, q=q, table=both[:S], ptable=both[S:], starts=offsets(members) + front, lens=list(tails),
                 plens=list(prefixes), page=page, members=members)
