@@ -1001,9 +1001,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 // The same as cache_attend_kernel's STATE form for short sequences: a segment to
 // `w` warps (1, 2 or 4), without a plan.  Blocks of four warps, two an SM.
 // (cache_attend_kernel goes through a block's segments one after another, 6 us
-// each where its 8 warps share one: 53 us for 127 sequences of up to 701 keys, 8
-// heads; with a warp a segment 39, as long as the longest takes it, with two
-// 26.)
+// each where its 8 warps share one.  127 sequences of up to 701 keys, 8 heads x
+// 128 bf16, from cold caches: 53 us so, 39 with a warp a segment, as long as the
+// longest takes it, 37 with two, which is what it gets; the whole call beside a
+// shared prefix 113, 102 and 98 in a stream.  Latency bounds it: a warp's loads
+// and products follow one another.)
 constexpr int kTailWarps = 4;
 
 template <typename T, int HD, int NT>

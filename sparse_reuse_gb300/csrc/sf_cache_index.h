@@ -284,10 +284,10 @@ struct RowsTiles {
   }
 };
 
-// The thread blocks that share a tile: those in which its first and last blocks start.
-SF_HD int rows_first_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0, per); }
+// Thread blocks share a tile from the one in which its first block starts (whose part begins with block 0) to the one
+// in which its last does.
 SF_HD int rows_last_cta(const RowsPart& p, int64_t per) { return (int)quotient(p.u0 + (int64_t)p.cost * (p.nb - 1), per); }
-// (The first is the one whose part begins with block 0.)  The partial slot of thread block `cta` for a cut tile.
+// The partial slot of thread block `cta` for a cut tile.
 SF_HD int rows_slot(int cta, bool first) { return 2 * cta + (first ? 1 : 0); }
 
 }  // namespace sf

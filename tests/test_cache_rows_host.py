@@ -138,7 +138,7 @@ int walk(const int* rows, const int* lens, int S, int group, int nkv, int half, 
       const RowsPart p = t.take(sh, end);
       if (p.b0 < p.b1) {
         if (n == room) return ~n;
-        out[n++] = Part{c, s, p.kvh, p.v0, p.nv, p.w, p.nb, p.b0, p.b1, rows_first_cta(p, per), rows_last_cta(p, per),
+        out[n++] = Part{c, s, p.kvh, p.v0, p.nv, p.w, p.nb, p.b0, p.b1, (int)(p.u0 / per), rows_last_cta(p, per),
                         rows_slot(c, p.b0 == 0)};
       }
     }

@@ -213,6 +213,53 @@ def test_reposition_reports(sf):
     c.close()
 
 
+def test_reposition_far_and_replayed(sf):
+    """Differences up to the largest, captured on a side stream and replayed with other positions and lengths; turned
+    back, a key is what it was but for two roundings."""
+    far, page, hd = 4194304, 16, 64
+    rng = np.random.default_rng(3)
+    c = sf.PagedCache(n_q_heads=2, n_kv_heads=1, head_dim=hd, dtype="f32", page_size=page, max_seqs=2, max_len=40,
+                      max_pos=far, rotary_dim=16)
+    table, total = make_pages(rng, [40, 40], page)
+    first = pool(rng, total, page, 1, hd, "f32")
+    k, t, lens = first.clone(), i32(table), i32([40, 40])
+    frm, to = (torch.zeros((2, 1, 40), dtype=torch.int32, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        c.reposition(k, t, lens, frm, pos_to=to)
+    freq = oc.frequencies(16, 10000.0)
+    for n in ([40, 40], [40, 0], [1, 33]):
+        f, x = rng.integers(0, far, (2, 2, 1, 40))
+        f[:, :, 0], x[:, :, 0] = 0, far - 1                          # the largest difference
+        for a, b in ((frm, f), (to, x)):
+            a.copy_(i32(b))
+        lens.copy_(i32(n))
+        k.copy_(first)
+        g.replay()
+        c.sync()
+        want = f64(first).reshape(-1, hd)
+        tol = np.zeros_like(want)
+        for s in range(2):
+            j = np.arange(n[s])
+            slot = table[s, j // page] * page + j % page
+            old = want[slot]
+            want[slot] = oc.turn(old[:, None], (x - f)[s, 0, j][:, None], freq, "half")[:, 0]
+            tol[slot, :16] = (8 * U * pair_sums(old, 16, "half") * (1 + U) + U * np.abs(want[slot]))[:, :16]
+        got = f64(k).reshape(-1, hd)
+        assert np.all(np.abs(got - want) <= tol)
+        frm.copy_(i32(x))
+        to.copy_(i32(f))
+        g.replay()
+        c.sync()
+        # back: the first error carried over (a rotation keeps lengths: of a and b together), the same again
+        back = np.abs(f64(k) - f64(first)).reshape(-1, hd)
+        sums = pair_sums(f64(first).reshape(-1, hd), 16, "half")[:, :16]
+        assert np.all(back[:, :16] <= 4 * 9 * U * sums) and not back[:, 16:].any()
+    c.close()
+
+
 def test_evicted_context_becomes_a_prefix(sf):
     """append, attend with weights, evict into dense pages, reposition: keys rotated at 0..budget-1, which the
     verification pass reads; the pass's own oracle on those keys agrees with it."""

@@ -264,6 +264,43 @@ def test_rows_share_pages_and_long_pools(sf):
     a["c"].close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [1, 4, 7, 8, 16, 17])
+def test_rows_smallest_pools(sf, dtype, page):
+    """A pool of one page: fewer positions than a load takes together."""
+    for n in {1, page}:
+        a = rows_inputs(sf, (4, 2, 64), dtype, page, [1, 70], [n, 0])
+        a["k"], a["v"] = (a[x][int(a["table"][0, 0])][None].contiguous() for x in ("k", "v"))
+        a["table"] = np.zeros_like(a["table"])
+        a["lens"] = [n, n]
+        out, lse = run_rows(a)
+        a["c"].sync()
+        check_rows(a, out, lse, dtype)
+        a["c"].close()
+
+
+def test_rows_largest_call(sf):
+    """1,048,576 rows: queries and outputs past 2^31 elements."""
+    rows = [5, 2 ** 20 - 105, 100]
+    a = rows_inputs(sf, (33, 3, 64), "bf16", 16, [1, 1, 1], [70, 33, 200], behind=0)
+    a["c"].close()
+    T = sum(rows)
+    a["q"] = torch.randn((T, 33, 64), device="cuda", dtype=torch.bfloat16)
+    a["starts"] = offsets(rows)
+    a["c"] = sf.PagedCache(n_q_heads=33, n_kv_heads=3, head_dim=64, dtype="bf16", page_size=16, max_seqs=3, max_len=200,
+                           max_rows=T)
+    out, lse = run_rows(a)
+    a["c"].sync()
+    for s, at in ((0, 0), (1, 5), (1, 500000), (1, T - 100 - 64), (2, T - 100), (2, T - 36)):
+        at = slice(at, at + (5 if s == 0 else 36))
+        check(a, (s, at), a["q"][at], out[at], lse[at], places(a["table"], s, a["lens"][s], 16), 64 ** -0.5, "bf16")
+    a["c"].close()
+    with pytest.raises(sf.SpecFoldError) as e:
+        sf.PagedCache(n_q_heads=33, n_kv_heads=3, head_dim=64, dtype="bf16", page_size=16, max_seqs=3, max_len=200,
+                      max_rows=T + 1)
+    assert e.value.status == sf.SF_ERR_UNSUPPORTED
+
+
 def test_rows_report_bad_lengths_pages_and_starts(sf):
     heads, page = (12, 2, 128), 16
     a = rows_inputs(sf, heads, "bf16", page, [30, 40, 5], [100, 50, 70])
@@ -551,6 +588,64 @@ def test_shared_in_graphs(sf):
             check_shared(dict(a, q=q, lens=[i + 1] * 9), out, lse, "bf16")
     a["c"].sync()
     a["c"].close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_largest_batches(sf, dtype):
+    """As many sequences and groups as an object takes: most groups empty, most prefixes unused."""
+    S, G = 4096, 65536
+    rng = np.random.default_rng(11)
+    members = np.zeros(G, np.int64)
+    members[np.sort(rng.choice(G, 300, replace=False))] = 13
+    members[-1] = S - 3 - members[:-1].sum()
+    used = np.flatnonzero(members)
+    prefixes = rng.integers(0, 60, G)
+    tails = rng.integers(0, 20, S)
+    a = shared_inputs(sf, (4, 2, 64), dtype, 16, members[used].tolist(), prefixes[used].tolist(), 1, 2, tails.tolist())
+    wide = np.full((G, a["ptable"].shape[1]), -1, np.int32)              # groups of none: pages never looked at
+    wide[used] = a["ptable"]
+    prefixes[members == 0] = np.minimum(prefixes[members == 0], a["c"].shapes.max_len)
+    a.update(ptable=wide, plens=prefixes.tolist(), starts=offsets(members) + 1)
+    out, lse = run_shared(a)
+    a["c"].sync()
+    some = np.r_[0, 1, 2, np.arange(13, 4096, 97), 4093, 4094, 4095]
+    group = np.searchsorted(a["starts"], np.arange(S), side="right") - 1
+    for s in some:
+        g = group[s]
+        pre = places(wide, g, int(prefixes[g]), 16) if 0 <= g < G else np.zeros(0, np.int64)
+        check(a, s, a["q"][s:s + 1], out[s:s + 1], lse[s:s + 1], np.r_[pre, places(a["table"], s, int(tails[s]), 16)],
+              64 ** -0.5, dtype)
+    assert torch.isfinite(out).all()
+    a["c"].close()
+
+
+def test_shared_beside_other_calls(sf):
+    """Two objects on two streams at once, and calls of one object that share its workspace one after another."""
+    a = shared_inputs(sf, (12, 2, 128), "bf16", 16, [5, 4], [900, 200], 1, 0, [30] * 9 + [2000])
+    b = shared_inputs(sf, (8, 8, 64), "bf16", 16, [70], [300], 0, 0, [9] * 70)
+    want = [run_shared(x) for x in (a, b)]
+    one = a["c"].attend(a["q"], a["k"], a["v"], i32(a["table"]), i32(a["lens"]))
+    rows = a["c"].attend_rows(a["q"], a["k"], a["v"], i32(a["ptable"]), i32(a["plens"]), i32(a["starts"]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            x = run_shared(a)
+            y = a["c"].attend(a["q"], a["k"], a["v"], i32(a["table"]), i32(a["lens"]))
+            z = a["c"].attend_rows(a["q"], a["k"], a["v"], i32(a["ptable"]), i32(a["plens"]), i32(a["starts"]))
+            w = run_shared(a)
+        with torch.cuda.stream(streams[1]):
+            got.append((x, y, z, w, run_shared(b), run_shared(b)))
+    torch.cuda.synchronize()
+    members = slice(int(a["starts"][0]), int(a["starts"][-1]))
+    for x, y, z, w, u, v in got:
+        for p, q in ((x, want[0]), (w, want[0]), (u, want[1]), (v, want[1])):
+            assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+        assert torch.equal(y, one) and torch.equal(z[members], rows[members])
+    for x in (a, b):
+        x["c"].sync()
+        x["c"].close()
 
 
 def test_many_calls_in_a_row(sf):
