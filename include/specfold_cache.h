@@ -1,6 +1,7 @@
 /*
  * specfold_cache.h — committed context as a paged key-value cache: what writes
- * it, reads it for one new token, and keeps it inside its capacity.
+ * it, reads it for one new token, for blocks of rows and for batches that share
+ * prefixes, keeps it inside its capacity, and moves its keys to new positions.
  *
  * sf_verify (specfold.h) reads the committed context of every request as
  * prefix keys (already rotary-encoded) and values, shared by all branches
@@ -23,10 +24,12 @@
  * sf_cache_attend and sf_cache_evict are a decode loop of their own beside
  * that pass.  The rows that append takes and the queries come from the
  * caller's own projections; the weights that evict goes by come from attend.
- * What an eviction leaves is read by attend, not by sf_verify: the kept keys
- * stay rotated at their original positions, lie at the front of buffers of the
- * old length and may differ in number from sequence to sequence, while
- * sf_verify takes dense keys of positions 0..P-1 with one P for all requests.
+ * sf_verify takes dense keys rotated at positions 0..P-1 with one P for all
+ * requests.  What an eviction leaves becomes that in two steps: evict to pages
+ * that are such a buffer (of P = budget positions, where every sequence had at
+ * least as many), then sf_cache_reposition with its `kept` positions, since
+ * the kept keys stay rotated at their original ones.  The object's rotation
+ * must be sf_verify's own then (the options' defaults).
  *
  * sf_cache_attend and sf_cache_evict plan their launches for the longest
  * sequence that the call could hold, min(max_len, table_cols * page_size)
@@ -47,16 +50,19 @@
  * a time, all work enqueued on the caller's stream (which belongs to the
  * object's device, the current one of the call), nothing allocated and no
  * synchronisation, so every call can be captured into a CUDA graph.
- * sf_cache_attend uses the object's workspace: attend calls (and replays of
- * graphs that captured them) that may run at the same time need an object
- * each; the other two calls keep nothing in the object.
+ * sf_cache_attend, sf_cache_attend_rows and sf_cache_attend_shared use the
+ * object's workspace: such calls (and replays of graphs that captured them)
+ * that may run at the same time need an object each; append, evict and
+ * reposition keep nothing in the object.
  *
  * Device-side checks: a page id outside [0, n_pages), a length or position
  * outside its range never becomes an access.  What the offending row or
  * sequence would have written is described with each call; the other rows and
  * sequences are not affected, and the check is reported as
  * SF_ERR_DEVICE_ASSERT by sf_cache_sync_status and by later calls on the
- * object, until sf_cache_sync_status clears it.
+ * object, until sf_cache_sync_status clears it.  A wait inside a kernel that
+ * does not end within 2 s is reported the same way; the outputs of that call
+ * are undefined.
  */
 #ifndef SPECFOLD_CACHE_H
 #define SPECFOLD_CACHE_H
@@ -87,7 +93,7 @@ typedef struct sf_cache_shapes {
 } sf_cache_shapes;
 
 /* Create a cache object on the current CUDA device: the rotary table (angles
- * in double) and the workspace of sf_cache_attend; the pools stay the
+ * in double) and the workspaces of the attend calls; the pools stay the
  * caller's.  Synchronous.
  * Errors: SF_ERR_INVALID_ARG (null pointer, a non-positive size, bad dtype,
  * negative eps, rope_theta not above 0), SF_ERR_UNSUPPORTED (head_dim not
@@ -205,13 +211,16 @@ sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t 
  *            they do not ascend so, nothing is written (device check).
  *   out      device [T] rows likewise, ld_out apart; not overlapping q.
  *   lse      device fp32 [T, n_q_heads] or NULL; not overlapping q or out.
- * Products and sums are fp32.
+ * Products and sums are fp32.  In bf16, softmax weights enter their product
+ * with the values rounded to bf16 where more than 128 query vectors (rows times
+ * query heads of a KV head) go together, half a step of 2^-8 each, and as the
+ * sum of two bf16 numbers (2^-16) where fewer do.
  * The rest as for sf_cache_attend: what else is in the batch changes results
  * by rounding only, the same call gives the same bits; NaN and infinities;
  * lengths and pages out of range.  The workspace is the object's.
  * Errors: as above; SF_ERR_INVALID_ARG for an object without max_rows, a scale
  * as for sf_cache_attend, overlapping outputs; SF_ERR_SHAPE for T beyond
- * max_rows. */
+ * max_rows and, in bf16, for pools of more than 2147483646 positions. */
 sf_status sf_cache_attend_rows(sf_cache* cache, void* stream, const void* q, int64_t ld_q, int T, const void* k_pages,
                                const void* v_pages, int64_t n_pages, const int32_t* page_table, int S, int table_cols,
                                int64_t ld_table, const int32_t* lens, const int32_t* starts, float scale, void* out,
