@@ -22,12 +22,16 @@
 // there is nothing to wait for, and the tensor core's queue is short (one warp
 // for both took 3,700 cycles for a block of two halves).  The two issue in turns:
 // left alone they fall into step, both softmaxes and then both products at once
-// (4,200 cycles).  So a block of two halves takes some 2,950 cycles, 2,048 of
+// (4,200 cycles).  So a block of two halves takes some 3,000 cycles, 2,048 of
 // them the tensor core's (128 dimensions): what is left is a half's softmax
 // (1,690, of which 512 are the exponentials at 32 a cycle) and its products' round
 // trips, a chain that two halves cannot hide altogether.  16 ragged sequences of
-// up to 1,021 rows over up to 8,191 keys, 32/8 heads: 518 us a call (62 % of the
-// cuBLAS rate); 4 of 288 rows over 4,096, 40/8 heads: 102 (50 %).
+// up to 1,021 rows over up to 8,191 keys, 32/8 heads: 518 to 530 us a call (61 %
+// of the cuBLAS rate); 4 of 288 rows over 4,096, 40/8 heads: 102 (50 %).  Scores of
+// both halves in one region of TMEM, so that a half's next scores come before its
+// product, take 2,700 cycles a block where the keys are in L2, but large calls are
+// no faster (1,280 TFLOP/s back to back either way), 4 of 288 rows 97, and a batch
+// with shared prefixes 99 instead of 98.
 //
 // P enters the second product of a wide tile rounded to bf16, half a step of 2^-8
 // a weight, the output type's own: a second product for the remainder would cost
