@@ -26,7 +26,7 @@
 // them the tensor core's (128 dimensions): what is left is a half's softmax
 // (1,690, of which 512 are the exponentials at 32 a cycle) and its products' round
 // trips, a chain that two halves cannot hide altogether.  16 ragged sequences of
-// up to 1,021 rows over up to 8,191 keys, 32/8 heads: 518 to 530 us a call (61 %
+// up to 1,021 rows over up to 8,191 keys, 32/8 heads: 518 to 540 us a call (61 %
 // of the cuBLAS rate); 4 of 288 rows over 4,096, 40/8 heads: 102 (50 %).  Scores of
 // both halves in one region of TMEM, so that a half's next scores come before its
 // product, take 2,700 cycles a block where the keys are in L2, but large calls are

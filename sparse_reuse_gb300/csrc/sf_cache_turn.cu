@@ -8,7 +8,7 @@
 namespace sf {
 namespace {
 
-// 4 x 4,096 places of 8 heads x 128 bf16, and 1,024 of 2 heads: 16.5 and 2.5 us so; 32 places and 256 threads 17.3 and
+// 4 x 4,096 places of 8 heads x 128 bf16, and 1,024 of 2 heads: 15.7 to 16.5 and 2.5 us so; 32 places and 256 threads 17.3 and
 // 3.1, 16 and 256 17.0 and 2.4, 2 and 128 17.6 and 2.7.
 constexpr int kTurnThreads = 128;
 constexpr int kTurnPlaces = 4;  // places of a sequence that a block takes at a time
