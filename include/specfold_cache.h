@@ -212,9 +212,10 @@ sf_status sf_cache_attend(sf_cache* cache, void* stream, const void* q, int64_t 
  *   out      device [T] rows likewise, ld_out apart; not overlapping q.
  *   lse      device fp32 [T, n_q_heads] or NULL; not overlapping q or out.
  * Products and sums are fp32.  In bf16, softmax weights enter their product
- * with the values rounded to bf16 where more than 128 query vectors (rows times
- * query heads of a KV head) go together, half a step of 2^-8 each, and as the
- * sum of two bf16 numbers (2^-16) where fewer do.
+ * with the values as the sum of two bf16 numbers (2^-16).  Only where the
+ * tensor core bounds the call, more than 128 query vectors (rows times query
+ * heads of a KV head) that go together, with more than two blocks of 256 of
+ * them and 128 keys for each SM, are they rounded to one, half a step of 2^-8.
  * The rest as for sf_cache_attend: what else is in the batch changes results
  * by rounding only, the same call gives the same bits; NaN and infinities;
  * lengths and pages out of range.  The workspace is the object's.

@@ -34,8 +34,13 @@
 // with shared prefixes 99 instead of 98.
 //
 // P enters the second product of a wide tile rounded to bf16, half a step of 2^-8
-// a weight, the output type's own: a second product for the remainder would cost
-// half as much again where the tensor core is the bound.
+// a weight, the output type's own, in calls that give a thread block more than
+// two of its blocks (kTcExact): the product for the remainder costs 16 ragged
+// sequences of up to 1,021 rows 535 -> 700 us, 4 of 288 rows 102 -> 124, a ragged
+// batch with shared prefixes 98 -> 112, 288 rows over 1,024 to 4,096 keys 10 to
+// 18 %.  Smaller calls wait for latency, not the tensor core: P is the sum of two
+// bf16 numbers there too, for 2 to 7 % (32 rows over 512 keys, 12/2 heads 15.2 ->
+// 15.6 us; over 4,096 keys, 40/8 heads 20.4 -> 21.7).
 //
 // Warps: 0-3 softmax and epilogue of half 0, 4-7 of half 1, 8 and 9 the MMAs of
 // the halves (8 owns TMEM), 10 keys, 11 values.  Warp 10 also walks along the
@@ -64,6 +69,7 @@ constexpr int kTcHalf = 128;   // query vectors of a half
 constexpr int kTcKeys = 128;   // keys of a block
 // Units of a tile, and of a block of it with one half and with two.
 constexpr int kTcFixed = 24, kTcNarrow = 5, kTcWide = 6, kTcLeast = 6;
+constexpr int kTcExact = 2 * kTcWide;  // units a thread block up to which wide tiles keep P as two numbers
 constexpr int kLiveRing = 8;   // blocks whose masks of live keys are kept
 constexpr float kSlack = 8.f;
 constexpr int kMmaWarp = 8, kKeyWarp = 10, kValueWarp = 11;
@@ -96,6 +102,7 @@ struct Barriers {
 struct TcPart {
   int nb;        // 0: nothing more
   int wide;      // two halves
+  int split;     // P as the sum of two bf16 numbers
   int nv;        // query vectors
   int kvh;
   int t0, rem;   // row and head (within the KV head) of its first vector
@@ -231,6 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       waits_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1);
       const TcPart& p = ring_of_parts[x % kPartRing];
       const int nb = __shfl_sync(kFull, *dead ? 0 : p.nb, 0), wide = __shfl_sync(kFull, p.wide, 0);
+      const int split = __shfl_sync(kFull, p.split, 0);
       if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
       if (nb == 0) break;
       const Share share = share_of(nb, wide, w);
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: two groups of V, 8 columns of P
             tc::mma_bf16_ts_by(leader, o_at, s_at + kk * 8, va + (uint64_t)((kk * 2 * Lay::GROUP) >> 4), idesc_o,
                                i > 0 || kk > 0 ? 1u : 0u);
-          if (!wide)
+          if (split)
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
               tc::mma_bf16_ts_by(leader, o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2 * Lay::GROUP) >> 4), idesc_o, 1u);
@@ -315,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           TcPart n{};
           if (more) {
             const int r = (int)quick_quotient(p.v0, a.group);
-            n = TcPart{p.b1 - p.b0, p.w == 2, p.nv, p.kvh, q.row0 + r, p.v0 - r * a.group,
+            n = TcPart{p.b1 - p.b0, p.w == 2, p.w == 1 || walk.per <= kTcExact, p.nv, p.kvh, q.row0 + r, p.v0 - r * a.group,
                        is_cut(p) ? rows_slot(blockIdx.x, p.b0 == 0) : -1, q.s, q.len, p.b0};
           }
           slot_of = n;
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         l += x.x + x.y;
         ++steps;
       };
-      if (wide) {
+      if (!p.split) {
 #pragma unroll 1
         for (int i = 0; i < share.n; ++i) step(i, std::false_type());
       } else {

@@ -1,6 +1,6 @@
 """How many bits of a softmax weight the bf16 forms of attend_rows and
 attend_shared keep: 2^-16 (the sum of two bf16 numbers) for tiles of up to 128
-query vectors.
+query vectors, and for larger ones in calls of little work.
 
 The tolerance is that of test_gpu_cache_rows.py with 2^-16 in the place of
 2^-8 (u = 2^-24, e = 2^-8 the half step of the output):
@@ -92,7 +92,17 @@ NARROW = [
 ]
 
 
-@pytest.mark.parametrize("heads,page,rows,lens,apart", NARROW)
+# More vectors together, two blocks of 256 of them and 128 keys at most for each SM.
+SMALL = [
+    ((12, 2, 128), 32, [32], [512], 5),
+    ((40, 8, 128), 32, [32], [20], 0),
+    ((40, 8, 128), 16, [52, 26], [700, 9], 6),
+    ((4, 2, 64), 5, [100, 65, 129], [17, 257, 5], 6),
+    ((16, 1, 128), 100, [40], [2000], 4),
+]
+
+
+@pytest.mark.parametrize("heads,page,rows,lens,apart", NARROW + SMALL)
 def test_the_bound_tells_one_bf16_number_from_two(heads, page, rows, lens, apart):
     q, k, v, table = inputs(heads, lens, rows, page, 1, apart)
     st, one, two = offsets(rows), [], []
@@ -114,8 +124,8 @@ def rows_of(sf, q, k, v, table, lens, rows, page):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("heads,page,rows,lens,apart", NARROW)
-def test_narrow_tiles_keep_two(sf, heads, page, rows, lens, apart):  # noqa: F811
+@pytest.mark.parametrize("heads,page,rows,lens,apart", NARROW + SMALL)
+def test_rows_keep_two(sf, heads, page, rows, lens, apart):  # noqa: F811
     q, k, v, table = inputs(heads, lens, rows, page, 1, apart)
     q, k, v = q.cuda(), k.cuda(), v.cuda()
     out, st = rows_of(sf, q, k, v, table, lens, rows, page), offsets(rows)
@@ -127,8 +137,8 @@ def test_narrow_tiles_keep_two(sf, heads, page, rows, lens, apart):  # noqa: F81
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,members,prefix,tail,apart", [((12, 2, 128), 21, 9, 3, 0), ((40, 8, 128), 25, 300, 70, 6),
-                                                             ((4, 2, 64), 64, 700, 1, 5)])
-def test_shared_prefixes_of_small_groups_keep_two(sf, heads, members, prefix, tail, apart):  # noqa: F811
+                                                             ((4, 2, 64), 64, 700, 1, 5), ((32, 8, 128), 61, 400, 9, 6)])
+def test_shared_prefixes_keep_two(sf, heads, members, prefix, tail, apart):  # noqa: F811
     nq, nkv, hd = heads
     page, lens = 16, [tail] * members + [prefix]
     q, k, v, table = inputs(heads, lens, [1] * members + [0], page, 2, apart)
