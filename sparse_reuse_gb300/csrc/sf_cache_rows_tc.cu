@@ -422,19 +422,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         const uint32_t to = sq + q_place(row);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
                      "l"(from + (int64_t)(t0 + t) * a.ld_q + (v - t * a.group) * HD),
-                     "r"(row < nv && q_sign != 0 ? 16 : 0)
+                     "r"(row < nv ? 16 : 0)
                      : "memory");
       }
       return true;
     };
     auto queries_there = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (q_sign < 0) {
+      if (q_sign <= 0) {
+        const __nv_bfloat162 sign = __float2bfloat162_rn((float)q_sign);
+        auto times = [&](uint32_t x) {  // exact; 0 times NaN or infinity is NaN
+          const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), sign);
+          return *reinterpret_cast<const uint32_t*>(&y);
+        };
 #pragma unroll 1
         for (int k = 0; k < CH; ++k) {
           const int row = qr + k * (128 / CH);
           uint4* u = reinterpret_cast<uint4*>(base + Lay::Q + w * Lay::STAGE + q_place(row));
-          *u = make_uint4(u->x ^ 0x80008000u, u->y ^ 0x80008000u, u->z ^ 0x80008000u, u->w ^ 0x80008000u);
+          *u = make_uint4(times(u->x), times(u->y), times(u->z), times(u->w));
         }
       }
       tc::fence_proxy_async_smem();
@@ -684,8 +689,8 @@ cudaError_t rows_tc(cudaStream_t st, CacheRowsArgs a) {
         !make_tmap_pool_run(&maps.box[i], pool, HD, a.nkv, slots, run))
       return cudaErrorInvalidValue;
   }
-  // a negative scale turns the queries' signs, 0 makes them 0: the maximum of
-  // the scaled scores is then that of the scores
+  // a negative scale turns the queries' signs, 0 makes them 0 (NaN and infinite
+  // ones NaN): the maximum of the scaled scores is then that of the scores
   const int sign = a.scale_log2 > 0.f ? 1 : a.scale_log2 < 0.f ? -1 : 0;
   a.scale_log2 = sign == 0 ? 1.f : fabsf(a.scale_log2);
   a.least = kTcLeast;

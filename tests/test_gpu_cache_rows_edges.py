@@ -1,0 +1,54 @@
+"""attend_rows and attend_shared on calls at the edge of what their
+documentation allows (needs a GB300).  Tolerances are test_gpu_cache_rows.py's."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_cache import DT, i32, sf  # noqa: F401
+from test_gpu_cache_rows import check, check_rows, places, rows_inputs, run_rows, run_shared, shared_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [3, 90, 300])
+def test_rows_of_scale_zero_keep_nan_and_infinite_queries(sf, dtype, rows):  # noqa: F811
+    """0 times a NaN or infinite score is NaN; finite queries get the values' mean."""
+    a = rows_inputs(sf, (4, 2, 64), dtype, 16, [rows, 2], [300, 40])
+    a["q"][1, 0, 5] = torch.nan
+    a["q"][rows - 1, 3, 63] = torch.inf
+    a["q"][rows, 2, 0] = -torch.inf
+    bad = torch.zeros(a["q"].shape[:2], dtype=torch.bool, device="cuda")
+    bad[1, 0] = bad[rows - 1, 3] = bad[rows, 2] = True
+    out, lse = run_rows(a, scale=0.0)
+    a["c"].sync()
+    live = slice(0, rows + 2)
+    assert torch.equal(~torch.isfinite(out[live]).any(-1), bad[live])
+    assert torch.equal(torch.isnan(out[live]).all(-1), bad[live]) and torch.equal(torch.isnan(lse[live]), bad[live])
+    clean = a["q"].clone()
+    clean[bad] = 0.0
+    out[bad], lse[bad] = (t[bad] for t in run_rows(dict(a, q=clean), scale=0.0))
+    check_rows(dict(a, q=clean), out, lse, dtype, scale=0.0)
+    a["c"].close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("members", [4, 80])
+def test_shared_of_scale_zero_keeps_nan_queries(sf, dtype, members):  # noqa: F811
+    """Whether or not a sequence has positions of its own."""
+    tails = [7 * (s % 2) for s in range(members)]
+    a = shared_inputs(sf, (4, 2, 64), dtype, 16, [members], [100], 0, 0, tails)
+    bad = torch.zeros(a["q"].shape[:2], dtype=torch.bool, device="cuda")
+    for s, h, x in ((0, 1, torch.nan), (1, 2, torch.nan), (2, 0, torch.inf), (3, 3, -torch.inf)):
+        a["q"][s, h, 9] = x
+        bad[s, h] = True
+    out, lse = run_shared(a, scale=0.0)
+    a["c"].sync()
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(lse), bad)
+    q = a["q"].clone()
+    q[bad] = 0.0
+    for s in range(members):
+        if not bad[s].any():
+            slots = np.r_[places(a["ptable"], 0, 100, 16), places(a["table"], s, tails[s], 16)]
+            check(a, s, q[s:s + 1], out[s:s + 1], lse[s:s + 1], slots, 0.0, dtype)
+    a["c"].close()
