@@ -62,7 +62,7 @@
  * SF_ERR_DEVICE_ASSERT by sf_cache_sync_status and by later calls on the
  * object, until sf_cache_sync_status clears it.  A wait inside a kernel that
  * does not end within 2 s is reported the same way; the outputs of that call
- * are undefined.
+ * are undefined then, and nothing else is written.
  */
 #ifndef SPECFOLD_CACHE_H
 #define SPECFOLD_CACHE_H
@@ -303,6 +303,17 @@ sf_status sf_cache_evict(sf_cache* cache, void* stream, const void* k_pages, con
 /* Wait for the work on `stream` and report a device-side check that fired
  * (SF_ERR_DEVICE_ASSERT, once: it is cleared on return) or a CUDA error. */
 sf_status sf_cache_sync_status(sf_cache* cache, void* stream);
+
+/* Failure injection for tests of the detection path: in later calls of
+ * sf_cache_attend_rows and sf_cache_attend_shared on a bf16 object, one of the
+ * signals between the warps of a thread block (1..13, as CacheStallAt in
+ * csrc/sf_cache.h names them) is never complete.  Waits for it, and all others
+ * meanwhile, give up after 50 ms; the kernels end, with the outputs undefined,
+ * and the call is reported as described at the top.  0: no more.  A call that
+ * does not need the signal is not affected but for the 50 ms.  No GPU fault,
+ * trap or hang is involved.
+ * Errors: SF_ERR_INVALID_ARG (null object, another signal). */
+sf_status sf_cache_inject_stall(sf_cache* cache, int signal);
 
 /* Text of the last error recorded on this object (empty if none). */
 const char* sf_cache_last_error(const sf_cache* cache);

@@ -34,7 +34,7 @@ EXPORTS = ["sf_create", "sf_verify", "sf_set_debug", "sf_set_rho_dump", "sf_set_
            "sf_head_create", "sf_head_verify", "sf_head_last_error", "sf_head_destroy",
            "sf_cache_create", "sf_cache_append", "sf_cache_attend", "sf_cache_evict", "sf_cache_sync_status",
            "sf_cache_last_error", "sf_cache_destroy", "sf_cache_create_with", "sf_cache_reposition",
-           "sf_cache_attend_rows", "sf_cache_attend_shared"]
+           "sf_cache_attend_rows", "sf_cache_attend_shared", "sf_cache_inject_stall"]
 SF_ROTARY_HALVES, SF_ROTARY_NEIGHBOURS = 0, 1
 
 
@@ -125,6 +125,7 @@ def _load() -> ctypes.CDLL:
                                          vp, i64, vp]
     lib.sf_cache_attend_shared.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp, c_int, c_int, i64, vp, vp, c_int, c_int,
                                            i64, vp, vp, c_float, vp, i64, vp]
+    lib.sf_cache_inject_stall.argtypes = [vp, c_int]
     lib.sf_cache_sync_status.argtypes = [vp, vp]
     lib.sf_cache_last_error.argtypes = [vp]
     lib.sf_cache_last_error.restype = ctypes.c_char_p
@@ -341,6 +342,10 @@ def sf_cache_attend_shared(cache, stream, q, ld_q, k_pages, v_pages, n_pages, pa
                                       ld_table, lens, prefix_table, G, prefix_cols, ld_prefix, prefix_lens, starts,
                                       scale, out, ld_out, lse),
            None, "sf_cache_attend_shared", cache=cache)
+
+
+def sf_cache_inject_stall(cache, signal: int) -> None:
+    _check(lib.sf_cache_inject_stall(cache, signal), None, "sf_cache_inject_stall", cache=cache)
 
 
 def sf_cache_append(cache, stream, qkv, ld_qkv, T, q_gain, k_gain, index, pos, seq, page_table, S, table_cols,

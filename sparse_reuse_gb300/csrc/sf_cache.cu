@@ -313,6 +313,8 @@ CacheRowsArgs rows_args(const sf_cache* c, const void* q, int64_t ld_q, int T, f
   a.part_ml = c->row_ml;
   a.joins = c->row_joins;
   a.ctas = cache_rows_ctas(c->sm_count, c->s.dtype == SF_BF16);
+  a.wait_ns = c->stall == kStallNone ? 2000000000u : 50000000u;
+  a.stall = c->stall;
   a.err = c->err_dev;
   return a;
 }
@@ -699,6 +701,13 @@ sf_status sf_cache_sync_status(sf_cache* c, void* stream) {
   if (st == SF_ERR_DEVICE_ASSERT)
     for (int i = 0; i < kCacheErrWords; ++i) c->err[i] = 0;
   return st;
+}
+
+sf_status sf_cache_inject_stall(sf_cache* c, int signal) {
+  if (!c) return SF_ERR_INVALID_ARG;
+  if (signal < kStallNone || signal >= kStallEnd) return fail(c, SF_ERR_INVALID_ARG, "no signal %d", signal);
+  c->stall = signal;
+  return SF_OK;
 }
 
 const char* sf_cache_last_error(const sf_cache* c) { return c ? c->last_error : ""; }

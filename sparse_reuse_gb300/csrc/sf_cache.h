@@ -53,6 +53,7 @@ struct sf_cache {
   float2* tail_ml = nullptr;       // [max_rows][n_q_heads]
   float* whole_o = nullptr;        // the same of the prefixes
   float2* whole_ml = nullptr;
+  int stall = 0;                   // sf_cache_inject_stall
   unsigned* err = nullptr;    // [kCacheErrWords] pinned, written by the kernels through its device address
   unsigned* err_dev = nullptr;
   char last_error[256] = {0};
@@ -68,6 +69,12 @@ enum CacheErr { kCacheBadPage = 0, kCacheBadLength = 1, kCacheBadRow = 2, kCache
 __device__ __forceinline__ void cache_error(unsigned* err, CacheErr which) {
   *reinterpret_cast<volatile unsigned*>(err + which) = 1u;
 }
+
+// The signal between the warps of the rows kernel that sf_cache_inject_stall withholds.
+enum CacheStallAt {
+  kStallNone, kStallPart, kStallPartRead, kStallQueries, kStallKeys, kStallKeysRead, kStallValues, kStallValuesRead,
+  kStallScores, kStallWeights, kStallLateWeights, kStallTurn, kStallOutputs, kStallMeet, kStallEnd
+};
 
 struct CacheAppendArgs {
   const void* qkv; int64_t ld_qkv;
@@ -143,6 +150,8 @@ struct CacheRowsArgs {
   float* parts; float2* part_ml;
   RowsJoin* joins;         // [ctas]
   int ctas, least;         // thread blocks; units that each takes at least
+  uint32_t wait_ns;        // what a wait inside the kernel takes at most
+  int stall;               // CacheStallAt
   unsigned* err;
 };
 int cache_rows_ctas(int sm_count, int bf16);

@@ -96,6 +96,7 @@ struct Barriers {
   uint64_t part_full[kPartRing], part_empty[kPartRing];
   uint64_t meet;  // of both softmax groups
   uint64_t turn[2];  // whose MMAs come next
+  uint64_t drain[2];  // after a stall: a half's MMAs so far are done
 };
 
 // What a thread block does next: blocks b0 .. b0 + nb - 1 of a tile.
@@ -110,36 +111,47 @@ struct TcPart {
   int s, len, b0;
 };
 
-// Bounded wait: after 2 s without the phase, or once another wait of the block
-// has given up, it returns; the call is reported as stalled.
-__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
-  if (tc::mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = tc::globaltimer_ns();
-  while (!tc::mbar_try_wait(bar, parity)) {
-    if (*dead) return;
-    if (tc::globaltimer_ns() - t0 > 2000000000ull) {
-      *dead = 1;
-      cache_error(err, kCacheStall);
-      return;
-    }
-  }
-}
+// Waits are bounded.  One that gives up (limit_ns without its phase, or another
+// wait of the block has given up) returns false, and the call is reported as
+// stalled.  Who gets false leaves its loops there and then: it issues, loads,
+// stores and arrives nothing more, so that a wait that returns true has seen
+// what it waited for, and everybody else's waits end as well.  What is in flight
+// by then, copies and products, is waited for at the end of the kernel.
+struct Waits {
+  volatile int* dead;
+  unsigned* err;
+  uint32_t limit_ns;
 
-// Until the loads of block `b` of a ring have been issued.  A reader that skips
-// blocks (the other half's, in narrow tiles) may come to a stage two phases
-// early, where the phase's parity alone would let it through.
-__device__ __forceinline__ void wait_issued(volatile uint32_t* issued, uint32_t b, volatile int* dead, unsigned* err) {
-  if (*issued > b) return;
-  const uint64_t t0 = tc::globaltimer_ns();
-  while (*issued <= b) {
-    if (*dead) return;
-    if (tc::globaltimer_ns() - t0 > 2000000000ull) {
-      *dead = 1;
-      cache_error(err, kCacheStall);
-      return;
+  template <typename Ready>
+  __device__ __forceinline__ bool until(Ready ready) const {
+    if (ready()) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!ready()) {
+      if (*dead) return false;
+      if (tc::globaltimer_ns() - t0 > limit_ns) {
+        *dead = 1;
+        cache_error(err, kCacheStall);
+        return false;
+      }
+    }
+    return true;
+  }
+  __device__ __forceinline__ bool phase(uint64_t* bar, uint32_t parity) const {
+    return until([&]() { return tc::mbar_try_wait(bar, parity); });
+  }
+  // The loads of block `b` of a ring have been issued.  A reader that skips
+  // blocks (the other half's, in narrow tiles) may come to a stage two phases
+  // early, where the phase's parity alone would let it through.
+  __device__ __forceinline__ bool load(volatile uint32_t* issued, uint32_t b) const {
+    return until([&]() { return *issued > b; });
+  }
+  // By whole warps, for copies and products, which end by themselves.
+  __device__ __forceinline__ void drained(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer_ns() - t0 < limit_ns) {
     }
   }
-}
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -176,31 +188,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   __shared__ uint32_t tmem_slot;
   __shared__ int dead_;
   __shared__ volatile uint32_t issued[2];  // blocks of keys, of values
-  volatile int* dead = &dead_;
+  const Waits waits{&dead_, a.err, a.wait_ns};
   unsigned char* base = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const RowsShape sh{a.group, a.nkv, kTcHalf, 2, kTcKeys, kTcFixed, {kTcNarrow, kTcWide}};
 
   if (tid == 0) {
+    // an injected stall: one arrival more than there are, which nothing makes
+    auto init = [&](uint64_t* b, int arrivals, CacheStallAt of) { tc::mbar_init(b, arrivals + (a.stall == of ? 1 : 0)); };
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bar.qfull[i], kTcHalf);
-      tc::mbar_init(&bar.sfull[i], 1);
-      tc::mbar_init(&bar.pfull[i][0], kTcHalf);
-      tc::mbar_init(&bar.pfull[i][1], kTcHalf);
-      tc::mbar_init(&bar.odone[i], 1);
-      tc::mbar_init(&bar.turn[i], 1);
+      init(&bar.qfull[i], kTcHalf, kStallQueries);
+      init(&bar.sfull[i], 1, kStallScores);
+      init(&bar.pfull[i][0], kTcHalf, kStallWeights);
+      init(&bar.pfull[i][1], kTcHalf, kStallLateWeights);
+      init(&bar.odone[i], 1, kStallOutputs);
+      init(&bar.turn[i], 1, kStallTurn);
+      tc::mbar_init(&bar.drain[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
-      tc::mbar_init(&bar.kfull[i], 1);
-      tc::mbar_init(&bar.kempty[i], 2);  // both halves, or one of them twice
-      tc::mbar_init(&bar.vfull[i], 1);
-      tc::mbar_init(&bar.vempty[i], 2);
+      init(&bar.kfull[i], 1, kStallKeys);
+      init(&bar.kempty[i], 2, kStallKeysRead);  // both halves, or one of them twice
+      init(&bar.vfull[i], 1, kStallValues);
+      init(&bar.vempty[i], 2, kStallValuesRead);
     }
     for (int i = 0; i < kPartRing; ++i) {
-      tc::mbar_init(&bar.part_full[i], 1);
-      tc::mbar_init(&bar.part_empty[i], 11);  // 8 softmax warps, 2 issuers, values
+      init(&bar.part_full[i], 1, kStallPart);
+      init(&bar.part_empty[i], 11, kStallPartRead);  // 8 softmax warps, 2 issuers, values
     }
-    tc::mbar_init(&bar.meet, 2 * kTcHalf);
+    init(&bar.meet, 2 * kTcHalf, kStallMeet);
     dead_ = 0;
     issued[0] = issued[1] = 0;
     tc::fence_barrier_init();
@@ -229,23 +244,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     const uint64_t dk = tc::sw128_kmajor_desc(base_u + Lay::K, Lay::GROUP);
     const uint64_t dv = tc::sw128_mnmajor_desc(base_u + Lay::V, 1024, Lay::GROUP);
     const uint32_t o_at = tmem_u + Lay::O_COL + w * HD, s_at = tmem_u + w * kTcKeys;
-    auto waits_for = [&](uint64_t* b, uint32_t parity) {
-      wait_for(b, parity, dead, a.err);
-      __syncwarp();
+    auto waits_for = [&](uint64_t* b, uint32_t parity) { return __all_sync(kFull, waits.phase(b, parity)); };
+    auto loaded = [&](int ring, uint32_t b, uint64_t* full) {
+      return waits.load(&issued[ring], b) && waits.phase(full, (b / ST) & 1);
     };
     uint32_t blocks = 0, parts = 0, steps = 0, turns = 0;  // so far: of the rings, of this half
     for (uint32_t x = 0;; ++x) {
-      waits_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1);
+      if (!waits_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1)) break;
       const TcPart& p = ring_of_parts[x % kPartRing];
-      const int nb = __shfl_sync(kFull, *dead ? 0 : p.nb, 0), wide = __shfl_sync(kFull, p.wide, 0);
+      const int nb = __shfl_sync(kFull, p.nb, 0), wide = __shfl_sync(kFull, p.wide, 0);
       const int split = __shfl_sync(kFull, p.split, 0);
       if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
       if (nb == 0) break;
       const Share share = share_of(nb, wide, w);
       auto scores = [&](int i) {
         const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
-        wait_issued(&issued[0], b, dead, a.err);
-        waits_for(&bar.kfull[st], (b / ST) & 1);
+        if (!__all_sync(kFull, loaded(0, b, &bar.kfull[st]))) return false;
         tc::fence_after_sync();
         const uint64_t ka = dk + (uint64_t)((st * Lay::STAGE) >> 4);
 #pragma unroll
@@ -256,22 +270,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         tc::mma_commit_by(leader, &bar.sfull[w]);
         tc::mma_commit_by(leader, &bar.kempty[st]);
         if (!wide) tc::mma_commit_by(leader, &bar.kempty[st]);
+        return true;
       };
       if (share.n > 0) {
-        waits_for(&bar.qfull[w], parts & 1);
+        if (!waits_for(&bar.qfull[w], parts & 1) || !scores(0)) break;
         ++parts;
-        scores(0);
       }
-      for (int i = 0; i < share.n; ++i, ++steps) {
+      int i = 0;
+      for (; i < share.n; ++i, ++steps) {
         const uint32_t b = blocks + share.first + share.step * i, st = b % ST;
-        wait_issued(&issued[1], b, dead, a.err);
-        waits_for(&bar.vfull[st], (b / ST) & 1);
         const uint64_t va = dv + (uint64_t)((st * Lay::STAGE) >> 4);
-        waits_for(&bar.pfull[w][0], steps & 1);
-        if (wide) waits_for(&bar.turn[w], (turns & 1) ^ (w == 0 ? 1 : 0));
+        bool alive = loaded(1, b, &bar.vfull[st]) && waits.phase(&bar.pfull[w][0], steps & 1) &&
+                     (!wide || waits.phase(&bar.turn[w], (turns & 1) ^ (w == 0 ? 1 : 0)));
+        if (!__all_sync(kFull, alive)) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (half) waits_for(&bar.pfull[w][1], steps & 1);
+          if (half && !(alive = waits_for(&bar.pfull[w][1], steps & 1))) break;
           tc::fence_after_sync();
 #pragma unroll
           for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: two groups of V, 8 columns of P
@@ -282,17 +296,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // what rounding P left
               tc::mma_bf16_ts_by(leader, o_at, s_at + 64 + kk * 8, va + (uint64_t)((kk * 2 * Lay::GROUP) >> 4), idesc_o, 1u);
         }
+        if (!alive) break;
         tc::mma_commit_by(leader, &bar.vempty[st]);
         if (!wide) tc::mma_commit_by(leader, &bar.vempty[st]);
-        if (i + 1 < share.n)
-          scores(i + 1);
-        else
+        if (i + 1 == share.n)
           tc::mma_commit_by(leader, &bar.odone[w]);
+        else if (!scores(i + 1))
+          break;
         if (wide) {
-          if (lane == 0) tc::mbar_arrive(&bar.turn[w ^ 1]);
+          if (leader) tc::mbar_arrive(&bar.turn[w ^ 1]);
           ++turns;
         }
       }
+      if (i < share.n) break;
       blocks += nb;
     }
   } else if (warp == kKeyWarp || warp == kValueWarp) {
@@ -317,8 +333,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
       if (keys) {  // the walk
         RowsPart p;
         SeqRows q;
-        const bool more = walk.next(a, sh, p, q) && !*dead;
-        if (x >= kPartRing) wait_for(&bar.part_empty[x % kPartRing], (x / kPartRing - 1) & 1, dead, a.err);
+        const bool more = walk.next(a, sh, p, q);
+        const bool free = x < kPartRing || waits.phase(&bar.part_empty[x % kPartRing], (x / kPartRing - 1) & 1);
+        if (!__all_sync(kFull, free)) break;  // nothing goes over a part that is still read
         if (lane == 0) {
           TcPart n{};
           if (more) {
@@ -331,10 +348,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           if (more && is_cut(p) && p.b0 == 0) rows_record(a, p, q, walk.per);
         }
         __syncwarp();
-      } else {
-        wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+      } else if (!__all_sync(kFull, waits.phase(&bar.part_full[x % kPartRing], (x / kPartRing) & 1))) {
+        break;
       }
-      const int nb = *dead ? 0 : slot_of.nb, s = slot_of.s, len = slot_of.len, kvh = slot_of.kvh, b0 = slot_of.b0;
+      const int nb = slot_of.nb, s = slot_of.s, len = slot_of.len, kvh = slot_of.kvh, b0 = slot_of.b0;
       __syncwarp();
       if (!keys && lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
       if (__any_sync(kFull, nb == 0)) break;
@@ -347,7 +364,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         }
       };
       look(b0);
-      for (int b = b0; b < b0 + nb; ++b, ++blocks) {
+      int b = b0;
+      for (; b < b0 + nb; ++b, ++blocks) {
         int slot[4];
         uint32_t there = 0;
 #pragma unroll
@@ -363,18 +381,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
           }
         }
         if (b + 1 < b0 + nb) look(b + 1);
+        // the lane's run is there and in one piece (runs from 16 on lie within a page)
+        const int after = __shfl_down_sync(kFull, slot[0], 1);
+        const bool joined = there == 15u && slot[3] == slot[0] + 3 && (run > 8 || (lane & 1) || after == slot[0] + 4);
+        const bool whole = (__ballot_sync(kFull, joined) & peers) == peers;
         const uint32_t st = blocks % ST;
-        if (blocks >= ST) wait_for(&empty[st], (blocks / ST - 1) & 1, dead, a.err);
+        const bool free = blocks < ST || waits.phase(&empty[st], (blocks / ST - 1) & 1);
+        if (!__all_sync(kFull, free)) break;
         if (keys) reinterpret_cast<unsigned char*>(live[blocks % kLiveRing])[lane] = (unsigned char)there;
         __syncwarp();
         if (lane == 0) {
           tc::mbar_expect_tx(&full[st], Lay::STAGE);
           issued[keys ? 0 : 1] = blocks + 1;
         }
-        // the lane's run is there and in one piece (runs from 16 on lie within a page)
-        const int after = __shfl_down_sync(kFull, slot[0], 1);
-        const bool joined = there == 15u && slot[3] == slot[0] + 3 && (run > 8 || (lane & 1) || after == slot[0] + 4);
-        const bool whole = (__ballot_sync(kFull, joined) & peers) == peers;
+        __syncwarp();
         if (!whole) {
 #pragma unroll
           for (int y = 0; y < HD / 64; ++y)
@@ -388,14 +408,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         }
         __syncwarp();
       }
+      if (b < b0 + nb) break;
     }
-    // after a stall nothing waits for the last copies: they land before the block ends
-    if (*dead)
-      for (uint32_t b = blocks > ST ? blocks - ST : 0; b < blocks; ++b) {
-        const uint64_t t0 = tc::globaltimer_ns();
-        while (!tc::mbar_try_wait(&full[b % ST], (b / ST) & 1) && tc::globaltimer_ns() - t0 < 2000000000ull) {
-        }
-      }
   } else {
     const int w = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -410,11 +424,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     auto q_place = [&](int row) {
       return (row >> 3) * Lay::GROUP + (qc >> 3) * 1024 + (row & 7) * 128 + (((qc ^ row) & 7) << 4);
     };
-    auto fetch_queries = [&](uint32_t x) {
-      wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+    auto waits_for = [&](uint64_t* b, uint32_t parity) { return __all_sync(kFull, waits.phase(b, parity)); };
+    auto there = [&](uint32_t x) { return waits_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1); };
+    auto fetch_queries = [&](uint32_t x) {  // false: this group takes nothing of the part
       const TcPart& p = ring_of_parts[x % kPartRing];
       const int wide = p.wide, nv = p.nv - (wide ? w * kTcHalf : 0), t0 = p.t0, rem = p.rem + (wide ? w * kTcHalf : 0);
-      if (*dead || share_of(p.nb, wide, w).n == 0) return false;
+      if (share_of(p.nb, wide, w).n == 0) return false;
       const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)p.kvh * a.group * HD + qc * 8;
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
@@ -449,29 +464,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
     auto groups_meet = [&]() {  // not a bar.sync: a wait that ends
       tc::fence_before_sync();
       tc::mbar_arrive(&bar.meet);
-      wait_for(&bar.meet, meetings & 1, dead, a.err);
+      const bool ok = waits_for(&bar.meet, meetings & 1);
       ++meetings;
-      __syncwarp();
       tc::fence_after_sync();
+      return ok;
     };
-    if (fetch_queries(0)) queries_there();
-    for (uint32_t x = 0;; ++x) {
-      wait_for(&bar.part_full[x % kPartRing], (x / kPartRing) & 1, dead, a.err);
+    bool alive = there(0);
+    if (alive && fetch_queries(0)) queries_there();
+    for (uint32_t x = 0; alive; ++x) {
       const TcPart& p = ring_of_parts[x % kPartRing];
-      const int nb = *dead ? 0 : p.nb, wide = p.wide;
+      const int nb = p.nb, wide = p.wide;
       if (__any_sync(kFull, nb == 0)) break;
       const Share share = share_of(nb, wide, w);
       float m = -INFINITY, l = 0.f;
       auto step = [&](int i, auto split) {
         constexpr bool SPLIT = decltype(split)::value;  // P as two bf16 numbers
-        wait_for(&bar.sfull[w], steps & 1, dead, a.err);
+        const bool ok = waits.phase(&bar.sfull[w], steps & 1);
         __syncwarp();  // tensor-memory accesses are the whole warp's
         tc::fence_after_sync();
         const uint32_t* on = live[(blocks + share.first + share.step * i) % kLiveRing];
         const bool holes = on[lane >> 2] != 0x0f0f0f0fu;
         float s[128];
         tc::tmem_ld128(s_at, s);
-        if (__any_sync(kFull, holes)) {
+        if (__any_sync(kFull, holes || !ok)) {
+          if (__any_sync(kFull, !ok)) return false;
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const uint32_t word = on[x];
@@ -543,20 +559,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         const float2 x = both(sum[0] + sum[1]);
         l += x.x + x.y;
         ++steps;
+        return true;
       };
       if (!p.split) {
 #pragma unroll 1
-        for (int i = 0; i < share.n; ++i) step(i, std::false_type());
+        for (int i = 0; alive && i < share.n; ++i) alive = step(i, std::false_type());
       } else {
 #pragma unroll 1
-        for (int i = 0; i < share.n; ++i) step(i, std::true_type());
+        for (int i = 0; alive && i < share.n; ++i) alive = step(i, std::true_type());
       }
+      if (!alive) break;
       blocks += nb;
       // the next part's queries on their way, then on the tensor core while this part's results go out
+      if (!(alive = there(x + 1))) break;
       const bool next = fetch_queries(x + 1);
       if (share.n > 0) {
-        wait_for(&bar.odone[w], parts & 1, dead, a.err);
-        __syncwarp();
+        if (!waits_for(&bar.odone[w], parts & 1)) break;
         ++parts;
         tc::fence_after_sync();
       }
@@ -568,7 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
         float f0 = 1.f, f1 = 0.f;
         if (meet) {
           sml[w][r] = make_float2(m, l);
-          groups_meet();
+          if (!groups_meet()) break;
           const float2 y = sml[0][r], z = sml[1][r];
           const float top = fmaxf(y.x, z.x), b = top == -INFINITY ? 0.f : top;
           f0 = ex2(y.x - b);
@@ -657,9 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
             rows_out(u, static_cast<char*>(a.out) + c * 2, a.ld_out * 2, HD * 2);
           }
         }
-        if (meet) {  // both O are read before either group lets the next part begin
-          groups_meet();
-        }
+        if (meet && !groups_meet()) break;  // both O are read before either group lets the next part begin
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.part_empty[x % kPartRing]);
@@ -670,6 +686,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_rows_tc_kernel(const __gr
   if (a.tail_ml) pdl_wait();  // the join waits for this kernel only
   tc::fence_before_sync();
   __syncthreads();
+  if (dead_) {  // nobody waits any more, so this is the same for all
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      tc::mma_commit_by(tc::elect_one(), &bar.drain[warp - kMmaWarp]);  // the same lane as ever
+      waits.drained(&bar.drain[warp - kMmaWarp], 0);
+    } else if (warp == kKeyWarp || warp == kValueWarp) {
+      const uint32_t n = issued[warp - kKeyWarp];
+      for (uint32_t b = n > ST ? n - ST : 0; b < n; ++b)
+        waits.drained(&(warp == kKeyWarp ? bar.kfull : bar.vfull)[b % ST], (b / ST) & 1);
+    }
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
