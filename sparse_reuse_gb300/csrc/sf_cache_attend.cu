@@ -1114,10 +1114,6 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const __g
   if (!waited) pdl_wait();
 }
 
-// Tiles of the longest sequence for each of a segment's warps, for every segment that an SM gets, up to which tails go
-// by warps: a warp takes 0.4 to 0.9 us a tile, a block some 6 us a segment.
-constexpr int kTailTiles = 16;
-
 template <typename T, int HD, int NT>
 constexpr int ring_bytes() {
   return kWarps * WarpOf<T, HD, NT>::type::kBytes;
@@ -1134,9 +1130,7 @@ cudaError_t attend_t(cudaStream_t st, CacheAttendArgs a, int sm_count) {
   a.heads = a.nkv * a.nsub;
   if (a.state_o) {
     const int64_t segments = (int64_t)a.S * a.heads;
-    int w = 1;
-    while (w < kTailWarps && longest > 4 * w && segments * 2 * w <= 16 * (int64_t)sm_count) w *= 2;
-    if (longest <= kTailTiles * w * (segments > sm_count ? segments / sm_count : 1))
+    if (const int w = tail_warps(longest, segments, kTailWarps, sm_count))
       return launch_pdl(st, dim3((unsigned)((segments * w + kTailWarps - 1) / kTailWarps)), dim3(32 * kTailWarps),
                         kTailWarps * Warp::kBytes, 1, cache_tails_kernel<T, HD, NT>, a, w);
   }

@@ -141,6 +141,24 @@ SF_HD bool may_need_join(int longest_tiles, int heads, int blocks) {
   return (longest_tiles - 1) / kLeast + 2 > kInlineParts && blocks / heads + 2 > kInlineParts;
 }
 
+// Tails of a batch (sf_cache_attend_shared) without a plan: the warps (1, 2 or 4; at most `most`) that each segment gets
+// where the table lets a segment have up to `longest` tiles; 0: planned blocks by the real lengths instead.  A block
+// takes some 6 us a segment, a warp 0.6 us a tile, and a long segment among short ones is not shared out: so a warp may
+// get 16 tiles for every segment of an SM, but never more than kTailMost.  us by warps and by blocks, 8 KV heads x 128
+// bf16 (all of the longest length; random ones up to it; one of it, the others 50):
+//   8 x 700 keys       16.5, 16.4   16.3, 15.0   16.3, 14.5     128 x 2,048   167, 178   110, 115    45, 23
+//   36 x 700           22.4, 30.9   17.9, 25.6   16.9, 20.1     512 x 1,024   324, 343   180, 207    58, 45
+//   128 x 700          68.7, 78.2   45.1, 52.5   24.1, 23.0     512 x 4,096  1213, 1290  657, 689   158, 45
+//   512 x 700           229, 248     130, 147    48.7, 43.8     1,024, one of 32,768                1115, 90
+constexpr int kTailMost = 48, kTailLeast = 4;
+SF_HD int tail_warps(int longest, int64_t segments, int most, int sm_count) {
+  int w = 1;
+  while (w < most && longest > 4 * w && segments * 2 * w <= 16 * (int64_t)sm_count) w *= 2;
+  const int64_t share = 16 * segments / sm_count;
+  const int64_t tiles = share < kTailLeast ? kTailLeast : share > kTailMost ? kTailMost : share;
+  return longest <= tiles * w ? w : 0;
+}
+
 // -- line
 
 // Units in front of a block's work: what is left, from tile t0 on, of a short segment of an earlier block.

@@ -52,3 +52,19 @@ def test_shared_of_scale_zero_keeps_nan_queries(sf, dtype, members):  # noqa: F8
             slots = np.r_[places(a["ptable"], 0, 100, 16), places(a["table"], s, tails[s], 16)]
             check(a, s, q[s:s + 1], out[s:s + 1], lse[s:s + 1], slots, 0.0, dtype)
     a["c"].close()
+
+
+@pytest.mark.parametrize("heads,dtype,n,long", [((40, 8, 128), "bf16", 1024, 8192), ((12, 2, 128), "bf16", 36, 4096),
+                                                ((40, 8, 128), "bf16", 128, 700), ((8, 8, 64), "f32", 200, 1000)])
+def test_shared_one_long_tail_among_short_ones(sf, heads, dtype, n, long):  # noqa: F811
+    tails = [(50 * s + 1) % 51 for s in range(n)]
+    tails[n // 3] = long
+    a = shared_inputs(sf, heads, dtype, 32, [n - 2], [70], 1, 1, tails)
+    out, lse = run_shared(a)
+    a["c"].sync()
+    pre = places(a["ptable"], 0, 70, 32)
+    for s in (0, 1, 2, n // 3 - 1, n // 3, n // 3 + 1, n - 2, n - 1):
+        slots = np.r_[pre if 1 <= s < n - 1 else pre[:0], places(a["table"], s, tails[s], 32)]
+        check(a, s, a["q"][s:s + 1], out[s:s + 1], lse[s:s + 1], slots, heads[2] ** -0.5, dtype)
+    assert torch.isfinite(out).all()
+    a["c"].close()
