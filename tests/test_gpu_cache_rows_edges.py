@@ -68,3 +68,25 @@ def test_shared_one_long_tail_among_short_ones(sf, heads, dtype, n, long):  # no
         check(a, s, a["q"][s:s + 1], out[s:s + 1], lse[s:s + 1], slots, heads[2] ** -0.5, dtype)
     assert torch.isfinite(out).all()
     a["c"].close()
+
+
+@pytest.mark.parametrize("heads,page,members,prefix,tails", [
+    ((4, 2, 64), 16, 3, 50, [5000, 1, 300]),                  # chunks, joined by the last block to arrive
+    ((2, 1, 64), 24, 1, 70, [40000]),                         # cut over more blocks than that: the join kernel
+    ((12, 2, 128), 7, 2, 130, [30000, 9, 0]),
+    ((8, 8, 64), 16, 20, 33, [3000] + [40 * s for s in range(29)]),   # a line of short and cut segments
+    ((16, 1, 128), 100, 0, 10, [3000, 0, 2000]),              # a group of none
+])
+def test_shared_long_tails_in_fp32(sf, heads, page, members, prefix, tails):  # noqa: F811
+    """Own positions too many for a warp: planned blocks, as in bf16."""
+    behind = len(tails) - members
+    a = shared_inputs(sf, heads, "f32", page, [members], [prefix], 0, behind, tails)
+    out, lse = run_shared(a)
+    a["c"].sync()
+    for s, n in enumerate(tails):
+        pre = places(a["ptable"], 0, prefix, page)[:prefix if s < members else 0]
+        check(a, s, a["q"][s:s + 1], out[s:s + 1], lse[s:s + 1], np.r_[pre, places(a["table"], s, n, page)],
+              heads[2] ** -0.5, "f32")
+    o2, l2 = run_shared(a)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    a["c"].close()
