@@ -258,7 +258,8 @@ sf_status sf_cache_attend_shared(sf_cache* cache, void* stream, const void* q, i
  * already).  Computed in fp32, rounded once to dtype.
  *   pos_from, pos_to   device int32 [S, n_kv_heads, ld_pos]; pos_to NULL = the
  *            place i.  evict's `kept` is a pos_from where positions are
- *            places.  Where either is negative the key stays as it is.
+ *            places.  Where either is negative, or both are the same, the key
+ *            stays as it is.
  * What an eviction left in dense pages becomes so a prefix for sf_verify.
  * A sequence longer than ld_pos counts as out of range (nothing of it is
  * turned, device check), so does a position from max_pos on (that key stays).

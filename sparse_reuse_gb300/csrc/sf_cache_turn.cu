@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kTurnThreads) cache_turn_kernel(const __grid_c
         continue;
       }
       const int steps = to - from;
+      if (steps == 0) continue;  // the same key, to the bit
       T* key = static_cast<T*>(a.k) + (slot * a.nkv + c) * HD;
       const int c0 = NEIGHBOURS ? 2 * lane : lane, c1 = NEIGHBOURS ? 2 * lane + 1 : lane + lanes;
       uint4* p0 = reinterpret_cast<uint4*>(key + c0 * VEC);

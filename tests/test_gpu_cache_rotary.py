@@ -304,3 +304,40 @@ def test_evicted_context_becomes_a_prefix(sf):
     assert np.max(np.abs(got - ref).max(1) / np.maximum(np.abs(ref).max(1), 1e-6)) <= 1e-4
     ctx.close()
     c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_keys_that_keep_their_position_keep_their_bits(sf, dtype, layout):
+    """No rotation by nothing: not the rounding of a magnitude and its reciprocal, no NaN beside an infinite value; the
+    keys that do move are turned as ever."""
+    nkv, hd, page, n, magnitude = 2, 64, 16, 200, 1.3
+    rng = np.random.default_rng(8)
+    table, total = make_pages(rng, [n], page)
+    c = sf.PagedCache(n_q_heads=4, n_kv_heads=nkv, head_dim=hd, dtype=dtype, page_size=page, max_seqs=1, max_len=n,
+                      max_pos=5000, rotary_dim=48, rotary_layout=layout, rotary_magnitude=magnitude)
+    k = pool(rng, total, page, nkv, hd, dtype)
+    frm = np.tile(np.arange(n, dtype=np.int32), (1, nkv, 1))
+    moved = rng.random((nkv, n)) < 0.3
+    frm[0][moved] += rng.integers(1, 4000, int(moved.sum())).astype(np.int32)
+    slot = table[0, np.arange(n) // page] * page + np.arange(n) % page
+    flat = k.view(-1, nkv, hd)
+    for h in range(nkv):
+        for x, value in zip(np.flatnonzero(~moved[h])[:2], (np.inf, -0.0)):
+            flat[int(slot[x]), h, 5] = value
+    before, first = f64(k).reshape(-1, nkv, hd), k.clone()
+    for pos_to in (None, i32(np.tile(np.arange(n, dtype=np.int32), (1, nkv, 1)))):
+        k.copy_(first)
+        c.reposition(k, i32(table), i32([n]), i32(frm), pos_to=pos_to)
+        c.sync()
+        got, bits, same = f64(k).reshape(-1, nkv, hd), torch.int16 if dtype == "bf16" else torch.int32, first.clone()
+        for h in range(nkv):
+            at = slot[moved[h]]
+            x = before[at, h]
+            want = oc.turn(x[:, None], (np.arange(n)[moved[h]] - frm[0, h][moved[h]])[:, None], oc.frequencies(48, 10000.0),
+                           layout)[:, 0]
+            tol = 8 * U * pair_sums(x, 48, layout) * (1 + E[dtype]) + E[dtype] * np.abs(want)
+            assert np.all(np.abs(got[at, h] - want) <= tol)
+            same.view(-1, nkv, hd)[torch.as_tensor(at), h] = flat[torch.as_tensor(at), h]
+        assert torch.equal(k.view(bits), same.view(bits))
+    c.close()
