@@ -214,36 +214,39 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
 
 // ---- fp32: CUDA cores --------------------------------------------------------
 //
-// MR query vectors and blocks of 64 keys: thread (ty, tx) of 16 x 16 has
-// MR / 16 x 4 scores (vectors ty * MR / 16 .., keys tx, tx + 16, ...) and
-// MR / 16 x HD / 16 outputs (columns 4 tx .., 64 + 4 tx ..), in packed fp32.  The
+// 64 query vectors and blocks of 64 keys: thread (ty, tx) of 16 x 16 has
+// 4 x 4 scores (vectors 4 ty .., keys tx, tx + 16, ...) and
+// 4 x HD / 16 outputs (columns 4 tx .., 64 + 4 tx ..), in packed fp32.  The
 // scores' operands come 4 dimensions at a time from rows padded by 16 bytes; the
 // weights lie over the keys.  Two blocks an SM: one loads while the other
 // computes.  The products bound large calls: 36 TFLOP/s of the cores' 74 (27 with
 // scalar arithmetic and one block an SM), operands from shared memory being the
 // rest; 5 sequences of up to 33 rows over up to 1,999 keys, 4/2 heads x 64, take
-// 21.6 us with the join, some 5 us a block of keys and part.
+// 21.6 us with the join, some 5 us a block of keys and part.  A tile of fewer
+// vectors costs as much as a full one: one token of few heads a KV head reads its
+// keys at a fraction of the bandwidth that sf_cache_attend has.
+constexpr int kSimtRows = 64;
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;
 constexpr int kSimtCtasPerSM = 2;
 
-template <int HD, int MR>
+template <int HD>
 struct SimtLayout {
   static constexpr int LD = HD + 4, PLD = kSimtKeys + 4;
-  static constexpr int Q = 0, K = Q + MR * LD, V = K + kSimtKeys * LD, SLOTS = V + kSimtKeys * HD;
+  static constexpr int Q = 0, K = Q + kSimtRows * LD, V = K + kSimtKeys * LD, SLOTS = V + kSimtKeys * HD;
   static constexpr int BYTES = (SLOTS + 2 * kSimtKeys) * 4;
-  static_assert(MR * PLD <= kSimtKeys * LD, "weights over the keys");
+  static_assert(kSimtRows * PLD <= kSimtKeys * LD, "weights over the keys");
   static_assert(kSimtCtasPerSM * (BYTES + 2048) <= 227 * 1024, "two blocks an SM");
 };
 
-template <int HD, int MR>
+template <int HD>
 __global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSM) cache_rows_simt_kernel(const __grid_constant__ CacheRowsArgs a) {
-  using Lay = SimtLayout<HD, MR>;
-  constexpr int RPT = MR / 16, KPT = kSimtKeys / 16, CPT = HD / 64, COLS = HD / 4;
+  using Lay = SimtLayout<HD>;
+  constexpr int RPT = kSimtRows / 16, KPT = kSimtKeys / 16, CPT = HD / 64, COLS = HD / 4;
   extern __shared__ __align__(16) float sm[];
   float *sq = sm + Lay::Q, *sk = sm + Lay::K, *sv = sm + Lay::V, *sp = sk;
   uint32_t* slots = reinterpret_cast<uint32_t*>(sm + Lay::SLOTS);  // of two blocks in turn
-  const RowsShape sh{a.group, a.nkv, MR, 1, kSimtKeys, 1, {1, 1}};
+  const RowsShape sh{a.group, a.nkv, kSimtRows, 1, kSimtKeys, 1, {1, 1}};
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (!a.tail_ml) pdl_wait();  // beside the tail's kernel, which has waited for everything before it
   pdl_trigger();
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSM) cache_rows_simt_
     };
     __syncthreads();  // the last part's queries and slots are read
     look(p.b0);
-    for (int i = tid; i < MR * COLS; i += kSimtThreads) {
+    for (int i = tid; i < kSimtRows * COLS; i += kSimtThreads) {
       const int r = i / COLS, d = i % COLS * 4, v = p.v0 + r;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < p.nv)
@@ -396,13 +399,13 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtCtasPerSM) cache_rows_simt_
         const float2 y0 = both(o[i][c][0]), y1 = both(o[i][c][1]);
         const float4 y = make_float4(y0.x, y0.y, y1.x, y1.y);
         if (cut)
-          *part_at<HD, MR>(a, slot, 16 * c + tx, r) = y;
+          *part_at<HD, kSimtRows>(a, slot, 16 * c + tx, r) = y;
         else if (a.tail_ml)
           *reinterpret_cast<float4*>(a.whole_o + at * HD + 64 * c + 4 * tx) = y;
         else
           rows_finish<float, HD>(a, q.row0 + t, h, 64 * c + 4 * tx, y, m[i], l[i]);
       }
-      if (cut && tx == 0) *part_ml<MR>(a, slot, r) = make_float2(m[i], l[i]);
+      if (cut && tx == 0) *part_ml<kSimtRows>(a, slot, r) = make_float2(m[i], l[i]);
       if (a.tail_ml && tx == 0 && p.b0 == 0) a.whole_ml[at] = make_float2(m[i], cut ? kRowCut : l[i]);
     }
   }
@@ -414,18 +417,18 @@ cudaError_t join_rows(cudaStream_t st, const CacheRowsArgs& a, int sm_count) {
   return launch_pdl(st, dim3(4 * sm_count), dim3(kRowsJoinThreads), 0, 1, cache_rows_join_kernel<T, HD, ROWS>, a);
 }
 
-template <int HD, int MR>
+template <int HD>
 cudaError_t simt_rows(cudaStream_t st, CacheRowsArgs a, int sm_count) {
   a.least = 1;
-  const cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD, MR>::BYTES, 1,
-                                   cache_rows_simt_kernel<HD, MR>, a);
-  return e == cudaSuccess ? join_rows<float, HD, MR>(st, a, sm_count) : e;
+  const cudaError_t e = launch_pdl(st, dim3(a.ctas), dim3(kSimtThreads), SimtLayout<HD>::BYTES, 1,
+                                   cache_rows_simt_kernel<HD>, a);
+  return e == cudaSuccess ? join_rows<float, HD, kSimtRows>(st, a, sm_count) : e;
 }
 
 template <int HD>
 cudaError_t allow_simt() {
-  return cudaFuncSetAttribute(cache_rows_simt_kernel<HD, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              SimtLayout<HD, 64>::BYTES);
+  return cudaFuncSetAttribute(cache_rows_simt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SimtLayout<HD>::BYTES);
 }
 
 }  // namespace
@@ -434,7 +437,7 @@ int cache_rows_ctas(int sm_count, int bf16) {
   const int n = (bf16 ? 1 : kSimtCtasPerSM) * sm_count;
   return n < kRowsMaxCtas ? n : kRowsMaxCtas;
 }
-int cache_rows_slot_rows(int bf16) { return bf16 ? kTcTileRows : 64; }
+int cache_rows_slot_rows(int bf16) { return bf16 ? kTcTileRows : kSimtRows; }
 
 cudaError_t prepare_cache_rows() {
   cudaError_t e = allow_simt<128>();
@@ -444,7 +447,7 @@ cudaError_t prepare_cache_rows() {
 }
 
 cudaError_t launch_cache_rows(cudaStream_t st, const CacheRowsArgs& a, int bf16, int hd, int sm_count) {
-  if (!bf16) return hd == 128 ? simt_rows<128, 64>(st, a, sm_count) : simt_rows<64, 64>(st, a, sm_count);
+  if (!bf16) return hd == 128 ? simt_rows<128>(st, a, sm_count) : simt_rows<64>(st, a, sm_count);
   const cudaError_t e = launch_cache_rows_tc(st, a, hd);
   if (e != cudaSuccess) return e;
   return hd == 128 ? join_rows<__nv_bfloat16, 128, kTcTileRows>(st, a, sm_count)
