@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 // each where its 8 warps share one.  127 sequences of up to 701 keys, 8 heads x
 // 128 bf16, from cold caches: 53 us so, 39 with a warp a segment, as long as the
 // longest takes it, 37 with two, which is what it gets; the whole call beside a
-// shared prefix 113, 102 and 98 in a stream.  Latency bounds it: a warp's loads
+// shared prefix 113, 102 and 99 in a stream.  Latency bounds it: a warp's loads
 // and products follow one another.)
 constexpr int kTailWarps = 4;
 

@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kRowsJoinThreads) cache_rows_join_kernel(const
 // scalar arithmetic and one block an SM), operands from shared memory being the
 // rest; 5 sequences of up to 33 rows over up to 1,999 keys, 4/2 heads x 64, take
 // 21.6 us with the join, some 5 us a block of keys and part.  A tile of fewer
-// vectors costs as much as a full one: one token of few heads a KV head reads its
-// keys at a fraction of the bandwidth that sf_cache_attend has.
+// vectors costs as much as a full one: one token over 20,000 keys, 28/4 heads x
+// 128, takes 100 us here and 27 by sf_cache_attend.
 constexpr int kSimtRows = 64;
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;

@@ -27,11 +27,11 @@
 // (1,690, of which 512 are the exponentials at 32 a cycle) and its products' round
 // trips, a chain that two halves cannot hide altogether.  16 ragged sequences of
 // up to 1,021 rows over up to 8,191 keys, 32/8 heads: 518 to 540 us a call (61 %
-// of the cuBLAS rate); 4 of 288 rows over 4,096, 40/8 heads: 102 (50 %).  Scores of
+// of the cuBLAS rate); 4 of 288 rows over 4,096, 40/8 heads: 97 (52 %).  Scores of
 // both halves in one region of TMEM, so that a half's next scores come before its
 // product, take 2,700 cycles a block where the keys are in L2, but large calls are
-// no faster (1,280 TFLOP/s back to back either way), 4 of 288 rows 97, and a batch
-// with shared prefixes 99 instead of 98.
+// no faster (1,280 TFLOP/s back to back either way), 4 of 288 rows took 97 instead
+// of 102 then, and a batch with shared prefixes 99 instead of 98.
 //
 // P enters the second product of a wide tile rounded to bf16, half a step of 2^-8
 // a weight, the output type's own, in calls that give a thread block more than
